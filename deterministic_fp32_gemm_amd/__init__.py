@@ -5,6 +5,9 @@ every chunk n = ti*P + p of step ti, row i < C and column c < hd, d_u[n, i, c] +
 acc = fmaf(x[n, j, i], d_dv[n, j, c], acc) over j = 0..C-1 from +0 and one separately rounded add. Phase A, the
 consumer of the updated d_u (page "... gx_pa2_cuda.py", gx_pa2_kernel), is in the same library. The C ABI is in
 include/sdm_gx_gemm.h and include/sdm_gx_pa2.h; the functions below carry the same names and only marshal arguments.
+
+The gated delta rule (gdr_forward, gdr_backward, gdr_step) and the block norm (norm_forward, norm_backward) are in
+libsdm_delta: include/sdm_gdr.h, include/sdm_nrm.h and delta.py.
 """
 
 from ._binding import (  # noqa: F401
@@ -60,3 +63,11 @@ from ._binding import (  # noqa: F401
     sdm_pa2_steps,
 )
 from .step import make_step, tensor_layout  # noqa: F401
+from .delta import (  # noqa: F401
+    gdr_backward,
+    gdr_forward,
+    gdr_step,
+    norm_backward,
+    norm_forward,
+)
+from .delta import load as load_delta  # noqa: F401

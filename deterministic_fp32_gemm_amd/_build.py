@@ -1,10 +1,11 @@
-"""Ahead-of-time build of libsdm_gx_gemm.so for gfx950 with hipcc (in-tree, no JIT cache)."""
+"""Ahead-of-time build of libsdm_gx_gemm.so and libsdm_delta.so for gfx950 with hipcc (in-tree, no JIT cache)."""
 
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -12,6 +13,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libsdm_gx_gemm.so")
 SOURCES = ("gx_gemm_kernel.hip", "gx_gemm_mfma.hip", "gx_gemm_api.cpp", "gx_pa2_kernel.hip", "gx_pa2_api.cpp")
+# the gated delta rule and the block norm: a library of their own
+DELTA_LIB_PATH = os.path.join(PKG, "libsdm_delta.so")
+DELTA_SOURCES = ("gdr_chunk.hip", "gdr_scan.hip", "gdr_grad.hip", "gdr_step.hip", "gdr_api.cpp", "nrm_kernel.hip",
+                 "nrm_api.cpp")
+JOBS = 6    # compilers at once
 
 # Numerics-relevant flags: no contraction or fast-math (the chain's fmaf and the final add are what runs), f32
 # denormals kept, and no packed-FP32 instructions (scalar v_fma_f32 / v_fmac_f32 only).
@@ -36,28 +42,36 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build libsdm_gx_gemm)")
 
 
-def build(out: str = LIB_PATH, verbose: bool = False) -> str:
+def build(out: str = LIB_PATH, verbose: bool = False, sources=SOURCES) -> str:
     """Compile every source for gfx950 and link the shared library (always recompiles)."""
-    objs = []
     tmpdir = os.path.join(PKG, "_objs")
     os.makedirs(tmpdir, exist_ok=True)
     cc = hipcc()
-    for src in SOURCES:
-        obj = os.path.join(tmpdir, os.path.splitext(src)[0] + ".o")
-        lang = ["-x", "hip"] if src.endswith(".hip") else []
-        cmd = [cc, *HIP_FLAGS, "-I", INCLUDE, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+
+    def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-        objs.append(obj)
+
+    def one(src):
+        obj = os.path.join(tmpdir, os.path.splitext(src)[0] + ".o")
+        lang = ["-x", "hip"] if src.endswith(".hip") else []
+        run([cc, *HIP_FLAGS, "-I", INCLUDE, *lang, "-c", os.path.join(CSRC, src), "-o", obj])
+        return obj
+
+    with ThreadPoolExecutor(JOBS) as pool:
+        objs = list(pool.map(one, sources))
     tmp = out + ".tmp"
-    cmd = [cc, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    run([cc, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs])
     os.replace(tmp, out)
     return out
 
 
+def build_delta(out: str = DELTA_LIB_PATH, verbose: bool = False) -> str:
+    """The same for the gated delta rule and the block norm."""
+    return build(out, verbose, DELTA_SOURCES)
+
+
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_delta(verbose=True))

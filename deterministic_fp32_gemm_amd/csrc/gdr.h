@@ -1,0 +1,50 @@
+// Internal interface between the gated-delta-rule kernels and their host entry points (not the C ABI).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "../../include/sdm_gdr.h"
+
+namespace sdm_delta {
+
+constexpr int kChunk = 64;      // tokens a chunk
+
+// Where a call's intermediate results live. A chunk slot is one chunk of one sequence; "fragments" are matrix-core
+// operand tiles, [16-row tile][32-wide k block][bfloat16 part][64 lanes][8 values].
+struct GdrWork {
+    float* tok;         // [slots][Hv][kTokFields][64]: per-token factors
+    uint16_t* inv;      // [slots][Hv] fragments of (I + A)^-1, 64 x 64
+    uint16_t* invt;     // of its transpose (backward)
+    uint16_t* pm;       // of P (forward) or P^T (backward), 64 x 64
+    uint16_t* kt;       // [slots][Hk] fragments of K^T, dkp x 64
+    uint16_t* qt;       // of Q^T (backward)
+    float* st;          // [slots][Hv][dk][dv]: each chunk's entering state (backward)
+    float* dst;         // [slots][Hv][dk][dv]: gradient of each chunk's last state (backward)
+    float* u;           // [slots][Hv][64][dv] (backward)
+    float* dr;          // [slots][Hv][64][dv] (backward)
+    float* dqp;         // [slots][Hv][64][dk] per-value-head parts of dq and dk, when value heads share a q/k head
+    float* dkp;
+};
+
+enum { kTokG = 0, kTokGlo, kTokEg, kTokLast, kTokBeta, kTokFields };
+
+struct GdrLaunch {
+    sdm_gdr_args_t a;
+    GdrWork w;
+    int32_t slots;      // chunk slots
+    int32_t dkp;        // dk padded to 64, 128 or 256
+    int32_t cols;       // state columns a workgroup of the scans owns: 16 or 32
+    int32_t vec_qk, vec_v;      // rows of q and k / v, o, d_o and their gradients start on 16-byte boundaries
+    int32_t vec_st;     // state rows do
+};
+
+// bfloat16 parts that hold an element of a type exactly: 3, 1, 2
+inline int parts_of(int dtype) { return dtype == SDM_F32 ? 3 : dtype == SDM_BF16 ? 1 : 2; }
+// bfloat16 parts of P: what the type of o can show
+inline int pm_parts(int dtype) { return dtype == SDM_F32 ? 3 : 2; }
+
+hipError_t launch_gdr_forward(const GdrLaunch& g, hipStream_t stream);
+hipError_t launch_gdr_backward(const GdrLaunch& g, hipStream_t stream);
+hipError_t launch_gdr_step(const sdm_gdr_step_args_t& a, bool vec, hipStream_t stream);
+
+}  // namespace sdm_delta

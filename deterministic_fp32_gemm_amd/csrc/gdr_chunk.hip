@@ -1,0 +1,255 @@
+// What a chunk's tokens alone determine: the decays, P = scale (Q K^T) decay, the inverse of I + A, and K and Q
+// transposed, all laid out as matrix-core fragments for the scans.
+//
+// With G the running sum of g in a chunk, u of the chunk solves (I + A) U = R, A_ij = beta_i exp(G_i - G_j) k_i . k_j
+// for j < i, R = beta (V - exp(G) K S). T = (I + A)^-1 is unit lower triangular. The 16 x 16 blocks on its diagonal
+// come from forward substitution, one wavefront each; two levels of T21 = -T22 A21 T11 give the rest on the float32
+// matrix cores. (Products of powers of A would need no substitution, but lose everything when keys repeat: the powers
+// grow to 10^17 before they cancel.)
+//
+// G is summed in float64 and kept as two float32: a token that forgets almost everything (g = -100, or -inf, which is
+// held at -1000: exp gives 0 either way) leaves the differences after it exact.
+//
+// One workgroup per chunk and value head. Bounded by latency: about 1 MFLOP of matrix work against two chains of 16
+// substitution steps; 4 workgroups share a CU and fill each other's gaps.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdr_device.h"
+
+namespace sdm_delta {
+namespace {
+
+constexpr int kLd = 68;     // row of a 64 x 64 float32 matrix in LDS
+
+template <int DT, int DKP, bool BWD>
+__global__ __launch_bounds__(256) void gdr_chunk(const GdrLaunch g) {
+    constexpr int NP = kParts<DT>, PP = BWD ? 3 : kOutParts<DT>, NKB = DKP / 32;
+    using T = elem_t<DT>;
+    __shared__ alignas(16) float As[64][kLd];
+    __shared__ alignas(16) float Ts[64][kLd];
+    __shared__ float Gh[64], Gl[64], Be[64];
+    const sdm_gdr_args_t& a = g.a;
+    int seq, chunk;
+    Seq s;
+    const int slot = blockIdx.x, hv = blockIdx.y, r = static_cast<int>(a.Hv / a.Hk), hk = hv / r;
+    if (!owner(a, slot, seq, chunk, s)) return;
+    const int t0 = chunk * kChunk, n = min(kChunk, s.len - t0), dk = static_cast<int>(a.dk);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = lane & 15, grp = lane >> 4;
+    const int64_t sv = static_cast<int64_t>(slot) * a.Hv + hv;
+
+    if (wave == 0) {
+        double x = 0.0;
+        float be = 0.f;
+        if (lane < n) {
+            const float gt = rows_at<const float>(a.g, s, hv)[(t0 + lane) * a.g.token];
+            x = gt < -1000.f ? -1000.f : gt;
+            be = rows_at<const float>(a.beta, s, hv)[(t0 + lane) * a.beta.token];
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double y = __shfl_up(x, d, 64);
+            if (lane >= d) x += y;
+        }
+        const double last = __shfl(x, 63, 64);
+        const float hi = static_cast<float>(x), lo = static_cast<float>(x - hi);
+        Gh[lane] = hi;
+        Gl[lane] = lo;
+        Be[lane] = be;
+        float* tok = g.w.tok + sv * (kTokFields * 64);
+        tok[kTokG * 64 + lane] = hi;
+        tok[kTokGlo * 64 + lane] = lo;
+        tok[kTokEg * 64 + lane] = expf(hi) * (1.f + lo);
+        tok[kTokLast * 64 + lane] = expf(static_cast<float>(last - x));
+        tok[kTokBeta * 64 + lane] = be;
+    }
+
+    // K K^T and Q K^T, row tile `wave`. All column tiles, also those above the diagonal: the last wavefront needs
+    // them all, so leaving them out of the others saves no time
+    const T* kr = rows_at<const T>(a.k, s, hk) + t0 * a.k.token;
+    const T* qr = rows_at<const T>(a.q, s, hk) + t0 * a.q.token;
+    f32x4 kk[4], qk[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int ti = wave * 16 + row;
+#pragma unroll 2
+    for (int kb = 0; kb < NKB; ++kb) {
+        const int c = kb * 32 + grp * 8;
+        Raw<DT> x;
+        Frag<NP> qf, kf;
+        load_raw<DT>(x, qr + ti * a.q.token, c, ti < n ? dk : 0, g.vec_qk);
+        raw_frag<DT>(qf, x);
+        load_raw<DT>(x, kr + ti * a.k.token, c, ti < n ? dk : 0, g.vec_qk);
+        raw_frag<DT>(kf, x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int tj = j * 16 + row;
+            Frag<NP> bf;
+            load_raw<DT>(x, kr + tj * a.k.token, c, tj < n ? dk : 0, g.vec_qk);
+            raw_frag<DT>(bf, x);
+            mma<3>(kk[j], kf, bf);
+            mma<3>(qk[j], qf, bf);
+        }
+    }
+    lds_barrier();
+
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = wave * 16 + grp * 4 + e, c = j * 16 + row;
+            float av = 0.f, pv = 0.f;
+            if (j <= wave && c <= i) {
+                const float d = expf((Gh[i] - Gh[c]) + (Gl[i] - Gl[c]));
+                pv = a.scale * qk[j][e] * d;
+                if (c < i) av = Be[i] * kk[j][e] * d;
+            }
+            As[i][c] = av;
+            Ts[i][c] = pv;
+        }
+    lds_barrier();
+
+    // P, row tiles in order; the backward's P^T, of columns
+    {
+        uint16_t* out = g.w.pm + sv * (PP * 4096);
+        Frag<PP> f;
+        float v[8];
+        const int t = wave;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int m = t * 16 + row, k = kb * 32 + grp * 8 + e;
+                v[e] = BWD ? Ts[k][m] : Ts[m][k];
+            }
+            split8(f, v);
+            store_frag<PP>(frag_at<PP>(out, t, kb, 2), f);
+        }
+    }
+    lds_barrier();
+
+    // the diagonal blocks of T: lane c solves column c (the four lane groups repeat each other)
+    {
+        float t[16];
+        const int b = wave * 16;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = i == row ? 1.f : 0.f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) v = fmaf(-As[b + i][b + j], t[j], v);
+            t[i] = v;
+        }
+        // this wavefront's 16 rows of T, zero off the diagonal block until the levels below fill them
+#pragma unroll
+        for (int i = 0; i < 16; ++i) Ts[b + i][lane] = 0.f;
+        if (grp == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) Ts[b + i][b + row] = t[i];
+        }
+    }
+    lds_barrier();
+    // 16 -> 32: wavefronts 0 and 1, one 32 x 32 block each
+    if (wave < 2) {
+        const int b = wave * 32;
+        f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x = __builtin_amdgcn_mfma_f32_16x16x4f32(As[b + 16 + row][b + grp * 4 + e], Ts[b + grp * 4 + e][b + row], x, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            y = __builtin_amdgcn_mfma_f32_16x16x4f32(-Ts[b + 16 + row][b + 16 + grp * 4 + e], x[e], y, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Ts[b + 16 + grp * 4 + e][b + row] = y[e];
+    }
+    lds_barrier();
+    // 32 -> 64: wavefront (tile row, tile column) of the lower left 32 x 32; the blocks above the diagonal are zero
+    {
+        const int tr = wave >> 1, tc = wave & 1;
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x = __builtin_amdgcn_mfma_f32_16x16x4f32(As[32 + m * 16 + row][k * 16 + grp * 4 + e],
+                                                             Ts[k * 16 + grp * 4 + e][tc * 16 + row], x, 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y = __builtin_amdgcn_mfma_f32_16x16x4f32(-Ts[32 + tr * 16 + row][32 + m * 16 + grp * 4 + e], x[e], y, 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Ts[32 + tr * 16 + grp * 4 + e][tc * 16 + row] = y[e];
+    }
+    lds_barrier();
+    {
+        Frag<3> f;
+        float v[8];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const int m = wave * 16 + row, k = kb * 32 + grp * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = Ts[m][k + e];
+            split8(f, v);
+            store_frag<3>(frag_at<3>(g.w.inv + sv * (3 * 4096), wave, kb, 2), f);
+            if constexpr (BWD) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = Ts[k + e][m];
+                split8(f, v);
+                store_frag<3>(frag_at<3>(g.w.invt + sv * (3 * 4096), wave, kb, 2), f);
+            }
+        }
+    }
+
+    // K^T, and Q^T in the backward: once per q/k head
+    if (hv % r == 0) {
+        const int64_t sk = static_cast<int64_t>(slot) * a.Hk + hk;
+        for (int i = wave; i < DKP / 16 * 2; i += 4) {
+            const int t = i >> 1, kb = i & 1, c = t * 16 + row;
+            float v[8];
+            Frag<NP> f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = kb * 32 + grp * 8 + e;
+                v[e] = j < n && c < dk ? static_cast<float>(kr[j * a.k.token + c]) : 0.f;
+            }
+            split8(f, v);
+            store_frag<NP>(frag_at<NP>(g.w.kt + sk * (NP * 64 * DKP), t, kb, 2), f);
+            if constexpr (BWD) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = kb * 32 + grp * 8 + e;
+                    v[e] = j < n && c < dk ? static_cast<float>(qr[j * a.q.token + c]) : 0.f;
+                }
+                split8(f, v);
+                store_frag<NP>(frag_at<NP>(g.w.qt + sk * (NP * 64 * DKP), t, kb, 2), f);
+            }
+        }
+    }
+}
+
+template <int DT, bool BWD>
+hipError_t run(const GdrLaunch& g, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(g.slots), static_cast<unsigned>(g.a.Hv));
+    if (g.dkp == 64)
+        gdr_chunk<DT, 64, BWD><<<grid, 256, 0, s>>>(g);
+    else if (g.dkp == 128)
+        gdr_chunk<DT, 128, BWD><<<grid, 256, 0, s>>>(g);
+    else
+        gdr_chunk<DT, 256, BWD><<<grid, 256, 0, s>>>(g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gdr_chunk(const GdrLaunch& g, bool backward, hipStream_t s) {
+    switch (g.a.dtype) {
+        case SDM_F32: return backward ? run<0, true>(g, s) : run<0, false>(g, s);
+        case SDM_BF16: return backward ? run<1, true>(g, s) : run<1, false>(g, s);
+        default: return backward ? run<2, true>(g, s) : run<2, false>(g, s);
+    }
+}
+
+}  // namespace sdm_delta

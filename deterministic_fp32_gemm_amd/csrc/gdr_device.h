@@ -1,0 +1,221 @@
+// Device pieces of the gated-delta-rule kernels: split operands, matrix-core steps, chunk geometry.
+//
+// Split operands. The bfloat16 matrix cores run 16 times the float32 ones' rate. A float32 x is h + m + l with
+// h = bf16(x), m = bf16(x - h), l = bf16(x - h - m), each difference exact: 24 bits. A product of two such sums keeps
+// the part products whose parts' numbers add up to 2 or less; what is left out is below 2^-25 of the product, so a
+// product costs 6 matrix-core steps and is as exact as float32's own (a quarter of the time of a float32 matrix-core
+// product). Elements that are bfloat16 to begin with are one part (3 steps against a float32 operand), float16 ones
+// two. ORD = 2 leaves out the third parts where only a 16-bit result depends on the product (2^-17).
+//
+// Fragments. One matrix-core operand of v_mfma_f32_16x16x32_bf16: lane l holds row l % 16, elements
+// 8 (l / 16) .. + 7 of a 32-wide block of the summed axis. Both operands have this layout, each with its summed axis
+// contiguous. Results: lane l holds rows 4 (l / 16) .. + 3 of column l % 16.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "delta_types.h"
+#include "gdr.h"
+
+namespace sdm_delta {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+template <int DT> constexpr int kParts = DT == 0 ? 3 : DT == 1 ? 1 : 2;
+template <int DT> constexpr int kOutParts = DT == 0 ? 3 : 2;
+
+template <int N>
+struct Frag {
+    bf16x8 p[N];
+};
+
+// f as N bfloat16 parts, largest first
+template <int N>
+__device__ __forceinline__ void split8(Frag<N>& o, const float (&f)[8]) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = f[i];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.p[n][i] = static_cast<__bf16>(r[i]);
+        if (n + 1 < N) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] -= static_cast<float>(o.p[n][i]);
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void split4(bf16x4 (&o)[N], f32x4 f) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][i] = static_cast<__bf16>(f[i]);
+        if (n + 1 < N) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] -= static_cast<float>(o[n][i]);
+        }
+    }
+}
+
+// acc += a b, the part products of order below ORD, smallest first
+template <int ORD, int NA, int NB>
+__device__ __forceinline__ void mma(f32x4& acc, const Frag<NA>& a, const Frag<NB>& b) {
+#pragma unroll
+    for (int s = ORD - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], acc, 0, 0, 0);
+}
+
+// Eight elements of a row as they lie in memory, kept until they are needed: a prefetch costs no more registers than
+// its bytes.
+template <int DT>
+struct Raw {
+    u32x4 w[DT == 0 ? 2 : 1];
+};
+template <int DT>
+__device__ __forceinline__ void load_raw(Raw<DT>& o, const elem_t<DT>* __restrict__ row, int c, int lim, bool vec) {
+    if (vec && c + 8 <= lim) {
+        const u32x4* p = reinterpret_cast<const u32x4*>(row + c);
+        o.w[0] = p[0];
+        if constexpr (DT == 0) o.w[1] = p[1];
+        return;
+    }
+    if (c >= lim) {
+        o.w[0] = u32x4{0, 0, 0, 0};
+        if constexpr (DT == 0) o.w[1] = u32x4{0, 0, 0, 0};
+        return;
+    }
+    if constexpr (DT == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.w[i / 4][i % 4] = c + i < lim ? __float_as_uint(row[c + i]) : 0u;
+    } else {
+        const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = c + 2 * i < lim ? r[c + 2 * i] : 0u, hi = c + 2 * i + 1 < lim ? r[c + 2 * i + 1] : 0u;
+            o.w[0][i] = lo | hi << 16;
+        }
+    }
+}
+template <int DT>
+__device__ __forceinline__ void raw_floats(float (&f)[8], const Raw<DT>& r) {
+    if constexpr (DT == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.w[i / 4][i % 4]);
+    } else {
+        typedef elem_t<DT> t8 __attribute__((ext_vector_type(8)));
+        const t8 a = __builtin_bit_cast(t8, r.w[0]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(a[i]);
+    }
+}
+template <int DT>
+__device__ __forceinline__ void raw_frag(Frag<kParts<DT>>& o, const Raw<DT>& r) {
+    if constexpr (DT == 1) {
+        o.p[0] = __builtin_bit_cast(bf16x8, r.w[0]);
+    } else {
+        float f[8];
+        raw_floats<DT>(f, r);
+        split8(o, f);
+    }
+}
+
+// A fragment stored as [part][64 lanes][8]: tile t, k block kb of a matrix of `kbs` k blocks.
+template <int N>
+__device__ __forceinline__ uint16_t* frag_at(uint16_t* base, int t, int kb, int kbs) {
+    return base + static_cast<int64_t>(t * kbs + kb) * N * 512;
+}
+template <int N>
+__device__ __forceinline__ void load_frag(Frag<N>& o, const uint16_t* __restrict__ at) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        o.p[n] = *reinterpret_cast<const bf16x8*>(at + n * 512 + (threadIdx.x & 63) * 8);
+}
+template <int N>
+__device__ __forceinline__ void store_frag(uint16_t* at, const Frag<N>& f) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x8*>(at + n * 512 + (threadIdx.x & 63) * 8) = f.p[n];
+}
+
+// A split matrix in LDS: [part][rows][LD], the summed axis contiguous. LD is 8 more than a multiple of 32, so that the
+// 16 rows of a fragment start on different banks.
+template <int N, int ROWS, int LD>
+struct Tile {
+    alignas(16) __bf16 v[N][ROWS][LD];
+    __device__ __forceinline__ void frag(Frag<N>& o, int row0, int k0) const {
+        const int l = threadIdx.x & 63;
+#pragma unroll
+        for (int n = 0; n < N; ++n) o.p[n] = *reinterpret_cast<const bf16x8*>(&v[n][row0 + (l & 15)][k0 + 8 * (l >> 4)]);
+    }
+    // a result tile, transposed: its column is the row here
+    __device__ __forceinline__ void put(int row0, int k0, const f32x4& d) {
+        const int l = threadIdx.x & 63;
+        bf16x4 s[N];
+        split4<N>(s, d);
+#pragma unroll
+        for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x4*>(&v[n][row0 + (l & 15)][k0 + 4 * (l >> 4)]) = s[n];
+    }
+};
+
+// One sequence: its first token, length and first chunk slot.
+struct Seq {
+    int64_t base;       // of its row's first token: strides.batch * b is added by rows_at
+    int32_t b, start, len, slot;
+};
+__device__ __forceinline__ Seq sequence(const sdm_gdr_args_t& a, int i) {
+    Seq s;
+    if (a.cu_seqlens) {
+        const int T = static_cast<int>(a.T);
+        const int lo = min(max(a.cu_seqlens[i], 0), T), hi = min(max(a.cu_seqlens[i + 1], lo), T);
+        s.b = 0;
+        s.start = lo;
+        s.len = hi - lo;
+        s.slot = lo / kChunk + i;
+    } else {
+        s.b = i;
+        s.start = 0;
+        s.len = static_cast<int>(a.T);
+        s.slot = i * ((s.len + kChunk - 1) / kChunk);
+    }
+    s.base = 0;
+    return s;
+}
+// The sequence that owns a chunk slot and the chunk's number in it; false for a slot that none uses.
+__device__ __forceinline__ bool owner(const sdm_gdr_args_t& a, int slot, int& seq, int& chunk, Seq& s) {
+    if (a.cu_seqlens) {
+        int lo = 0, hi = static_cast<int>(a.nseq) - 1;      // the last run whose first slot is not past this one
+        const int T = static_cast<int>(a.T);
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (min(max(a.cu_seqlens[mid], 0), T) / kChunk + mid <= slot)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        seq = lo;
+    } else {
+        seq = slot / ((static_cast<int>(a.T) + kChunk - 1) / kChunk);
+    }
+    s = sequence(a, seq);
+    chunk = slot - s.slot;
+    return chunk >= 0 && static_cast<int64_t>(chunk) * kChunk < s.len;
+}
+
+// The first element of a sequence's row of one head; tokens follow at r.token.
+template <class T>
+__device__ __forceinline__ T* rows_at(const sdm_rows_t& r, const Seq& s, int head) {
+    return static_cast<T*>(r.data) + s.b * r.batch + s.start * r.token + head * r.head;
+}
+
+// Consecutive logical workgroups on one XCD (hardware deals workgroup ids round the 8 XCDs): those that share a head's
+// chunks then share an L2. n logical workgroups run on a grid of 8 * ceil(n / 8); false past the last.
+__device__ __forceinline__ bool on_one_xcd(int n, int& id) {
+    id = static_cast<int>((blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3));
+    return id < n;
+}
+
+}  // namespace sdm_delta

@@ -1,0 +1,148 @@
+// The recurrent form of the gated delta rule: one token (or the few of a draft) of each stream against its state,
+// updated in place.
+//
+//     S = exp(g) S;  u = beta (v - S^T k);  S = S + k u^T;  o = scale S^T q
+//
+// Bounded by the state's bytes, once in and once out (2 x 64 KB a head at dk = dv = 128). A workgroup owns 4 CT columns
+// of one stream and head: each thread 4 columns of dk / (256 / CT) rows, held in registers from the load to the store
+// whatever the number of tokens; the sums over dk go through LDS. Columns of S never meet, so small batches take
+// CT = 8 (32 columns a workgroup, four times the workgroups of CT = 32).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdr_device.h"
+
+namespace sdm_delta {
+namespace {
+
+template <int DT, int CT, int ROWS>
+__global__ __launch_bounds__(256) void gdr_step(const sdm_gdr_step_args_t a, const bool vec, const int slices) {
+    using T = elem_t<DT>;
+    constexpr int RG = 256 / CT, COLS = CT * 4;     // row groups, columns
+    __shared__ float K[256], Q[256];
+    __shared__ f32x4 red[RG][CT];
+    const int dk = static_cast<int>(a.dk), dv = static_cast<int>(a.dv), Hv = static_cast<int>(a.Hv);
+    const int slice = blockIdx.x % slices, bh = blockIdx.x / slices, b = bh / Hv, hv = bh % Hv;
+    const int hk = hv / (Hv / static_cast<int>(a.Hk));
+    const int ct = threadIdx.x % CT, rg = threadIdx.x / CT, c = slice * COLS + ct * 4;
+    const int64_t slot = a.slots ? a.slots[b] : b;
+    T* o = static_cast<T*>(a.o.data) + b * a.o.batch + hv * a.o.head;
+    if (slot < 0 || slot >= a.pool) {
+        for (int64_t t = 0; t < a.T; ++t)
+            for (int i = threadIdx.x; i < COLS; i += 256)
+                if (slice * COLS + i < dv) o[t * a.o.token + slice * COLS + i] = static_cast<T>(0.f);
+        return;
+    }
+    float* st = a.state + (slot * Hv + hv) * dk * static_cast<int64_t>(dv);
+    f32x4 S[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int d = i * RG + rg;
+        S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (d < dk) {
+            const float* p = st + static_cast<int64_t>(d) * dv + c;
+            if (vec) {
+                if (c < dv) S[i] = *reinterpret_cast<const f32x4*>(p);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < dv) S[i][e] = p[e];
+            }
+        }
+    }
+    const T* qr = static_cast<const T*>(a.q.data) + b * a.q.batch + hk * a.q.head;
+    const T* kr = static_cast<const T*>(a.k.data) + b * a.k.batch + hk * a.k.head;
+    const T* vr = static_cast<const T*>(a.v.data) + b * a.v.batch + hv * a.v.head;
+    const float* gr = static_cast<const float*>(a.g.data) + b * a.g.batch + hv * a.g.head;
+    const float* br = static_cast<const float*>(a.beta.data) + b * a.beta.batch + hv * a.beta.head;
+    for (int64_t t = 0; t < a.T; ++t) {
+        if (static_cast<int>(threadIdx.x) < dk) {
+            K[threadIdx.x] = static_cast<float>(kr[t * a.k.token + threadIdx.x]);
+            Q[threadIdx.x] = static_cast<float>(qr[t * a.q.token + threadIdx.x]);
+        }
+        const float eg = expf(gr[t * a.g.token]), beta = br[t * a.beta.token];
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < dv) v[e] = static_cast<float>(vr[t * a.v.token + c + e]);
+        lds_barrier();
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int d = i * RG + rg;
+            if (d >= dk) continue;
+            S[i] *= eg;
+            x += S[i] * K[d];
+        }
+        red[rg][ct] = x;
+        lds_barrier();
+        x = red[0][ct];
+#pragma unroll
+        for (int i = 1; i < RG; ++i) x += red[i][ct];
+        const f32x4 u = beta * (v - x);
+        x = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int d = i * RG + rg;
+            if (d >= dk) continue;
+            S[i] += K[d] * u;
+            x += S[i] * Q[d];
+        }
+        lds_barrier();
+        red[rg][ct] = x;
+        lds_barrier();
+        if (rg == 0) {
+#pragma unroll
+            for (int i = 1; i < RG; ++i) x += red[i][ct];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < dv) o[t * a.o.token + c + e] = static_cast<T>(a.scale * x[e]);
+        }
+        // K, Q are read before the last barrier; red is written again only after the next token's first
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int d = i * RG + rg;
+        if (d >= dk) continue;
+        float* p = st + static_cast<int64_t>(d) * dv + c;
+        if (vec) {
+            if (c < dv) *reinterpret_cast<f32x4*>(p) = S[i];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < dv) p[e] = S[i][e];
+        }
+    }
+}
+
+template <int DT>
+hipError_t run(const sdm_gdr_step_args_t& a, bool vec, hipStream_t s) {
+    const int64_t bh = a.B * a.Hv;
+    const bool narrow = bh * ((a.dv + 127) / 128) < 1024;
+    const int cols = narrow ? 32 : 128, slices = static_cast<int>((a.dv + cols - 1) / cols);
+    const unsigned grid = static_cast<unsigned>(bh * slices);
+    if (narrow) {
+        if (a.dk <= 128)
+            gdr_step<DT, 8, 4><<<grid, 256, 0, s>>>(a, vec, slices);
+        else
+            gdr_step<DT, 8, 8><<<grid, 256, 0, s>>>(a, vec, slices);
+    } else {
+        if (a.dk <= 128)
+            gdr_step<DT, 32, 16><<<grid, 256, 0, s>>>(a, vec, slices);
+        else
+            gdr_step<DT, 32, 32><<<grid, 256, 0, s>>>(a, vec, slices);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gdr_step(const sdm_gdr_step_args_t& a, bool vec, hipStream_t s) {
+    switch (a.dtype) {
+        case SDM_F32: return run<0>(a, vec, s);
+        case SDM_BF16: return run<1>(a, vec, s);
+        default: return run<2>(a, vec, s);
+    }
+}
+
+}  // namespace sdm_delta

@@ -1,0 +1,21 @@
+// Internal interface between the norm kernels and their host entry points (not the C ABI).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "../../include/sdm_nrm.h"
+
+namespace sdm_delta {
+
+struct NrmPlan {
+    int threads;    // of a workgroup, which takes one row at a time
+    int vecs;       // groups of 8 columns a thread: threads * vecs * 8 >= D
+    int groups;     // workgroups; workgroup i takes rows i, i + groups, ...
+    bool vec;       // rows on 16-byte boundaries
+};
+
+hipError_t launch_nrm_forward(const sdm_nrm_args_t& a, const NrmPlan& p, hipStream_t stream);
+// part: float [groups][3][D], the workgroups' sums of the three weights' gradients
+hipError_t launch_nrm_backward(const sdm_nrm_args_t& a, const NrmPlan& p, float* part, hipStream_t stream);
+
+}  // namespace sdm_delta

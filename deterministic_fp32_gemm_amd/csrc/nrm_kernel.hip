@@ -1,0 +1,310 @@
+// The norms after a block and before the next with the block's gate and residual scale (sdm_nrm.h), forward and
+// backward, for gfx950.
+//
+// What bounds them is memory: the forward reads x, o, z and writes x', y, the backward reads dx', dy, x', o, z and
+// writes dx, do, dz, each once. A row lives in the registers of one workgroup from its load to its store, so the two
+// norms of a row, which depend on each other, cost two workgroup reductions and no second pass. Workgroups take many
+// rows each: the weights stay in registers, and in the backward so do their gradients' sums, which leave once per
+// workgroup as partial sums that a second kernel adds in workgroup order.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "delta_types.h"
+#include "nrm.h"
+
+namespace sdm_delta {
+namespace {
+
+// The sum of v over the workgroup, in an order set by the lane and wavefront numbers alone. `buf` alternates between
+// two LDS rows: a row is written again only after a barrier that follows its last read.
+template <int NT>
+__device__ __forceinline__ float row_sum(float v, float (*red)[16], int buf) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) red[buf][threadIdx.x >> 6] = v;
+        lds_barrier();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < NT / 64; ++i) v += red[buf][i];
+    }
+    return v;
+}
+
+// act(z) and act'(z). The 16-bit types take the hardware's exponential and reciprocal (1 ulp of float32), float32 the
+// library's.
+template <int DT>
+__device__ __forceinline__ void gate(float z, int act, float& a, float& d) {
+    float p;
+    if constexpr (DT == 0)
+        p = 1.f / (1.f + expf(-z));
+    else
+        p = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+    if (act == SDM_ACT_SIGMOID) {
+        a = p;
+        d = p * (1.f - p);
+    } else {
+        a = z * p;
+        d = p * (1.f + z * (1.f - p));
+    }
+}
+
+template <int DT, int WT, int NT, int NV>
+__global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a, const bool vec) {
+    using T = elem_t<DT>;
+    using W = elem_t<WT>;
+    __shared__ float red[2][16];
+    const int D = static_cast<int>(a.D);
+    const float inv = 1.f / static_cast<float>(D);
+    const bool has_o = a.o != nullptr, has_x = a.x != nullptr, has_y = a.w_pre != nullptr;
+    float w1[NV][8], w2[NV][8], sc[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
+        if (has_o) {
+            load8(w1[v], static_cast<const W*>(a.w_post), c, D, vec);
+            load8(sc[v], static_cast<const W*>(a.scale), c, D, vec);
+        }
+        if (has_y) load8(w2[v], static_cast<const W*>(a.w_pre), c, D, vec);
+    }
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        float x[NV][8], o[NV][8], z[NV][8];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
+            if (has_o) load8(o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D, vec);
+            if (a.act != SDM_ACT_NONE) load8(z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D, vec);
+            if (has_x) {
+                load8(x[v], static_cast<const T*>(a.x) + r * a.ld_x, c, D, vec);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[v][i] = 0.f;
+            }
+        }
+        float r1 = 0.f, r2 = 0.f;
+        if (has_o) {
+            float s = 0.f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s = fmaf(o[v][i], o[v][i], s);
+            r1 = 1.f / sqrtf(fmaf(row_sum<NT>(s, red, 0), inv, a.eps));
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float g = 1.f, d;
+                    if (a.act != SDM_ACT_NONE) gate<DT>(z[v][i], a.act, g, d);
+                    // rounded to the residual's type here: the second norm is that of the stored row
+                    x[v][i] = static_cast<float>(static_cast<T>(fmaf(sc[v][i], o[v][i] * r1 * w1[v][i] * g, x[v][i])));
+                }
+                store8(static_cast<T*>(a.x_new) + r * a.ld_xn, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, vec,
+                       x[v]);
+            }
+        }
+        if (has_y) {
+            float s = 0.f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s = fmaf(x[v][i], x[v][i], s);
+            r2 = 1.f / sqrtf(fmaf(row_sum<NT>(s, red, 1), inv, a.eps));
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[v][i] = x[v][i] * r2 * w2[v][i];
+                store8(static_cast<T*>(a.y) + r * a.ld_y, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, vec, x[v]);
+            }
+        }
+        if (threadIdx.x == 0) {
+            a.rstd[2 * r] = r1;
+            a.rstd[2 * r + 1] = r2;
+        }
+        // a call with one norm reads and writes one LDS row only: keep a fast wavefront out of the next row's
+        if (NT > 64 && has_o != has_y) lds_barrier();
+    }
+}
+
+template <int DT, int WT, int NT, int NV>
+__global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, const bool vec, float* __restrict__ part) {
+    using T = elem_t<DT>;
+    using W = elem_t<WT>;
+    __shared__ float red[2][16];
+    const int D = static_cast<int>(a.D);
+    const float inv = 1.f / static_cast<float>(D);
+    const bool has_o = a.o != nullptr, has_y = a.w_pre != nullptr, has_up = a.dxn != nullptr;
+    float w1[NV][8], w2[NV][8], sc[NV][8], s1[NV][8], s2[NV][8], s3[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
+        if (has_o) {
+            load8(w1[v], static_cast<const W*>(a.w_post), c, D, vec);
+            load8(sc[v], static_cast<const W*>(a.scale), c, D, vec);
+        }
+        if (has_y) load8(w2[v], static_cast<const W*>(a.w_pre), c, D, vec);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s1[v][i] = s2[v][i] = s3[v][i] = 0.f;
+    }
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        float dx[NV][8], y[NV][8], xn[NV][8], o[NV][8], z[NV][8];
+        const float r1 = a.rstd[2 * r], r2 = a.rstd[2 * r + 1];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
+            if (has_y) {
+                load8(y[v], static_cast<const T*>(a.dy) + r * a.ld_dy, c, D, vec);
+                load8(xn[v], static_cast<const T*>(a.x_new) + r * a.ld_xn, c, D, vec);
+            }
+            if (has_up) {
+                load8(dx[v], static_cast<const T*>(a.dxn) + r * a.ld_dxn, c, D, vec);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dx[v][i] = 0.f;
+            }
+            if (has_o) load8(o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D, vec);
+            if (a.act != SDM_ACT_NONE) load8(z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D, vec);
+        }
+        if (has_y) {
+            float s = 0.f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    xn[v][i] *= r2;
+                    s2[v][i] = fmaf(y[v][i], xn[v][i], s2[v][i]);
+                    y[v][i] *= w2[v][i];
+                    s = fmaf(y[v][i], xn[v][i], s);
+                }
+            const float m = row_sum<NT>(s, red, 0) * inv;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dx[v][i] = fmaf(r2, fmaf(-m, xn[v][i], y[v][i]), dx[v][i]);
+        }
+        if (a.dx) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                store8(static_cast<T*>(a.dx) + r * a.ld_dx, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, vec,
+                       dx[v]);
+        }
+        if (has_o) {
+            float s = 0.f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float g = 1.f, d = 0.f;
+                    if (a.act != SDM_ACT_NONE) gate<DT>(z[v][i], a.act, g, d);
+                    const float n = o[v][i] * r1, u = dx[v][i] * n;
+                    z[v][i] = u * sc[v][i] * w1[v][i] * d;
+                    s3[v][i] = fmaf(u * w1[v][i], g, s3[v][i]);
+                    const float dn = dx[v][i] * sc[v][i] * g;
+                    s1[v][i] = fmaf(dn, n, s1[v][i]);
+                    dx[v][i] = dn * w1[v][i];
+                    o[v][i] = n;
+                    s = fmaf(dx[v][i], n, s);
+                }
+            const float m = row_sum<NT>(s, red, 1) * inv;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
+                if (a.dz) store8(static_cast<T*>(a.dz) + r * a.ld_dz, c, D, vec, z[v]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dx[v][i] = r1 * fmaf(-m, o[v][i], dx[v][i]);
+                store8(static_cast<T*>(a.d_o) + r * a.ld_do, c, D, vec, dx[v]);
+            }
+        }
+        if (NT > 64 && has_o != has_y) lds_barrier();
+    }
+    float* p = part + static_cast<int64_t>(blockIdx.x) * 3 * D;
+    const bool pv = vec && D % 4 == 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
+        if (has_o) store8(p, c, D, pv, s1[v]);
+        if (has_y) store8(p + D, c, D, pv, s2[v]);
+        if (has_o) store8(p + 2 * static_cast<int64_t>(D), c, D, pv, s3[v]);
+    }
+}
+
+// The weights' gradients: column sums of the partial sums. 32 columns by 8 groups of consecutive workgroups; a
+// group's sum runs in workgroup order and the eight are added in order.
+template <int WT>
+__global__ __launch_bounds__(256) void nrm_weights(const sdm_nrm_args_t a, const float* __restrict__ part, int groups) {
+    using W = elem_t<WT>;
+    __shared__ float red[8][33];
+    const int D = static_cast<int>(a.D), which = blockIdx.y;
+    W* out = static_cast<W*>(which == 0 ? a.dw_post : which == 1 ? a.dw_pre : a.dscale);
+    if (!out) return;
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    const int per = (groups + 7) / 8, lo = grp * per, hi = min(groups, lo + per);
+    float s = 0.f;
+    if (c < D) {
+        const float* p = part + static_cast<int64_t>(which) * D + c;
+#pragma unroll 8
+        for (int i = lo; i < hi; ++i) s += p[static_cast<int64_t>(i) * 3 * D];
+    }
+    red[grp][lane] = s;
+    lds_barrier();
+    if (grp == 0 && c < D) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += red[i][lane];
+        out[c] = static_cast<W>(s);
+    }
+}
+
+template <int DT, int WT, int NT, int NV>
+hipError_t run_forward(const sdm_nrm_args_t& a, const NrmPlan& p, hipStream_t s) {
+    nrm_forward<DT, WT, NT, NV><<<p.groups, NT, 0, s>>>(a, p.vec);
+    return hipGetLastError();
+}
+template <int DT, int WT, int NT, int NV>
+hipError_t run_backward(const sdm_nrm_args_t& a, const NrmPlan& p, float* part, hipStream_t s) {
+    nrm_backward<DT, WT, NT, NV><<<p.groups, NT, 0, s>>>(a, p.vec, part);
+    return hipGetLastError();
+}
+
+#define SDM_NRM_SHAPES(F, ...)                                        \
+    if (p.threads == 64) return F<DT, WT, 64, 1>(__VA_ARGS__);        \
+    if (p.threads == 256 && p.vecs == 1) return F<DT, WT, 256, 1>(__VA_ARGS__); \
+    if (p.threads == 256) return F<DT, WT, 256, 2>(__VA_ARGS__);      \
+    return F<DT, WT, 512, 2>(__VA_ARGS__);
+
+template <int DT, int WT>
+hipError_t forward_of(const sdm_nrm_args_t& a, const NrmPlan& p, hipStream_t s) {
+    SDM_NRM_SHAPES(run_forward, a, p, s)
+}
+template <int DT, int WT>
+hipError_t backward_of(const sdm_nrm_args_t& a, const NrmPlan& p, float* part, hipStream_t s) {
+    SDM_NRM_SHAPES(run_backward, a, p, part, s)
+}
+
+}  // namespace
+
+// wtype is dtype or float32 (the host checks)
+hipError_t launch_nrm_forward(const sdm_nrm_args_t& a, const NrmPlan& p, hipStream_t s) {
+    if (a.dtype == SDM_F32) return forward_of<0, 0>(a, p, s);
+    if (a.dtype == SDM_BF16) return a.wtype == SDM_F32 ? forward_of<1, 0>(a, p, s) : forward_of<1, 1>(a, p, s);
+    return a.wtype == SDM_F32 ? forward_of<2, 0>(a, p, s) : forward_of<2, 2>(a, p, s);
+}
+
+hipError_t launch_nrm_backward(const sdm_nrm_args_t& a, const NrmPlan& p, float* part, hipStream_t s) {
+    hipError_t e;
+    if (a.dtype == SDM_F32)
+        e = backward_of<0, 0>(a, p, part, s);
+    else if (a.dtype == SDM_BF16)
+        e = a.wtype == SDM_F32 ? backward_of<1, 0>(a, p, part, s) : backward_of<1, 1>(a, p, part, s);
+    else
+        e = a.wtype == SDM_F32 ? backward_of<2, 0>(a, p, part, s) : backward_of<2, 2>(a, p, part, s);
+    if (e != hipSuccess) return e;
+    const dim3 grid(static_cast<unsigned>((a.D + 31) / 32), 3);
+    if (a.wtype == SDM_F32)
+        nrm_weights<0><<<grid, 256, 0, s>>>(a, part, p.groups);
+    else if (a.wtype == SDM_BF16)
+        nrm_weights<1><<<grid, 256, 0, s>>>(a, part, p.groups);
+    else
+        nrm_weights<2><<<grid, 256, 0, s>>>(a, part, p.groups);
+    return hipGetLastError();
+}
+
+}  // namespace sdm_delta
