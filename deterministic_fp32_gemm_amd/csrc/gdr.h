@@ -16,7 +16,9 @@ struct GdrWork {
     uint16_t* inv;      // [slots][Hv] fragments of (I + A)^-1, 64 x 64
     uint16_t* invt;     // of its transpose (backward)
     uint16_t* pm;       // of P (forward) or P^T (backward), 64 x 64
-    uint16_t* kt;       // [slots][Hk] fragments of K^T, dkp x 64
+    uint16_t* kf;       // [slots][Hk] fragments of K, 64 x dkp
+    uint16_t* qf;       // of Q (forward)
+    uint16_t* kt;       // of K^T, dkp x 64
     uint16_t* qt;       // of Q^T (backward)
     float* st;          // [slots][Hv][dk][dv]: each chunk's entering state (backward)
     float* dst;         // [slots][Hv][dk][dv]: gradient of each chunk's last state (backward)

@@ -15,6 +15,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gdr_device.h"
 
 namespace sdm_delta {
@@ -26,8 +28,12 @@ template <int DT, int DKP, bool BWD>
 __global__ __launch_bounds__(256) void gdr_chunk(const GdrLaunch g) {
     constexpr int NP = kParts<DT>, PP = BWD ? 3 : kOutParts<DT>, NKB = DKP / 32;
     using T = elem_t<DT>;
-    __shared__ alignas(16) float As[64][kLd];
-    __shared__ alignas(16) float Ts[64][kLd];
+    // K's (or Q's) fragments, then A and the matrix that P, and after it T, are laid out in
+    constexpr int kFragBytes = 64 * DKP * NP * 2, kMatBytes = 2 * 64 * kLd * 4;
+    __shared__ alignas(16) char buf[kFragBytes > kMatBytes ? kFragBytes : kMatBytes];
+    auto& As = *reinterpret_cast<float(*)[64][kLd]>(buf);
+    auto& Ts = *reinterpret_cast<float(*)[64][kLd]>(buf + 64 * kLd * 4);
+    uint16_t* const Kf = reinterpret_cast<uint16_t*>(buf);
     __shared__ float Gh[64], Gl[64], Be[64];
     const sdm_gdr_args_t& a = g.a;
     int seq, chunk;
@@ -64,34 +70,80 @@ __global__ __launch_bounds__(256) void gdr_chunk(const GdrLaunch g) {
         tok[kTokBeta * 64 + lane] = be;
     }
 
-    // K K^T and Q K^T, row tile `wave`. All column tiles, also those above the diagonal: the last wavefront needs
-    // them all, so leaving them out of the others saves no time
+    // This wavefront's 16 tokens of K and Q as fragments: to LDS for the others, to memory for the scans
+    const bool first = hv % r == 0;
+    const int64_t sk = static_cast<int64_t>(slot) * a.Hk + hk, frag = sk * (NP * 64 * DKP);
     const T* kr = rows_at<const T>(a.k, s, hk) + t0 * a.k.token;
     const T* qr = rows_at<const T>(a.q, s, hk) + t0 * a.q.token;
-    f32x4 kk[4], qk[4];
+    Frag<NP> kf[NKB], qf[NKB];
+    {
+        const int ti = wave * 16 + row, at = min(ti, n - 1);
+        Raw<DT> xk[NKB], xq[NKB];
+        auto fetch = [&](auto vec) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int ti = wave * 16 + row;
-#pragma unroll 2
-    for (int kb = 0; kb < NKB; ++kb) {
-        const int c = kb * 32 + grp * 8;
-        Raw<DT> x;
-        Frag<NP> qf, kf;
-        load_raw<DT>(x, qr + ti * a.q.token, c, ti < n ? dk : 0, g.vec_qk);
-        raw_frag<DT>(qf, x);
-        load_raw<DT>(x, kr + ti * a.k.token, c, ti < n ? dk : 0, g.vec_qk);
-        raw_frag<DT>(kf, x);
+            for (int kb = 0; kb < NKB; ++kb) {
+                load_raw<DT, decltype(vec)::value>(xk[kb], kr + at * a.k.token, kb * 32 + grp * 8, dk, ti < n);
+                load_raw<DT, decltype(vec)::value>(xq[kb], qr + at * a.q.token, kb * 32 + grp * 8, dk, ti < n);
+            }
+        };
+        if (g.vec_qk)
+            fetch(std::true_type{});
+        else
+            fetch(std::false_type{});
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int tj = j * 16 + row;
-            Frag<NP> bf;
-            load_raw<DT>(x, kr + tj * a.k.token, c, tj < n ? dk : 0, g.vec_qk);
-            raw_frag<DT>(bf, x);
-            mma<3>(kk[j], kf, bf);
-            mma<3>(qk[j], qf, bf);
+        for (int kb = 0; kb < NKB; ++kb) {
+            raw_frag<DT>(kf[kb], xk[kb]);
+            raw_frag<DT>(qf[kb], xq[kb]);
+            store_frag<NP>(frag_at<NP>(Kf, wave, kb, NKB), kf[kb]);
+            if (first) {
+                store_frag<NP>(frag_at<NP>(g.w.kf + frag, wave, kb, NKB), kf[kb]);
+                if constexpr (!BWD) store_frag<NP>(frag_at<NP>(g.w.qf + frag, wave, kb, NKB), qf[kb]);
+            }
         }
     }
     lds_barrier();
+    // K K^T and Q K^T, row tile `wave`. All column tiles, also those above the diagonal: the last wavefront needs them
+    // all, so leaving them out of the others saves no time
+    f32x4 kk[4], qk[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        kk[j] = qk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) {
+            Frag<NP> bf;
+            load_frag<NP>(bf, frag_at<NP>(Kf, j, kb, NKB));
+            mma<3>(kk[j], kf[kb], bf);
+            mma<3>(qk[j], qf[kb], bf);
+        }
+    }
+    // K^T, and Q^T in the backward, once per q/k head: a fragment's eight tokens are eight 2-byte LDS reads
+    auto transposed = [&](uint16_t* out) {
+#pragma unroll 2
+        for (int i = wave; i < DKP / 16 * 2; i += 4) {
+            const int t = i >> 1, kb = i & 1, c = t * 16 + row;
+            Frag<NP> f;
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = kb * 32 + grp * 8 + e;
+                    const uint16_t x = frag_at<NP>(Kf, j >> 4, c >> 5, NKB)[p * 512 + ((j & 15) + (c >> 3 & 3) * 16) * 8 + (c & 7)];
+                    f.p[p][e] = __builtin_bit_cast(__bf16, x);
+                }
+            store_frag<NP>(frag_at<NP>(out, t, kb, 2), f);
+        }
+    };
+    if (first) transposed(g.w.kt + frag);
+    lds_barrier();
+    if constexpr (BWD) {
+        if (first) {
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) store_frag<NP>(frag_at<NP>(Kf, wave, kb, NKB), qf[kb]);
+            lds_barrier();
+            transposed(g.w.qt + frag);
+            lds_barrier();
+        }
+    }
 
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -199,32 +251,6 @@ __global__ __launch_bounds__(256) void gdr_chunk(const GdrLaunch g) {
                 for (int e = 0; e < 8; ++e) v[e] = Ts[k + e][m];
                 split8(f, v);
                 store_frag<3>(frag_at<3>(g.w.invt + sv * (3 * 4096), wave, kb, 2), f);
-            }
-        }
-    }
-
-    // K^T, and Q^T in the backward: once per q/k head
-    if (hv % r == 0) {
-        const int64_t sk = static_cast<int64_t>(slot) * a.Hk + hk;
-        for (int i = wave; i < DKP / 16 * 2; i += 4) {
-            const int t = i >> 1, kb = i & 1, c = t * 16 + row;
-            float v[8];
-            Frag<NP> f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int j = kb * 32 + grp * 8 + e;
-                v[e] = j < n && c < dk ? static_cast<float>(kr[j * a.k.token + c]) : 0.f;
-            }
-            split8(f, v);
-            store_frag<NP>(frag_at<NP>(g.w.kt + sk * (NP * 64 * DKP), t, kb, 2), f);
-            if constexpr (BWD) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int j = kb * 32 + grp * 8 + e;
-                    v[e] = j < n && c < dk ? static_cast<float>(qr[j * a.q.token + c]) : 0.f;
-                }
-                split8(f, v);
-                store_frag<NP>(frag_at<NP>(g.w.qt + sk * (NP * 64 * DKP), t, kb, 2), f);
             }
         }
     }

@@ -76,28 +76,31 @@ template <int DT>
 struct Raw {
     u32x4 w[DT == 0 ? 2 : 1];
 };
-template <int DT>
-__device__ __forceinline__ void load_raw(Raw<DT>& o, const elem_t<DT>* __restrict__ row, int c, int lim, bool vec) {
-    if (vec && c + 8 <= lim) {
-        const u32x4* p = reinterpret_cast<const u32x4*>(row + c);
-        o.w[0] = p[0];
-        if constexpr (DT == 0) o.w[1] = p[1];
-        return;
-    }
-    if (c >= lim) {
-        o.w[0] = u32x4{0, 0, 0, 0};
-        if constexpr (DT == 0) o.w[1] = u32x4{0, 0, 0, 0};
-        return;
-    }
-    if constexpr (DT == 0) {
+// Always from a place inside the row (`row` itself has to be readable), zero where c is past `lim` or !ok: no branch
+// around a load, so that loads stay in flight together. VEC: the row starts on a 16-byte boundary, lim is a multiple
+// of 8.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load_raw(Raw<DT>& o, const elem_t<DT>* __restrict__ row, int c, int lim, bool ok) {
+    const u32x4 zero = {0, 0, 0, 0};
+    if constexpr (VEC) {
+        ok = ok && c < lim;
+        const u32x4* p = reinterpret_cast<const u32x4*>(row + (ok ? c : 0));
+        o.w[0] = ok ? p[0] : zero;
+        if constexpr (DT == 0) o.w[1] = ok ? p[1] : zero;
+    } else if constexpr (DT == 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o.w[i / 4][i % 4] = c + i < lim ? __float_as_uint(row[c + i]) : 0u;
+        for (int i = 0; i < 8; ++i) {
+            const bool in = ok && c + i < lim;
+            const uint32_t x = __float_as_uint(row[in ? c + i : 0]);
+            o.w[i / 4][i % 4] = in ? x : 0u;
+        }
     } else {
         const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = c + 2 * i < lim ? r[c + 2 * i] : 0u, hi = c + 2 * i + 1 < lim ? r[c + 2 * i + 1] : 0u;
-            o.w[0][i] = lo | hi << 16;
+            const bool il = ok && c + 2 * i < lim, ih = ok && c + 2 * i + 1 < lim;
+            const uint32_t lo = r[il ? c + 2 * i : 0], hi = r[ih ? c + 2 * i + 1 : 0];
+            o.w[0][i] = (il ? lo : 0u) | (ih ? hi << 16 : 0u);
         }
     }
 }
@@ -160,6 +163,10 @@ struct Tile {
         for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x4*>(&v[n][row0 + (l & 15)][k0 + 4 * (l >> 4)]) = s[n];
     }
 };
+
+// All loads so far have landed. Before a loop whose loads cross its back edge: the compiler otherwise waits at the
+// loop's head for the order in which the loads before the loop happen to stand, every time round.
+__device__ __forceinline__ void loads_landed() { __builtin_amdgcn_s_waitcnt(0x0f70); }
 
 // One sequence: its first token, length and first chunk slot.
 struct Seq {

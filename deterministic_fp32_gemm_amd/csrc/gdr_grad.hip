@@ -85,7 +85,11 @@ __global__ __launch_bounds__(256, DKP <= 128 ? 2 : 1) void gdr_grad(const GdrLau
             Frag<3> f;
             Raw<DT> raw;
             Frag<NP> fo;
-            load_raw<DT>(raw, dor + i * a.d_o.token, c, i < n ? dv : 0, g.vec_v);
+            const int at = min(i, n - 1);
+            if (g.vec_v)
+                load_raw<DT, true>(raw, dor + at * a.d_o.token, c, dv, i < n);
+            else
+                load_raw<DT, false>(raw, dor + at * a.d_o.token, c, dv, i < n);
             raw_frag<DT>(fo, raw);
             load8(x, ur + i * dv, c, dv, vst);
             split8(f, x);
@@ -97,7 +101,10 @@ __global__ __launch_bounds__(256, DKP <= 128 ? 2 : 1) void gdr_grad(const GdrLau
             split8(f, x);
 #pragma unroll
             for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(&L.s.r.v[p][i][cc]) = f.p[p];
-            load_raw<DT>(raw, vr + i * a.v.token, c, i < n ? dv : 0, g.vec_v);
+            if (g.vec_v)
+                load_raw<DT, true>(raw, vr + at * a.v.token, c, dv, i < n);
+            else
+                load_raw<DT, false>(raw, vr + at * a.v.token, c, dv, i < n);
             raw_floats<DT>(y, raw);
 #pragma unroll
             for (int e = 0; e < 8; ++e) rv[h] = fmaf(x[e], y[e], rv[h]);

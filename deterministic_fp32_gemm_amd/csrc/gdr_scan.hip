@@ -20,25 +20,30 @@
 namespace sdm_delta {
 namespace {
 
-// Four consecutive tokens of one column, zero past the chunk's tokens and the head's columns.
+// Four consecutive tokens of one column (the row of token t + e, or the chunk's last where there is none and the value
+// is dropped; a column past the head's is the caller's to leave out).
 template <int DT>
-__device__ __forceinline__ f32x4 tokens4(const elem_t<DT>* __restrict__ p, int64_t stride, int t, int n, bool col) {
+__device__ __forceinline__ f32x4 tokens4(const elem_t<DT>* __restrict__ p, int64_t stride, int t, int n) {
     f32x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = col && t + e < n ? static_cast<float>(p[(t + e) * stride]) : 0.f;
+    for (int e = 0; e < 4; ++e) {
+        const float x = static_cast<float>(p[min(t + e, n - 1) * stride]);
+        v[e] = t + e < n ? x : 0.f;
+    }
     return v;
 }
-
-// One chunk's operands in memory layout.
-template <int DT, int DKP, bool QP>
-struct Fetched {
-    Raw<DT> k[DKP / 32], q[QP ? DKP / 32 : 1];
-    Frag<3> inv[2];
-    Frag<kOutParts<DT>> pm[QP ? 2 : 1];
-    Frag<kParts<DT>> kt[DKP / 64][2];
-    f32x4 eg, last, beta;
-    float whole;
-};
+// and back: tokens below n only
+template <class T>
+__device__ __forceinline__ void put4(T* __restrict__ p, int64_t stride, int t, int n, const f32x4& v) {
+    if (t + 4 <= n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[(t + e) * stride] = static_cast<T>(v[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (t + e < n) p[(t + e) * stride] = static_cast<T>(v[e]);
+    }
+}
 
 template <int DT, int DKP, int NT, bool STORE>
 __global__ __launch_bounds__(256, 1) void gdr_scan(const GdrLaunch g, const int total) {
@@ -58,8 +63,6 @@ __global__ __launch_bounds__(256, 1) void gdr_scan(const GdrLaunch g, const int 
     const Seq s = sequence(a, seq);
     const int chunks = (s.len + kChunk - 1) / kChunk;
     const int64_t head = static_cast<int64_t>(seq) * Hv + hv;
-    const T* kr = rows_at<const T>(a.k, s, hk);
-    const T* qr = STORE ? nullptr : rows_at<const T>(a.q, s, hk);
     const T* vr = rows_at<const T>(a.v, s, hv);
     T* orow = STORE ? nullptr : rows_at<T>(a.o, s, hv);
 
@@ -76,50 +79,54 @@ __global__ __launch_bounds__(256, 1) void gdr_scan(const GdrLaunch g, const int 
             Sx.put(t * 16, d - grp * 4, S[m][t]);
         }
 
-    Fetched<DT, DKP, !STORE> f;
-    f32x4 v[NT];
+    Frag<NP> kf[NKB], qf[STORE ? 1 : NKB], kt[MT][2];
+    Frag<3> inv[2];
+    Frag<PP> pm[2];
+    f32x4 eg, last, beta, v[NT];
+    float whole = 0.f;
     const int tok = wave * 16;      // this wavefront's tokens of a chunk
     auto fetch_kq = [&](int chunk) {
-        const int t0 = chunk * kChunk, n = min(kChunk, s.len - t0), ti = tok + row, lim = ti < n ? dk : 0;
+        const int64_t sk = (static_cast<int64_t>(s.slot + chunk) * a.Hk + hk) * (NP * 64 * DKP);
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb) {
-            const int c = kb * 32 + grp * 8;
-            load_raw<DT>(f.k[kb], kr + (t0 + ti) * a.k.token, c, lim, g.vec_qk);
-            if constexpr (!STORE) load_raw<DT>(f.q[kb], qr + (t0 + ti) * a.q.token, c, lim, g.vec_qk);
+            load_frag<NP>(kf[kb], frag_at<NP>(g.w.kf + sk, wave, kb, NKB));
+            if constexpr (!STORE) load_frag<NP>(qf[kb], frag_at<NP>(g.w.qf + sk, wave, kb, NKB));
         }
     };
     auto fetch_inv = [&](int chunk) {
         const int64_t sv = static_cast<int64_t>(s.slot + chunk) * Hv + hv;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) load_frag<3>(f.inv[kb], frag_at<3>(g.w.inv + sv * (3 * 4096), wave, kb, 2));
+        for (int kb = 0; kb < 2; ++kb) load_frag<3>(inv[kb], frag_at<3>(g.w.inv + sv * (3 * 4096), wave, kb, 2));
     };
     auto fetch_rest = [&](int chunk) {
         const int64_t slot = s.slot + chunk, sv = slot * Hv + hv, sk = slot * a.Hk + hk;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            if constexpr (!STORE) load_frag<PP>(f.pm[kb], frag_at<PP>(g.w.pm + sv * (PP * 4096), wave, kb, 2));
+            if constexpr (!STORE) load_frag<PP>(pm[kb], frag_at<PP>(g.w.pm + sv * (PP * 4096), wave, kb, 2));
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-                load_frag<NP>(f.kt[m][kb], frag_at<NP>(g.w.kt + sk * (NP * 64 * DKP), wave * MT + m, kb, 2));
+                load_frag<NP>(kt[m][kb], frag_at<NP>(g.w.kt + sk * (NP * 64 * DKP), wave * MT + m, kb, 2));
         }
     };
+    f32x4 eg_n, last_n, beta_n;
+    float whole_n = 0.f;
     auto fetch_tok = [&](int chunk) {
         const int t0 = chunk * kChunk, n = min(kChunk, s.len - t0);
         const float* t = g.w.tok + (static_cast<int64_t>(s.slot + chunk) * Hv + hv) * (kTokFields * 64);
-        f.eg = *reinterpret_cast<const f32x4*>(t + kTokEg * 64 + tok + grp * 4);
-        f.last = *reinterpret_cast<const f32x4*>(t + kTokLast * 64 + tok + grp * 4);
-        f.beta = *reinterpret_cast<const f32x4*>(t + kTokBeta * 64 + tok + grp * 4);
-        f.whole = t[kTokEg * 64 + 63];
+        eg_n = *reinterpret_cast<const f32x4*>(t + kTokEg * 64 + tok + grp * 4);
+        last_n = *reinterpret_cast<const f32x4*>(t + kTokLast * 64 + tok + grp * 4);
+        beta_n = *reinterpret_cast<const f32x4*>(t + kTokBeta * 64 + tok + grp * 4);
+        whole_n = t[kTokEg * 64 + 63];
 #pragma unroll
         for (int c = 0; c < NT; ++c)
-            v[c] = tokens4<DT>(vr + t0 * a.v.token + c0 + c * 16 + row, a.v.token, tok + grp * 4, n,
-                               c0 + c * 16 + row < dv);
+            v[c] = tokens4<DT>(vr + t0 * a.v.token + min(c0 + c * 16 + row, dv - 1), a.v.token, tok + grp * 4, n);
     };
     if (chunks) {
         fetch_kq(0);
         fetch_tok(0);
         fetch_inv(0);
         fetch_rest(0);
+        loads_landed();
     }
     for (int chunk = 0; chunk < chunks; ++chunk) {
         const int t0 = chunk * kChunk, n = min(kChunk, s.len - t0);
@@ -136,27 +143,30 @@ __global__ __launch_bounds__(256, 1) void gdr_scan(const GdrLaunch g, const int 
                         if (d < dk && c < dv) st[static_cast<int64_t>(d) * dv + c] = S[m][t][e];
                     }
         }
-        const bool more = chunk + 1 < chunks;
+        // each operand's next chunk is fetched as soon as this one's is used (the last step fetches itself again)
+        const int next = min(chunk + 1, chunks - 1);
+        eg = eg_n;
+        last = last_n;
+        beta = beta_n;
+        whole = whole_n;
         lds_barrier();      // S of all wavefronts is in LDS
         f32x4 x[NT], o[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) x[t] = o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb) {
-            Frag<NP> kf, qf;
-            raw_frag<DT>(kf, f.k[kb]);
-            if constexpr (!STORE) raw_frag<DT>(qf, f.q[kb]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 Frag<3> b;
                 Sx.frag(b, t * 16, kb * 32);
-                mma<3>(x[t], kf, b);
-                if constexpr (!STORE) mma<PP>(o[t], qf, b);
+                mma<3>(x[t], kf[kb], b);
+                if constexpr (!STORE) mma<PP>(o[t], qf[kb], b);
             }
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) Rx.put(t * 16, tok, f.beta * (v[t] - f.eg * x[t]));
-        if (more) fetch_kq(chunk + 1);      // each operand's next chunk as soon as this one's is used
+        for (int t = 0; t < NT; ++t) Rx.put(t * 16, tok, beta * (v[t] - eg * x[t]));
+        fetch_kq(next);
+        fetch_tok(next);
         lds_barrier();
         f32x4 u[NT];
 #pragma unroll
@@ -166,20 +176,18 @@ __global__ __launch_bounds__(256, 1) void gdr_scan(const GdrLaunch g, const int 
             for (int kb = 0; kb < 2; ++kb) {
                 Frag<3> b;
                 Rx.frag(b, t * 16, kb * 32);
-                mma<3>(u[t], f.inv[kb], b);
+                mma<3>(u[t], inv[kb], b);
             }
             if constexpr (!STORE) Ux.put(t * 16, tok, u[t]);
-            Dx.put(t * 16, tok, f.last * u[t]);
+            Dx.put(t * 16, tok, last * u[t]);
         }
-        if (more) fetch_inv(chunk + 1);
+        fetch_inv(next);
         lds_barrier();
         if constexpr (STORE) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c0 + t * 16 + row < dv)
-                        g.w.u[(sv * 64 + tok + grp * 4 + e) * dv + c0 + t * 16 + row] = u[t][e];
+                if (c0 + t * 16 + row < dv)
+                    put4(g.w.u + sv * 64 * dv + c0 + t * 16 + row, dv, tok + grp * 4, kChunk, u[t]);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -188,35 +196,29 @@ __global__ __launch_bounds__(256, 1) void gdr_scan(const GdrLaunch g, const int 
             Dx.frag(b[1], t * 16, 32);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                S[m][t] *= f.whole;
-                mma<3>(S[m][t], f.kt[m][0], b[0]);
-                mma<3>(S[m][t], f.kt[m][1], b[1]);
+                S[m][t] *= whole;
+                mma<3>(S[m][t], kt[m][0], b[0]);
+                mma<3>(S[m][t], kt[m][1], b[1]);
                 Sx.put(t * 16, (wave * MT + m) * 16, S[m][t]);
             }
         }
         if constexpr (!STORE) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                o[t] = o[t] * (f.eg * a.scale);
+                o[t] = o[t] * (eg * a.scale);
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
                     Frag<PP> b;
 #pragma unroll
                     for (int p = 0; p < PP; ++p)
                         b.p[p] = *reinterpret_cast<const bf16x8*>(&Ux.v[p][t * 16 + row][kb * 32 + 8 * grp]);
-                    mma<PP>(o[t], f.pm[kb], b);
+                    mma<PP>(o[t], pm[kb], b);
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = tok + grp * 4 + e, c = c0 + t * 16 + row;
-                    if (i < n && c < dv) orow[(t0 + i) * a.o.token + c] = static_cast<T>(o[t][e]);
-                }
+                if (c0 + t * 16 + row < dv)
+                    put4(orow + t0 * a.o.token + c0 + t * 16 + row, a.o.token, tok + grp * 4, n, o[t]);
             }
         }
-        if (more) {
-            fetch_tok(chunk + 1);
-            fetch_rest(chunk + 1);
-        }
+        fetch_rest(next);
     }
     float* out = STORE ? nullptr : a.s_final;
     if (!out) return;
@@ -249,7 +251,6 @@ __global__ __launch_bounds__(256, 1) void gdr_scan_back(const GdrLaunch g, const
     const Seq s = sequence(a, seq);
     const int chunks = (s.len + kChunk - 1) / kChunk;
     const int64_t head = static_cast<int64_t>(seq) * Hv + hv;
-    const T* kr = rows_at<const T>(a.k, s, hk);
     const T* dor = rows_at<const T>(a.d_o, s, hv);
     T* dvr = rows_at<T>(a.d_v, s, hv);
 
@@ -265,17 +266,15 @@ __global__ __launch_bounds__(256, 1) void gdr_scan_back(const GdrLaunch g, const
             Sx.put(t * 16, d - grp * 4, S[m][t]);
         }
     const int tok = wave * 16;
-    Raw<DT> kraw[NKB];
+    Frag<NP> kf[NKB];
     Frag<3> invt[2], pmt[2];
     Frag<NP> kt[MT][2], qt[MT][2];
     f32x4 eg, last, beta, dof[NT];
     float whole = 0.f;
     auto fetch_kp = [&](int chunk) {
-        const int t0 = chunk * kChunk, n = min(kChunk, s.len - t0), ti = tok + row;
-        const int64_t sv = static_cast<int64_t>(s.slot + chunk) * Hv + hv;
+        const int64_t slot = s.slot + chunk, sv = slot * Hv + hv, sk = (slot * a.Hk + hk) * (NP * 64 * DKP);
 #pragma unroll
-        for (int kb = 0; kb < NKB; ++kb)
-            load_raw<DT>(kraw[kb], kr + (t0 + ti) * a.k.token, kb * 32 + grp * 8, ti < n ? dk : 0, g.vec_qk);
+        for (int kb = 0; kb < NKB; ++kb) load_frag<NP>(kf[kb], frag_at<NP>(g.w.kf + sk, wave, kb, NKB));
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) load_frag<3>(pmt[kb], frag_at<3>(g.w.pm + sv * (3 * 4096), wave, kb, 2));
     };
@@ -305,18 +304,19 @@ __global__ __launch_bounds__(256, 1) void gdr_scan_back(const GdrLaunch g, const
         whole_n = t[kTokEg * 64 + 63];
 #pragma unroll
         for (int c = 0; c < NT; ++c)
-            dof[c] = tokens4<DT>(dor + t0 * a.d_o.token + c0 + c * 16 + row, a.d_o.token, tok + grp * 4, n,
-                                 c0 + c * 16 + row < dv);
+            dof[c] = tokens4<DT>(dor + t0 * a.d_o.token + min(c0 + c * 16 + row, dv - 1), a.d_o.token, tok + grp * 4, n);
     };
     if (chunks) {
         fetch_tok(chunks - 1);
         fetch_kp(chunks - 1);
         fetch_inv(chunks - 1);
         fetch_t(chunks - 1);
+        loads_landed();
     }
     for (int chunk = chunks - 1; chunk >= 0; --chunk) {
         const int t0 = chunk * kChunk, n = min(kChunk, s.len - t0);
         const int64_t sv = static_cast<int64_t>(s.slot + chunk) * Hv + hv;
+        const int next = max(chunk - 1, 0);
         float* st = g.w.dst + sv * dk * dv;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -336,18 +336,16 @@ __global__ __launch_bounds__(256, 1) void gdr_scan_back(const GdrLaunch g, const
         lds_barrier();
 #pragma unroll
         for (int t = 0; t < NT; ++t) Qx.put(t * 16, tok, dof[t] * (eg * a.scale));
-        if (chunk) fetch_tok(chunk - 1);
+        fetch_tok(next);
         f32x4 u[NT], d[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             u[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb) {
-                Frag<NP> kf;
                 Frag<3> b;
-                raw_frag<DT>(kf, kraw[kb]);
                 Sx.frag(b, t * 16, kb * 32);
-                mma<3>(u[t], kf, b);
+                mma<3>(u[t], kf[kb], b);
             }
             u[t] *= last;
 #pragma unroll
@@ -358,7 +356,7 @@ __global__ __launch_bounds__(256, 1) void gdr_scan_back(const GdrLaunch g, const
             }
             Ux.put(t * 16, tok, u[t]);
         }
-        if (chunk) fetch_kp(chunk - 1);
+        fetch_kp(next);
         lds_barrier();
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -371,7 +369,7 @@ __global__ __launch_bounds__(256, 1) void gdr_scan_back(const GdrLaunch g, const
             }
             Rx.put(t * 16, tok, -(beta * eg) * d[t]);
         }
-        if (chunk) fetch_inv(chunk - 1);
+        fetch_inv(next);
         lds_barrier();
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -391,15 +389,13 @@ __global__ __launch_bounds__(256, 1) void gdr_scan_back(const GdrLaunch g, const
                 }
                 Sx.put(t * 16, (wave * MT + m) * 16, S[m][t]);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = tok + grp * 4 + e, c = c0 + t * 16 + row;
-                if (c >= dv) continue;
-                g.w.dr[(sv * 64 + i) * dv + c] = d[t][e];
-                if (i < n) dvr[(t0 + i) * a.d_v.token + c] = static_cast<T>(beta[e] * d[t][e]);
+            const int c = c0 + t * 16 + row;
+            if (c < dv) {
+                put4(g.w.dr + sv * 64 * dv + c, dv, tok + grp * 4, kChunk, d[t]);
+                put4(dvr + t0 * a.d_v.token + c, a.d_v.token, tok + grp * 4, n, beta * d[t]);
             }
         }
-        if (chunk) fetch_t(chunk - 1);
+        fetch_t(next);
     }
     if (!a.ds0) return;
 #pragma unroll
