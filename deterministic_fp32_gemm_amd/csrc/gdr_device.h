@@ -31,32 +31,45 @@ struct Frag {
     bf16x8 p[N];
 };
 
-// f as N bfloat16 parts, largest first
+// f as N bfloat16 parts, largest first. Two elements at a time: one conversion makes both halves of a register, a shift
+// and a mask take them out again.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 template <int N>
-__device__ __forceinline__ void split8(Frag<N>& o, const float (&f)[8]) {
-    float r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = f[i];
+__device__ __forceinline__ void split2(uint32_t (&o)[N], float a, float b) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o.p[n][i] = static_cast<__bf16>(r[i]);
+        const f32x2 v = {a, b};
+        const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+        o[n] = w;
         if (n + 1 < N) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] -= static_cast<float>(o.p[n][i]);
+            a -= __uint_as_float(w << 16);
+            b -= __uint_as_float(w & 0xffff0000u);
         }
     }
 }
 template <int N>
-__device__ __forceinline__ void split4(bf16x4 (&o)[N], f32x4 f) {
+__device__ __forceinline__ void split8(Frag<N>& o, const float (&f)[8]) {
+    u32x4 w[N];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t x[N];
+        split2<N>(x, f[2 * i], f[2 * i + 1]);
+#pragma unroll
+        for (int n = 0; n < N; ++n) w[n][i] = x[n];
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) o.p[n] = __builtin_bit_cast(bf16x8, w[n]);
+}
+template <int N>
+__device__ __forceinline__ void split4(bf16x4 (&o)[N], const f32x4& f) {
+    uint32_t x[N], y[N];
+    split2<N>(x, f[0], f[1]);
+    split2<N>(y, f[2], f[3]);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[n][i] = static_cast<__bf16>(f[i]);
-        if (n + 1 < N) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] -= static_cast<float>(o[n][i]);
-        }
+        const u32x2 w = {x[n], y[n]};
+        o[n] = __builtin_bit_cast(bf16x4, w);
     }
 }
 
