@@ -73,12 +73,12 @@ struct Operand {
 
 int check_rows(const Operand& o, int64_t B, int64_t T, Extent* e) {
     if (!o.r->data) return SDM_GX_ERR_NULL;
-    const int64_t lim = int64_t(1) << 40;
     const sdm_rows_t& r = *o.r;
-    if (r.batch < 0 || r.token < 0 || r.head < 0 || r.batch >= lim || r.token >= lim || r.head >= lim)
+    if (r.batch < 0 || r.token < 0 || r.head < 0 || r.batch >= (int64_t(1) << 40) || r.token >= SDM_GX_LD_LIMIT ||
+        r.head >= SDM_GX_LD_LIMIT)
         return SDM_GX_ERR_STRIDE;
     if (!aligned(r.data, o.size)) return SDM_GX_ERR_ALIGN;
-    // B * T < 2^31 and strides < 2^40 would overflow together: bound each product before the sum
+    // the products may overflow together: bound them before the sum
     const double span = double(B - 1) * double(r.batch) + double(T > 0 ? T - 1 : 0) * double(r.token) +
                         double(o.heads - 1) * double(r.head) + double(o.cols);
     if (span >= 4e17) return SDM_GX_ERR_STRIDE;

@@ -157,15 +157,21 @@ __device__ __forceinline__ void store_frag(uint16_t* at, const Frag<N>& f) {
     for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x8*>(at + n * 512 + (threadIdx.x & 63) * 8) = f.p[n];
 }
 
-// A split matrix in LDS: [part][rows][LD], the summed axis contiguous. LD is 8 more than a multiple of 32, so that the
-// 16 rows of a fragment start on different banks.
-template <int N, int ROWS, int LD>
+// A split matrix in LDS, as fragments: [part][32-wide k block][16-row tile][64 lanes][8]. A fragment's read is 1 KB in
+// lane order and a transposed result tile's write 512 bytes without a gap, so neither meets a bank conflict (rows
+// padded to 8 more than a multiple of 32 elements had one on every second read).
+template <int N, int ROWS, int KS>
 struct Tile {
-    alignas(16) __bf16 v[N][ROWS][LD];
-    __device__ __forceinline__ void frag(Frag<N>& o, int row0, int k0) const {
-        const int l = threadIdx.x & 63;
+    alignas(16) __bf16 v[N][KS / 32][ROWS / 16][64][8];
+    // where element (row, k) lies; k a multiple of 4 (8) for 8-byte (16-byte) access
+    __device__ __forceinline__ __bf16* at(int part, int row, int k) {
+        return &v[part][k >> 5][row >> 4][(row & 15) + 16 * (k >> 3 & 3)][k & 7];
+    }
+    // the first M parts of a fragment
+    template <int M>
+    __device__ __forceinline__ void frag(Frag<M>& o, int row0, int k0) const {
 #pragma unroll
-        for (int n = 0; n < N; ++n) o.p[n] = *reinterpret_cast<const bf16x8*>(&v[n][row0 + (l & 15)][k0 + 8 * (l >> 4)]);
+        for (int n = 0; n < M; ++n) o.p[n] = *reinterpret_cast<const bf16x8*>(v[n][k0 >> 5][row0 >> 4][threadIdx.x & 63]);
     }
     // a result tile, transposed: its column is the row here
     __device__ __forceinline__ void put(int row0, int k0, const f32x4& d) {
@@ -173,7 +179,7 @@ struct Tile {
         bf16x4 s[N];
         split4<N>(s, d);
 #pragma unroll
-        for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x4*>(&v[n][row0 + (l & 15)][k0 + 4 * (l >> 4)]) = s[n];
+        for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x4*>(at(n, row0 + (l & 15), k0 + 4 * (l >> 4))) = s[n];
     }
 };
 

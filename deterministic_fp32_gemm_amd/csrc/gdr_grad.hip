@@ -21,18 +21,16 @@
 namespace sdm_delta {
 namespace {
 
-constexpr int kLds = 72;
-
 template <int DT, int DKP>
 __global__ __launch_bounds__(256, DKP <= 128 ? 2 : 1) void gdr_grad(const GdrLaunch g) {
     constexpr int NP = kParts<DT>, MT = DKP / 64;
     using T = elem_t<DT>;
     struct Staged {
-        Tile<NP, 64, kLds> o;
-        Tile<3, 64, kLds> u, r;
+        Tile<NP, 64, 64> o;
+        Tile<3, 64, 64> u, r;
     };
     struct Pairs {
-        Tile<3, 64, kLds> m, t;     // a 64 x 64 matrix by rows and by columns
+        Tile<3, 64, 64> m, t;     // a 64 x 64 matrix by rows and by columns
     };
     union Shared {
         Staged s;
@@ -94,13 +92,13 @@ __global__ __launch_bounds__(256, DKP <= 128 ? 2 : 1) void gdr_grad(const GdrLau
             load8(x, ur + i * dv, c, dv, vst);
             split8(f, x);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) *reinterpret_cast<bf16x8*>(&L.s.o.v[p][i][cc]) = fo.p[p];
+            for (int p = 0; p < NP; ++p) *reinterpret_cast<bf16x8*>(L.s.o.at(p, i, cc)) = fo.p[p];
 #pragma unroll
-            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(&L.s.u.v[p][i][cc]) = f.p[p];
+            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(L.s.u.at(p, i, cc)) = f.p[p];
             load8(x, rp + i * dv, c, dv, vst);
             split8(f, x);
 #pragma unroll
-            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(&L.s.r.v[p][i][cc]) = f.p[p];
+            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(L.s.r.at(p, i, cc)) = f.p[p];
             if (g.vec_v)
                 load_raw<DT, true>(raw, vr + at * a.v.token, c, dv, i < n);
             else
@@ -200,7 +198,7 @@ __global__ __launch_bounds__(256, DKP <= 128 ? 2 : 1) void gdr_grad(const GdrLau
 #pragma unroll
             for (int p = 0; p < 3; ++p)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) L.p.m.v[p][wave * 16 + grp * 4 + e][j * 16 + row] = xs[p][e];
+                for (int e = 0; e < 4; ++e) *L.p.m.at(p, wave * 16 + grp * 4 + e, j * 16 + row) = xs[p][e];
             L.p.t.put(j * 16, wave * 16, y);
         }
         lds_barrier();

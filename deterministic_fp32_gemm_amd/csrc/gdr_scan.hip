@@ -32,9 +32,9 @@ struct Tokens4 {
     elem_t<DT> x[4];
 };
 template <int DT>
-__device__ __forceinline__ void load4(Tokens4<DT>& v, const elem_t<DT>* __restrict__ p, int64_t stride, int t, int n) {
+__device__ __forceinline__ void load4(Tokens4<DT>& v, const elem_t<DT>* __restrict__ p, int stride, int t, int n) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v.x[e] = p[min(t + e, n - 1) * stride];
+    for (int e = 0; e < 4; ++e) v.x[e] = p[static_cast<int64_t>(min(t + e, n - 1)) * stride];
 }
 template <int DT>
 __device__ __forceinline__ f32x4 floats4(const Tokens4<DT>& v, int t, int n) {
@@ -45,16 +45,41 @@ __device__ __forceinline__ f32x4 floats4(const Tokens4<DT>& v, int t, int n) {
 }
 // and back: tokens below n only
 template <class T>
-__device__ __forceinline__ void put4(T* __restrict__ p, int64_t stride, int t, int n, const f32x4& v) {
+__device__ __forceinline__ void put4(T* __restrict__ p, int stride, int t, int n, const f32x4& v) {
+    p += static_cast<int64_t>(t) * stride;
     if (t + 4 <= n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[(t + e) * stride] = static_cast<T>(v[e]);
+        for (int e = 0; e < 4; ++e) p[static_cast<int64_t>(e) * stride] = static_cast<T>(v[e]);
     } else {
 #pragma unroll
         for (int e = 0; e < 3; ++e)
-            if (t + e < n) p[(t + e) * stride] = static_cast<T>(v[e]);
+            if (t + e < n) p[static_cast<int64_t>(e) * stride] = static_cast<T>(v[e]);
     }
 }
+
+// Sums of products of fragments over k blocks, in two accumulators that take turns: a product that waits for the one
+// before takes half as long again.
+template <int ORD, int KBS, int NA, int NB>
+__device__ __forceinline__ void products(f32x4 (&x)[2], const Frag<NA>* a, const Frag<NB>* b) {
+    int i = 0;
+#pragma unroll
+    for (int k = 0; k < KBS; ++k)
+#pragma unroll
+        for (int s = ORD - 1; s >= 0; --s)
+#pragma unroll
+            for (int p = 0; p < NA; ++p)
+                if (s - p >= 0 && s - p < NB) {
+                    x[i & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[k].p[p], b[k].p[s - p], x[i & 1], 0, 0, 0);
+                    ++i;
+                }
+}
+template <int KBS, class TileT, int N>
+__device__ __forceinline__ void read(Frag<N>* b, const TileT& B, int row0, int k0) {
+#pragma unroll
+    for (int k = 0; k < KBS; ++k) B.frag(b[k], row0, k0 + k * 32);
+}
+// LDS reads above are issued before anything below
+__device__ __forceinline__ void reads_first() { __builtin_amdgcn_sched_barrier(0); }
 
 // What a workgroup of a scan works on.
 struct Scan {
@@ -152,20 +177,45 @@ struct Operands {
     __device__ __forceinline__ float whole(int chunk) const { return g.w.tok[(sv(chunk) * kTokFields + kTokEg) * 64 + 63]; }
 };
 
-// The two kinds of wavefronts run loops of their own: where two paths of one loop meet, registers that loads are still
-// on their way to would be moved, and the moves wait.
+// How many chunks ahead operands are fetched: a step takes less than a load from memory, so two where the registers
+// hold two chunks (a step of 16384 tokens x 32 heads in bfloat16: 2.0 us with one, 1.5 with two); with wide float32
+// heads not even one: K^T (and Q^T) come in the middle of their own step.
+template <int DT, int DKP> constexpr int kDepth = DT != 0 && DKP <= 128 ? 2 : 1;
+template <int DT, int DKP> constexpr bool kLate = DT != 1 && DKP > 128;
+template <int DKP> constexpr int kHalf = DKP == 64 || DKP == 256 ? 2 : 4;     // k blocks of S in registers at once
+
+// step(chunk, set), sets of operands taking turns. Where two paths meet inside a loop, registers that loads are still on
+// their way to would be moved, and the moves wait: hence no branch in it, and a loop of its own for each kind of
+// wavefront.
+template <int DEPTH, class F>
+__device__ __forceinline__ void in_turn(int chunks, F step) {
+    if constexpr (DEPTH == 1) {
+        for (int i = 0; i < chunks; ++i) step(i, std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
+    } else {
+        int i = 0;
+        for (; i + 1 < chunks; i += 2) {
+            step(i, std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
+            step(i + 1, std::integral_constant<int, 1>{}, std::integral_constant<int, 0>{});
+        }
+        if (i < chunks) step(i, std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
+    }
+}
+
 template <int DT, int DKP, int NT, bool STORE>
 __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, PP = kOutParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
+    constexpr int HALF = kHalf<DKP>, DEPTH = kDepth<DT, DKP>;
+    constexpr bool LATE = kLate<DT, DKP>;
     using T = elem_t<DT>;
-    __shared__ Tile<3, COLS, DKP + 8> Sx;           // S, [column][dk]
-    __shared__ Tile<3, COLS, 72> Rx, Dx;            // R and exp(G_C - G) U, [column][token]
-    __shared__ Tile<PP, COLS, 72> Ux[STORE ? 1 : 2];    // U, of even and odd chunks
+    __shared__ Tile<3, COLS, DKP> Sx;           // S, [column][dk]
+    __shared__ Tile<3, COLS, 64> Rx, Dx;            // R and exp(G_C - G) U, [column][token]
+    __shared__ Tile<PP, COLS, 64> Ux[STORE ? 1 : 2];    // U, of even and odd chunks
     const sdm_gdr_args_t& a = g.a;
     Scan w;
     if (!scan_of(w, a, total, COLS)) return;
     const int tok = w.part * 16, t4 = tok + w.grp * 4, hv = w.hv, dv = w.dv, chunks = w.chunks;
     const Operands<NP, DKP> from{g, w};
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     f32x4 S[MT][NT];
     load_state<DKP, NT>(S, w, Tiles<DKP>::owner(w) ? a.s0 : nullptr);
     if (Tiles<DKP>::owner(w)) {
@@ -178,156 +228,189 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
         if constexpr (STORE && Tiles<DKP>::owns(decltype(chain)::value))
             store_state<DKP, NT>(S, w, g.w.st + from.sv(chunk) * w.dk * dv);
     };
-    auto update = [&](const Frag<NP> (&kt)[MT][2], float whole, auto chain) {
+    auto update = [&](const Frag<NP> (&kt)[MT][2], float whole, auto chain, auto meanwhile) {
         if constexpr (!Tiles<DKP>::owns(decltype(chain)::value)) return;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             Frag<3> b[2];
-            Dx.frag(b[0], t * 16, 0);
-            Dx.frag(b[1], t * 16, 32);
+            read<2>(b, Dx, t * 16, 0);
+            reads_first();
+            if (t == 0) meanwhile();
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                S[m][t] *= whole;
-                mma<3>(S[m][t], kt[m][0], b[0]);
-                mma<3>(S[m][t], kt[m][1], b[1]);
+                f32x4 y[2] = {S[m][t] * whole, zero};
+                products<3, 2>(y, kt[m], b);
+                S[m][t] = y[0] + y[1];
                 Sx.put(t * 16, (Tiles<DKP>::first(w) + m) * 16, S[m][t]);
             }
         }
     };
-    // Each operand's next chunk is fetched as soon as this one's is used (the last step fetches itself again).
+    // Each operand's next chunk is fetched as soon as this one's is used (the last steps fetch the last chunk again).
     if (w.chain && chunks) {
         const T* vr = rows_at<const T>(a.v, w.s, hv);
-        Frag<NP> kf[NKB], kt[MT][2];
-        Frag<3> inv[2];
-        Tokens4<DT> v[NT];
-        f32x4 eg_n, last_n, beta_n;
-        float whole_n;
-        auto fetch_tok = [&](int chunk) {
+        struct Set {
+            Frag<NP> kf[NKB], kt[MT][2];
+            Frag<3> inv[2];
+            Tokens4<DT> v[NT];
+            f32x4 eg, last, beta;
+            float whole;
+        } set[DEPTH];
+        auto fetch_r = [&](Set& f, int chunk) {
             const int t0 = chunk * kChunk, n = min(kChunk, w.s.len - t0);
-            eg_n = from.token(kTokEg, chunk);
-            last_n = from.token(kTokLast, chunk);
-            beta_n = from.token(kTokBeta, chunk);
-            whole_n = from.whole(chunk);
+            from.rows(f.kf, g.w.kf, chunk);
+            f.eg = from.token(kTokEg, chunk);
+            f.beta = from.token(kTokBeta, chunk);
 #pragma unroll
             for (int c = 0; c < NT; ++c)
-                load4<DT>(v[c], vr + t0 * a.v.token + min(w.c0 + c * 16 + w.row, dv - 1), a.v.token, t4, n);
+                load4<DT>(f.v[c], vr + t0 * a.v.token + min(w.c0 + c * 16 + w.row, dv - 1), static_cast<int>(a.v.token), t4, n);
         };
-        from.rows(kf, g.w.kf, 0);
-        fetch_tok(0);
-        from.square(inv, g.w.inv, 0);
-        from.template cols<true>(kt, g.w.kt, 0);
+        auto fetch_u = [&](Set& f, int chunk) {
+            from.square(f.inv, g.w.inv, chunk);
+            f.last = from.token(kTokLast, chunk);
+        };
+        auto fetch_s = [&](Set& f, int chunk) {
+            from.template cols<true>(f.kt, g.w.kt, chunk);
+            f.whole = from.whole(chunk);
+        };
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+            fetch_r(set[i], min(i, chunks - 1));
+            fetch_u(set[i], min(i, chunks - 1));
+            if constexpr (!LATE) fetch_s(set[i], min(i, chunks - 1));
+        }
         loads_landed();
-        for (int chunk = 0; chunk < chunks; ++chunk) {
-            const int next = min(chunk + 1, chunks - 1), n = min(kChunk, w.s.len - chunk * kChunk);
-            keep(chunk, std::bool_constant<true>{});
-            const f32x4 eg = eg_n, last = last_n, beta = beta_n;
-            const float whole = whole_n;
+        __builtin_amdgcn_s_setprio(2);      // over the outputs' wavefronts
+        in_turn<DEPTH>(chunks, [&](int chunk, auto turn, auto) {
+            Set& f = set[turn];
+            const int next = min(chunk + DEPTH, chunks - 1), n = min(kChunk, w.s.len - chunk * kChunk);
+            keep(chunk, std::true_type{});
             lds_barrier();      // S is in LDS
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                f32x4 x = {0.f, 0.f, 0.f, 0.f};
+                f32x4 x[2] = {zero, zero};
 #pragma unroll
-                for (int kb = 0; kb < NKB; ++kb) {
-                    Frag<3> b;
-                    Sx.frag(b, t * 16, kb * 32);
-                    mma<3>(x, kf[kb], b);
+                for (int k0 = 0; k0 < NKB; k0 += HALF) {
+                    Frag<3> b[HALF];
+                    read<HALF>(b, Sx, t * 16, k0 * 32);
+                    reads_first();
+                    products<3, HALF>(x, f.kf + k0, b);
                 }
-                Rx.put(t * 16, tok, beta * (floats4<DT>(v[t], t4, n) - eg * x));
+                Rx.put(t * 16, tok, f.beta * (floats4<DT>(f.v[t], t4, n) - f.eg * (x[0] + x[1])));
             }
-            from.rows(kf, g.w.kf, next);
-            fetch_tok(next);
             lds_barrier();
+            f32x4 u[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                f32x4 u = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    Frag<3> b;
-                    Rx.frag(b, t * 16, kb * 32);
-                    mma<3>(u, inv[kb], b);
+                Frag<3> b[2];
+                read<2>(b, Rx, t * 16, 0);
+                reads_first();
+                if (t == 0) {
+                    if constexpr (LATE) fetch_s(f, chunk);
+                    fetch_r(f, next);
                 }
-                Dx.put(t * 16, tok, last * u);
-                if constexpr (!STORE) Ux[chunk & 1].put(t * 16, tok, u);
-                if constexpr (STORE) {
-                    if (w.c0 + t * 16 + w.row < dv)
-                        put4(g.w.u + from.sv(chunk) * 64 * dv + w.c0 + t * 16 + w.row, dv, t4, kChunk, u);
-                }
+                f32x4 y[2] = {zero, zero};
+                products<3, 2>(y, f.inv, b);
+                u[t] = y[0] + y[1];
+                Dx.put(t * 16, tok, f.last * u[t]);
             }
-            from.square(inv, g.w.inv, next);
             lds_barrier();
-            update(kt, whole, std::bool_constant<true>{});
-            from.template cols<true>(kt, g.w.kt, next);
-        }
+            update(f.kt, f.whole, std::true_type{}, [&] {
+                fetch_u(f, next);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if constexpr (!STORE) Ux[chunk & 1].put(t * 16, tok, u[t]);
+            });
+            if constexpr (STORE) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (w.c0 + t * 16 + w.row < dv)
+                        put4(g.w.u + from.sv(chunk) * 64 * dv + w.c0 + t * 16 + w.row, dv, t4, kChunk, u[t]);
+            }
+            if constexpr (!LATE) fetch_s(f, next);
+        });
+        if constexpr (!STORE) lds_barrier();    // the last chunk's U
     }
     if (!w.chain && chunks) {
         T* orow = STORE ? nullptr : rows_at<T>(a.o, w.s, hv);
-        Frag<NP> qf[NKB], kt[MT][2];
-        Frag<PP> pm[2];
-        f32x4 o[NT], eg_o = {0.f, 0.f, 0.f, 0.f}, eg_n;
-        float whole_n;
+        struct Set {
+            Frag<NP> qf[STORE ? 1 : NKB], kt[MT][2];
+            Frag<PP> pm[2];
+            f32x4 eg;
+            float whole;
+        } set[DEPTH];
+        f32x4 o[NT];
         // the outputs of a chunk: P U on top of what Q S left
-        auto finish = [&](int chunk) {
+        auto finish = [&](int chunk, const Frag<PP>* pm) {
             const int t0 = chunk * kChunk, n = min(kChunk, w.s.len - t0);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                o[t] = o[t] * (eg_o * a.scale);
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    Frag<PP> b;
-                    Ux[STORE ? 0 : chunk & 1].frag(b, t * 16, kb * 32);
-                    mma<PP>(o[t], pm[kb], b);
-                }
+                Frag<PP> b[2];
+                read<2>(b, Ux[STORE ? 0 : chunk & 1], t * 16, 0);
+                reads_first();
+                f32x4 y[2] = {o[t], zero};
+                products<PP, 2>(y, pm, b);
+                y[0] += y[1];
                 if (w.c0 + t * 16 + w.row < dv)
-                    put4(orow + t0 * a.o.token + w.c0 + t * 16 + w.row, a.o.token, t4, n, o[t]);
+                    put4(orow + t0 * a.o.token + w.c0 + t * 16 + w.row, static_cast<int>(a.o.token), t4, n, y[0]);
             }
         };
-        if constexpr (!STORE) {
-            from.rows(qf, g.w.qf, 0);
-            from.square(pm, g.w.pm, 0);
+        auto fetch_q = [&](Set& f, int chunk) {
+            if constexpr (!STORE) {
+                from.rows(f.qf, g.w.qf, chunk);
+                f.eg = from.token(kTokEg, chunk);
+            }
+        };
+        auto fetch_s = [&](Set& f, int chunk) {
+            from.template cols<false>(f.kt, g.w.kt, chunk);
+            f.whole = from.whole(chunk);
+        };
 #pragma unroll
-            for (int t = 0; t < NT; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < DEPTH; ++i) {
+            fetch_q(set[i], min(i, chunks - 1));
+            if constexpr (!STORE) from.square(set[i].pm, g.w.pm, min(i, chunks - 1));
+            if constexpr (!LATE) fetch_s(set[i], min(i, chunks - 1));
         }
-        eg_n = from.token(kTokEg, 0);
-        whole_n = from.whole(0);
-        from.template cols<false>(kt, g.w.kt, 0);
         loads_landed();
-        for (int chunk = 0; chunk < chunks; ++chunk) {
-            const int next = min(chunk + 1, chunks - 1);
-            keep(chunk, std::bool_constant<false>{});
-            const f32x4 eg = eg_n;
-            const float whole = whole_n;
+        in_turn<DEPTH>(chunks, [&](int chunk, auto turn, auto other) {
+            Set &f = set[turn], &before = set[other];
+            const int next = min(chunk + DEPTH, chunks - 1);
+            keep(chunk, std::false_type{});
             lds_barrier();
-            f32x4 x[NT];
+            if constexpr (!STORE) {
+                if (chunk) {
+                    finish(chunk - 1, before.pm);
+                    from.square(before.pm, g.w.pm, min(chunk + DEPTH - 1, chunks - 1));
+                }
+            }
+            lds_barrier();
+            if constexpr (LATE) fetch_s(f, chunk);
             if constexpr (!STORE) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    x[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    f32x4 x[2] = {zero, zero};
 #pragma unroll
-                    for (int kb = 0; kb < NKB; ++kb) {
-                        Frag<PP> b;
-#pragma unroll
-                        for (int p = 0; p < PP; ++p)
-                            b.p[p] = *reinterpret_cast<const bf16x8*>(&Sx.v[p][t * 16 + w.row][kb * 32 + 8 * w.grp]);
-                        mma<PP>(x[t], qf[kb], b);
+                    for (int k0 = 0; k0 < NKB; k0 += HALF) {
+                        Frag<PP> b[HALF];
+                        read<HALF>(b, Sx, t * 16, k0 * 32);
+                        reads_first();
+                        products<PP, HALF>(x, f.qf + k0, b);
                     }
+                    o[t] = (x[0] + x[1]) * (f.eg * a.scale);
                 }
-                from.rows(qf, g.w.qf, next);
             }
-            eg_n = from.token(kTokEg, next);
-            whole_n = from.whole(next);
+            fetch_q(f, next);
             lds_barrier();
-            if constexpr (!STORE) {
-                if (chunk) finish(chunk - 1);
-                from.square(pm, g.w.pm, chunk);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) o[t] = x[t];
-                eg_o = eg;
-            }
+            update(f.kt, f.whole, std::false_type{}, [] {});
+            if constexpr (!LATE) fetch_s(f, next);
+        });
+        if constexpr (!STORE) {
             lds_barrier();
-            update(kt, whole, std::bool_constant<false>{});
-            from.template cols<false>(kt, g.w.kt, next);
+            const int last = chunks - 1;
+            if (DEPTH == 1 || (last & 1) == 0)
+                finish(last, set[0].pm);
+            else
+                finish(last, set[DEPTH - 1].pm);
         }
-        if constexpr (!STORE) finish(chunks - 1);
     }
     if constexpr (!STORE)
         if (a.s_final && Tiles<DKP>::owner(w)) store_state<DKP, NT>(S, w, a.s_final + w.head * w.dk * dv);
@@ -336,15 +419,18 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
 template <int DT, int DKP, int NT>
 __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
+    constexpr int HALF = kHalf<DKP>, DEPTH = kDepth<DT, DKP>;
+    constexpr bool LATE = kLate<DT, DKP>;
     using T = elem_t<DT>;
-    __shared__ Tile<3, COLS, DKP + 8> Sx;           // dS, [column][dk]
-    __shared__ Tile<3, COLS, 72> Ox, Qx, Ux, Rx;    // the next chunk's dO, scale exp(G) dO, dU and -beta exp(G) dR
+    __shared__ Tile<3, COLS, DKP> Sx;           // dS, [column][dk]
+    __shared__ Tile<3, COLS, 64> Ox, Qx, Ux, Rx;    // the next chunk's dO, scale exp(G) dO, dU and -beta exp(G) dR
     __shared__ f32x4 Wx[NT][4][64];                 // P^T dO, as the chain's wavefronts hold dU
     const sdm_gdr_args_t& a = g.a;
     Scan w;
     if (!scan_of(w, a, total, COLS)) return;
     const int tok = w.part * 16, t4 = tok + w.grp * 4, hv = w.hv, dv = w.dv, top = w.chunks - 1;
     const Operands<NP, DKP> from{g, w};
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     f32x4 S[MT][NT];
     load_state<DKP, NT>(S, w, Tiles<DKP>::owner(w) ? a.ds_final : nullptr);
     if (Tiles<DKP>::owner(w)) {
@@ -353,159 +439,185 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
 #pragma unroll
             for (int t = 0; t < NT; ++t) Sx.put(t * 16, (Tiles<DKP>::first(w) + m) * 16, S[m][t]);
     }
-    Frag<NP> kt[MT][2], qt[MT][2];
     auto keep = [&](int chunk, auto chain) {
         if constexpr (Tiles<DKP>::owns(decltype(chain)::value))
             store_state<DKP, NT>(S, w, g.w.dst + from.sv(chunk) * w.dk * dv);
     };
-    auto update = [&](float whole, auto chain) {
+    auto update = [&](const Frag<NP> (&qt)[MT][2], const Frag<NP> (&kt)[MT][2], float whole, auto chain, auto meanwhile) {
         if constexpr (!Tiles<DKP>::owns(decltype(chain)::value)) return;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             Frag<3> bq[2], br[2];
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                Qx.frag(bq[kb], t * 16, kb * 32);
-                Rx.frag(br[kb], t * 16, kb * 32);
-            }
+            read<2>(bq, Qx, t * 16, 0);
+            read<2>(br, Rx, t * 16, 0);
+            reads_first();
+            if (t == 0) meanwhile();
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                S[m][t] *= whole;
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    mma<3>(S[m][t], qt[m][kb], bq[kb]);
-                    mma<3>(S[m][t], kt[m][kb], br[kb]);
-                }
+                f32x4 y[2] = {S[m][t] * whole, zero};
+                products<3, 2>(y, qt[m], bq);
+                products<3, 2>(y, kt[m], br);
+                S[m][t] = y[0] + y[1];
                 Sx.put(t * 16, (Tiles<DKP>::first(w) + m) * 16, S[m][t]);
             }
         }
     };
+    const auto back = [&](int i) { return max(top - i, 0); };       // the i-th chunk from the end
     if (w.chain && top >= 0) {
         T* dvr = rows_at<T>(a.d_v, w.s, hv);
-        Frag<NP> kf[NKB];
-        Frag<3> inv[2];
-        f32x4 eg_n, last_n, beta_n;
-        float whole_n;
-        auto fetch_tok = [&](int chunk) {
-            eg_n = from.token(kTokEg, chunk);
-            last_n = from.token(kTokLast, chunk);
-            beta_n = from.token(kTokBeta, chunk);
-            whole_n = from.whole(chunk);
+        struct Set {
+            Frag<NP> kf[NKB], kt[MT][2], qt[MT][2];
+            Frag<3> inv[2];
+            f32x4 eg, last, beta;
+            float whole;
+        } set[DEPTH];
+        auto fetch_u = [&](Set& f, int chunk) {
+            from.rows(f.kf, g.w.kf, chunk);
+            f.last = from.token(kTokLast, chunk);
         };
-        from.rows(kf, g.w.kf, top);
-        fetch_tok(top);
-        from.square(inv, g.w.invt, top);
-        from.template cols<true>(kt, g.w.kt, top);
-        from.template cols<true>(qt, g.w.qt, top);
+        auto fetch_r = [&](Set& f, int chunk) {
+            from.square(f.inv, g.w.invt, chunk);
+        };
+        auto fetch_s = [&](Set& f, int chunk) {
+            from.template cols<true>(f.kt, g.w.kt, chunk);
+            from.template cols<true>(f.qt, g.w.qt, chunk);
+            f.whole = from.whole(chunk);
+        };
+        auto fetch_v = [&](Set& f, int chunk) {
+            f.eg = from.token(kTokEg, chunk);
+            f.beta = from.token(kTokBeta, chunk);
+        };
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+            fetch_u(set[i], back(i));
+            fetch_r(set[i], back(i));
+            fetch_v(set[i], back(i));
+            if constexpr (!LATE) fetch_s(set[i], back(i));
+        }
         loads_landed();
+        __builtin_amdgcn_s_setprio(2);
         lds_barrier();
-        for (int chunk = top; chunk >= 0; --chunk) {
-            const int t0 = chunk * kChunk, n = min(kChunk, w.s.len - t0), next = max(chunk - 1, 0);
-            keep(chunk, std::bool_constant<true>{});
-            const f32x4 eg = eg_n, last = last_n, beta = beta_n;
-            const float whole = whole_n;
+        in_turn<DEPTH>(top + 1, [&](int i, auto turn, auto) {
+            Set& f = set[turn];
+            const int chunk = top - i, next = back(i + DEPTH), t0 = chunk * kChunk, n = min(kChunk, w.s.len - t0);
+            keep(chunk, std::true_type{});
             lds_barrier();      // dS and P^T dO are in LDS
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                f32x4 u = {0.f, 0.f, 0.f, 0.f};
+                f32x4 x[2] = {zero, zero};
 #pragma unroll
-                for (int kb = 0; kb < NKB; ++kb) {
-                    Frag<3> b;
-                    Sx.frag(b, t * 16, kb * 32);
-                    mma<3>(u, kf[kb], b);
+                for (int k0 = 0; k0 < NKB; k0 += HALF) {
+                    Frag<3> b[HALF];
+                    read<HALF>(b, Sx, t * 16, k0 * 32);
+                    reads_first();
+                    products<3, HALF>(x, f.kf + k0, b);
                 }
-                Ux.put(t * 16, tok, u * last + Wx[t][w.part][w.lane]);
+                Ux.put(t * 16, tok, (x[0] + x[1]) * f.last + Wx[t][w.part][w.lane]);
             }
-            from.rows(kf, g.w.kf, next);
-            fetch_tok(next);
             lds_barrier();
+            f32x4 d[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                f32x4 d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    Frag<3> b;
-                    Ux.frag(b, t * 16, kb * 32);
-                    mma<3>(d, inv[kb], b);
+                Frag<3> b[2];
+                read<2>(b, Ux, t * 16, 0);
+                reads_first();
+                if (t == 0) {
+                    if constexpr (LATE) fetch_s(f, chunk);
+                    else fetch_u(f, next);
                 }
-                Rx.put(t * 16, tok, -(beta * eg) * d);
+                f32x4 y[2] = {zero, zero};
+                products<3, 2>(y, f.inv, b);
+                d[t] = y[0] + y[1];
+                Rx.put(t * 16, tok, -(f.beta * f.eg) * d[t]);
+            }
+            lds_barrier();
+            const f32x4 beta = f.beta;
+            update(f.qt, f.kt, f.whole, std::true_type{}, [&] {
+                fetch_r(f, next);
+                fetch_v(f, next);
+            });
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
                 const int c = w.c0 + t * 16 + w.row;
                 if (c < dv) {
-                    put4(g.w.dr + from.sv(chunk) * 64 * dv + c, dv, t4, kChunk, d);
-                    put4(dvr + t0 * a.d_v.token + c, a.d_v.token, t4, n, beta * d);
+                    put4(g.w.dr + from.sv(chunk) * 64 * dv + c, dv, t4, kChunk, d[t]);
+                    put4(dvr + t0 * a.d_v.token + c, static_cast<int>(a.d_v.token), t4, n, beta * d[t]);
                 }
             }
-            from.square(inv, g.w.invt, next);
-            lds_barrier();
-            update(whole, std::bool_constant<true>{});
-            from.template cols<true>(kt, g.w.kt, next);
-            from.template cols<true>(qt, g.w.qt, next);
-        }
+            if constexpr (LATE) fetch_u(f, next);
+            else fetch_s(f, next);
+        });
     }
     if (!w.chain && top >= 0) {
         const T* dor = rows_at<const T>(a.d_o, w.s, hv);
-        Frag<3> pm[2];                  // P^T of the next chunk
-        Tokens4<DT> raw[NT];            // dO of the chunk after the next
-        f32x4 o1[NT], eg_n;             // dO of this chunk
-        float whole_n;
-        auto fetch_do = [&](int chunk) {
+        struct Set {
+            Frag<NP> kt[MT][2], qt[MT][2];
+            Frag<3> pm[2];                  // P^T of the next chunk
+            Tokens4<DT> raw[NT];            // dO of the next chunk
+            f32x4 eg;
+            float whole;
+        } set[DEPTH];
+        f32x4 o1[NT];                       // dO of this chunk
+        auto fetch_do = [&](Set& f, int chunk) {
             const int t0 = chunk * kChunk, n = min(kChunk, w.s.len - t0);
 #pragma unroll
             for (int c = 0; c < NT; ++c)
-                load4<DT>(raw[c], dor + t0 * a.d_o.token + min(w.c0 + c * 16 + w.row, dv - 1), a.d_o.token, t4, n);
+                load4<DT>(f.raw[c], dor + t0 * a.d_o.token + min(w.c0 + c * 16 + w.row, dv - 1), static_cast<int>(a.d_o.token), t4, n);
         };
-        auto p_do = [&]() {     // P^T dO of the chunk in Ox, for the chain's next step
+        auto fetch_s = [&](Set& f, int chunk) {
+            from.template cols<false>(f.kt, g.w.kt, chunk);
+            from.template cols<false>(f.qt, g.w.qt, chunk);
+            f.whole = from.whole(chunk);
+        };
+        auto p_do = [&](const Frag<3>* pm) {    // P^T dO of the chunk in Ox, for the chain's next step
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                f32x4 x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    Frag<3> b;
-                    Ox.frag(b, t * 16, kb * 32);
-                    mma<3>(x, pm[kb], b);
-                }
-                Wx[t][w.part][w.lane] = x;
+                Frag<3> b[2];
+                read<2>(b, Ox, t * 16, 0);
+                reads_first();
+                f32x4 y[2] = {zero, zero};
+                products<3, 2>(y, pm, b);
+                Wx[t][w.part][w.lane] = y[0] + y[1];
             }
         };
-        eg_n = from.token(kTokEg, top);
-        whole_n = from.whole(top);
-        from.square(pm, g.w.pm, top);
-        fetch_do(top);
-        from.template cols<false>(kt, g.w.kt, top);
-        from.template cols<false>(qt, g.w.qt, top);
+        from.square(set[0].pm, g.w.pm, top);
+        fetch_do(set[0], top);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            o1[t] = floats4<DT>(raw[t], t4, min(kChunk, w.s.len - top * kChunk));
+            o1[t] = floats4<DT>(set[0].raw[t], t4, min(kChunk, w.s.len - top * kChunk));
             Ox.put(t * 16, tok, o1[t]);
         }
         lds_barrier();
-        p_do();
-        from.square(pm, g.w.pm, max(top - 1, 0));
-        fetch_do(max(top - 1, 0));
+        p_do(set[0].pm);
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+            from.square(set[i].pm, g.w.pm, back(i + 1));
+            fetch_do(set[i], back(i + 1));
+            set[i].eg = from.token(kTokEg, back(i));
+            if constexpr (!LATE) fetch_s(set[i], back(i));
+        }
         loads_landed();
-        for (int chunk = top; chunk >= 0; --chunk) {
-            const int next = max(chunk - 1, 0), n = min(kChunk, w.s.len - next * kChunk);
-            keep(chunk, std::bool_constant<false>{});
-            const f32x4 eg = eg_n;
-            const float whole = whole_n;
+        in_turn<DEPTH>(top + 1, [&](int i, auto turn, auto) {
+            Set& f = set[turn];
+            const int chunk = top - i, n = min(kChunk, w.s.len - back(i + 1) * kChunk);
+            keep(chunk, std::false_type{});
             lds_barrier();
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                Qx.put(t * 16, tok, o1[t] * (eg * a.scale));
-                o1[t] = floats4<DT>(raw[t], t4, n);
+                Qx.put(t * 16, tok, o1[t] * (f.eg * a.scale));
+                o1[t] = floats4<DT>(f.raw[t], t4, n);
                 Ox.put(t * 16, tok, o1[t]);
             }
-            eg_n = from.token(kTokEg, next);
-            whole_n = from.whole(next);
-            fetch_do(max(chunk - 2, 0));
+            f.eg = from.token(kTokEg, back(i + DEPTH));
+            fetch_do(f, back(i + 1 + DEPTH));
             lds_barrier();
-            p_do();
-            from.square(pm, g.w.pm, max(chunk - 2, 0));
+            if constexpr (LATE) fetch_s(f, chunk);
+            p_do(f.pm);
+            from.square(f.pm, g.w.pm, back(i + 1 + DEPTH));
             lds_barrier();
-            update(whole, std::bool_constant<false>{});
-            from.template cols<false>(kt, g.w.kt, next);
-            from.template cols<false>(qt, g.w.qt, next);
-        }
+            update(f.qt, f.kt, f.whole, std::false_type{}, [] {});
+            if constexpr (!LATE) fetch_s(f, back(i + DEPTH));
+        });
     }
     if (a.ds0 && Tiles<DKP>::owner(w)) store_state<DKP, NT>(S, w, a.ds0 + w.head * w.dk * dv);
 }
