@@ -20,10 +20,10 @@ struct GdrWork {
     uint16_t* qf;       // of Q (forward)
     uint16_t* kt;       // of K^T, dkp x 64
     uint16_t* qt;       // of Q^T (backward)
-    float* st;          // [slots][Hv][dk][dv]: each chunk's entering state (backward)
-    float* dst;         // [slots][Hv][dk][dv]: gradient of each chunk's last state (backward)
-    float* u;           // [slots][Hv][64][dv] (backward)
-    float* dr;          // [slots][Hv][64][dv] (backward)
+    float* st;          // [slots][Hv][dk][dvp]: each chunk's entering state (backward)
+    float* dst;         // [slots][Hv][dk][dvp]: gradient of each chunk's last state (backward)
+    float* u;           // [slots][Hv][64][dvp] (backward)
+    float* dr;          // [slots][Hv][64][dvp] (backward)
     float* dqp;         // [slots][Hv][64][dk] per-value-head parts of dq and dk, when value heads share a q/k head
     float* dkp;
 };
@@ -35,9 +35,8 @@ struct GdrLaunch {
     GdrWork w;
     int32_t slots;      // chunk slots
     int32_t dkp;        // dk padded to 64, 128 or 256
-    int32_t cols;       // state columns a workgroup of the scans owns: 16 or 32
+    int32_t dvp;        // dv rounded up to a multiple of 8: rows of st, dst, u, dr, zero past dv
     int32_t vec_qk, vec_v;      // rows of q and k / v, o, d_o and their gradients start on 16-byte boundaries
-    int32_t vec_st;     // state rows do
 };
 
 // bfloat16 parts that hold an element of a type exactly: 3, 1, 2

@@ -168,7 +168,7 @@ int64_t padded_dk(int64_t dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
 // Lays the workspace out from `base`; its size.
 int64_t lay_out(const sdm_gdr_args_t* a, bool backward, char* base, GdrWork* w) {
     const int64_t slots = slots_of(a), sv = slots * a->Hv, sk = slots * a->Hk;
-    const int64_t in = parts_of(a->dtype), dkp = padded_dk(a->dk);
+    const int64_t in = parts_of(a->dtype), dkp = padded_dk(a->dk), dvp = (a->dv + 7) / 8 * 8;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         char* p = base + at;
@@ -185,10 +185,10 @@ int64_t lay_out(const sdm_gdr_args_t* a, bool backward, char* base, GdrWork* w) 
     if (backward) {
         t.invt = reinterpret_cast<uint16_t*>(take(sv * kChunk * kChunk * 3 * 2));
         t.qt = reinterpret_cast<uint16_t*>(take(sk * dkp * kChunk * in * 2));
-        t.st = reinterpret_cast<float*>(take(sv * a->dk * a->dv * 4));
-        t.dst = reinterpret_cast<float*>(take(sv * a->dk * a->dv * 4));
-        t.u = reinterpret_cast<float*>(take(sv * kChunk * a->dv * 4));
-        t.dr = reinterpret_cast<float*>(take(sv * kChunk * a->dv * 4));
+        t.st = reinterpret_cast<float*>(take(sv * a->dk * dvp * 4));
+        t.dst = reinterpret_cast<float*>(take(sv * a->dk * dvp * 4));
+        t.u = reinterpret_cast<float*>(take(sv * kChunk * dvp * 4));
+        t.dr = reinterpret_cast<float*>(take(sv * kChunk * dvp * 4));
         if (a->Hv != a->Hk) {
             t.dqp = reinterpret_cast<float*>(take(sv * kChunk * a->dk * 4));
             t.dkp = reinterpret_cast<float*>(take(sv * kChunk * a->dk * 4));
@@ -210,7 +210,7 @@ GdrLaunch plan(const sdm_gdr_args_t* a, bool backward, void* workspace) {
     lay_out(a, backward, static_cast<char*>(workspace), &g.w);
     g.slots = static_cast<int32_t>(slots_of(a));
     g.dkp = static_cast<int32_t>(padded_dk(a->dk));
-    g.cols = 16;
+    g.dvp = static_cast<int32_t>((a->dv + 7) / 8 * 8);
     g.vec_qk = vec_rows(a->q, a->dk, a->dtype) && vec_rows(a->k, a->dk, a->dtype);
     g.vec_v = vec_rows(a->v, a->dv, a->dtype);
     if (backward) {
@@ -219,8 +219,6 @@ GdrLaunch plan(const sdm_gdr_args_t* a, bool backward, void* workspace) {
     } else {
         g.vec_v = g.vec_v && vec_rows(a->o, a->dv, a->dtype);
     }
-    g.vec_st = a->dv % 8 == 0 && aligned(a->s0, 16) && aligned(a->s_final, 16) && aligned(a->ds_final, 16) &&
-               aligned(a->ds0, 16);
     return g;
 }
 

@@ -10,9 +10,13 @@
 //     and exp(G_C) <S, dE>: every factor exp(G_i ..) of a product is differentiated by the product itself
 //     dg = the sums of dG from each token to the chunk's end
 //
-// One workgroup per chunk and value head. Each wavefront owns dk columns of dq and dk for all 64 tokens, so S and dE
-// are read and split once; dO, U and dR are staged in LDS by 64 columns of dv at a time. About 18 x 64 dk dv flops on
-// up to six steps each: bounded by the matrix cores and the LDS reads that feed them.
+// One workgroup per chunk and value head. Each of eight wavefronts owns dk columns of dq and dk for all 64 tokens (half
+// of them for dk <= 64), so S and dE are read and split once; dO, U and dR are staged in LDS by 64 columns of dv at a
+// time. About 18 x 64 dk dv flops on up to six steps each: bounded by the matrix cores and the LDS reads that feed them.
+//
+// Token order. A result tile's lane holds rows 4 p .. 4 p + 3 (p = lane / 16), a fragment's lane elements 8 p .. 8 p + 7.
+// Row r of token tile j is token 32 (j / 2) + 8 (r / 4) + 4 (j % 2) + r % 4: then the four tokens of a result lane are
+// four of the eight in the same lane's fragment of K^T and Q^T, and the row sums with k and q need no further read.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -21,16 +25,32 @@
 namespace sdm_delta {
 namespace {
 
+// The sum over the 16 lanes of a row.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+    return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row_sum16(float x) {
+    x = dpp_add<0xb1>(x);       // lanes 1, 0, 3, 2 of each four
+    x = dpp_add<0x4e>(x);       // 2, 3, 0, 1
+    x = dpp_add<0x141>(x);      // 7 .. 0 of each eight
+    return dpp_add<0x140>(x);   // 15 .. 0
+}
+
+__device__ __forceinline__ constexpr int token_of(int j, int r) { return 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3); }
+
 template <int DT, int DKP>
-__global__ __launch_bounds__(256, DKP <= 128 ? 2 : 1) void gdr_grad(const GdrLaunch g) {
-    constexpr int NP = kParts<DT>, MT = DKP / 64;
+__global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
+    constexpr int NP = kParts<DT>;
+    constexpr int MT = 1, PASSES = DKP == 256 ? 2 : 1;  // dk tiles of a wavefront at a time; times
+    constexpr int NJ = DKP >= 128 ? 4 : 2;              // its token tiles
     using T = elem_t<DT>;
     struct Staged {
         Tile<NP, 64, 64> o;
         Tile<3, 64, 64> u, r;
     };
     struct Pairs {
-        Tile<3, 64, 64> m, t;     // a 64 x 64 matrix by rows and by columns
+        Tile<3, 64, 64> m[2], t[2];     // dP and dA by rows and by columns
     };
     union Shared {
         Staged s;
@@ -38,7 +58,7 @@ __global__ __launch_bounds__(256, DKP <= 128 ? 2 : 1) void gdr_grad(const GdrLau
         __device__ Shared() {}
     };
     __shared__ Shared L;
-    __shared__ alignas(16) float Gh[64], Gl[64], Eg[64], La[64], Be[64], Rv[64], red[4][2][64], tot[4][2];
+    __shared__ alignas(16) float Gh[64], Gl[64], Eg[64], La[64], Be[64], Rv[64], red[8][2][64], tot[8][2];
     const sdm_gdr_args_t& a = g.a;
     int seq, chunk;
     Seq s;
@@ -46,10 +66,11 @@ __global__ __launch_bounds__(256, DKP <= 128 ? 2 : 1) void gdr_grad(const GdrLau
     if (!owner(a, slot, seq, chunk, s)) return;
     const int t0 = chunk * kChunk, n = min(kChunk, s.len - t0);
     const int dk = static_cast<int>(a.dk), dv = static_cast<int>(a.dv);
-    const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
+    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int j0 = DKP >= 128 ? 0 : (wave >> 2) * 2;
     const int64_t sv = static_cast<int64_t>(slot) * a.Hv + hv, sk = static_cast<int64_t>(slot) * a.Hk + hk;
-    const bool vst = (dv & 7) == 0;
+    const int dvp = g.dvp;
 
     if (threadIdx.x < 64) {
         const float* t = g.w.tok + sv * (kTokFields * 64) + threadIdx.x;
@@ -61,82 +82,117 @@ __global__ __launch_bounds__(256, DKP <= 128 ? 2 : 1) void gdr_grad(const GdrLau
     }
     const T* dor = rows_at<const T>(a.d_o, s, hv) + t0 * a.d_o.token;
     const T* vr = rows_at<const T>(a.v, s, hv) + t0 * a.v.token;
-    const float* ur = g.w.u + sv * 64 * dv;
-    const float* rp = g.w.dr + sv * 64 * dv;
-    const float* st = g.w.st + sv * dk * dv;
-    const float* de = g.w.dst + sv * dk * dv;
+    const float* ur = g.w.u + sv * 64 * dvp;
+    const float* rp = g.w.dr + sv * 64 * dvp;
+    const float* st = g.w.st + sv * dk * dvp;
+    const float* de = g.w.dst + sv * dk * dvp;
+    const uint16_t* kt = g.w.kt + sk * (NP * 64 * DKP);
+    const uint16_t* qt = g.w.qt + sk * (NP * 64 * DKP);
 
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4 dp[4], da[4], aq[MT][4], ar[MT][4], as[MT][4];
+#pragma unroll 1
+    for (int pass = 0; pass < PASSES; ++pass) {     // more than 128 columns of dk: the second half after the first
+    const int tile0 = DKP >= 128 ? pass * 8 + wave : wave & 3;
+    if (pass) lds_barrier();
+    int row = lane & 15, grp = lane >> 4;
+    // not the same in every pass as far as the compiler knows: it would keep every address of a pass across the loop,
+    // in scratch memory
+    if constexpr (PASSES > 1) asm volatile("" : "+v"(row), "+v"(grp));
+    f32x4 dpa[4], aq[MT][NJ], ar[MT][NJ], as[MT][NJ];       // dpa: a row tile of dP (wavefronts 0 .. 3) or of dA
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        dp[j] = da[j] = zero;
+    for (int j = 0; j < 4; ++j) dpa[j] = zero;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int m = 0; m < MT; ++m) aq[m][j] = ar[m][j] = as[m][j] = zero;
-    }
-    float rv[2] = {0.f, 0.f}, sde = 0.f;
+    float rv = 0.f, sde = 0.f;
+    // staging: this thread's row and its token, 8 columns
+    const int si = threadIdx.x >> 3, sc = (threadIdx.x & 7) * 8, stok = token_of(si >> 4, si & 15);
+    struct {
+        Raw<DT> o, v;
+        Raw<0> u, r;
+    } in;
+    auto fetch = [&](int c0) {
+        const int c = c0 + sc, at = min(stok, n - 1);
+        if (g.vec_v) {
+            load_raw<DT, true>(in.o, dor + at * a.d_o.token, c, dv, stok < n);
+            load_raw<DT, true>(in.v, vr + at * a.v.token, c, dv, stok < n);
+        } else {
+            load_raw<DT, false>(in.o, dor + at * a.d_o.token, c, dv, stok < n);
+            load_raw<DT, false>(in.v, vr + at * a.v.token, c, dv, stok < n);
+        }
+        load_raw<0, true>(in.u, ur + stok * dvp, c, dvp, true);
+        load_raw<0, true>(in.r, rp + stok * dvp, c, dvp, true);
+    };
+    fetch(0);
     for (int c0 = 0; c0 < dv; c0 += 64) {
+        // S and dE of the block, on their way while dO, U and dR are split into LDS
+        Raw<0> xs[MT][2], ys[MT][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = h * 32 + (threadIdx.x >> 3), cc = (threadIdx.x & 7) * 8, c = c0 + cc;
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const int d = (tile0 + m) * 16 + row, c = c0 + kb * 32 + grp * 8;
+                const int64_t at = static_cast<int64_t>(min(d, dk - 1)) * dvp;
+                load_raw<0, true>(xs[m][kb], st + at, c, dvp, d < dk);
+                load_raw<0, true>(ys[m][kb], de + at, c, dvp, d < dk);
+            }
+        {
             float x[8], y[8];
-            Frag<3> f;
-            Raw<DT> raw;
             Frag<NP> fo;
-            const int at = min(i, n - 1);
-            if (g.vec_v)
-                load_raw<DT, true>(raw, dor + at * a.d_o.token, c, dv, i < n);
-            else
-                load_raw<DT, false>(raw, dor + at * a.d_o.token, c, dv, i < n);
-            raw_frag<DT>(fo, raw);
-            load8(x, ur + i * dv, c, dv, vst);
+            Frag<3> f;
+            raw_frag<DT>(fo, in.o);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) *reinterpret_cast<bf16x8*>(L.s.o.at(p, si, sc)) = fo.p[p];
+            raw_floats<0>(x, in.u);
             split8(f, x);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) *reinterpret_cast<bf16x8*>(L.s.o.at(p, i, cc)) = fo.p[p];
+            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(L.s.u.at(p, si, sc)) = f.p[p];
+            raw_floats<0>(y, in.r);
+            split8(f, y);
 #pragma unroll
-            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(L.s.u.at(p, i, cc)) = f.p[p];
-            load8(x, rp + i * dv, c, dv, vst);
-            split8(f, x);
+            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(L.s.r.at(p, si, sc)) = f.p[p];
+            raw_floats<DT>(x, in.v);
 #pragma unroll
-            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(L.s.r.at(p, i, cc)) = f.p[p];
-            if (g.vec_v)
-                load_raw<DT, true>(raw, vr + at * a.v.token, c, dv, i < n);
-            else
-                load_raw<DT, false>(raw, vr + at * a.v.token, c, dv, i < n);
-            raw_floats<DT>(y, raw);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) rv[h] = fmaf(x[e], y[e], rv[h]);
+            for (int e = 0; e < 8; ++e) rv = fmaf(x[e], y[e], rv);
         }
         lds_barrier();
+        fetch(c0 + 64);     // past dv: zeros, and no address past a row
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            Frag<NP> fo;
-            Frag<3> fr, fu;
-            L.s.o.frag(fo, wave * 16, kb * 32);
-            L.s.r.frag(fr, wave * 16, kb * 32);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                L.s.u.frag(fu, j * 16, kb * 32);
-                mma<3>(dp[j], fo, fu);
-                mma<3>(da[j], fr, fu);
-            }
             Frag<3> fs[MT], fe[MT];
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const int d = (wave * MT + m) * 16 + row, c = c0 + kb * 32 + grp * 8;
                 float x[8], y[8];
-                load8(x, st + static_cast<int64_t>(d) * dv, c, d < dk ? dv : 0, vst);
-                load8(y, de + static_cast<int64_t>(d) * dv, c, d < dk ? dv : 0, vst);
+                raw_floats<0>(x, xs[m][kb]);
+                raw_floats<0>(y, ys[m][kb]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sde = fmaf(x[e], y[e], sde);
                 split8(fs[m], x);
                 split8(fe[m], y);
             }
+            Frag<NP> fo;
+            Frag<3> fr, fu;
+            if (wave < 4) {
+                L.s.o.frag(fo, wave * 16, kb * 32);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                L.s.o.frag(fo, j * 16, kb * 32);
-                L.s.r.frag(fr, j * 16, kb * 32);
-                L.s.u.frag(fu, j * 16, kb * 32);
+                for (int j = 0; j < 4; ++j) {
+                    L.s.u.frag(fu, j * 16, kb * 32);
+                    mma<3>(dpa[j], fo, fu);
+                }
+            } else {
+                L.s.r.frag(fr, (wave - 4) * 16, kb * 32);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    L.s.u.frag(fu, j * 16, kb * 32);
+                    mma<3>(dpa[j], fr, fu);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                L.s.o.frag(fo, (j0 + j) * 16, kb * 32);
+                L.s.r.frag(fr, (j0 + j) * 16, kb * 32);
+                L.s.u.frag(fu, (j0 + j) * 16, kb * 32);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     mma<3>(aq[m][j], fo, fs[m]);
@@ -148,134 +204,136 @@ __global__ __launch_bounds__(256, DKP <= 128 ? 2 : 1) void gdr_grad(const GdrLau
         lds_barrier();
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int m = 1; m < 8; m <<= 1) rv[h] += __shfl_xor(rv[h], m, 64);
-        if ((threadIdx.x & 7) == 0) Rv[h * 32 + (threadIdx.x >> 3)] = rv[h];
-    }
+    for (int m = 1; m < 8; m <<= 1) rv += __shfl_xor(rv, m, 64);
+    if ((threadIdx.x & 7) == 0) Rv[stok] = rv;
+    if (DKP < 128 && wave >= 4) sde = 0.f;      // wavefronts 0 .. 3 have summed the same
 
-    const T* kr = rows_at<const T>(a.k, s, hk) + t0 * a.k.token;
-    const T* qr = rows_at<const T>(a.q, s, hk) + t0 * a.q.token;
-    // the state's part of each sum, and k . dks
-    float ks = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const f32x4 eg = *reinterpret_cast<const f32x4*>(&Eg[j * 16 + grp * 4]);
-        const f32x4 la = *reinterpret_cast<const f32x4*>(&La[j * 16 + grp * 4]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            aq[m][j] *= eg * a.scale;
-            ar[m][j] *= -eg;
-            as[m][j] *= la;
-            const int d = (wave * MT + m) * 16 + row;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = j * 16 + grp * 4 + e;
-                if (i < n && d < dk) ks = fmaf(static_cast<float>(kr[i * a.k.token + d]), as[m][j][e], ks);
-            }
-        }
-    }
-    // dP, then dA: by rows against K, by columns against Q and K
-    const uint16_t* kt = g.w.kt + sk * (NP * 64 * DKP);
-    const uint16_t* qt = g.w.qt + sk * (NP * 64 * DKP);
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        if (which) lds_barrier();
+    // dP and dA with their decays, by rows (against K) and, dA times beta, by columns (against Q and K)
+    {
+        const int which = wave >> 2, wi = wave & 3;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f32x4 x = zero, y = zero;
+            const int i0 = token_of(wi, grp * 4), c = token_of(j, row);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = wave * 16 + grp * 4 + e, c = j * 16 + row;
-                if (j <= wave && (which ? c < i : c <= i)) {
-                    const float d = expf((Gh[i] - Gh[c]) + (Gl[i] - Gl[c]));
-                    x[e] = which ? -da[j][e] * d : dp[j][e] * d * a.scale;
-                    y[e] = which ? Be[i] * x[e] : x[e];
-                }
+                const int i = i0 + e;
+                const float d = expf((Gh[i] - Gh[c]) + (Gl[i] - Gl[c]));
+                const bool in = which ? c < i : c <= i;
+                x[e] = in ? dpa[j][e] * d * (which ? -1.f : a.scale) : 0.f;
+                y[e] = in && which ? Be[i] * x[e] : x[e];
             }
             bf16x4 xs[3];
             split4<3>(xs, x);
 #pragma unroll
             for (int p = 0; p < 3; ++p)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) *L.p.m.at(p, wave * 16 + grp * 4 + e, j * 16 + row) = xs[p][e];
-            L.p.t.put(j * 16, wave * 16, y);
-        }
-        lds_barrier();
+                for (int e = 0; e < 4; ++e) *L.p.m[which].at(p, wi * 16 + grp * 4 + e, c) = xs[p][e];
+            split4<3>(xs, y);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            Frag<NP> fk[MT], fq[MT];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                load_frag<NP>(fk[m], kt + static_cast<int64_t>((wave * MT + m) * 2 + kb) * NP * 512);
-                if (!which) load_frag<NP>(fq[m], qt + static_cast<int64_t>((wave * MT + m) * 2 + kb) * NP * 512);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                Frag<3> fm, ft;
-                if (kb * 2 <= j) {
-                    L.p.m.frag(fm, j * 16, kb * 32);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        if (which)
-                            mma<3>(ar[m][j], fm, fk[m]);
-                        else
-                            mma<3>(aq[m][j], fm, fk[m]);
-                    }
-                }
-                if (kb * 2 + 1 >= j) {
-                    L.p.t.frag(ft, j * 16, kb * 32);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        if (which)
-                            mma<3>(as[m][j], ft, fk[m]);
-                        else
-                            mma<3>(as[m][j], ft, fq[m]);
-                    }
-                }
-            }
+            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x4*>(L.p.t[which].at(p, j * 16 + row, i0)) = xs[p];
         }
     }
+    Frag<NP> fk[MT][2], fq[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            load_frag<NP>(fk[m][kb], kt + static_cast<int64_t>((tile0 + m) * 2 + kb) * NP * 512);
+            load_frag<NP>(fq[m][kb], qt + static_cast<int64_t>((tile0 + m) * 2 + kb) * NP * 512);
+        }
+    auto value = [](const Frag<NP>& f, int e) {
+        float x = static_cast<float>(f.p[NP - 1][e]);
+#pragma unroll
+        for (int p = NP - 2; p >= 0; --p) x += static_cast<float>(f.p[p][e]);
+        return x;
+    };
+    // the state's part of each sum, and k . dks
+    float ks = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const int i0 = token_of(j0 + j, grp * 4);
+        const f32x4 eg = *reinterpret_cast<const f32x4*>(&Eg[i0]);
+        const f32x4 la = *reinterpret_cast<const f32x4*>(&La[i0]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            aq[m][j] *= eg * a.scale;
+            ar[m][j] *= -eg;
+            as[m][j] *= la;
+            const Frag<NP>& f = NJ == 4 || j0 == 0 ? fk[m][NJ == 4 ? j >> 1 : 0] : fk[m][1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ks = fmaf(value(f, 4 * (j & 1) + e), as[m][j][e], ks);
+        }
+    }
+    lds_barrier();
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            Frag<3> f;
+            if (NJ < 4 || kb <= j >> 1) {       // a token's row reaches back, its column forward, by blocks of 32
+                L.p.m[0].frag(f, (j0 + j) * 16, kb * 32);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma<3>(aq[m][j], f, fk[m][kb]);
+                L.p.m[1].frag(f, (j0 + j) * 16, kb * 32);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma<3>(ar[m][j], f, fk[m][kb]);
+            }
+            if (NJ < 4 || kb >= j >> 1) {
+                L.p.t[0].frag(f, (j0 + j) * 16, kb * 32);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma<3>(as[m][j], f, fq[m][kb]);
+                L.p.t[1].frag(f, (j0 + j) * 16, kb * 32);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma<3>(as[m][j], f, fk[m][kb]);
+            }
+        }
 
     // write dq and dk; the row sums of dG and dbeta
     const bool parts = rr > 1;
     T* dqr = rows_at<T>(a.d_q, s, hk) + t0 * a.d_q.token;
     T* dkr = rows_at<T>(a.d_k, s, hk) + t0 * a.d_k.token;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float dG[4] = {0.f, 0.f, 0.f, 0.f}, dB[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < NJ; ++j) {
+        f32x4 dG = zero, dB = zero;
+        const int i0 = token_of(j0 + j, grp * 4);
+        const f32x4 be = *reinterpret_cast<const f32x4*>(&Be[i0]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const int d = (wave * MT + m) * 16 + row;
+            const int d = (tile0 + m) * 16 + row;
+            const Frag<NP>& k8 = NJ == 4 || j0 == 0 ? fk[m][NJ == 4 ? j >> 1 : 0] : fk[m][1];
+            const Frag<NP>& q8 = NJ == 4 || j0 == 0 ? fq[m][NJ == 4 ? j >> 1 : 0] : fq[m][1];
+            const f32x4 own = be * ar[m][j], dkv = own + as[m][j];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = j * 16 + grp * 4 + e;
-                if (i >= n || d >= dk) continue;
-                const float q = static_cast<float>(qr[i * a.q.token + d]), k = static_cast<float>(kr[i * a.k.token + d]);
-                const float own_row = Be[i] * ar[m][j][e];
-                dG[e] = fmaf(q, aq[m][j][e], fmaf(k, own_row - as[m][j][e], dG[e]));
+                const float q = value(q8, 4 * (j & 1) + e), k = value(k8, 4 * (j & 1) + e);
+                dG[e] = fmaf(q, aq[m][j][e], fmaf(k, own[e] - as[m][j][e], dG[e]));
                 dB[e] = fmaf(k, ar[m][j][e], dB[e]);
-                const float dkv = own_row + as[m][j][e];
-                if (parts) {
-                    g.w.dqp[(sv * 64 + i) * dk + d] = aq[m][j][e];
-                    g.w.dkp[(sv * 64 + i) * dk + d] = dkv;
-                } else {
-                    dqr[i * a.d_q.token + d] = static_cast<T>(aq[m][j][e]);
-                    dkr[i * a.d_k.token + d] = static_cast<T>(dkv);
+            }
+            if (d < dk) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = i0 + e;
+                    if (i >= n) continue;
+                    if (parts) {
+                        g.w.dqp[(sv * 64 + i) * dk + d] = aq[m][j][e];
+                        g.w.dkp[(sv * 64 + i) * dk + d] = dkv[e];
+                    } else {
+                        dqr[i * a.d_q.token + d] = static_cast<T>(aq[m][j][e]);
+                        dkr[i * a.d_k.token + d] = static_cast<T>(dkv[e]);
+                    }
                 }
             }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-#pragma unroll
-            for (int x = 1; x < 16; x <<= 1) {
-                dG[e] += __shfl_xor(dG[e], x, 64);
-                dB[e] += __shfl_xor(dB[e], x, 64);
-            }
-            if (row == 0) {
-                red[wave][0][j * 16 + grp * 4 + e] = dG[e];
-                red[wave][1][j * 16 + grp * 4 + e] = dB[e];
-            }
+            dG[e] = row_sum16(dG[e]);
+            dB[e] = row_sum16(dB[e]);
+        }
+        if (row == 0) {
+            f32x4 &g4 = *reinterpret_cast<f32x4*>(&red[wave][0][i0]), &b4 = *reinterpret_cast<f32x4*>(&red[wave][1][i0]);
+            g4 = pass ? g4 + dG : dG;
+            b4 = pass ? b4 + dB : dB;
         }
     }
 #pragma unroll
@@ -284,21 +342,23 @@ __global__ __launch_bounds__(256, DKP <= 128 ? 2 : 1) void gdr_grad(const GdrLau
         sde += __shfl_xor(sde, x, 64);
     }
     if (lane == 0) {
-        tot[wave][0] = ks;
-        tot[wave][1] = sde;
+        tot[wave][0] = pass ? tot[wave][0] + ks : ks;
+        tot[wave][1] = pass ? tot[wave][1] + sde : sde;
+    }
     }
     lds_barrier();
     if (wave == 0) {
         double x = 0.0;
         float db = Rv[lane];
+        const int w0 = DKP >= 128 ? 0 : (lane >> 5) * 4;        // the wavefronts that hold this token
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            x += red[w][0][lane];
-            db += red[w][1][lane];
+        for (int w = 0; w < (DKP >= 128 ? 8 : 4); ++w) {
+            x += red[w0 + w][0][lane];
+            db += red[w0 + w][1][lane];
         }
         if (lane == 63) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) x += static_cast<double>(tot[w][0]) + static_cast<double>(Eg[63]) * tot[w][1];
+            for (int w = 0; w < 8; ++w) x += static_cast<double>(tot[w][0]) + static_cast<double>(Eg[63]) * tot[w][1];
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -338,11 +398,11 @@ template <int DT>
 hipError_t run(const GdrLaunch& g, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(g.slots), static_cast<unsigned>(g.a.Hv));
     if (g.dkp == 64)
-        gdr_grad<DT, 64><<<grid, 256, 0, s>>>(g);
+        gdr_grad<DT, 64><<<grid, 512, 0, s>>>(g);
     else if (g.dkp == 128)
-        gdr_grad<DT, 128><<<grid, 256, 0, s>>>(g);
+        gdr_grad<DT, 128><<<grid, 512, 0, s>>>(g);
     else
-        gdr_grad<DT, 256><<<grid, 256, 0, s>>>(g);
+        gdr_grad<DT, 256><<<grid, 512, 0, s>>>(g);
     if (g.a.Hv != g.a.Hk) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;

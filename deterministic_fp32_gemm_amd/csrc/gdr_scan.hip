@@ -131,14 +131,14 @@ __device__ __forceinline__ void load_state(f32x4 (&S)[Tiles<DKP>::MT][NT], const
             }
 }
 template <int DKP, int NT>
-__device__ __forceinline__ void store_state(const f32x4 (&S)[Tiles<DKP>::MT][NT], const Scan& w, float* st) {
+__device__ __forceinline__ void store_state(const f32x4 (&S)[Tiles<DKP>::MT][NT], const Scan& w, float* st, int dv) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int c = w.c0 + t * 16 + w.row;
-        if (c >= w.dv) continue;
+        if (c >= dv) continue;
 #pragma unroll
         for (int m = 0; m < Tiles<DKP>::MT; ++m)
-            put4(st + c, w.dv, (Tiles<DKP>::first(w) + m) * 16 + w.grp * 4, w.dk, S[m][t]);
+            put4(st + c, dv, (Tiles<DKP>::first(w) + m) * 16 + w.grp * 4, w.dk, S[m][t]);
     }
 }
 
@@ -180,9 +180,10 @@ struct Operands {
 // How many chunks ahead operands are fetched: a step takes less than a load from memory, so two where the registers
 // hold two chunks (a step of 16384 tokens x 32 heads in bfloat16: 2.0 us with one, 1.5 with two); with wide float32
 // heads not even one: K^T (and Q^T) come in the middle of their own step.
-template <int DT, int DKP> constexpr int kDepth = DT != 0 && DKP <= 128 ? 2 : 1;
+template <int DT, int DKP> constexpr int kDepth = DT == 1 && DKP <= 128 ? 2 : 1;
 template <int DT, int DKP> constexpr bool kLate = DT != 1 && DKP > 128;
-template <int DKP> constexpr int kHalf = DKP == 64 || DKP == 256 ? 2 : 4;     // k blocks of S in registers at once
+// k blocks of S in registers at once
+template <int DT, int DKP> constexpr int kHalf = DT == 0 ? (DKP == 256 ? 1 : 2) : DKP == 128 ? 4 : 2;
 
 // step(chunk, set), sets of operands taking turns. Where two paths meet inside a loop, registers that loads are still on
 // their way to would be moved, and the moves wait: hence no branch in it, and a loop of its own for each kind of
@@ -204,7 +205,7 @@ __device__ __forceinline__ void in_turn(int chunks, F step) {
 template <int DT, int DKP, int NT, bool STORE>
 __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, PP = kOutParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
-    constexpr int HALF = kHalf<DKP>, DEPTH = kDepth<DT, DKP>;
+    constexpr int HALF = kHalf<DT, DKP>, DEPTH = kDepth<DT, DKP>;
     constexpr bool LATE = kLate<DT, DKP>;
     using T = elem_t<DT>;
     __shared__ Tile<3, COLS, DKP> Sx;           // S, [column][dk]
@@ -216,6 +217,8 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
     const int tok = w.part * 16, t4 = tok + w.grp * 4, hv = w.hv, dv = w.dv, chunks = w.chunks;
     const Operands<NP, DKP> from{g, w};
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    // tokens with a value in this lane's column: none in a column past dv, whose state stays zero
+    auto held = [&](int t, int n) { return w.c0 + t * 16 + w.row < dv ? n : 0; };
     f32x4 S[MT][NT];
     load_state<DKP, NT>(S, w, Tiles<DKP>::owner(w) ? a.s0 : nullptr);
     if (Tiles<DKP>::owner(w)) {
@@ -226,7 +229,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
     }
     auto keep = [&](int chunk, auto chain) {
         if constexpr (STORE && Tiles<DKP>::owns(decltype(chain)::value))
-            store_state<DKP, NT>(S, w, g.w.st + from.sv(chunk) * w.dk * dv);
+            store_state<DKP, NT>(S, w, g.w.st + from.sv(chunk) * w.dk * g.dvp, g.dvp);
     };
     auto update = [&](const Frag<NP> (&kt)[MT][2], float whole, auto chain, auto meanwhile) {
         if constexpr (!Tiles<DKP>::owns(decltype(chain)::value)) return;
@@ -280,8 +283,8 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
         }
         loads_landed();
         __builtin_amdgcn_s_setprio(2);      // over the outputs' wavefronts
-        in_turn<DEPTH>(chunks, [&](int chunk, auto turn, auto) {
-            Set& f = set[turn];
+        in_turn<DEPTH>(chunks, [&](int chunk, auto turn, auto other) {
+            Set &f = set[turn], &before = set[other];
             const int next = min(chunk + DEPTH, chunks - 1), n = min(kChunk, w.s.len - chunk * kChunk);
             keep(chunk, std::true_type{});
             lds_barrier();      // S is in LDS
@@ -293,9 +296,13 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
                     Frag<3> b[HALF];
                     read<HALF>(b, Sx, t * 16, k0 * 32);
                     reads_first();
+                    if (DEPTH == 2 && t == 0 && k0 == 0) {
+                        fetch_u(before, min(chunk + 1, chunks - 1));
+                        fetch_s(before, min(chunk + 1, chunks - 1));
+                    }
                     products<3, HALF>(x, f.kf + k0, b);
                 }
-                Rx.put(t * 16, tok, f.beta * (floats4<DT>(f.v[t], t4, n) - f.eg * (x[0] + x[1])));
+                Rx.put(t * 16, tok, f.beta * (floats4<DT>(f.v[t], t4, held(t, n)) - f.eg * (x[0] + x[1])));
             }
             lds_barrier();
             f32x4 u[NT];
@@ -306,7 +313,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
                 reads_first();
                 if (t == 0) {
                     if constexpr (LATE) fetch_s(f, chunk);
-                    fetch_r(f, next);
+                    else fetch_r(f, next);
                 }
                 f32x4 y[2] = {zero, zero};
                 products<3, 2>(y, f.inv, b);
@@ -315,7 +322,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
             }
             lds_barrier();
             update(f.kt, f.whole, std::true_type{}, [&] {
-                fetch_u(f, next);
+                if constexpr (DEPTH == 1) fetch_u(f, next);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     if constexpr (!STORE) Ux[chunk & 1].put(t * 16, tok, u[t]);
@@ -323,10 +330,11 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
             if constexpr (STORE) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    if (w.c0 + t * 16 + w.row < dv)
-                        put4(g.w.u + from.sv(chunk) * 64 * dv + w.c0 + t * 16 + w.row, dv, t4, kChunk, u[t]);
+                    if (w.c0 + t * 16 + w.row < g.dvp)
+                        put4(g.w.u + from.sv(chunk) * 64 * g.dvp + w.c0 + t * 16 + w.row, g.dvp, t4, kChunk, u[t]);
             }
-            if constexpr (!LATE) fetch_s(f, next);
+            if constexpr (LATE) fetch_r(f, next);
+            else if constexpr (DEPTH == 1) fetch_s(f, next);
         });
         if constexpr (!STORE) lds_barrier();    // the last chunk's U
     }
@@ -398,10 +406,11 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
                     o[t] = (x[0] + x[1]) * (f.eg * a.scale);
                 }
             }
-            fetch_q(f, next);
+            if constexpr (!LATE) fetch_q(f, next);
             lds_barrier();
             update(f.kt, f.whole, std::false_type{}, [] {});
-            if constexpr (!LATE) fetch_s(f, next);
+            if constexpr (LATE) fetch_q(f, next);
+            else fetch_s(f, next);
         });
         if constexpr (!STORE) {
             lds_barrier();
@@ -413,13 +422,13 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
         }
     }
     if constexpr (!STORE)
-        if (a.s_final && Tiles<DKP>::owner(w)) store_state<DKP, NT>(S, w, a.s_final + w.head * w.dk * dv);
+        if (a.s_final && Tiles<DKP>::owner(w)) store_state<DKP, NT>(S, w, a.s_final + w.head * w.dk * dv, dv);
 }
 
 template <int DT, int DKP, int NT>
 __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
-    constexpr int HALF = kHalf<DKP>, DEPTH = kDepth<DT, DKP>;
+    constexpr int HALF = kHalf<DT, DKP>, DEPTH = kDepth<DT, DKP>;
     constexpr bool LATE = kLate<DT, DKP>;
     using T = elem_t<DT>;
     __shared__ Tile<3, COLS, DKP> Sx;           // dS, [column][dk]
@@ -431,6 +440,8 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
     const int tok = w.part * 16, t4 = tok + w.grp * 4, hv = w.hv, dv = w.dv, top = w.chunks - 1;
     const Operands<NP, DKP> from{g, w};
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    // tokens with a value in this lane's column: none in a column past dv, whose state stays zero
+    auto held = [&](int t, int n) { return w.c0 + t * 16 + w.row < dv ? n : 0; };
     f32x4 S[MT][NT];
     load_state<DKP, NT>(S, w, Tiles<DKP>::owner(w) ? a.ds_final : nullptr);
     if (Tiles<DKP>::owner(w)) {
@@ -441,7 +452,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
     }
     auto keep = [&](int chunk, auto chain) {
         if constexpr (Tiles<DKP>::owns(decltype(chain)::value))
-            store_state<DKP, NT>(S, w, g.w.dst + from.sv(chunk) * w.dk * dv);
+            store_state<DKP, NT>(S, w, g.w.dst + from.sv(chunk) * w.dk * g.dvp, g.dvp);
     };
     auto update = [&](const Frag<NP> (&qt)[MT][2], const Frag<NP> (&kt)[MT][2], float whole, auto chain, auto meanwhile) {
         if constexpr (!Tiles<DKP>::owns(decltype(chain)::value)) return;
@@ -497,8 +508,8 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
         loads_landed();
         __builtin_amdgcn_s_setprio(2);
         lds_barrier();
-        in_turn<DEPTH>(top + 1, [&](int i, auto turn, auto) {
-            Set& f = set[turn];
+        in_turn<DEPTH>(top + 1, [&](int i, auto turn, auto other) {
+            Set &f = set[turn], &before = set[other];
             const int chunk = top - i, next = back(i + DEPTH), t0 = chunk * kChunk, n = min(kChunk, w.s.len - t0);
             keep(chunk, std::true_type{});
             lds_barrier();      // dS and P^T dO are in LDS
@@ -510,6 +521,10 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
                     Frag<3> b[HALF];
                     read<HALF>(b, Sx, t * 16, k0 * 32);
                     reads_first();
+                    if (DEPTH == 2 && t == 0 && k0 == 0) {
+                        fetch_r(before, back(i + 1));
+                        fetch_s(before, back(i + 1));
+                    }
                     products<3, HALF>(x, f.kf + k0, b);
                 }
                 Ux.put(t * 16, tok, (x[0] + x[1]) * f.last + Wx[t][w.part][w.lane]);
@@ -533,19 +548,19 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
             lds_barrier();
             const f32x4 beta = f.beta;
             update(f.qt, f.kt, f.whole, std::true_type{}, [&] {
-                fetch_r(f, next);
+                if constexpr (DEPTH == 1) fetch_r(f, next);
                 fetch_v(f, next);
             });
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int c = w.c0 + t * 16 + w.row;
+                if (c < g.dvp) put4(g.w.dr + from.sv(chunk) * 64 * g.dvp + c, g.dvp, t4, kChunk, d[t]);
                 if (c < dv) {
-                    put4(g.w.dr + from.sv(chunk) * 64 * dv + c, dv, t4, kChunk, d[t]);
                     put4(dvr + t0 * a.d_v.token + c, static_cast<int>(a.d_v.token), t4, n, beta * d[t]);
                 }
             }
             if constexpr (LATE) fetch_u(f, next);
-            else fetch_s(f, next);
+            else if constexpr (DEPTH == 1) fetch_s(f, next);
         });
     }
     if (!w.chain && top >= 0) {
@@ -584,7 +599,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
         fetch_do(set[0], top);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            o1[t] = floats4<DT>(set[0].raw[t], t4, min(kChunk, w.s.len - top * kChunk));
+            o1[t] = floats4<DT>(set[0].raw[t], t4, held(t, min(kChunk, w.s.len - top * kChunk)));
             Ox.put(t * 16, tok, o1[t]);
         }
         lds_barrier();
@@ -605,7 +620,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 Qx.put(t * 16, tok, o1[t] * (f.eg * a.scale));
-                o1[t] = floats4<DT>(f.raw[t], t4, n);
+                o1[t] = floats4<DT>(f.raw[t], t4, held(t, n));
                 Ox.put(t * 16, tok, o1[t]);
             }
             f.eg = from.token(kTokEg, back(i + DEPTH));
@@ -619,7 +634,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
             if constexpr (!LATE) fetch_s(f, back(i + DEPTH));
         });
     }
-    if (a.ds0 && Tiles<DKP>::owner(w)) store_state<DKP, NT>(S, w, a.ds0 + w.head * w.dk * dv);
+    if (a.ds0 && Tiles<DKP>::owner(w)) store_state<DKP, NT>(S, w, a.ds0 + w.head * w.dk * dv, dv);
 }
 
 template <int DT, int DKP>
