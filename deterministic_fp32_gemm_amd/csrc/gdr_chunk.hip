@@ -34,7 +34,7 @@ __global__ __launch_bounds__(256, DT == 1 || DKP < 128 ? 4 : 2) void gdr_chunk(c
     auto& As = *reinterpret_cast<float(*)[64][kLd]>(buf);
     auto& Ts = *reinterpret_cast<float(*)[64][kLd]>(buf + 64 * kLd * 4);
     uint16_t* const Kf = reinterpret_cast<uint16_t*>(buf);
-    __shared__ float Gh[64], Gl[64], Be[64];
+    __shared__ alignas(16) float Gh[64], Gl[64], Be[64];
     const sdm_gdr_args_t& a = g.a;
     int seq, chunk;
     Seq s;
@@ -145,20 +145,20 @@ __global__ __launch_bounds__(256, DT == 1 || DKP < 128 ? 4 : 2) void gdr_chunk(c
         }
     }
 
+    const f32x4 gh = *reinterpret_cast<const f32x4*>(&Gh[wave * 16 + grp * 4]);
+    const f32x4 gl = *reinterpret_cast<const f32x4*>(&Gl[wave * 16 + grp * 4]);
+    const f32x4 be = *reinterpret_cast<const f32x4*>(&Be[wave * 16 + grp * 4]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j) {
+        const int i0 = wave * 16 + grp * 4, c = j * 16 + row;
+        const float ch = Gh[c], cl = Gl[c];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int i = wave * 16 + grp * 4 + e, c = j * 16 + row;
-            float av = 0.f, pv = 0.f;
-            if (j <= wave && c <= i) {
-                const float d = expf((Gh[i] - Gh[c]) + (Gl[i] - Gl[c]));
-                pv = a.scale * qk[j][e] * d;
-                if (c < i) av = Be[i] * kk[j][e] * d;
-            }
-            As[i][c] = av;
-            Ts[i][c] = pv;
+            const float d = c <= i0 + e ? exp_of((gh[e] - ch) + (gl[e] - cl)) : 0.f;
+            As[i0 + e][c] = c < i0 + e ? be[e] * kk[j][e] * d : 0.f;
+            Ts[i0 + e][c] = c <= i0 + e ? a.scale * qk[j][e] * d : 0.f;
         }
+    }
     lds_barrier();
 
     // P, row tiles in order; the backward's P^T, of columns

@@ -187,6 +187,16 @@ struct Tile {
 // loop's head for the order in which the loads before the loop happen to stand, every time round.
 __device__ __forceinline__ void loads_landed() { __builtin_amdgcn_s_waitcnt(0x0f70); }
 
+// e^x in 1 ulp or two: the hardware's 2^t with t = x log2(e) as a float, times 1 + ln(2) (what t's rounding left out).
+// (The library's expf is a quarter of the time of a chunk's 64 x 64 decays longer.) Below -103 it is 0, as e^x in
+// float32 nearly is.
+__device__ __forceinline__ float exp_of(float x) {
+    const float t = x * 1.44269502f;
+    const float rest = fmaf(x, 1.44269502f, -t) + x * 1.92596299e-8f;
+    const float y = __builtin_amdgcn_exp2f(t);
+    return fmaf(y, rest * 0.693147181f, y);
+}
+
 // One sequence: its first token, length and first chunk slot.
 struct Seq {
     int64_t base;       // of its row's first token: strides.batch * b is added by rows_at

@@ -124,19 +124,8 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
         load_raw<0, true>(in.u, ur + stok * dvp, c, dvp, true);
         load_raw<0, true>(in.r, rp + stok * dvp, c, dvp, true);
     };
-    fetch(0);
     for (int c0 = 0; c0 < dv; c0 += 64) {
-        // S and dE of the block, on their way while dO, U and dR are split into LDS
-        Raw<0> xs[MT][2], ys[MT][2];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                const int d = (tile0 + m) * 16 + row, c = c0 + kb * 32 + grp * 8;
-                const int64_t at = static_cast<int64_t>(min(d, dk - 1)) * dvp;
-                load_raw<0, true>(xs[m][kb], st + at, c, dvp, d < dk);
-                load_raw<0, true>(ys[m][kb], de + at, c, dvp, d < dk);
-            }
+        fetch(c0);
         {
             float x[8], y[8];
             Frag<NP> fo;
@@ -157,19 +146,15 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
             for (int e = 0; e < 8; ++e) rv = fmaf(x[e], y[e], rv);
         }
         lds_barrier();
-        fetch(c0 + 64);     // past dv: zeros, and no address past a row
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            Frag<3> fs[MT], fe[MT];
+            Raw<0> xs[MT], ys[MT];
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                float x[8], y[8];
-                raw_floats<0>(x, xs[m][kb]);
-                raw_floats<0>(y, ys[m][kb]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sde = fmaf(x[e], y[e], sde);
-                split8(fs[m], x);
-                split8(fe[m], y);
+                const int d = (tile0 + m) * 16 + row, c = c0 + kb * 32 + grp * 8;
+                const int64_t at = static_cast<int64_t>(min(d, dk - 1)) * dvp;
+                load_raw<0, true>(xs[m], st + at, c, dvp, d < dk);
+                load_raw<0, true>(ys[m], de + at, c, dvp, d < dk);
             }
             Frag<NP> fo;
             Frag<3> fr, fu;
@@ -188,17 +173,37 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
                     mma<3>(dpa[j], fr, fu);
                 }
             }
+            Frag<3> fs[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float x[8], y[8];
+                raw_floats<0>(x, xs[m]);
+                raw_floats<0>(y, ys[m]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sde = fmaf(x[e], y[e], sde);
+                split8(fs[m], x);
+            }
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 L.s.o.frag(fo, (j0 + j) * 16, kb * 32);
                 L.s.r.frag(fr, (j0 + j) * 16, kb * 32);
-                L.s.u.frag(fu, (j0 + j) * 16, kb * 32);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     mma<3>(aq[m][j], fo, fs[m]);
                     mma<3>(ar[m][j], fr, fs[m]);
-                    mma<3>(as[m][j], fu, fe[m]);
                 }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float y[8];
+                raw_floats<0>(y, ys[m]);
+                split8(fs[m], y);
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                L.s.u.frag(fu, (j0 + j) * 16, kb * 32);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma<3>(as[m][j], fu, fs[m]);
             }
         }
         lds_barrier();
@@ -208,32 +213,6 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
     if ((threadIdx.x & 7) == 0) Rv[stok] = rv;
     if (DKP < 128 && wave >= 4) sde = 0.f;      // wavefronts 0 .. 3 have summed the same
 
-    // dP and dA with their decays, by rows (against K) and, dA times beta, by columns (against Q and K)
-    {
-        const int which = wave >> 2, wi = wave & 3;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f32x4 x = zero, y = zero;
-            const int i0 = token_of(wi, grp * 4), c = token_of(j, row);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = i0 + e;
-                const float d = expf((Gh[i] - Gh[c]) + (Gl[i] - Gl[c]));
-                const bool in = which ? c < i : c <= i;
-                x[e] = in ? dpa[j][e] * d * (which ? -1.f : a.scale) : 0.f;
-                y[e] = in && which ? Be[i] * x[e] : x[e];
-            }
-            bf16x4 xs[3];
-            split4<3>(xs, x);
-#pragma unroll
-            for (int p = 0; p < 3; ++p)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) *L.p.m[which].at(p, wi * 16 + grp * 4 + e, c) = xs[p][e];
-            split4<3>(xs, y);
-#pragma unroll
-            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x4*>(L.p.t[which].at(p, j * 16 + row, i0)) = xs[p];
-        }
-    }
     Frag<NP> fk[MT][2], fq[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -263,6 +242,34 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
             const Frag<NP>& f = NJ == 4 || j0 == 0 ? fk[m][NJ == 4 ? j >> 1 : 0] : fk[m][1];
 #pragma unroll
             for (int e = 0; e < 4; ++e) ks = fmaf(value(f, 4 * (j & 1) + e), as[m][j][e], ks);
+        }
+    }
+    // dP and dA with their decays, half the wavefronts each: by rows against K, by columns against Q and, times beta, K
+    {
+        const int which = wave >> 2, wi = wave & 3, i0 = token_of(wi, grp * 4);
+        const f32x4 gh = *reinterpret_cast<const f32x4*>(&Gh[i0]), gl = *reinterpret_cast<const f32x4*>(&Gl[i0]);
+        const f32x4 one = {1.f, 1.f, 1.f, 1.f};
+        const f32x4 be = which ? *reinterpret_cast<const f32x4*>(&Be[i0]) : one;
+        const float sign = which ? -1.f : a.scale;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = token_of(j, row);
+            const float ch = Gh[c], cl = Gl[c];
+            f32x4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = c < i0 + e + 1 - which;
+                x[e] = in ? dpa[j][e] * sign * exp_of((gh[e] - ch) + (gl[e] - cl)) : 0.f;
+            }
+            bf16x4 xs[3];
+            split4<3>(xs, x);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) *L.p.m[which].at(p, wi * 16 + grp * 4 + e, c) = xs[p][e];
+            if (which) split4<3>(xs, x * be);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x4*>(L.p.t[which].at(p, j * 16 + row, i0)) = xs[p];
         }
     }
     lds_barrier();
