@@ -25,7 +25,7 @@ namespace {
 constexpr int kLd = 68;     // row of a 64 x 64 float32 matrix in LDS
 
 template <int DT, int DKP, bool BWD>
-__global__ __launch_bounds__(256, DT == 1 || DKP < 128 ? 4 : 2) void gdr_chunk(const GdrLaunch g) {
+__global__ __launch_bounds__(256, DKP < 256 || DT == 1 ? 3 : 1) void gdr_chunk(const GdrLaunch g) {
     constexpr int NP = kParts<DT>, PP = BWD ? 3 : kOutParts<DT>, NKB = DKP / 32;
     using T = elem_t<DT>;
     // K's (or Q's) fragments, then A and the matrix that P, and after it T, are laid out in

@@ -89,6 +89,8 @@ def load() -> ctypes.CDLL:
             fn.argtypes = args
             fn.restype = {"sdm_delta_strerror": ctypes.c_char_p, "sdm_gdr_workspace": _i64,
                           "sdm_nrm_workspace": _i64}.get(name, ctypes.c_int)
+        global _raw_stream
+        _raw_stream = _find_raw_stream()
         _lib = lib
         return lib
 
@@ -140,20 +142,80 @@ def _inner(t):
     return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
 
 
-def _rows(t) -> sdm_rows_t:
+def _rows(t, address=True) -> sdm_rows_t:
     st = t.stride()
-    return sdm_rows_t(t.data_ptr(), st[0], st[1], st[2])
+    return sdm_rows_t(t.data_ptr() if address else 0, st[0], st[1], st[2])
 
 
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
+def _find_raw_stream():
+    """torch's own call for a current stream's handle, without the Stream object around it (a microsecond)."""
+    import torch
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+_raw_stream = None
+
+
 def _stream(stream, device) -> int:
     if stream is None:
         import torch
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device.index)
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+class _Plans(threading.local):
+    """Checked argument structs by the layout of a call's tensors, a set for each host thread: a call whose tensors have
+    the layout of an earlier one fills in their addresses and nothing else. Addresses, values and results are never
+    kept."""
+
+    MOST = 256
+
+    def __init__(self):
+        self.known = {}
+
+    def get(self, key):
+        return self.known.get(key)
+
+    def put(self, key, plan):
+        if len(self.known) >= self.MOST:
+            self.known.clear()
+        self.known[key] = plan
+        return plan
+
+
+_plans = _Plans()
+
+
+def _layout(t):
+    """What of a tensor a plan depends on; None for None. Raises for what is not a tensor."""
+    if t is None:
+        return None
+    try:
+        return t.shape, t.stride(), t.dtype, t.get_device(), t.is_neg()
+    except AttributeError:
+        raise TypeError("a torch tensor is required") from None
+
+
+class _OnDevice:
+    """Makes a device current for a call where it is not."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        import torch
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def _workspace(nbytes: int, device):
@@ -181,26 +243,59 @@ def _gdr_shapes(q, k, v, g, beta):
     return B, T, Hk, Hv, dk, dv, dt, dev
 
 
-def _gdr_args(q, k, v, g, beta, scale, initial_state, cu_seqlens):
+def _gdr_plan(backward, q, k, v, g, beta, scale, s0, cu, do, ds):
+    """The checked argument struct of a forward or backward call, without addresses."""
     import torch
     B, T, Hk, Hv, dk, dv, dt, dev = _gdr_shapes(q, k, v, g, beta)
     nseq = B
-    if cu_seqlens is not None:
-        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+    if cu is not None:
+        if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 2:
             raise ValueError("cu_seqlens: an int32 tensor of one more entry than sequences, two at least")
         if B != 1:
             raise ValueError("cu_seqlens: packed sequences come in one row (B = 1)")
-        nseq = cu_seqlens.shape[0] - 1
-        _tensor(cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32, dev)
-        if not cu_seqlens.is_contiguous():
-            cu_seqlens = cu_seqlens.contiguous()
-    if initial_state is not None:
-        initial_state = _tensor(initial_state, "initial_state", (nseq, Hv, dk, dv), torch.float32, dev).contiguous()
+        nseq = cu.shape[0] - 1
+        _tensor(cu, "cu_seqlens", (nseq + 1,), torch.int32, dev)
+    state = (nseq, Hv, dk, dv)
+    for t, name in ((s0, "initial_state"), (ds, "dfinal_state")):
+        if t is not None:
+            _tensor(t, name, state, torch.float32, dev)
+    if backward:
+        _tensor(do, "do", v.shape, v.dtype, dev)
+    copied = (any(_inner(t) is not t for t in (q, k, v, do) if t is not None) or
+              any(not t.is_contiguous() for t in (cu, s0, ds) if t is not None))
     q, k, v = _inner(q), _inner(k), _inner(v)
     a = sdm_gdr_args_t(dtype=dt, scale=dk ** -0.5 if scale is None else float(scale), B=B, T=T, Hk=Hk, Hv=Hv, dk=dk,
-                       dv=dv, nseq=nseq, cu_seqlens=_ptr(cu_seqlens), q=_rows(q), k=_rows(k), v=_rows(v), g=_rows(g),
-                       beta=_rows(beta), s0=_ptr(initial_state))
-    return a, (q, k, v, cu_seqlens, initial_state), nseq, dev
+                       dv=dv, nseq=nseq, q=_rows(q, False), k=_rows(k, False), v=_rows(v, False), g=_rows(g, False),
+                       beta=_rows(beta, False))
+    whole = lambda t: _rows(torch.empty(t.shape, device="meta"), False)  # noqa: E731
+    if backward:
+        a.d_o = _rows(_inner(do), False)
+        a.d_q, a.d_k, a.d_v, a.d_g, a.d_beta = whole(q), whole(k), whole(v), whole(g), whole(beta)
+    else:
+        a.o = whole(v)
+    n = 0
+    if T and B:
+        if cu is not None:
+            a.cu_seqlens = 4        # the workspace of packed sequences is another
+        n = load().sdm_gdr_workspace(ctypes.byref(a), int(backward))
+        if n < 0:
+            _raise(n, "gdr_backward" if backward else "gdr_forward")
+        a.cu_seqlens = 0
+    return a, n, state, dev, copied
+
+
+def _gdr_operands(plan, a, q, k, v, g, beta, s0, cu):
+    """Fills the inputs' addresses in; returns what has to live until the call."""
+    copied = plan[4]
+    if copied:
+        q, k, v = _inner(q), _inner(k), _inner(v)
+        cu = None if cu is None else cu.contiguous()
+        s0 = None if s0 is None else s0.contiguous()
+    a.q.data, a.k.data, a.v.data, a.g.data, a.beta.data = (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                                           beta.data_ptr())
+    a.cu_seqlens = 0 if cu is None else cu.data_ptr()
+    a.s0 = 0 if s0 is None else s0.data_ptr()
+    return q, k, v, cu, s0
 
 
 def gdr_forward(q, k, v, g, beta, *, scale=None, initial_state=None, final_state=True, cu_seqlens=None, stream=None):
@@ -212,22 +307,26 @@ def gdr_forward(q, k, v, g, beta, *, scale=None, initial_state=None, final_state
     sequence get zeros. Any strides; a last axis that is not contiguous is copied first.
     """
     import torch
-    a, keep, nseq, dev = _gdr_args(q, k, v, g, beta, scale, initial_state, cu_seqlens)
-    make = torch.empty if cu_seqlens is None else torch.zeros
-    o = make(v.shape, dtype=v.dtype, device=dev)
-    s = torch.empty((nseq, a.Hv, a.dk, a.dv), dtype=torch.float32, device=dev) if final_state else None
-    if a.T == 0 or a.B == 0:
+    key = ("fwd", _layout(q), _layout(k), _layout(v), _layout(g), _layout(beta), _layout(initial_state),
+           _layout(cu_seqlens), scale)
+    plan = _plans.get(key)
+    if plan is None:
+        plan = _plans.put(key, _gdr_plan(False, q, k, v, g, beta, scale, initial_state, cu_seqlens, None, None))
+    a, n, state, dev, _ = plan
+    o = (torch.empty if cu_seqlens is None else torch.zeros)(v.shape, dtype=v.dtype, device=dev)
+    s = torch.empty(state, dtype=torch.float32, device=dev) if final_state else None
+    if not n:
         if s is not None:
             s.zero_() if initial_state is None else s.copy_(initial_state)
         return o, s
-    a.o, a.s_final = _rows(o), _ptr(s)
-    lib = load()
-    with torch.cuda.device(dev):
-        n = lib.sdm_gdr_workspace(ctypes.byref(a), 0)
-        if n < 0:
-            _raise(n, "gdr_forward")
-        ws = _workspace(n, dev)
-        _raise(lib.sdm_gdr_forward(ctypes.byref(a), ws.data_ptr(), n, _stream(stream, dev)), "gdr_forward")
+    keep = _gdr_operands(plan, a, q, k, v, g, beta, initial_state, cu_seqlens)
+    ws = _workspace(n, dev)
+    a.o.data, a.s_final = o.data_ptr(), 0 if s is None else s.data_ptr()
+    with _OnDevice(dev):
+        status = load().sdm_gdr_forward(ctypes.byref(a), ws.data_ptr(), n, _stream(stream, dev))
+    del keep
+    if status:
+        _raise(status, "gdr_forward")
     return o, s
 
 
@@ -237,26 +336,31 @@ def gdr_backward(q, k, v, g, beta, do, *, scale=None, initial_state=None, dfinal
     dfinal_state, that of the last state (None: zero). It recomputes the forward's states and needs nothing saved but
     the inputs. Gradients have their tensors' shapes and types; tokens of no sequence get zeros."""
     import torch
-    a, keep, nseq, dev = _gdr_args(q, k, v, g, beta, scale, initial_state, cu_seqlens)
-    do = _inner(_tensor(do, "do", v.shape, v.dtype, dev))
-    if dfinal_state is not None:
-        dfinal_state = _tensor(dfinal_state, "dfinal_state", (nseq, a.Hv, a.dk, a.dv), torch.float32, dev).contiguous()
+    key = ("bwd", _layout(q), _layout(k), _layout(v), _layout(g), _layout(beta), _layout(initial_state),
+           _layout(cu_seqlens), _layout(do), _layout(dfinal_state), scale)
+    plan = _plans.get(key)
+    if plan is None:
+        plan = _plans.put(key, _gdr_plan(True, q, k, v, g, beta, scale, initial_state, cu_seqlens, do, dfinal_state))
+    a, n, state, dev, copied = plan
     make = torch.empty if cu_seqlens is None else torch.zeros
     outs = [make(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v, g, beta)]
-    ds = torch.empty((nseq, a.Hv, a.dk, a.dv), dtype=torch.float32, device=dev)
-    if a.T == 0 or a.B == 0:
-        ds.zero_() if dfinal_state is None else ds.copy_(dfinal_state)
-        return (*outs, ds)
-    a.d_o, a.ds_final, a.ds0 = _rows(do), _ptr(dfinal_state), _ptr(ds)
-    a.d_q, a.d_k, a.d_v, a.d_g, a.d_beta = (_rows(t) for t in outs)
-    lib = load()
-    with torch.cuda.device(dev):
-        n = lib.sdm_gdr_workspace(ctypes.byref(a), 1)
-        if n < 0:
-            _raise(n, "gdr_backward")
-        ws = _workspace(n, dev)
-        _raise(lib.sdm_gdr_backward(ctypes.byref(a), ws.data_ptr(), n, _stream(stream, dev)), "gdr_backward")
-    return (*outs, ds)
+    s = torch.empty(state, dtype=torch.float32, device=dev)
+    if not n:
+        s.zero_() if dfinal_state is None else s.copy_(dfinal_state)
+        return (*outs, s)
+    keep = _gdr_operands(plan, a, q, k, v, g, beta, initial_state, cu_seqlens)
+    if copied:
+        do = _inner(do)
+        dfinal_state = None if dfinal_state is None else dfinal_state.contiguous()
+    a.d_o.data, a.ds_final, a.ds0 = do.data_ptr(), 0 if dfinal_state is None else dfinal_state.data_ptr(), s.data_ptr()
+    a.d_q.data, a.d_k.data, a.d_v.data, a.d_g.data, a.d_beta.data = (t.data_ptr() for t in outs)
+    ws = _workspace(n, dev)
+    with _OnDevice(dev):
+        status = load().sdm_gdr_backward(ctypes.byref(a), ws.data_ptr(), n, _stream(stream, dev))
+    del keep
+    if status:
+        _raise(status, "gdr_backward")
+    return (*outs, s)
 
 
 def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, out=None, stream=None):
@@ -266,6 +370,33 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, out=None, strea
     own number); a stream whose slot is not in the pool, such as -1, is idle: zeros in o, no state touched. No two
     streams may name one slot. The other tensors as in gdr_forward."""
     import torch
+    key = ("step", _layout(q), _layout(k), _layout(v), _layout(g), _layout(beta), _layout(state), _layout(slots),
+           _layout(out), scale)
+    plan = _plans.get(key)
+    if plan is None:
+        plan = _plans.put(key, _step_plan(q, k, v, g, beta, state, slots, scale, out))
+    a, shape, dtype, dev, copied = plan
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    if a is None:
+        return out
+    if copied:
+        q, k, v = _inner(q), _inner(k), _inner(v)
+        slots = None if slots is None else slots.contiguous()
+    a.q.data, a.k.data, a.v.data, a.g.data = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr()
+    a.beta.data, a.o.data, a.state = beta.data_ptr(), out.data_ptr(), state.data_ptr()
+    if slots is not None:
+        a.slots = slots.data_ptr()
+    with _OnDevice(dev):
+        status = load().sdm_gdr_step(ctypes.byref(a), _stream(stream, dev))
+    if status:
+        _raise(status, "gdr_step")
+    return out
+
+
+def _step_plan(q, k, v, g, beta, state, slots, scale, out):
+    """(argument struct or None for nothing to do, o's shape, type, device, whether an operand is copied first)"""
+    import torch
     B, T, Hk, Hv, dk, dv, dt, dev = _gdr_shapes(q, k, v, g, beta)
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state: [pool, Hv, dk, dv] required")
@@ -274,21 +405,20 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, out=None, strea
     if not state.is_contiguous():
         raise ValueError("state: must be contiguous (it is updated in place)")
     if slots is not None:
-        slots = _tensor(slots, "slots", (B,), torch.int32, dev).contiguous()
-    if out is None:
-        out = torch.empty((B, T, Hv, dv), dtype=v.dtype, device=dev)
-    else:
+        _tensor(slots, "slots", (B,), torch.int32, dev)
+    o = _rows(torch.empty((B, T, Hv, dv), dtype=v.dtype, device="meta"), False)
+    if out is not None:
         _tensor(out, "out", (B, T, Hv, dv), v.dtype, dev)
         if out.stride(-1) != 1 and dv > 1:
             raise ValueError("out: the last axis must be contiguous")
+        o = _rows(out, False)
     if B == 0 or T == 0:
-        return out
+        return None, (B, T, Hv, dv), v.dtype, dev, False
+    copied = any(_inner(t) is not t for t in (q, k, v)) or (slots is not None and not slots.is_contiguous())
     q, k, v = _inner(q), _inner(k), _inner(v)
-    a = sdm_gdr_step_args_t(dt, dk ** -0.5 if scale is None else float(scale), B, T, Hk, Hv, dk, dv, pool, _rows(q),
-                            _rows(k), _rows(v), _rows(g), _rows(beta), _rows(out), state.data_ptr(), _ptr(slots))
-    with torch.cuda.device(dev):
-        _raise(load().sdm_gdr_step(ctypes.byref(a), _stream(stream, dev)), "gdr_step")
-    return out
+    a = sdm_gdr_step_args_t(dt, dk ** -0.5 if scale is None else float(scale), B, T, Hk, Hv, dk, dv, pool,
+                            _rows(q, False), _rows(k, False), _rows(v, False), _rows(g, False), _rows(beta, False), o, 0, 0)
+    return a, (B, T, Hv, dv), v.dtype, dev, copied
 
 
 # ---- the block norm -------------------------------------------------------------------------------------------------
@@ -317,12 +447,55 @@ def _norm_common(first, o, z, w_post, w_pre, scale, act):
     return D, dev, wd
 
 
-def _flat(t, name, like, dtype, dev):
+def _flat(t):
+    """t as rows of its last axis, copied if they are not contiguous."""
     if t is None:
         return None
-    _tensor(t, name, like.shape, dtype, dev)
-    t = t.reshape(-1, like.shape[-1])
+    if t.dim() != 2:
+        t = t.reshape(-1, t.shape[-1])
     return t if t.stride(-1) == 1 and t.stride(0) >= t.shape[1] or t.is_contiguous() else t.contiguous()
+
+
+def _norm_plan(backward, x, o, z, w_post, w_pre, scale, act, eps, dy=None, xn=None, rstd=None):
+    """The checked argument struct of a forward or backward call, without addresses. x: dx_new in the backward call."""
+    import torch
+    first = o if o is not None else xn if backward else x
+    if not isinstance(first, torch.Tensor):
+        raise TypeError("x, o, x_new: a torch tensor")
+    D, dev, wd = _norm_common(first, o, z, w_post, w_pre, scale, act)
+    dt = _dtype(first, "o")
+    names = ("dx_new" if backward else "x", "o", "z", "dy", "x_new")
+    rows_of = [x, o, z, dy, xn]
+    for t, name in zip(rows_of, names):
+        if t is not None:
+            _tensor(t, name, first.shape, first.dtype, dev)
+    rows = first.numel() // D if D else 0
+    if backward:
+        if (dy is None) != (w_pre is None):
+            raise ValueError("dy: given exactly when w_pre is")
+        if dy is None and x is None:
+            raise ValueError("dx_new: required without dy")
+        if dy is not None and xn is None:
+            raise ValueError("x_new: required with dy")
+        _tensor(rstd, "rstd", (rows, 2), torch.float32, dev)
+    _tensor(first, "o", first.shape)
+    plain = [w_post, w_pre, scale, rstd]
+    flat = [_flat(t) for t in rows_of]
+    copied = (any(f is not t for f, t in zip(flat, rows_of)) or
+              any(t is not None and not t.is_contiguous() for t in plain))
+    fx, fo, fz, fy, fn = flat
+    wt = _dtype(w_post if w_post is not None else w_pre, "weights")
+    a = sdm_nrm_args_t(dtype=dt, wtype=wt, act=ACTS[act], eps=eps, rows=rows, D=D, ld_o=_ld(fo), ld_z=_ld(fz))
+    n = 0
+    if backward:
+        a.ld_dxn, a.ld_dy, a.ld_xn, a.ld_dx, a.ld_do, a.ld_dz = _ld(fx), _ld(fy), _ld(fn), D, D, D
+        if rows:
+            n = load().sdm_nrm_workspace(ctypes.byref(a))
+            if n < 0:
+                _raise(n, "norm_backward")
+    else:
+        a.ld_x, a.ld_xn, a.ld_y = _ld(fx), D, D
+    return a, n, rows, D, dev, wd, copied, first.shape, first.dtype
 
 
 def norm_forward(x, o, z, w_post, w_pre, scale, *, act="silu", eps=1e-6, stream=None):
@@ -334,26 +507,26 @@ def norm_forward(x, o, z, w_post, w_pre, scale, *, act="silu", eps=1e-6, stream=
     w_post, w_pre, scale [D] in that type or float32. x None: no residual. w_pre None: y is None. o None (with z,
     w_post and scale): y = rms_norm(x) w_pre alone, and x_new is x. act: "none" (z None), "sigmoid" or "silu"."""
     import torch
-    first = o if o is not None else x
-    if not isinstance(first, torch.Tensor):
-        raise TypeError("x, o: a torch tensor")
-    D, dev, wd = _norm_common(first, o, z, w_post, w_pre, scale, act)
-    dt = _dtype(first, "o" if o is not None else "x")
-    x2, o2, z2 = (_flat(t, n, first, first.dtype, dev) for t, n in ((x, "x"), (o, "o"), (z, "z")))
-    _tensor(first, "o" if o is not None else "x", first.shape)
-    rows = first.numel() // D if D else 0
-    x_new = x if o is None else torch.empty(first.shape, dtype=first.dtype, device=dev)
-    y = None if w_pre is None else torch.empty(first.shape, dtype=first.dtype, device=dev)
+    key = ("norm", _layout(x), _layout(o), _layout(z), _layout(w_post), _layout(w_pre), _layout(scale), act, eps)
+    plan = _plans.get(key)
+    if plan is None:
+        plan = _plans.put(key, _norm_plan(False, x, o, z, w_post, w_pre, scale, act, eps))
+    a, _, rows, D, dev, _, copied, shape, dtype = plan
+    x_new = x if o is None else torch.empty(shape, dtype=dtype, device=dev)
+    y = None if w_pre is None else torch.empty(shape, dtype=dtype, device=dev)
     rstd = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-    if rows == 0:
+    if not rows:
         return x_new, y, rstd
-    w = [None if t is None else t.contiguous() for t in (w_post, w_pre, scale)]
-    a = sdm_nrm_args_t(dtype=dt, wtype=_dtype(w[0] if w[0] is not None else w[1], "weights"), act=ACTS[act], eps=eps,
-                       rows=rows, D=D, x=_ptr(x2), o=_ptr(o2), z=_ptr(z2), ld_x=_ld(x2), ld_o=_ld(o2), ld_z=_ld(z2),
-                       w_post=_ptr(w[0]), w_pre=_ptr(w[1]), scale=_ptr(w[2]), x_new=0 if o is None else x_new.data_ptr(),
-                       y=_ptr(y), ld_xn=D, ld_y=D, rstd=rstd.data_ptr())
-    with torch.cuda.device(dev):
-        _raise(load().sdm_nrm_forward(ctypes.byref(a), _stream(stream, dev)), "norm_forward")
+    if copied:
+        x, o, z = _flat(x), _flat(o), _flat(z)
+        w_post, w_pre, scale = (None if t is None else t.contiguous() for t in (w_post, w_pre, scale))
+    a.x, a.o, a.z, a.rstd = _ptr(x), _ptr(o), _ptr(z), rstd.data_ptr()
+    a.w_post, a.w_pre, a.scale = _ptr(w_post), _ptr(w_pre), _ptr(scale)
+    a.x_new, a.y = 0 if o is None else x_new.data_ptr(), _ptr(y)
+    with _OnDevice(dev):
+        status = load().sdm_nrm_forward(ctypes.byref(a), _stream(stream, dev))
+    if status:
+        _raise(status, "norm_forward")
     return x_new, y, rstd
 
 
@@ -362,43 +535,32 @@ def norm_backward(dx_new, dy, x_new, o, z, w_post, w_pre, scale, rstd, *, act="s
     not have. dx_new, the gradient of x_new beside the one through y, may be None; dy is None when w_pre is. x_new and
     rstd are the forward's. dx is the gradient of x (of the residual branch); weights' gradients have their type."""
     import torch
-    first = o if o is not None else x_new
-    if not isinstance(first, torch.Tensor):
-        raise TypeError("x_new, o: a torch tensor")
-    D, dev, wd = _norm_common(first, o, z, w_post, w_pre, scale, act)
-    dt = _dtype(first, "o" if o is not None else "x_new")
-    _tensor(first, "o" if o is not None else "x_new", first.shape)
-    if (dy is None) != (w_pre is None):
-        raise ValueError("dy: given exactly when w_pre is")
-    if dy is None and dx_new is None:
-        raise ValueError("dx_new: required without dy")
-    if dy is not None and x_new is None:
-        raise ValueError("x_new: required with dy")
-    rows = first.numel() // D if D else 0
-    _tensor(rstd, "rstd", (rows, 2), torch.float32, dev)
-    rstd = rstd.contiguous()
-    u2, y2, xn2, o2, z2 = (_flat(t, n, first, first.dtype, dev) for t, n in
-                           ((dx_new, "dx_new"), (dy, "dy"), (x_new, "x_new"), (o, "o"), (z, "z")))
-    like = dict(dtype=first.dtype, device=dev)
-    dx = torch.empty(first.shape, **like)
-    do = None if o is None else torch.empty(first.shape, **like)
-    dz = None if z is None else torch.empty(first.shape, **like)
-    make = torch.zeros if rows == 0 else torch.empty
-    dw = [None if t is None else make(D, dtype=wd, device=dev) for t in (w_post, w_pre, scale)]
-    if rows == 0:
-        return dx, do, dz, *dw
-    w = [None if t is None else t.contiguous() for t in (w_post, w_pre, scale)]
-    a = sdm_nrm_args_t(dtype=dt, wtype=_dtype(w[0] if w[0] is not None else w[1], "weights"), act=ACTS[act], eps=0.0,
-                       rows=rows, D=D, o=_ptr(o2), z=_ptr(z2), ld_o=_ld(o2), ld_z=_ld(z2), w_post=_ptr(w[0]),
-                       w_pre=_ptr(w[1]), scale=_ptr(w[2]), x_new=0 if dy is None else xn2.data_ptr(), ld_xn=_ld(xn2),
-                       rstd=rstd.data_ptr(), dxn=_ptr(u2), dy=_ptr(y2), ld_dxn=_ld(u2), ld_dy=_ld(y2),
-                       dx=dx.data_ptr(), d_o=_ptr(do), dz=_ptr(dz), ld_dx=D, ld_do=D, ld_dz=D, dw_post=_ptr(dw[0]),
-                       dw_pre=_ptr(dw[1]), dscale=_ptr(dw[2]))
-    lib = load()
-    with torch.cuda.device(dev):
-        n = lib.sdm_nrm_workspace(ctypes.byref(a))
-        if n < 0:
-            _raise(n, "norm_backward")
-        ws = _workspace(n, dev)
-        _raise(lib.sdm_nrm_backward(ctypes.byref(a), ws.data_ptr(), n, _stream(stream, dev)), "norm_backward")
-    return dx, do, dz, *dw
+    key = ("norm_bwd", _layout(dx_new), _layout(dy), _layout(x_new), _layout(o), _layout(z), _layout(w_post),
+           _layout(w_pre), _layout(scale), _layout(rstd), act)
+    plan = _plans.get(key)
+    if plan is None:
+        plan = _plans.put(key, _norm_plan(True, dx_new, o, z, w_post, w_pre, scale, act, 0.0, dy, x_new, rstd))
+    a, n, rows, D, dev, wd, copied, shape, dtype = plan
+    dx = torch.empty(shape, dtype=dtype, device=dev)
+    do = None if o is None else torch.empty(shape, dtype=dtype, device=dev)
+    dz = None if z is None else torch.empty(shape, dtype=dtype, device=dev)
+    make = torch.empty if rows else torch.zeros
+    dw_post = None if w_post is None else make(D, dtype=wd, device=dev)
+    dw_pre = None if w_pre is None else make(D, dtype=wd, device=dev)
+    dscale = None if scale is None else make(D, dtype=wd, device=dev)
+    if not rows:
+        return dx, do, dz, dw_post, dw_pre, dscale
+    if copied:
+        dx_new, dy, x_new, o, z = (_flat(t) for t in (dx_new, dy, x_new, o, z))
+        w_post, w_pre, scale, rstd = (None if t is None else t.contiguous() for t in (w_post, w_pre, scale, rstd))
+    a.o, a.z, a.dxn, a.dy, a.rstd = _ptr(o), _ptr(z), _ptr(dx_new), _ptr(dy), rstd.data_ptr()
+    a.x_new = 0 if dy is None else x_new.data_ptr()
+    a.w_post, a.w_pre, a.scale = _ptr(w_post), _ptr(w_pre), _ptr(scale)
+    a.dx, a.d_o, a.dz = dx.data_ptr(), _ptr(do), _ptr(dz)
+    a.dw_post, a.dw_pre, a.dscale = _ptr(dw_post), _ptr(dw_pre), _ptr(dscale)
+    ws = _workspace(n, dev)
+    with _OnDevice(dev):
+        status = load().sdm_nrm_backward(ctypes.byref(a), ws.data_ptr(), n, _stream(stream, dev))
+    if status:
+        _raise(status, "norm_backward")
+    return dx, do, dz, dw_post, dw_pre, dscale
