@@ -16,44 +16,74 @@ template <> struct Elem<1> { using type = __bf16; };
 template <> struct Elem<2> { using type = _Float16; };
 template <int DT> using elem_t = typename Elem<DT>::type;
 
-// Eight elements of a row from column c as float, zero from column `lim` on; only columns < lim are read. `vec`: the
-// row starts on a 16-byte boundary and c is a multiple of 8, so eight elements are one or two 16-byte loads.
-template <class T>
-__device__ __forceinline__ void load8(float (&f)[8], const T* __restrict__ row, int c, int lim, bool vec) {
-    if (vec && c + 8 <= lim) {
-        if constexpr (sizeof(T) == 4) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(row + c), b = *reinterpret_cast<const f32x4*>(row + c + 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
-        } else {
-            typedef T t8 __attribute__((ext_vector_type(8)));
-            const t8 a = *reinterpret_cast<const t8*>(row + c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(a[i]);
-        }
+// 16 bytes on the boundary of an element: global memory takes them at any.
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+
+// Eight elements of a row as they lie in memory, kept until they are needed: a prefetch costs no more registers than
+// its bytes.
+template <int DT>
+struct Raw {
+    u32x4 w[DT == 0 ? 2 : 1];
+};
+// From column c, zero past `lim`; only columns < lim are read.
+template <int DT>
+__device__ __forceinline__ void load_row(Raw<DT>& o, const elem_t<DT>* __restrict__ row, int c, int lim) {
+    if (c + 8 <= lim) {
+        const u32x4u* p = reinterpret_cast<const u32x4u*>(row + c);
+        o.w[0] = p[0];
+        if constexpr (DT == 0) o.w[1] = p[1];
         return;
     }
+    o.w[0] = u32x4{0, 0, 0, 0};
+    if constexpr (DT == 0) {
+        o.w[1] = u32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < lim ? static_cast<float>(row[c + i]) : 0.f;
+        for (int i = 0; i < 7; ++i)
+            if (c + i < lim) o.w[i / 4][i % 4] = __float_as_uint(row[c + i]);
+    } else {
+        const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (c + i < lim) o.w[0][i / 2] |= static_cast<uint32_t>(r[c + i]) << (i % 2 * 16);
+    }
+}
+template <int DT>
+__device__ __forceinline__ void raw_floats(float (&f)[8], const Raw<DT>& r) {
+    if constexpr (DT == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.w[i / 4][i % 4]);
+    } else {
+        typedef elem_t<DT> t8 __attribute__((ext_vector_type(8)));
+        const t8 a = __builtin_bit_cast(t8, r.w[0]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(a[i]);
+    }
+}
+template <int DT>
+__device__ __forceinline__ void load8(float (&f)[8], const elem_t<DT>* __restrict__ row, int c, int lim) {
+    Raw<DT> r;
+    load_row<DT>(r, row, c, lim);
+    raw_floats<DT>(f, r);
 }
 
 template <class T>
-__device__ __forceinline__ void store8(T* __restrict__ row, int c, int lim, bool vec, const float (&f)[8]) {
-    if (vec && c + 8 <= lim) {
+__device__ __forceinline__ void store8(T* __restrict__ row, int c, int lim, const float (&f)[8]) {
+    if (c + 8 <= lim) {
+        u32x4u* p = reinterpret_cast<u32x4u*>(row + c);
         if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<f32x4*>(row + c) = f32x4{f[0], f[1], f[2], f[3]};
-            *reinterpret_cast<f32x4*>(row + c + 4) = f32x4{f[4], f[5], f[6], f[7]};
+            p[0] = u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+            p[1] = u32x4{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])};
         } else {
             typedef T t8 __attribute__((ext_vector_type(8)));
             t8 a;
 #pragma unroll
             for (int i = 0; i < 8; ++i) a[i] = static_cast<T>(f[i]);
-            *reinterpret_cast<t8*>(row + c) = a;
+            p[0] = __builtin_bit_cast(u32x4, a);
         }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 7; ++i)
         if (c + i < lim) row[c + i] = static_cast<T>(f[i]);
 }
 

@@ -36,7 +36,7 @@ struct GdrLaunch {
     int32_t slots;      // chunk slots
     int32_t dkp;        // dk padded to 64, 128 or 256
     int32_t dvp;        // dv rounded up to a multiple of 8: rows of st, dst, u, dr, zero past dv
-    int32_t vec_qk, vec_v;      // rows of q and k / v, o, d_o and their gradients start on 16-byte boundaries
+    int32_t vec_qk, vec_v;      // dk and dv are multiples of 8
 };
 
 // bfloat16 parts that hold an element of a type exactly: 3, 1, 2

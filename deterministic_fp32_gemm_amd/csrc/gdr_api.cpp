@@ -198,12 +198,6 @@ int64_t lay_out(const sdm_gdr_args_t* a, bool backward, char* base, GdrWork* w) 
     return at ? at : 1;
 }
 
-bool vec_rows(const sdm_rows_t& r, int64_t cols, int dtype) {
-    const int64_t per = 16 / elem_size(dtype);
-    return !r.data || (aligned(r.data, 16) && r.batch % per == 0 && r.token % per == 0 && r.head % per == 0 &&
-                       cols % 8 == 0);
-}
-
 GdrLaunch plan(const sdm_gdr_args_t* a, bool backward, void* workspace) {
     GdrLaunch g{};
     g.a = *a;
@@ -211,14 +205,8 @@ GdrLaunch plan(const sdm_gdr_args_t* a, bool backward, void* workspace) {
     g.slots = static_cast<int32_t>(slots_of(a));
     g.dkp = static_cast<int32_t>(padded_dk(a->dk));
     g.dvp = static_cast<int32_t>((a->dv + 7) / 8 * 8);
-    g.vec_qk = vec_rows(a->q, a->dk, a->dtype) && vec_rows(a->k, a->dk, a->dtype);
-    g.vec_v = vec_rows(a->v, a->dv, a->dtype);
-    if (backward) {
-        g.vec_qk = g.vec_qk && vec_rows(a->d_q, a->dk, a->dtype) && vec_rows(a->d_k, a->dk, a->dtype);
-        g.vec_v = g.vec_v && vec_rows(a->d_o, a->dv, a->dtype) && vec_rows(a->d_v, a->dv, a->dtype);
-    } else {
-        g.vec_v = g.vec_v && vec_rows(a->o, a->dv, a->dtype);
-    }
+    g.vec_qk = a->dk % 8 == 0;
+    g.vec_v = a->dv % 8 == 0;
     return g;
 }
 

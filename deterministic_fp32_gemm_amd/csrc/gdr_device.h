@@ -83,23 +83,20 @@ __device__ __forceinline__ void mma(f32x4& acc, const Frag<NA>& a, const Frag<NB
             if (s - i >= 0 && s - i < NB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], acc, 0, 0, 0);
 }
 
-// Eight elements of a row as they lie in memory, kept until they are needed: a prefetch costs no more registers than
-// its bytes.
-template <int DT>
-struct Raw {
-    u32x4 w[DT == 0 ? 2 : 1];
-};
 // Always from a place inside the row (`row` itself has to be readable), zero where c is past `lim` or !ok: no branch
-// around a load, so that loads stay in flight together. VEC: the row starts on a 16-byte boundary, lim is a multiple
-// of 8.
+// around a load, so that loads stay in flight together. VEC: lim is a multiple of 8.
 template <int DT, bool VEC>
 __device__ __forceinline__ void load_raw(Raw<DT>& o, const elem_t<DT>* __restrict__ row, int c, int lim, bool ok) {
     const u32x4 zero = {0, 0, 0, 0};
     if constexpr (VEC) {
         ok = ok && c < lim;
-        const u32x4* p = reinterpret_cast<const u32x4*>(row + (ok ? c : 0));
-        o.w[0] = ok ? p[0] : zero;
-        if constexpr (DT == 0) o.w[1] = ok ? p[1] : zero;
+        const u32x4u* p = reinterpret_cast<const u32x4u*>(row + (ok ? c : 0));
+        const u32x4 x = p[0];
+        o.w[0] = ok ? x : zero;
+        if constexpr (DT == 0) {
+            const u32x4 y = p[1];
+            o.w[1] = ok ? y : zero;
+        }
     } else if constexpr (DT == 0) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -115,18 +112,6 @@ __device__ __forceinline__ void load_raw(Raw<DT>& o, const elem_t<DT>* __restric
             const uint32_t lo = r[il ? c + 2 * i : 0], hi = r[ih ? c + 2 * i + 1 : 0];
             o.w[0][i] = (il ? lo : 0u) | (ih ? hi << 16 : 0u);
         }
-    }
-}
-template <int DT>
-__device__ __forceinline__ void raw_floats(float (&f)[8], const Raw<DT>& r) {
-    if constexpr (DT == 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.w[i / 4][i % 4]);
-    } else {
-        typedef elem_t<DT> t8 __attribute__((ext_vector_type(8)));
-        const t8 a = __builtin_bit_cast(t8, r.w[0]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(a[i]);
     }
 }
 template <int DT>

@@ -11,7 +11,6 @@ struct NrmPlan {
     int threads;    // of a workgroup, which takes one row at a time
     int vecs;       // groups of 8 columns a thread: threads * vecs * 8 >= D
     int groups;     // workgroups; workgroup i takes rows i, i + groups, ...
-    bool vec;       // rows on 16-byte boundaries
 };
 
 hipError_t launch_nrm_forward(const sdm_nrm_args_t& a, const NrmPlan& p, hipStream_t stream);

@@ -50,7 +50,7 @@ __device__ __forceinline__ void gate(float z, int act, float& a, float& d) {
 }
 
 template <int DT, int WT, int NT, int NV>
-__global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a, const bool vec) {
+__global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
     using T = elem_t<DT>;
     using W = elem_t<WT>;
     __shared__ float red[2][16];
@@ -62,20 +62,20 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a, const 
     for (int v = 0; v < NV; ++v) {
         const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
         if (has_o) {
-            load8(w1[v], static_cast<const W*>(a.w_post), c, D, vec);
-            load8(sc[v], static_cast<const W*>(a.scale), c, D, vec);
+            load8<WT>(w1[v], static_cast<const W*>(a.w_post), c, D);
+            load8<WT>(sc[v], static_cast<const W*>(a.scale), c, D);
         }
-        if (has_y) load8(w2[v], static_cast<const W*>(a.w_pre), c, D, vec);
+        if (has_y) load8<WT>(w2[v], static_cast<const W*>(a.w_pre), c, D);
     }
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         float x[NV][8], o[NV][8], z[NV][8];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
-            if (has_o) load8(o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D, vec);
-            if (a.act != SDM_ACT_NONE) load8(z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D, vec);
+            if (has_o) load8<DT>(o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D);
+            if (a.act != SDM_ACT_NONE) load8<DT>(z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D);
             if (has_x) {
-                load8(x[v], static_cast<const T*>(a.x) + r * a.ld_x, c, D, vec);
+                load8<DT>(x[v], static_cast<const T*>(a.x) + r * a.ld_x, c, D);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[v][i] = 0.f;
@@ -98,8 +98,7 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a, const 
                     // rounded to the residual's type here: the second norm is that of the stored row
                     x[v][i] = static_cast<float>(static_cast<T>(fmaf(sc[v][i], o[v][i] * r1 * w1[v][i] * g, x[v][i])));
                 }
-                store8(static_cast<T*>(a.x_new) + r * a.ld_xn, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, vec,
-                       x[v]);
+                store8(static_cast<T*>(a.x_new) + r * a.ld_xn, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, x[v]);
             }
         }
         if (has_y) {
@@ -113,7 +112,7 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a, const 
             for (int v = 0; v < NV; ++v) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[v][i] = x[v][i] * r2 * w2[v][i];
-                store8(static_cast<T*>(a.y) + r * a.ld_y, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, vec, x[v]);
+                store8(static_cast<T*>(a.y) + r * a.ld_y, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, x[v]);
             }
         }
         if (threadIdx.x == 0) {
@@ -125,44 +124,90 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a, const 
     }
 }
 
+// The weights wait in LDS and the next row's loads are in flight while a row is worked on: a row's two dependent sums
+// leave memory nothing to do otherwise.
 template <int DT, int WT, int NT, int NV>
-__global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, const bool vec, float* __restrict__ part) {
+__global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float* __restrict__ part) {
     using T = elem_t<DT>;
     using W = elem_t<WT>;
     __shared__ float red[2][16];
-    const int D = static_cast<int>(a.D);
+    __shared__ alignas(16) float wt[3][NV][NT][8];      // each thread's own columns: w_post, scale, w_pre
+    const int D = static_cast<int>(a.D), id = static_cast<int>(threadIdx.x);
     const float inv = 1.f / static_cast<float>(D);
     const bool has_o = a.o != nullptr, has_y = a.w_pre != nullptr, has_up = a.dxn != nullptr;
-    float w1[NV][8], w2[NV][8], sc[NV][8], s1[NV][8], s2[NV][8], s3[NV][8];
+    const bool has_z = a.act != SDM_ACT_NONE;
+    float s1[NV][8], s2[NV][8], s3[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
+        const int c = (v * NT + id) * 8;
+        float f[8];
+        auto keep = [&](int k, const void* w) {
+            load8<WT>(f, static_cast<const W*>(w), c, D);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) wt[k][v][id][i] = f[i];
+        };
         if (has_o) {
-            load8(w1[v], static_cast<const W*>(a.w_post), c, D, vec);
-            load8(sc[v], static_cast<const W*>(a.scale), c, D, vec);
+            keep(0, a.w_post);
+            keep(1, a.scale);
         }
-        if (has_y) load8(w2[v], static_cast<const W*>(a.w_pre), c, D, vec);
+        if (has_y) keep(2, a.w_pre);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s1[v][i] = s2[v][i] = s3[v][i] = 0.f;
     }
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        float dx[NV][8], y[NV][8], xn[NV][8], o[NV][8], z[NV][8];
-        const float r1 = a.rstd[2 * r], r2 = a.rstd[2 * r + 1];
+    struct {
+        Raw<DT> dx[NV], y[NV], xn[NV], o[NV], z[NV];
+        float r1, r2;
+    } in;
+    auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
+            const int c = (v * NT + id) * 8;
             if (has_y) {
-                load8(y[v], static_cast<const T*>(a.dy) + r * a.ld_dy, c, D, vec);
-                load8(xn[v], static_cast<const T*>(a.x_new) + r * a.ld_xn, c, D, vec);
+                load_row<DT>(in.y[v], static_cast<const T*>(a.dy) + r * a.ld_dy, c, D);
+                load_row<DT>(in.xn[v], static_cast<const T*>(a.x_new) + r * a.ld_xn, c, D);
+            }
+            if (has_up) load_row<DT>(in.dx[v], static_cast<const T*>(a.dxn) + r * a.ld_dxn, c, D);
+        }
+        in.r1 = a.rstd[2 * r];
+        in.r2 = a.rstd[2 * r + 1];
+    };
+    auto fetch_o = [&](int64_t r) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * NT + id) * 8;
+            if (has_o) load_row<DT>(in.o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D);
+            if (has_z) load_row<DT>(in.z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D);
+        }
+    };
+    constexpr bool AHEAD = NV == 1;     // registers hold the next row beside this one
+    int64_t r = blockIdx.x;
+    if (AHEAD && r < a.rows) {
+        fetch(r);
+        fetch_o(r);
+    }
+    for (; r < a.rows; r += gridDim.x) {
+        if (!AHEAD) fetch(r);
+        float dx[NV][8], y[NV][8], xn[NV][8], o[NV][8], z[NV][8];
+        const float r1 = in.r1, r2 = in.r2;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            raw_floats<DT>(y[v], in.y[v]);
+            raw_floats<DT>(xn[v], in.xn[v]);
+            if (AHEAD) {
+                raw_floats<DT>(o[v], in.o[v]);
+                raw_floats<DT>(z[v], in.z[v]);
             }
             if (has_up) {
-                load8(dx[v], static_cast<const T*>(a.dxn) + r * a.ld_dxn, c, D, vec);
+                raw_floats<DT>(dx[v], in.dx[v]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dx[v][i] = 0.f;
             }
-            if (has_o) load8(o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D, vec);
-            if (a.act != SDM_ACT_NONE) load8(z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D, vec);
+        }
+        if (AHEAD) {
+            const int64_t next = r + gridDim.x < a.rows ? r + gridDim.x : r;    // the last row again: it costs little
+            fetch(next);
+            fetch_o(next);
         }
         if (has_y) {
             float s = 0.f;
@@ -172,7 +217,7 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, const
                 for (int i = 0; i < 8; ++i) {
                     xn[v][i] *= r2;
                     s2[v][i] = fmaf(y[v][i], xn[v][i], s2[v][i]);
-                    y[v][i] *= w2[v][i];
+                    y[v][i] *= wt[2][v][id][i];
                     s = fmaf(y[v][i], xn[v][i], s);
                 }
             const float m = row_sum<NT>(s, red, 0) * inv;
@@ -183,47 +228,53 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, const
         }
         if (a.dx) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-                store8(static_cast<T*>(a.dx) + r * a.ld_dx, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, vec,
-                       dx[v]);
+            for (int v = 0; v < NV; ++v) store8(static_cast<T*>(a.dx) + r * a.ld_dx, (v * NT + id) * 8, D, dx[v]);
         }
         if (has_o) {
             float s = 0.f;
+            if (!AHEAD) {
+                fetch_o(r);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    raw_floats<DT>(o[v], in.o[v]);
+                    raw_floats<DT>(z[v], in.z[v]);
+                }
+            }
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     float g = 1.f, d = 0.f;
-                    if (a.act != SDM_ACT_NONE) gate<DT>(z[v][i], a.act, g, d);
+                    if (has_z) gate<DT>(z[v][i], a.act, g, d);
+                    const float w1 = wt[0][v][id][i], sc = wt[1][v][id][i];
                     const float n = o[v][i] * r1, u = dx[v][i] * n;
-                    z[v][i] = u * sc[v][i] * w1[v][i] * d;
-                    s3[v][i] = fmaf(u * w1[v][i], g, s3[v][i]);
-                    const float dn = dx[v][i] * sc[v][i] * g;
+                    z[v][i] = u * sc * w1 * d;
+                    s3[v][i] = fmaf(u * w1, g, s3[v][i]);
+                    const float dn = dx[v][i] * sc * g;
                     s1[v][i] = fmaf(dn, n, s1[v][i]);
-                    dx[v][i] = dn * w1[v][i];
+                    dx[v][i] = dn * w1;
                     o[v][i] = n;
                     s = fmaf(dx[v][i], n, s);
                 }
             const float m = row_sum<NT>(s, red, 1) * inv;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
-                if (a.dz) store8(static_cast<T*>(a.dz) + r * a.ld_dz, c, D, vec, z[v]);
+                const int c = (v * NT + id) * 8;
+                if (a.dz) store8(static_cast<T*>(a.dz) + r * a.ld_dz, c, D, z[v]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dx[v][i] = r1 * fmaf(-m, o[v][i], dx[v][i]);
-                store8(static_cast<T*>(a.d_o) + r * a.ld_do, c, D, vec, dx[v]);
+                store8(static_cast<T*>(a.d_o) + r * a.ld_do, c, D, dx[v]);
             }
         }
         if (NT > 64 && has_o != has_y) lds_barrier();
     }
     float* p = part + static_cast<int64_t>(blockIdx.x) * 3 * D;
-    const bool pv = vec && D % 4 == 0;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
-        if (has_o) store8(p, c, D, pv, s1[v]);
-        if (has_y) store8(p + D, c, D, pv, s2[v]);
-        if (has_o) store8(p + 2 * static_cast<int64_t>(D), c, D, pv, s3[v]);
+        const int c = (v * NT + id) * 8;
+        if (has_o) store8(p, c, D, s1[v]);
+        if (has_y) store8(p + D, c, D, s2[v]);
+        if (has_o) store8(p + 2 * static_cast<int64_t>(D), c, D, s3[v]);
     }
 }
 
@@ -255,28 +306,30 @@ __global__ __launch_bounds__(256) void nrm_weights(const sdm_nrm_args_t a, const
 
 template <int DT, int WT, int NT, int NV>
 hipError_t run_forward(const sdm_nrm_args_t& a, const NrmPlan& p, hipStream_t s) {
-    nrm_forward<DT, WT, NT, NV><<<p.groups, NT, 0, s>>>(a, p.vec);
+    nrm_forward<DT, WT, NT, NV><<<p.groups, NT, 0, s>>>(a);
     return hipGetLastError();
 }
 template <int DT, int WT, int NT, int NV>
 hipError_t run_backward(const sdm_nrm_args_t& a, const NrmPlan& p, float* part, hipStream_t s) {
-    nrm_backward<DT, WT, NT, NV><<<p.groups, NT, 0, s>>>(a, p.vec, part);
+    nrm_backward<DT, WT, NT, NV><<<p.groups, NT, 0, s>>>(a, part);
     return hipGetLastError();
 }
 
-#define SDM_NRM_SHAPES(F, ...)                                        \
-    if (p.threads == 64) return F<DT, WT, 64, 1>(__VA_ARGS__);        \
-    if (p.threads == 256 && p.vecs == 1) return F<DT, WT, 256, 1>(__VA_ARGS__); \
-    if (p.threads == 256) return F<DT, WT, 256, 2>(__VA_ARGS__);      \
-    return F<DT, WT, 512, 2>(__VA_ARGS__);
+#define SDM_NRM_SHAPES(F, ...)                                                  \
+    if (p.threads == 64) return F<DT, WT, 64, 1>(__VA_ARGS__);                  \
+    if (p.threads == 256 && p.vecs == 1) return F<DT, WT, 256, 1>(__VA_ARGS__);
 
 template <int DT, int WT>
 hipError_t forward_of(const sdm_nrm_args_t& a, const NrmPlan& p, hipStream_t s) {
     SDM_NRM_SHAPES(run_forward, a, p, s)
+    if (p.threads == 256) return run_forward<DT, WT, 256, 2>(a, p, s);
+    return run_forward<DT, WT, 512, 2>(a, p, s);
 }
 template <int DT, int WT>
 hipError_t backward_of(const sdm_nrm_args_t& a, const NrmPlan& p, float* part, hipStream_t s) {
     SDM_NRM_SHAPES(run_backward, a, p, part, s)
+    if (p.vecs == 1) return run_backward<DT, WT, 512, 1>(a, p, part, s);
+    return run_backward<DT, WT, 512, 2>(a, p, part, s);
 }
 
 }  // namespace
