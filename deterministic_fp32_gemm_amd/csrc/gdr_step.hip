@@ -119,19 +119,16 @@ template <int DT>
 hipError_t run(const sdm_gdr_step_args_t& a, bool vec, hipStream_t s) {
     const int64_t bh = a.B * a.Hv;
     const bool narrow = bh * ((a.dv + 127) / 128) < 1024;
-    const int cols = narrow ? 32 : 128, slices = static_cast<int>((a.dv + cols - 1) / cols);
+    const int cols = narrow ? 32 : a.dk <= 128 ? 128 : 64, slices = static_cast<int>((a.dv + cols - 1) / cols);
     const unsigned grid = static_cast<unsigned>(bh * slices);
-    if (narrow) {
-        if (a.dk <= 128)
-            gdr_step<DT, 8, 4><<<grid, 256, 0, s>>>(a, vec, slices);
-        else
-            gdr_step<DT, 8, 8><<<grid, 256, 0, s>>>(a, vec, slices);
-    } else {
-        if (a.dk <= 128)
-            gdr_step<DT, 32, 16><<<grid, 256, 0, s>>>(a, vec, slices);
-        else
-            gdr_step<DT, 32, 32><<<grid, 256, 0, s>>>(a, vec, slices);
-    }
+    if (narrow && a.dk <= 128)
+        gdr_step<DT, 8, 4><<<grid, 256, 0, s>>>(a, vec, slices);
+    else if (narrow)
+        gdr_step<DT, 8, 8><<<grid, 256, 0, s>>>(a, vec, slices);
+    else if (a.dk <= 128)
+        gdr_step<DT, 32, 16><<<grid, 256, 0, s>>>(a, vec, slices);
+    else
+        gdr_step<DT, 16, 16><<<grid, 256, 0, s>>>(a, vec, slices);
     return hipGetLastError();
 }
 

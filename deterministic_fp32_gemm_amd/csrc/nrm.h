@@ -14,7 +14,7 @@ struct NrmPlan {
 };
 
 hipError_t launch_nrm_forward(const sdm_nrm_args_t& a, const NrmPlan& p, hipStream_t stream);
-// part: float [groups][3][D], the workgroups' sums of the three weights' gradients
+// part: float [groups][2][D], the workgroups' sums
 hipError_t launch_nrm_backward(const sdm_nrm_args_t& a, const NrmPlan& p, float* part, hipStream_t stream);
 
 }  // namespace sdm_delta

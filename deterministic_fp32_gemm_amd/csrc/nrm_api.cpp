@@ -134,7 +134,7 @@ int64_t sdm_nrm_workspace(const sdm_nrm_args_t* args) {
     if (!args) return SDM_GX_ERR_ARG;
     if (args->rows < 0 || args->rows >= (int64_t(1) << 40) || args->D < 1 || args->D > SDM_NRM_MAX_D)
         return SDM_GX_ERR_SHAPE;
-    return static_cast<int64_t>(plan(args, true).groups) * 3 * args->D * 4;
+    return static_cast<int64_t>(plan(args, true).groups) * 2 * args->D * 4;
 }
 
 int sdm_nrm_forward(const sdm_nrm_args_t* args, void* stream) {
@@ -152,7 +152,7 @@ int sdm_nrm_backward(const sdm_nrm_args_t* args, void* workspace, int64_t worksp
     if (!workspace) return SDM_GX_ERR_NULL;
     if (!aligned(workspace, 16)) return SDM_GX_ERR_ALIGN;
     const NrmPlan p = plan(args, true);
-    if (workspace_bytes < static_cast<int64_t>(p.groups) * 3 * args->D * 4) return SDM_GX_ERR_LIMIT;
+    if (workspace_bytes < static_cast<int64_t>(p.groups) * 2 * args->D * 4) return SDM_GX_ERR_LIMIT;
     if ((st = current_gfx950(&dev)) || (st = pointers_on(args, true, dev)) || (st = pointer_on(workspace, dev))) return st;
     const hipError_t e = launch_nrm_backward(*args, p, static_cast<float*>(workspace), static_cast<hipStream_t>(stream));
     return e == hipSuccess ? SDM_GX_OK : record_hip_error(e);

@@ -136,7 +136,8 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
     const float inv = 1.f / static_cast<float>(D);
     const bool has_o = a.o != nullptr, has_y = a.w_pre != nullptr, has_up = a.dxn != nullptr;
     const bool has_z = a.act != SDM_ACT_NONE;
-    float s1[NV][8], s2[NV][8], s3[NV][8];
+    // sums over this workgroup's rows: dx n act(z), which times scale is dw_post's and times w_post dscale's, and dw_pre's
+    float s1[NV][8], s2[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int c = (v * NT + id) * 8;
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
         }
         if (has_y) keep(2, a.w_pre);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s1[v][i] = s2[v][i] = s3[v][i] = 0.f;
+        for (int i = 0; i < 8; ++i) s1[v][i] = s2[v][i] = 0.f;
     }
     struct {
         Raw<DT> dx[NV], y[NV], xn[NV], o[NV], z[NV];
@@ -249,10 +250,8 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
                     const float w1 = wt[0][v][id][i], sc = wt[1][v][id][i];
                     const float n = o[v][i] * r1, u = dx[v][i] * n;
                     z[v][i] = u * sc * w1 * d;
-                    s3[v][i] = fmaf(u * w1, g, s3[v][i]);
-                    const float dn = dx[v][i] * sc * g;
-                    s1[v][i] = fmaf(dn, n, s1[v][i]);
-                    dx[v][i] = dn * w1;
+                    s1[v][i] = fmaf(u, g, s1[v][i]);
+                    dx[v][i] *= sc * g * w1;
                     o[v][i] = n;
                     s = fmaf(dx[v][i], n, s);
                 }
@@ -268,13 +267,12 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
         }
         if (NT > 64 && has_o != has_y) lds_barrier();
     }
-    float* p = part + static_cast<int64_t>(blockIdx.x) * 3 * D;
+    float* p = part + static_cast<int64_t>(blockIdx.x) * 2 * D;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int c = (v * NT + id) * 8;
         if (has_o) store8(p, c, D, s1[v]);
         if (has_y) store8(p + D, c, D, s2[v]);
-        if (has_o) store8(p + 2 * static_cast<int64_t>(D), c, D, s3[v]);
     }
 }
 
@@ -285,22 +283,26 @@ __global__ __launch_bounds__(256) void nrm_weights(const sdm_nrm_args_t a, const
     using W = elem_t<WT>;
     __shared__ float red[8][33];
     const int D = static_cast<int>(a.D), which = blockIdx.y;
-    W* out = static_cast<W*>(which == 0 ? a.dw_post : which == 1 ? a.dw_pre : a.dscale);
-    if (!out) return;
+    if (!(which ? a.w_pre : a.o)) return;
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     const int per = (groups + 7) / 8, lo = grp * per, hi = min(groups, lo + per);
     float s = 0.f;
     if (c < D) {
         const float* p = part + static_cast<int64_t>(which) * D + c;
 #pragma unroll 8
-        for (int i = lo; i < hi; ++i) s += p[static_cast<int64_t>(i) * 3 * D];
+        for (int i = lo; i < hi; ++i) s += p[static_cast<int64_t>(i) * 2 * D];
     }
     red[grp][lane] = s;
     lds_barrier();
     if (grp == 0 && c < D) {
 #pragma unroll
         for (int i = 1; i < 8; ++i) s += red[i][lane];
-        out[c] = static_cast<W>(s);
+        if (which) {
+            static_cast<W*>(a.dw_pre)[c] = static_cast<W>(s);
+        } else {
+            static_cast<W*>(a.dw_post)[c] = static_cast<W>(s * static_cast<float>(static_cast<const W*>(a.scale)[c]));
+            static_cast<W*>(a.dscale)[c] = static_cast<W>(s * static_cast<float>(static_cast<const W*>(a.w_post)[c]));
+        }
     }
 }
 
@@ -350,7 +352,7 @@ hipError_t launch_nrm_backward(const sdm_nrm_args_t& a, const NrmPlan& p, float*
     else
         e = a.wtype == SDM_F32 ? backward_of<2, 0>(a, p, part, s) : backward_of<2, 2>(a, p, part, s);
     if (e != hipSuccess) return e;
-    const dim3 grid(static_cast<unsigned>((a.D + 31) / 32), 3);
+    const dim3 grid(static_cast<unsigned>((a.D + 31) / 32), 2);
     if (a.wtype == SDM_F32)
         nrm_weights<0><<<grid, 256, 0, s>>>(a, part, p.groups);
     else if (a.wtype == SDM_BF16)
