@@ -34,17 +34,17 @@ __device__ __forceinline__ void load_row(Raw<DT>& o, const elem_t<DT>* __restric
         if constexpr (DT == 0) o.w[1] = p[1];
         return;
     }
-    o.w[0] = u32x4{0, 0, 0, 0};
-    if constexpr (DT == 0) {
-        o.w[1] = u32x4{0, 0, 0, 0};
+    // the row's end: eight single loads, all in flight together, from inside the row
 #pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (c + i < lim) o.w[i / 4][i % 4] = __float_as_uint(row[c + i]);
-    } else {
-        const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (c + i < lim) o.w[0][i / 2] |= static_cast<uint32_t>(r[c + i]) << (i % 2 * 16);
+    for (int i = 0; i < 8; ++i) {
+        const int k = min(c + i, lim - 1);
+        if constexpr (DT == 0) {
+            const uint32_t x = __float_as_uint(row[k]);
+            o.w[i / 4][i % 4] = c + i < lim ? x : 0u;
+        } else {
+            const uint32_t x = reinterpret_cast<const uint16_t*>(row)[k], y = c + i < lim ? x : 0u;
+            o.w[0][i / 2] = i % 2 ? o.w[0][i / 2] | y << 16 : y;
+        }
     }
 }
 template <int DT>

@@ -102,7 +102,7 @@ int check(const sdm_nrm_args_t* a, bool backward) {
 NrmPlan plan(const sdm_nrm_args_t* a, bool backward) {
     NrmPlan p{};
     // 16384 rows of 4096 in bfloat16: forward 136 us with 256 threads of two groups of columns, 151 with 512 of one;
-    // backward, which holds three sums a column, 243 with 512 of one, 340 with 256 of two
+    // backward, which holds two sums a column beside, 215 with 512 of one, 340 with 256 of two
     const bool middle = a->D > 2048 && a->D <= 4096;
     p.threads = a->D <= 512 ? 64 : a->D <= 2048 || (middle && !backward) ? 256 : 512;
     p.vecs = static_cast<int>(cdiv(a->D, p.threads * 8));

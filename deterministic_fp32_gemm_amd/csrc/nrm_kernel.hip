@@ -131,30 +131,14 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
     using T = elem_t<DT>;
     using W = elem_t<WT>;
     __shared__ float red[2][16];
-    __shared__ alignas(16) float wt[3][NV][NT][8];      // each thread's own columns: w_post, scale, w_pre
+    // each thread's own columns: w_post, scale, w_pre; for long rows, whose values fill the registers, dw_pre's sum too
+    __shared__ alignas(16) float wt[NV == 1 ? 3 : 4][NV][NT][8];
     const int D = static_cast<int>(a.D), id = static_cast<int>(threadIdx.x);
     const float inv = 1.f / static_cast<float>(D);
     const bool has_o = a.o != nullptr, has_y = a.w_pre != nullptr, has_up = a.dxn != nullptr;
     const bool has_z = a.act != SDM_ACT_NONE;
     // sums over this workgroup's rows: dx n act(z), which times scale is dw_post's and times w_post dscale's, and dw_pre's
     float s1[NV][8], s2[NV][8];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int c = (v * NT + id) * 8;
-        float f[8];
-        auto keep = [&](int k, const void* w) {
-            load8<WT>(f, static_cast<const W*>(w), c, D);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) wt[k][v][id][i] = f[i];
-        };
-        if (has_o) {
-            keep(0, a.w_post);
-            keep(1, a.scale);
-        }
-        if (has_y) keep(2, a.w_pre);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s1[v][i] = s2[v][i] = 0.f;
-    }
     struct {
         Raw<DT> dx[NV], y[NV], xn[NV], o[NV], z[NV];
         float r1, r2;
@@ -185,6 +169,25 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
     if (AHEAD && r < a.rows) {
         fetch(r);
         fetch_o(r);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * NT + id) * 8;
+        float f[8];
+        auto keep = [&](int k, const void* w) {
+            load8<WT>(f, static_cast<const W*>(w), c, D);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) wt[k][v][id][i] = f[i];
+        };
+        if (has_o) {
+            keep(0, a.w_post);
+            keep(1, a.scale);
+        }
+        if (has_y) keep(2, a.w_pre);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s1[v][i] = s2[v][i] = 0.f;
+        if constexpr (NV > 1)
+            for (int i = 0; i < 8; ++i) wt[3][v][id][i] = 0.f;
     }
     for (; r < a.rows; r += gridDim.x) {
         if (!AHEAD) fetch(r);
@@ -217,15 +220,17 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     xn[v][i] *= r2;
-                    s2[v][i] = fmaf(y[v][i], xn[v][i], s2[v][i]);
-                    y[v][i] *= wt[2][v][id][i];
-                    s = fmaf(y[v][i], xn[v][i], s);
+                    float& s2r = NV == 1 ? s2[v][i] : wt[NV == 1 ? 0 : 3][v][id][i];
+                    s2r = fmaf(y[v][i], xn[v][i], s2r);
+                    const float yw = y[v][i] * wt[2][v][id][i];
+                    s = fmaf(yw, xn[v][i], s);
+                    dx[v][i] = fmaf(r2, yw, dx[v][i]);
                 }
-            const float m = row_sum<NT>(s, red, 0) * inv;
+            const float m = row_sum<NT>(s, red, 0) * inv * r2;
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dx[v][i] = fmaf(r2, fmaf(-m, xn[v][i], y[v][i]), dx[v][i]);
+                for (int i = 0; i < 8; ++i) dx[v][i] = fmaf(-m, xn[v][i], dx[v][i]);
         }
         if (a.dx) {
 #pragma unroll
@@ -255,11 +260,14 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
                     o[v][i] = n;
                     s = fmaf(dx[v][i], n, s);
                 }
+            if (has_z) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) store8(static_cast<T*>(a.dz) + r * a.ld_dz, (v * NT + id) * 8, D, z[v]);
+            }
             const float m = row_sum<NT>(s, red, 1) * inv;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 const int c = (v * NT + id) * 8;
-                if (a.dz) store8(static_cast<T*>(a.dz) + r * a.ld_dz, c, D, z[v]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dx[v][i] = r1 * fmaf(-m, o[v][i], dx[v][i]);
                 store8(static_cast<T*>(a.d_o) + r * a.ld_do, c, D, dx[v]);
@@ -272,6 +280,8 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
     for (int v = 0; v < NV; ++v) {
         const int c = (v * NT + id) * 8;
         if (has_o) store8(p, c, D, s1[v]);
+        if constexpr (NV > 1)
+            for (int i = 0; i < 8; ++i) s2[v][i] = wt[3][v][id][i];
         if (has_y) store8(p + D, c, D, s2[v]);
     }
 }
