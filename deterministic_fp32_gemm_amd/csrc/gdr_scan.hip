@@ -178,12 +178,12 @@ struct Operands {
 };
 
 // How many chunks ahead operands are fetched: a step takes less than a load from memory, so two where the registers
-// hold two chunks (a step of 16384 tokens x 32 heads in bfloat16: 2.0 us with one, 1.5 with two); with wide float32
-// heads not even one: K^T (and Q^T) come in the middle of their own step.
+// hold two chunks (the scans of 2 x 4096 tokens x 16 heads in bfloat16: 160 and 223 us with one, 153 and 212 with two);
+// with wide float32 heads not even one: K^T (and Q^T) come in the middle of their own step.
 template <int DT, int DKP> constexpr int kDepth = DT == 1 && DKP <= 128 ? 2 : 1;
-template <int DT, int DKP> constexpr bool kLate = DT != 1 && DKP > 128;
+template <int DT, int DKP, int NT> constexpr bool kLate = (DT != 1 && DKP > 128) || (DT == 0 && DKP * NT >= 256);
 // k blocks of S in registers at once
-template <int DT, int DKP> constexpr int kHalf = DT == 0 ? (DKP == 256 ? 1 : 2) : DKP == 128 ? 4 : 2;
+template <int DT, int DKP, int NT> constexpr int kHalf = DT == 0 ? (DKP * NT >= 256 ? 1 : 2) : DKP == 128 ? 4 : 2;
 
 // step(chunk, set), sets of operands taking turns. Where two paths meet inside a loop, registers that loads are still on
 // their way to would be moved, and the moves wait: hence no branch in it, and a loop of its own for each kind of
@@ -205,8 +205,8 @@ __device__ __forceinline__ void in_turn(int chunks, F step) {
 template <int DT, int DKP, int NT, bool STORE>
 __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, PP = kOutParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
-    constexpr int HALF = kHalf<DT, DKP>, DEPTH = kDepth<DT, DKP>;
-    constexpr bool LATE = kLate<DT, DKP>;
+    constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kDepth<DT, DKP>;
+    constexpr bool LATE = kLate<DT, DKP, NT>;
     using T = elem_t<DT>;
     __shared__ Tile<3, COLS, DKP> Sx;           // S, [column][dk]
     __shared__ Tile<3, COLS, 64> Rx, Dx;            // R and exp(G_C - G) U, [column][token]
@@ -428,8 +428,8 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
 template <int DT, int DKP, int NT>
 __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
-    constexpr int HALF = kHalf<DT, DKP>, DEPTH = kDepth<DT, DKP>;
-    constexpr bool LATE = kLate<DT, DKP>;
+    constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kDepth<DT, DKP>;
+    constexpr bool LATE = kLate<DT, DKP, NT>;
     using T = elem_t<DT>;
     __shared__ Tile<3, COLS, DKP> Sx;           // dS, [column][dk]
     __shared__ Tile<3, COLS, 64> Ox, Qx, Ux, Rx;    // the next chunk's dO, scale exp(G) dO, dU and -beta exp(G) dR
@@ -637,16 +637,25 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
     if (a.ds0 && Tiles<DKP>::owner(w)) store_state<DKP, NT>(S, w, a.ds0 + w.head * w.dk * dv, dv);
 }
 
+template <int DT, int DKP, int NT>
+hipError_t scan(const GdrLaunch& g, int mode, hipStream_t s) {
+    const int total = static_cast<int>((g.a.dv + 16 * NT - 1) / (16 * NT) * g.a.Hv * g.a.nseq), grid = 8 * ((total + 7) / 8);
+    if (mode == 0)
+        gdr_scan<DT, DKP, NT, false><<<grid, 512, 0, s>>>(g, total);
+    else if (mode == 1)
+        gdr_scan<DT, DKP, NT, true><<<grid, 512, 0, s>>>(g, total);
+    else
+        gdr_scan_back<DT, DKP, NT><<<grid, 512, 0, s>>>(g, total);
+    return hipGetLastError();
+}
 template <int DT, int DKP>
 hipError_t scan(const GdrLaunch& g, int mode, hipStream_t s) {
-    const int total = static_cast<int>((g.a.dv + 15) / 16 * g.a.Hv * g.a.nseq), grid = 8 * ((total + 7) / 8);
-    if (mode == 0)
-        gdr_scan<DT, DKP, 1, false><<<grid, 512, 0, s>>>(g, total);
-    else if (mode == 1)
-        gdr_scan<DT, DKP, 1, true><<<grid, 512, 0, s>>>(g, total);
-    else
-        gdr_scan_back<DT, DKP, 1><<<grid, 512, 0, s>>>(g, total);
-    return hipGetLastError();
+    // Workgroups of 32 columns where those of 16 would be more than one a CU: half the operands for 1.45 times the
+    // step (tokens x 32 heads of 128 in bfloat16, forward: 4 x 2048 383 us with 16 columns, 294 with 32; 2 x 2048 180
+    // and 150).
+    if constexpr (DKP <= 128)
+        if ((g.a.dv + 15) / 16 * g.a.Hv * g.a.nseq > 256) return scan<DT, DKP, 2>(g, mode, s);
+    return scan<DT, DKP, 1>(g, mode, s);
 }
 
 template <int DT>
