@@ -25,7 +25,7 @@ namespace {
 constexpr int kLd = 68;     // row of a 64 x 64 float32 matrix in LDS
 
 template <int DT, int DKP, bool BWD>
-__global__ __launch_bounds__(256, DKP < 256 || DT == 1 ? 3 : 1) void gdr_chunk(const GdrLaunch g) {
+__global__ __launch_bounds__(256, DT == 0 && DKP == 128 ? 3 : DKP < 256 || DT == 1 ? 4 : 1) void gdr_chunk(const GdrLaunch g) {
     constexpr int NP = kParts<DT>, PP = BWD ? 3 : kOutParts<DT>, NKB = DKP / 32;
     using T = elem_t<DT>;
     // K's (or Q's) fragments, then A and the matrix that P, and after it T, are laid out in
@@ -44,32 +44,6 @@ __global__ __launch_bounds__(256, DKP < 256 || DT == 1 ? 3 : 1) void gdr_chunk(c
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = lane & 15, grp = lane >> 4;
     const int64_t sv = static_cast<int64_t>(slot) * a.Hv + hv;
 
-    if (wave == 0) {
-        double x = 0.0;
-        float be = 0.f;
-        if (lane < n) {
-            const float gt = rows_at<const float>(a.g, s, hv)[(t0 + lane) * a.g.token];
-            x = gt < -1000.f ? -1000.f : gt;
-            be = rows_at<const float>(a.beta, s, hv)[(t0 + lane) * a.beta.token];
-        }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double y = __shfl_up(x, d, 64);
-            if (lane >= d) x += y;
-        }
-        const double last = __shfl(x, 63, 64);
-        const float hi = static_cast<float>(x), lo = static_cast<float>(x - hi);
-        Gh[lane] = hi;
-        Gl[lane] = lo;
-        Be[lane] = be;
-        float* tok = g.w.tok + sv * (kTokFields * 64);
-        tok[kTokG * 64 + lane] = hi;
-        tok[kTokGlo * 64 + lane] = lo;
-        tok[kTokEg * 64 + lane] = expf(hi) * (1.f + lo);
-        tok[kTokLast * 64 + lane] = expf(static_cast<float>(last - x));
-        tok[kTokBeta * 64 + lane] = be;
-    }
-
     // This wavefront's 16 tokens of K and Q as fragments: to LDS for the others, to memory for the scans
     const bool first = hv % r == 0;
     const int64_t sk = static_cast<int64_t>(slot) * a.Hk + hk, frag = sk * (NP * 64 * DKP);
@@ -79,6 +53,12 @@ __global__ __launch_bounds__(256, DKP < 256 || DT == 1 ? 3 : 1) void gdr_chunk(c
     {
         const int ti = wave * 16 + row, at = min(ti, n - 1);
         Raw<DT> xk[NKB], xq[NKB];
+        float gt = 0.f, be = 0.f;
+        if (wave == 0) {
+            const int l = min(lane, n - 1);
+            gt = rows_at<const float>(a.g, s, hv)[(t0 + l) * a.g.token];
+            be = rows_at<const float>(a.beta, s, hv)[(t0 + l) * a.beta.token];
+        }
         auto fetch = [&](auto vec) {
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb) {
@@ -90,6 +70,27 @@ __global__ __launch_bounds__(256, DKP < 256 || DT == 1 ? 3 : 1) void gdr_chunk(c
             fetch(std::true_type{});
         else
             fetch(std::false_type{});
+        // the decays, while K and Q are on their way
+        if (wave == 0) {
+            double x = lane < n ? (gt < -1000.f ? -1000.f : gt) : 0.f;
+            be = lane < n ? be : 0.f;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const double y = __shfl_up(x, d, 64);
+                if (lane >= d) x += y;
+            }
+            const double last = __shfl(x, 63, 64);
+            const float hi = static_cast<float>(x), lo = static_cast<float>(x - hi);
+            Gh[lane] = hi;
+            Gl[lane] = lo;
+            Be[lane] = be;
+            float* tok = g.w.tok + sv * (kTokFields * 64);
+            tok[kTokG * 64 + lane] = hi;
+            tok[kTokGlo * 64 + lane] = lo;
+            tok[kTokEg * 64 + lane] = exp_of(hi) * (1.f + lo);
+            tok[kTokLast * 64 + lane] = exp_of(static_cast<float>(last - x));
+            tok[kTokBeta * 64 + lane] = be;
+        }
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb) {
             raw_frag<DT>(kf[kb], xk[kb]);
@@ -151,12 +152,17 @@ __global__ __launch_bounds__(256, DKP < 256 || DT == 1 ? 3 : 1) void gdr_chunk(c
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int i0 = wave * 16 + grp * 4, c = j * 16 + row;
+        if (j > wave) {     // above the diagonal: A is not read there
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Ts[i0 + e][c] = 0.f;
+            continue;
+        }
         const float ch = Gh[c], cl = Gl[c];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float d = c <= i0 + e ? exp_of((gh[e] - ch) + (gl[e] - cl)) : 0.f;
-            As[i0 + e][c] = c < i0 + e ? be[e] * kk[j][e] * d : 0.f;
-            Ts[i0 + e][c] = c <= i0 + e ? a.scale * qk[j][e] * d : 0.f;
+            As[i0 + e][c] = be[e] * kk[j][e] * d;
+            Ts[i0 + e][c] = a.scale * qk[j][e] * d;
         }
     }
     lds_barrier();
@@ -169,6 +175,7 @@ __global__ __launch_bounds__(256, DKP < 256 || DT == 1 ? 3 : 1) void gdr_chunk(c
         const int t = wave;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
+            if (kSkipZero<DT, DKP> && (BWD ? kb * 2 + 1 < t : kb * 2 > t)) continue;    // all zero: nothing reads it
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int m = t * 16 + row, k = kb * 32 + grp * 8 + e;
@@ -184,11 +191,14 @@ __global__ __launch_bounds__(256, DKP < 256 || DT == 1 ? 3 : 1) void gdr_chunk(c
     {
         float t[16];
         const int b = wave * 16;
+        int from = b;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
+            // A's rows are read four at a time, once the four before are nearly used: all at once are 120 registers
+            if (i % 4 == 0 && i) asm volatile("" : "+v"(from) : "v"(t[i - 2]));
             float v = i == row ? 1.f : 0.f;
 #pragma unroll
-            for (int j = 0; j < i; ++j) v = fmaf(-As[b + i][b + j], t[j], v);
+            for (int j = 0; j < i; ++j) v = fmaf(-As[from + i][b + j], t[j], v);
             t[i] = v;
         }
         // this wavefront's 16 rows of T, zero off the diagonal block until the levels below fill them
@@ -242,11 +252,13 @@ __global__ __launch_bounds__(256, DKP < 256 || DT == 1 ? 3 : 1) void gdr_chunk(c
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             const int m = wave * 16 + row, k = kb * 32 + grp * 8;
+            if (!kSkipZero<DT, DKP> || kb * 2 <= wave) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = Ts[m][k + e];
-            split8(f, v);
-            store_frag<3>(frag_at<3>(g.w.inv + sv * (3 * 4096), wave, kb, 2), f);
-            if constexpr (BWD) {
+                for (int e = 0; e < 8; ++e) v[e] = Ts[m][k + e];
+                split8(f, v);
+                store_frag<3>(frag_at<3>(g.w.inv + sv * (3 * 4096), wave, kb, 2), f);
+            }
+            if (BWD && (!kSkipZero<DT, DKP> || kb * 2 + 1 >= wave)) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = Ts[k + e][m];
                 split8(f, v);

@@ -168,6 +168,10 @@ struct Tile {
     }
 };
 
+// Whether the k blocks of the triangular 64 x 64 matrices that are all zero are left out, unwritten and unread, by loops
+// of their own for the wavefronts concerned: the registers of wide and float32 heads do not bear the second copy.
+template <int DT, int DKP> constexpr bool kSkipZero = DKP == 64 || (DT != 0 && DKP == 128);
+
 // All loads so far have landed. Before a loop whose loads cross its back edge: the compiler otherwise waits at the
 // loop's head for the order in which the loads before the loop happen to stand, every time round.
 __device__ __forceinline__ void loads_landed() { __builtin_amdgcn_s_waitcnt(0x0f70); }

@@ -165,11 +165,11 @@ struct Operands {
             for (int kb = 0; kb < 2; ++kb)
                 load_frag<NP>(f[m][kb], frag_at<NP>(from + sk(chunk) * (NP * 64 * DKP), Tiles<DKP>::first(w) + m, kb, 2));
     }
-    // a 64 x 64 matrix: this wavefront's rows
-    template <int N>
-    __device__ __forceinline__ void square(Frag<N> (&f)[2], uint16_t* from, int chunk) const {
+    // a 64 x 64 matrix: this wavefront's rows, the k blocks K0 .. K0 + KN - 1 that are not all zero
+    template <int K0, int KN, int N>
+    __device__ __forceinline__ void square(Frag<N> (&f)[KN], uint16_t* from, int chunk) const {
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) load_frag<N>(f[kb], frag_at<N>(from + sv(chunk) * (N * 4096), w.part, kb, 2));
+        for (int k = 0; k < KN; ++k) load_frag<N>(f[k], frag_at<N>(from + sv(chunk) * (N * 4096), w.part, K0 + k, 2));
     }
     __device__ __forceinline__ f32x4 token(int field, int chunk) const {
         return *reinterpret_cast<const f32x4*>(g.w.tok + (sv(chunk) * kTokFields + field) * 64 + w.part * 16 + w.grp * 4);
@@ -180,7 +180,7 @@ struct Operands {
 // How many chunks ahead operands are fetched: a step takes less than a load from memory, so two where the registers
 // hold two chunks (the scans of 2 x 4096 tokens x 16 heads in bfloat16: 160 and 223 us with one, 153 and 212 with two);
 // with wide float32 heads not even one: K^T (and Q^T) come in the middle of their own step.
-template <int DT, int DKP> constexpr int kDepth = DT == 1 && DKP <= 128 ? 2 : 1;
+template <int DT, int DKP, int NT, bool BACK> constexpr int kDepth = DT == 1 && DKP <= 128 && !(BACK && NT == 2) ? 2 : 1;
 template <int DT, int DKP, int NT> constexpr bool kLate = (DT != 1 && DKP > 128) || (DT == 0 && DKP * NT >= 256);
 // k blocks of S in registers at once
 template <int DT, int DKP, int NT> constexpr int kHalf = DT == 0 ? (DKP * NT >= 256 ? 1 : 2) : DKP == 128 ? 4 : 2;
@@ -205,7 +205,7 @@ __device__ __forceinline__ void in_turn(int chunks, F step) {
 template <int DT, int DKP, int NT, bool STORE>
 __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, PP = kOutParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
-    constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kDepth<DT, DKP>;
+    constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kDepth<DT, DKP, NT, false>;
     constexpr bool LATE = kLate<DT, DKP, NT>;
     using T = elem_t<DT>;
     __shared__ Tile<3, COLS, DKP> Sx;           // S, [column][dk]
@@ -249,11 +249,13 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
         }
     };
     // Each operand's next chunk is fetched as soon as this one's is used (the last steps fetch the last chunk again).
-    if (w.chain && chunks) {
+    // T and P are lower triangular: the first 32 tokens' rows have one k block
+    auto run_chain = [&](auto kn) {
+        constexpr int KN = decltype(kn)::value;
         const T* vr = rows_at<const T>(a.v, w.s, hv);
         struct Set {
             Frag<NP> kf[NKB], kt[MT][2];
-            Frag<3> inv[2];
+            Frag<3> inv[KN];
             Tokens4<DT> v[NT];
             f32x4 eg, last, beta;
             float whole;
@@ -268,7 +270,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
                 load4<DT>(f.v[c], vr + t0 * a.v.token + min(w.c0 + c * 16 + w.row, dv - 1), static_cast<int>(a.v.token), t4, n);
         };
         auto fetch_u = [&](Set& f, int chunk) {
-            from.square(f.inv, g.w.inv, chunk);
+            from.template square<0, KN>(f.inv, g.w.inv, chunk);
             f.last = from.token(kTokLast, chunk);
         };
         auto fetch_s = [&](Set& f, int chunk) {
@@ -308,15 +310,15 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
             f32x4 u[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                Frag<3> b[2];
-                read<2>(b, Rx, t * 16, 0);
+                Frag<3> b[KN];
+                read<KN>(b, Rx, t * 16, 0);
                 reads_first();
                 if (t == 0) {
                     if constexpr (LATE) fetch_s(f, chunk);
                     else fetch_r(f, next);
                 }
                 f32x4 y[2] = {zero, zero};
-                products<3, 2>(y, f.inv, b);
+                products<3, KN>(y, f.inv, b);
                 u[t] = y[0] + y[1];
                 Dx.put(t * 16, tok, f.last * u[t]);
             }
@@ -337,12 +339,13 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
             else if constexpr (DEPTH == 1) fetch_s(f, next);
         });
         if constexpr (!STORE) lds_barrier();    // the last chunk's U
-    }
-    if (!w.chain && chunks) {
+    };
+    auto run_outputs = [&](auto kn) {
+        constexpr int KN = decltype(kn)::value;
         T* orow = STORE ? nullptr : rows_at<T>(a.o, w.s, hv);
         struct Set {
             Frag<NP> qf[STORE ? 1 : NKB], kt[MT][2];
-            Frag<PP> pm[2];
+            Frag<PP> pm[KN];
             f32x4 eg;
             float whole;
         } set[DEPTH];
@@ -352,11 +355,11 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
             const int t0 = chunk * kChunk, n = min(kChunk, w.s.len - t0);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                Frag<PP> b[2];
-                read<2>(b, Ux[STORE ? 0 : chunk & 1], t * 16, 0);
+                Frag<PP> b[KN];
+                read<KN>(b, Ux[STORE ? 0 : chunk & 1], t * 16, 0);
                 reads_first();
                 f32x4 y[2] = {o[t], zero};
-                products<PP, 2>(y, pm, b);
+                products<PP, KN>(y, pm, b);
                 y[0] += y[1];
                 if (w.c0 + t * 16 + w.row < dv)
                     put4(orow + t0 * a.o.token + w.c0 + t * 16 + w.row, static_cast<int>(a.o.token), t4, n, y[0]);
@@ -375,7 +378,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i) {
             fetch_q(set[i], min(i, chunks - 1));
-            if constexpr (!STORE) from.square(set[i].pm, g.w.pm, min(i, chunks - 1));
+            if constexpr (!STORE) from.template square<0, KN>(set[i].pm, g.w.pm, min(i, chunks - 1));
             if constexpr (!LATE) fetch_s(set[i], min(i, chunks - 1));
         }
         loads_landed();
@@ -387,7 +390,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
             if constexpr (!STORE) {
                 if (chunk) {
                     finish(chunk - 1, before.pm);
-                    from.square(before.pm, g.w.pm, min(chunk + DEPTH - 1, chunks - 1));
+                    from.template square<0, KN>(before.pm, g.w.pm, min(chunk + DEPTH - 1, chunks - 1));
                 }
             }
             lds_barrier();
@@ -420,6 +423,19 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
             else
                 finish(last, set[DEPTH - 1].pm);
         }
+    };
+    using One = std::integral_constant<int, kSkipZero<DT, DKP> ? 1 : 2>;
+    using Two = std::integral_constant<int, 2>;
+    if (chunks) {
+        const bool one = kSkipZero<DT, DKP> && w.part < 2;
+        if (w.chain && one)
+            run_chain(One{});
+        else if (w.chain)
+            run_chain(Two{});
+        else if (one)
+            run_outputs(One{});
+        else
+            run_outputs(Two{});
     }
     if constexpr (!STORE)
         if (a.s_final && Tiles<DKP>::owner(w)) store_state<DKP, NT>(S, w, a.s_final + w.head * w.dk * dv, dv);
@@ -428,7 +444,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
 template <int DT, int DKP, int NT>
 __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
-    constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kDepth<DT, DKP>;
+    constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kDepth<DT, DKP, NT, true>;
     constexpr bool LATE = kLate<DT, DKP, NT>;
     using T = elem_t<DT>;
     __shared__ Tile<3, COLS, DKP> Sx;           // dS, [column][dk]
@@ -474,11 +490,13 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
         }
     };
     const auto back = [&](int i) { return max(top - i, 0); };       // the i-th chunk from the end
-    if (w.chain && top >= 0) {
+    // T^T and P^T are upper triangular: the last 32 tokens' rows have one k block
+    auto run_chain = [&](auto kn) {
+        constexpr int KN = decltype(kn)::value, K0 = 2 - KN;
         T* dvr = rows_at<T>(a.d_v, w.s, hv);
         struct Set {
             Frag<NP> kf[NKB], kt[MT][2], qt[MT][2];
-            Frag<3> inv[2];
+            Frag<3> inv[KN];
             f32x4 eg, last, beta;
             float whole;
         } set[DEPTH];
@@ -487,7 +505,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
             f.last = from.token(kTokLast, chunk);
         };
         auto fetch_r = [&](Set& f, int chunk) {
-            from.square(f.inv, g.w.invt, chunk);
+            from.template square<K0, KN>(f.inv, g.w.invt, chunk);
         };
         auto fetch_s = [&](Set& f, int chunk) {
             from.template cols<true>(f.kt, g.w.kt, chunk);
@@ -533,15 +551,15 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
             f32x4 d[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                Frag<3> b[2];
-                read<2>(b, Ux, t * 16, 0);
+                Frag<3> b[KN];
+                read<KN>(b, Ux, t * 16, K0 * 32);
                 reads_first();
                 if (t == 0) {
                     if constexpr (LATE) fetch_s(f, chunk);
                     else fetch_u(f, next);
                 }
                 f32x4 y[2] = {zero, zero};
-                products<3, 2>(y, f.inv, b);
+                products<3, KN>(y, f.inv, b);
                 d[t] = y[0] + y[1];
                 Rx.put(t * 16, tok, -(f.beta * f.eg) * d[t]);
             }
@@ -562,12 +580,13 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
             if constexpr (LATE) fetch_u(f, next);
             else if constexpr (DEPTH == 1) fetch_s(f, next);
         });
-    }
-    if (!w.chain && top >= 0) {
+    };
+    auto run_outputs = [&](auto kn) {
+        constexpr int KN = decltype(kn)::value, K0 = 2 - KN;
         const T* dor = rows_at<const T>(a.d_o, w.s, hv);
         struct Set {
             Frag<NP> kt[MT][2], qt[MT][2];
-            Frag<3> pm[2];                  // P^T of the next chunk
+            Frag<3> pm[KN];                 // P^T of the next chunk
             Tokens4<DT> raw[NT];            // dO of the next chunk
             f32x4 eg;
             float whole;
@@ -587,15 +606,15 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
         auto p_do = [&](const Frag<3>* pm) {    // P^T dO of the chunk in Ox, for the chain's next step
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                Frag<3> b[2];
-                read<2>(b, Ox, t * 16, 0);
+                Frag<3> b[KN];
+                read<KN>(b, Ox, t * 16, K0 * 32);
                 reads_first();
                 f32x4 y[2] = {zero, zero};
-                products<3, 2>(y, pm, b);
+                products<3, KN>(y, pm, b);
                 Wx[t][w.part][w.lane] = y[0] + y[1];
             }
         };
-        from.square(set[0].pm, g.w.pm, top);
+        from.template square<K0, KN>(set[0].pm, g.w.pm, top);
         fetch_do(set[0], top);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -606,7 +625,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
         p_do(set[0].pm);
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i) {
-            from.square(set[i].pm, g.w.pm, back(i + 1));
+            from.template square<K0, KN>(set[i].pm, g.w.pm, back(i + 1));
             fetch_do(set[i], back(i + 1));
             set[i].eg = from.token(kTokEg, back(i));
             if constexpr (!LATE) fetch_s(set[i], back(i));
@@ -628,11 +647,24 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
             lds_barrier();
             if constexpr (LATE) fetch_s(f, chunk);
             p_do(f.pm);
-            from.square(f.pm, g.w.pm, back(i + 1 + DEPTH));
+            from.template square<K0, KN>(f.pm, g.w.pm, back(i + 1 + DEPTH));
             lds_barrier();
             update(f.qt, f.kt, f.whole, std::false_type{}, [] {});
             if constexpr (!LATE) fetch_s(f, back(i + DEPTH));
         });
+    };
+    using One = std::integral_constant<int, kSkipZero<DT, DKP> ? 1 : 2>;
+    using Two = std::integral_constant<int, 2>;
+    if (top >= 0) {
+        const bool one = kSkipZero<DT, DKP> && w.part >= 2;
+        if (w.chain && one)
+            run_chain(One{});
+        else if (w.chain)
+            run_chain(Two{});
+        else if (one)
+            run_outputs(One{});
+        else
+            run_outputs(Two{});
     }
     if (a.ds0 && Tiles<DKP>::owner(w)) store_state<DKP, NT>(S, w, a.ds0 + w.head * w.dk * dv, dv);
 }
