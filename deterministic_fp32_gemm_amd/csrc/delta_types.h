@@ -25,13 +25,13 @@ template <int DT>
 struct Raw {
     u32x4 w[DT == 0 ? 2 : 1];
 };
-// From column c, zero past `lim`; only columns < lim are read.
-template <int DT>
+// From column c, zero past `lim`; only columns < lim are read. STREAM: the caches need not keep what is read.
+template <int DT, bool STREAM = false>
 __device__ __forceinline__ void load_row(Raw<DT>& o, const elem_t<DT>* __restrict__ row, int c, int lim) {
     if (c + 8 <= lim) {
         const u32x4u* p = reinterpret_cast<const u32x4u*>(row + c);
-        o.w[0] = p[0];
-        if constexpr (DT == 0) o.w[1] = p[1];
+        o.w[0] = STREAM ? __builtin_nontemporal_load(p) : p[0];
+        if constexpr (DT == 0) o.w[1] = STREAM ? __builtin_nontemporal_load(p + 1) : p[1];
         return;
     }
     // the row's end: eight single loads, all in flight together, from inside the row
@@ -59,10 +59,10 @@ __device__ __forceinline__ void raw_floats(float (&f)[8], const Raw<DT>& r) {
         for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(a[i]);
     }
 }
-template <int DT>
+template <int DT, bool STREAM = false>
 __device__ __forceinline__ void load8(float (&f)[8], const elem_t<DT>* __restrict__ row, int c, int lim) {
     Raw<DT> r;
-    load_row<DT>(r, row, c, lim);
+    load_row<DT, STREAM>(r, row, c, lim);
     raw_floats<DT>(f, r);
 }
 

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(256) void gdr_step(const sdm_gdr_step_args_t a, con
         if (d < dk) {
             const float* p = st + static_cast<int64_t>(d) * dv + c;
             if (vec) {
-                if (c < dv) S[i] = *reinterpret_cast<const f32x4*>(p);
+                if (c < dv) S[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(256) void gdr_step(const sdm_gdr_step_args_t a, con
         if (d >= dk) continue;
         float* p = st + static_cast<int64_t>(d) * dv + c;
         if (vec) {
-            if (c < dv) *reinterpret_cast<f32x4*>(p) = S[i];
+            if (c < dv) __builtin_nontemporal_store(S[i], reinterpret_cast<f32x4*>(p));
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)

@@ -15,6 +15,9 @@
 namespace sdm_delta {
 namespace {
 
+// Rows are read once: past the caches (16384 x 4096 rows, inputs in turn: forward 169 -> 159 us).
+constexpr bool kStream = true;
+
 // The sum of v over the workgroup, in an order set by the lane and wavefront numbers alone. `buf` alternates between
 // two LDS rows: a row is written again only after a barrier that follows its last read.
 template <int NT>
@@ -72,10 +75,10 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
-            if (has_o) load8<DT>(o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D);
-            if (a.act != SDM_ACT_NONE) load8<DT>(z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D);
+            if (has_o) load8<DT, kStream>(o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D);
+            if (a.act != SDM_ACT_NONE) load8<DT, kStream>(z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D);
             if (has_x) {
-                load8<DT>(x[v], static_cast<const T*>(a.x) + r * a.ld_x, c, D);
+                load8<DT, kStream>(x[v], static_cast<const T*>(a.x) + r * a.ld_x, c, D);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[v][i] = 0.f;
@@ -148,10 +151,10 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
         for (int v = 0; v < NV; ++v) {
             const int c = (v * NT + id) * 8;
             if (has_y) {
-                load_row<DT>(in.y[v], static_cast<const T*>(a.dy) + r * a.ld_dy, c, D);
-                load_row<DT>(in.xn[v], static_cast<const T*>(a.x_new) + r * a.ld_xn, c, D);
+                load_row<DT, kStream>(in.y[v], static_cast<const T*>(a.dy) + r * a.ld_dy, c, D);
+                load_row<DT, kStream>(in.xn[v], static_cast<const T*>(a.x_new) + r * a.ld_xn, c, D);
             }
-            if (has_up) load_row<DT>(in.dx[v], static_cast<const T*>(a.dxn) + r * a.ld_dxn, c, D);
+            if (has_up) load_row<DT, kStream>(in.dx[v], static_cast<const T*>(a.dxn) + r * a.ld_dxn, c, D);
         }
         in.r1 = a.rstd[2 * r];
         in.r2 = a.rstd[2 * r + 1];
@@ -160,8 +163,8 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * NT + id) * 8;
-            if (has_o) load_row<DT>(in.o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D);
-            if (has_z) load_row<DT>(in.z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D);
+            if (has_o) load_row<DT, kStream>(in.o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D);
+            if (has_z) load_row<DT, kStream>(in.z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D);
         }
     };
     constexpr bool AHEAD = NV == 1;     // registers hold the next row beside this one
