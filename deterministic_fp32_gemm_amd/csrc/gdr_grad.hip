@@ -40,7 +40,7 @@ __device__ __forceinline__ float row_sum16(float x) {
 __device__ __forceinline__ constexpr int token_of(int j, int r) { return 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3); }
 
 template <int DT, int DKP>
-__global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
+__global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g, const int heads) {
     constexpr int NP = kParts<DT>;
     constexpr int MT = 1, PASSES = DKP == 256 ? 2 : 1;  // dk tiles of a wavefront at a time; times
     constexpr int NJ = DKP >= 128 ? 4 : 2;              // its token tiles
@@ -62,16 +62,32 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
     const sdm_gdr_args_t& a = g.a;
     int seq, chunk;
     Seq s;
-    const int slot = blockIdx.x, hv = blockIdx.y, rr = static_cast<int>(a.Hv / a.Hk), hk = hv / rr;
+    const int slot = blockIdx.x, rr = static_cast<int>(a.Hv / a.Hk), hk = blockIdx.y * heads / rr;
     if (!owner(a, slot, seq, chunk, s)) return;
     const int t0 = chunk * kChunk, n = min(kChunk, s.len - t0);
     const int dk = static_cast<int>(a.dk), dv = static_cast<int>(a.dv);
-    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j0 = DKP >= 128 ? 0 : (wave >> 2) * 2;
-    const int64_t sv = static_cast<int64_t>(slot) * a.Hv + hv, sk = static_cast<int64_t>(slot) * a.Hk + hk;
+    const int64_t sk = static_cast<int64_t>(slot) * a.Hk + hk;
     const int dvp = g.dvp;
-
+    const uint16_t* kt = g.w.kt + sk * (NP * 64 * DKP);
+    const uint16_t* qt = g.w.qt + sk * (NP * 64 * DKP);
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    // the value heads of this workgroup: all that share the q/k head, whose dq and dk are summed here, or one of them
+    constexpr bool SUM = PASSES == 1;
+    f32x4 sq[SUM ? NJ : 1], sk4[SUM ? NJ : 1];
+#pragma unroll
+    for (int j = 0; j < (SUM ? NJ : 1); ++j) sq[j] = sk4[j] = zero;
+#pragma unroll 1
+    for (int h = 0; h < heads; ++h) {
+    const int hv = blockIdx.y * heads + h;
+    const int64_t sv = static_cast<int64_t>(slot) * a.Hv + hv;
+    // not the same for every head (and pass) as far as the compiler knows: it would keep every address of one across the
+    // loop, in scratch memory
+    int id = threadIdx.x;
+    asm volatile("" : "+v"(id));
+    const int lane = id & 63;
+    if (h) lds_barrier();
     if (threadIdx.x < 64) {
         const float* t = g.w.tok + sv * (kTokFields * 64) + threadIdx.x;
         Gh[threadIdx.x] = t[kTokG * 64];
@@ -86,17 +102,12 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
     const float* rp = g.w.dr + sv * 64 * dvp;
     const float* st = g.w.st + sv * dk * dvp;
     const float* de = g.w.dst + sv * dk * dvp;
-    const uint16_t* kt = g.w.kt + sk * (NP * 64 * DKP);
-    const uint16_t* qt = g.w.qt + sk * (NP * 64 * DKP);
 
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int pass = 0; pass < PASSES; ++pass) {     // more than 128 columns of dk: the second half after the first
     const int tile0 = DKP >= 128 ? pass * 8 + wave : wave & 3;
     if (pass) lds_barrier();
     int row = lane & 15, grp = lane >> 4;
-    // not the same in every pass as far as the compiler knows: it would keep every address of a pass across the loop,
-    // in scratch memory
     if constexpr (PASSES > 1) asm volatile("" : "+v"(row), "+v"(grp));
     f32x4 dpa[4], aq[MT][NJ], ar[MT][NJ], as[MT][NJ];       // dpa: a row tile of dP (wavefronts 0 .. 3) or of dA
 #pragma unroll
@@ -107,7 +118,7 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
         for (int m = 0; m < MT; ++m) aq[m][j] = ar[m][j] = as[m][j] = zero;
     float rv = 0.f, sde = 0.f;
     // staging: this thread's row and its token, 8 columns
-    const int si = threadIdx.x >> 3, sc = (threadIdx.x & 7) * 8, stok = token_of(si >> 4, si & 15);
+    const int si = id >> 3, sc = (id & 7) * 8, stok = token_of(si >> 4, si & 15);
     struct {
         Raw<DT> o, v;
         Raw<0> u, r;
@@ -210,7 +221,7 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
     }
 #pragma unroll
     for (int m = 1; m < 8; m <<= 1) rv += __shfl_xor(rv, m, 64);
-    if ((threadIdx.x & 7) == 0) Rv[stok] = rv;
+    if ((id & 7) == 0) Rv[stok] = rv;
     if (DKP < 128 && wave >= 4) sde = 0.f;      // wavefronts 0 .. 3 have summed the same
 
     Frag<NP> fk[MT][2], fq[MT][2];
@@ -297,7 +308,7 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
         }
 
     // write dq and dk; the row sums of dG and dbeta
-    const bool parts = rr > 1;
+    const bool parts = rr > heads, write = h + 1 == heads;
     T* dqr = rows_at<T>(a.d_q, s, hk) + t0 * a.d_q.token;
     T* dkr = rows_at<T>(a.d_k, s, hk) + t0 * a.d_k.token;
 #pragma unroll
@@ -310,23 +321,28 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
             const int d = (tile0 + m) * 16 + row;
             const Frag<NP>& k8 = NJ == 4 || j0 == 0 ? fk[m][NJ == 4 ? j >> 1 : 0] : fk[m][1];
             const Frag<NP>& q8 = NJ == 4 || j0 == 0 ? fq[m][NJ == 4 ? j >> 1 : 0] : fq[m][1];
-            const f32x4 own = be * ar[m][j], dkv = own + as[m][j];
+            const f32x4 own = be * ar[m][j];
+            f32x4 dqv = aq[m][j], dkv = own + as[m][j];
+            if constexpr (SUM) {
+                dqv = sq[j] += dqv;
+                dkv = sk4[j] += dkv;
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float q = value(q8, 4 * (j & 1) + e), k = value(k8, 4 * (j & 1) + e);
                 dG[e] = fmaf(q, aq[m][j][e], fmaf(k, own[e] - as[m][j][e], dG[e]));
                 dB[e] = fmaf(k, ar[m][j][e], dB[e]);
             }
-            if (d < dk) {
+            if (d < dk && write) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = i0 + e;
                     if (i >= n) continue;
                     if (parts) {
-                        g.w.dqp[(sv * 64 + i) * dk + d] = aq[m][j][e];
+                        g.w.dqp[(sv * 64 + i) * dk + d] = dqv[e];
                         g.w.dkp[(sv * 64 + i) * dk + d] = dkv[e];
                     } else {
-                        dqr[i * a.d_q.token + d] = static_cast<T>(aq[m][j][e]);
+                        dqr[i * a.d_q.token + d] = static_cast<T>(dqv[e]);
                         dkr[i * a.d_k.token + d] = static_cast<T>(dkv[e]);
                     }
                 }
@@ -377,6 +393,7 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g) {
             rows_at<float>(a.d_beta, s, hv)[(t0 + lane) * a.d_beta.token] = db;
         }
     }
+    }
 }
 
 // dq and dk of shared q/k heads: the value heads' parts, added in head order.
@@ -403,14 +420,19 @@ __global__ __launch_bounds__(256) void gdr_shared(const GdrLaunch g) {
 
 template <int DT>
 hipError_t run(const GdrLaunch& g, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(g.slots), static_cast<unsigned>(g.a.Hv));
+    // One workgroup for all value heads of a q/k head saves their parts of dq and dk a way through memory and a kernel;
+    // few chunks go by one head each, for time (chunks x q/k heads, two value heads each, 128 wide in bfloat16, the whole
+    // gradient: 32: 126 us together, 102 apart; 128: 118 both; 256: 174 and 196; 1024: 586 and 650).
+    const int rr = static_cast<int>(g.a.Hv / g.a.Hk);
+    const int heads = g.dkp <= 128 && static_cast<int64_t>(g.slots) * g.a.Hk >= 256 ? rr : 1;
+    const dim3 grid(static_cast<unsigned>(g.slots), static_cast<unsigned>(g.a.Hv / heads));
     if (g.dkp == 64)
-        gdr_grad<DT, 64><<<grid, 512, 0, s>>>(g);
+        gdr_grad<DT, 64><<<grid, 512, 0, s>>>(g, heads);
     else if (g.dkp == 128)
-        gdr_grad<DT, 128><<<grid, 512, 0, s>>>(g);
+        gdr_grad<DT, 128><<<grid, 512, 0, s>>>(g, heads);
     else
-        gdr_grad<DT, 256><<<grid, 512, 0, s>>>(g);
-    if (g.a.Hv != g.a.Hk) {
+        gdr_grad<DT, 256><<<grid, 512, 0, s>>>(g, heads);
+    if (heads != rr) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         gdr_shared<DT><<<dim3(grid.x, static_cast<unsigned>(g.a.Hk), 2), 256, 0, s>>>(g);

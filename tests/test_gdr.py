@@ -101,6 +101,24 @@ def test_backward(shape, ty):
     check_backward(make(*shape, TYPES[ty]), TYPES[ty], shape[4] ** -0.5)
 
 
+@pytest.mark.parametrize("ty", TYPES)
+@pytest.mark.parametrize("shape", [(9, 70, 4, 8, 64, 64), (9, 66, 2, 4, 128, 116)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_many_heads(shape, ty):
+    """More than 256 slices of 16 state columns: the scans take 32 columns a workgroup."""
+    print("many heads", shape, ty, flush=True)
+    d = make(*shape, TYPES[ty])
+    check_forward(d, TYPES[ty], shape[4] ** -0.5)
+    check_backward(d, TYPES[ty], shape[4] ** -0.5)
+
+
+@pytest.mark.parametrize("ty,dk", [("f32", 24), ("bf16", 72), ("f16", 64)])
+def test_shared_heads_of_many_chunks(ty, dk):
+    """256 chunks and key heads: one workgroup sums dq and dk over the value heads of a key head."""
+    d = make(16, 60, 16, 48, dk, 16, TYPES[ty])
+    check_backward(d, TYPES[ty], dk ** -0.5)
+
+
 def test_packed_sequences():
     """Runs of every awkward length in one row, empty ones first, last and between; the tokens of none get zeros."""
     lens = [0, 1, 64, 0, 63, 65, 130, 2, 0]
