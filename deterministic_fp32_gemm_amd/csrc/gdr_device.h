@@ -188,7 +188,6 @@ __device__ __forceinline__ float exp_of(float x) {
 
 // One sequence: its first token, length and first chunk slot.
 struct Seq {
-    int64_t base;       // of its row's first token: strides.batch * b is added by rows_at
     int32_t b, start, len, slot;
 };
 __device__ __forceinline__ Seq sequence(const sdm_gdr_args_t& a, int i) {
@@ -206,7 +205,6 @@ __device__ __forceinline__ Seq sequence(const sdm_gdr_args_t& a, int i) {
         s.len = static_cast<int>(a.T);
         s.slot = i * ((s.len + kChunk - 1) / kChunk);
     }
-    s.base = 0;
     return s;
 }
 // The sequence that owns a chunk slot and the chunk's number in it; false for a slot that none uses.

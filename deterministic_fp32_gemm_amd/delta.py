@@ -3,8 +3,8 @@
 The functions take and return tensors on the current GPU: they allocate outputs and workspaces with torch's allocator,
 check types and shapes, and call the C ABI of libsdm_delta on torch's current stream (or ``stream``). Every arithmetic
 step runs in the library's HIP kernels; there is no other path. A wrong argument raises TypeError or ValueError before
-anything runs. Tensors used on a stream other than the one they were made on are the caller's to keep alive, as with
-any torch operation called under that stream.
+anything runs. A call with ``stream`` is the call under ``torch.cuda.stream(stream)``: what it allocates is that
+stream's, and tensors made on another stream are the caller's to order and keep alive, as for any torch operation.
 """
 
 from __future__ import annotations
@@ -160,11 +160,23 @@ def _find_raw_stream():
 _raw_stream = None
 
 
-def _stream(stream, device) -> int:
-    if stream is None:
+def _stream(device) -> int:
+    """The handle of torch's current stream on the device."""
+    if _raw_stream is None:
         import torch
-        return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device.index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
+
+
+def _under(stream, device):
+    """Makes the stream a call names (a torch stream or a handle) the current one: its outputs, copies and workspace
+    then come from that stream's memory, so none of them is given to another stream while the call's kernels run."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"stream: one of {device} required, got one of {stream.device}")
+    return torch.cuda.stream(stream)
 
 
 class _Plans(threading.local):
@@ -307,12 +319,17 @@ def gdr_forward(q, k, v, g, beta, *, scale=None, initial_state=None, final_state
     sequence get zeros. Any strides; a last axis that is not contiguous is copied first.
     """
     import torch
+    scale = None if scale is None else float(scale)       # a value, also where a tensor holds it
     key = ("fwd", _layout(q), _layout(k), _layout(v), _layout(g), _layout(beta), _layout(initial_state),
            _layout(cu_seqlens), scale)
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _gdr_plan(False, q, k, v, g, beta, scale, initial_state, cu_seqlens, None, None))
     a, n, state, dev, _ = plan
+    if stream is not None:
+        with _under(stream, dev):
+            return gdr_forward(q, k, v, g, beta, scale=scale, initial_state=initial_state, final_state=final_state,
+                               cu_seqlens=cu_seqlens)
     o = (torch.empty if cu_seqlens is None else torch.zeros)(v.shape, dtype=v.dtype, device=dev)
     s = torch.empty(state, dtype=torch.float32, device=dev) if final_state else None
     if not n:
@@ -323,7 +340,7 @@ def gdr_forward(q, k, v, g, beta, *, scale=None, initial_state=None, final_state
     ws = _workspace(n, dev)
     a.o.data, a.s_final = o.data_ptr(), 0 if s is None else s.data_ptr()
     with _OnDevice(dev):
-        status = load().sdm_gdr_forward(ctypes.byref(a), ws.data_ptr(), n, _stream(stream, dev))
+        status = load().sdm_gdr_forward(ctypes.byref(a), ws.data_ptr(), n, _stream(dev))
     del keep
     if status:
         _raise(status, "gdr_forward")
@@ -336,12 +353,17 @@ def gdr_backward(q, k, v, g, beta, do, *, scale=None, initial_state=None, dfinal
     dfinal_state, that of the last state (None: zero). It recomputes the forward's states and needs nothing saved but
     the inputs. Gradients have their tensors' shapes and types; tokens of no sequence get zeros."""
     import torch
+    scale = None if scale is None else float(scale)       # a value, also where a tensor holds it
     key = ("bwd", _layout(q), _layout(k), _layout(v), _layout(g), _layout(beta), _layout(initial_state),
            _layout(cu_seqlens), _layout(do), _layout(dfinal_state), scale)
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _gdr_plan(True, q, k, v, g, beta, scale, initial_state, cu_seqlens, do, dfinal_state))
     a, n, state, dev, copied = plan
+    if stream is not None:
+        with _under(stream, dev):
+            return gdr_backward(q, k, v, g, beta, do, scale=scale, initial_state=initial_state,
+                                dfinal_state=dfinal_state, cu_seqlens=cu_seqlens)
     make = torch.empty if cu_seqlens is None else torch.zeros
     outs = [make(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v, g, beta)]
     s = torch.empty(state, dtype=torch.float32, device=dev)
@@ -356,7 +378,7 @@ def gdr_backward(q, k, v, g, beta, do, *, scale=None, initial_state=None, dfinal
     a.d_q.data, a.d_k.data, a.d_v.data, a.d_g.data, a.d_beta.data = (t.data_ptr() for t in outs)
     ws = _workspace(n, dev)
     with _OnDevice(dev):
-        status = load().sdm_gdr_backward(ctypes.byref(a), ws.data_ptr(), n, _stream(stream, dev))
+        status = load().sdm_gdr_backward(ctypes.byref(a), ws.data_ptr(), n, _stream(dev))
     del keep
     if status:
         _raise(status, "gdr_backward")
@@ -370,12 +392,16 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, out=None, strea
     own number); a stream whose slot is not in the pool, such as -1, is idle: zeros in o, no state touched. No two
     streams may name one slot. The other tensors as in gdr_forward."""
     import torch
+    scale = None if scale is None else float(scale)       # a value, also where a tensor holds it
     key = ("step", _layout(q), _layout(k), _layout(v), _layout(g), _layout(beta), _layout(state), _layout(slots),
            _layout(out), scale)
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _step_plan(q, k, v, g, beta, state, slots, scale, out))
     a, shape, dtype, dev, copied = plan
+    if stream is not None:
+        with _under(stream, dev):
+            return gdr_step(q, k, v, g, beta, state, slots=slots, scale=scale, out=out)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=dev)
     if a is None:
@@ -388,7 +414,7 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, out=None, strea
     if slots is not None:
         a.slots = slots.data_ptr()
     with _OnDevice(dev):
-        status = load().sdm_gdr_step(ctypes.byref(a), _stream(stream, dev))
+        status = load().sdm_gdr_step(ctypes.byref(a), _stream(dev))
     if status:
         _raise(status, "gdr_step")
     return out
@@ -507,11 +533,15 @@ def norm_forward(x, o, z, w_post, w_pre, scale, *, act="silu", eps=1e-6, stream=
     w_post, w_pre, scale [D] in that type or float32. x None: no residual. w_pre None: y is None. o None (with z,
     w_post and scale): y = rms_norm(x) w_pre alone, and x_new is x. act: "none" (z None), "sigmoid" or "silu"."""
     import torch
+    eps = float(eps)
     key = ("norm", _layout(x), _layout(o), _layout(z), _layout(w_post), _layout(w_pre), _layout(scale), act, eps)
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _norm_plan(False, x, o, z, w_post, w_pre, scale, act, eps))
     a, _, rows, D, dev, _, copied, shape, dtype = plan
+    if stream is not None:
+        with _under(stream, dev):
+            return norm_forward(x, o, z, w_post, w_pre, scale, act=act, eps=eps)
     x_new = x if o is None else torch.empty(shape, dtype=dtype, device=dev)
     y = None if w_pre is None else torch.empty(shape, dtype=dtype, device=dev)
     rstd = torch.empty((rows, 2), dtype=torch.float32, device=dev)
@@ -524,7 +554,7 @@ def norm_forward(x, o, z, w_post, w_pre, scale, *, act="silu", eps=1e-6, stream=
     a.w_post, a.w_pre, a.scale = _ptr(w_post), _ptr(w_pre), _ptr(scale)
     a.x_new, a.y = 0 if o is None else x_new.data_ptr(), _ptr(y)
     with _OnDevice(dev):
-        status = load().sdm_nrm_forward(ctypes.byref(a), _stream(stream, dev))
+        status = load().sdm_nrm_forward(ctypes.byref(a), _stream(dev))
     if status:
         _raise(status, "norm_forward")
     return x_new, y, rstd
@@ -541,6 +571,9 @@ def norm_backward(dx_new, dy, x_new, o, z, w_post, w_pre, scale, rstd, *, act="s
     if plan is None:
         plan = _plans.put(key, _norm_plan(True, dx_new, o, z, w_post, w_pre, scale, act, 0.0, dy, x_new, rstd))
     a, n, rows, D, dev, wd, copied, shape, dtype = plan
+    if stream is not None:
+        with _under(stream, dev):
+            return norm_backward(dx_new, dy, x_new, o, z, w_post, w_pre, scale, rstd, act=act)
     dx = torch.empty(shape, dtype=dtype, device=dev)
     do = None if o is None else torch.empty(shape, dtype=dtype, device=dev)
     dz = None if z is None else torch.empty(shape, dtype=dtype, device=dev)
@@ -560,7 +593,7 @@ def norm_backward(dx_new, dy, x_new, o, z, w_post, w_pre, scale, rstd, *, act="s
     a.dw_post, a.dw_pre, a.dscale = _ptr(dw_post), _ptr(dw_pre), _ptr(dscale)
     ws = _workspace(n, dev)
     with _OnDevice(dev):
-        status = load().sdm_nrm_backward(ctypes.byref(a), ws.data_ptr(), n, _stream(stream, dev))
+        status = load().sdm_nrm_backward(ctypes.byref(a), ws.data_ptr(), n, _stream(dev))
     if status:
         _raise(status, "norm_backward")
     return dx, do, dz, dw_post, dw_pre, dscale

@@ -19,10 +19,10 @@
  *
  * Memory. sdm_rows_t: element (b, t, h, c) is data[b*batch + t*token + h*head + c], strides in elements; g and beta
  * have no c. Token and head strides below 2^31, any element
- * alignment; 16-byte rows are faster. The states are contiguous
- * [sequences][Hv][dk][dv]. Outputs must not overlap inputs or each other. Workspaces are the caller's
- * (sdm_gdr_workspace bytes, 256-byte aligned, contents free to lose after the call). Calls are asynchronous on `stream`, allocate nothing
- * and may be captured into a graph.
+ * alignment; dk and dv that are multiples of 8 are faster. The states are contiguous [sequences][Hv][dk][dv]. Outputs
+ * must not overlap inputs or each other. Workspaces are the caller's (sdm_gdr_workspace bytes, 256-byte aligned,
+ * contents free to lose after the call). Calls are asynchronous on `stream`, allocate nothing and may be captured into
+ * a graph.
  */
 #ifndef SDM_GDR_H
 #define SDM_GDR_H

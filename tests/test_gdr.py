@@ -341,3 +341,35 @@ def test_step_wide_offsets():
     near(o.cpu(), wo, dk + 8, "o")
     near(state[-1:].cpu(), ws, dk + 8, "state")
     assert not state[0].any() and not state[-2].any()
+
+
+def test_stream_argument():
+    """A call on a named stream that waits behind other work, while the current stream allocates and writes."""
+    import deterministic_fp32_gemm_amd as g
+    d = dev(make(2, 300, 2, 6, 128, 128, torch.bfloat16))
+    x = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    o, s = g.gdr_forward(*x, initial_state=d["s0"])
+    want = [o, s, *g.gdr_backward(*x, d["do"], initial_state=d["s0"])]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = [*g.gdr_forward(*x, initial_state=d["s0"], stream=stream),
+               *g.gdr_backward(*x, d["do"], initial_state=d["s0"], stream=stream)]
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (2 ** 20, 2 ** 22, 2 ** 24, 2 ** 25) * 3]
+        torch.cuda.synchronize()
+        del junk
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_scale_is_a_value():
+    """A scale held by a tensor is read at every call."""
+    import deterministic_fp32_gemm_amd as g
+    d = dev(make(1, 30, 1, 1, 32, 32, torch.float32))
+    x = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    scale = torch.tensor(0.5)
+    one = g.gdr_forward(*x, scale=scale)[0]
+    scale.fill_(1.0)
+    assert torch.equal(g.gdr_forward(*x, scale=scale)[0], 2 * one)
