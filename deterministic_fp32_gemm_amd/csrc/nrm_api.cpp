@@ -101,10 +101,11 @@ int check(const sdm_nrm_args_t* a, bool backward) {
 
 NrmPlan plan(const sdm_nrm_args_t* a, bool backward) {
     NrmPlan p{};
-    // 16384 rows of 4096 in bfloat16: forward 136 us with 256 threads of two groups of columns, 151 with 512 of one;
-    // backward, which holds two sums a column beside, 215 with 512 of one, 340 with 256 of two
+    // 16384 rows of 4096: forward 109 us in bfloat16 and 256 in float32 with 256 threads of two groups of columns, 113
+    // and 250 with 512 of one; backward in bfloat16, which holds two sums a column beside, 340 with 256 of two, 215 with
+    // 512 of one
     const bool middle = a->D > 2048 && a->D <= 4096;
-    p.threads = a->D <= 512 ? 64 : a->D <= 2048 || (middle && !backward) ? 256 : 512;
+    p.threads = a->D <= 512 ? 64 : a->D <= 1024 ? 128 : a->D <= 2048 || (middle && !backward) ? 256 : 512;
     p.vecs = static_cast<int>(cdiv(a->D, p.threads * 8));
     // forward: workgroups for 8 wavefronts a SIMD; backward: each leaves a partial sum, so a quarter of that
     const int64_t most = (backward ? 2048 : 8192) / (p.threads / 64);

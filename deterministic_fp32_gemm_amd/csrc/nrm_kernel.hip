@@ -4,8 +4,8 @@
 // What bounds them is memory: the forward reads x, o, z and writes x', y, the backward reads dx', dy, x', o, z and
 // writes dx, do, dz, each once. A row lives in the registers of one workgroup from its load to its store, so the two
 // norms of a row, which depend on each other, cost two workgroup reductions and no second pass. Workgroups take many
-// rows each: the weights stay in registers, and in the backward so do their gradients' sums, which leave once per
-// workgroup as partial sums that a second kernel adds in workgroup order.
+// rows each: the weights stay in registers (in LDS in the backward), and in the backward so do their gradients' sums,
+// which leave once per workgroup as partial sums that a second kernel adds in workgroup order.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -15,7 +15,8 @@
 namespace sdm_delta {
 namespace {
 
-// Rows are read once: past the caches (16384 x 4096 rows, inputs in turn: forward 169 -> 159 us).
+// Rows are read once: past the caches (16384 x 4096 rows in bfloat16, inputs in turn, before the next row was fetched
+// ahead: forward 169 -> 159 us).
 constexpr bool kStream = true;
 
 // The sum of v over the workgroup, in an order set by the lane and wavefront numbers alone. `buf` alternates between
@@ -52,6 +53,16 @@ __device__ __forceinline__ void gate(float z, int act, float& a, float& d) {
     }
 }
 
+// A weight's floats as of this use: left to itself the compiler converts 16-bit weights before the row loop and keeps
+// twice the registers.
+template <int WT>
+__device__ __forceinline__ void weight_floats(float (&f)[8], Raw<WT> r) {
+    if constexpr (WT != 0) asm volatile("" : "+v"(r.w[0]));
+    raw_floats<WT>(f, r);
+}
+
+// The next row's loads are in flight while a row is worked on (in bfloat16, inputs in turn: 16384 x 4096 rows 157 -> 109
+// us, 6.2 TB/s; 8192 x 8192 197 -> 119; 2048 x 4096 29.6 -> 21.2).
 template <int DT, int WT, int NT, int NV>
 __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
     using T = elem_t<DT>;
@@ -60,30 +71,44 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
     const int D = static_cast<int>(a.D);
     const float inv = 1.f / static_cast<float>(D);
     const bool has_o = a.o != nullptr, has_x = a.x != nullptr, has_y = a.w_pre != nullptr;
-    float w1[NV][8], w2[NV][8], sc[NV][8];
+    const bool has_z = a.act != SDM_ACT_NONE;
+    struct {
+        Raw<DT> x[NV], o[NV], z[NV];
+    } in;
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
+            if (has_o) load_row<DT, kStream>(in.o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D);
+            if (has_z) load_row<DT, kStream>(in.z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D);
+            if (has_x) load_row<DT, kStream>(in.x[v], static_cast<const T*>(a.x) + r * a.ld_x, c, D);
+        }
+    };
+    fetch(blockIdx.x);
+    Raw<WT> w1[NV], w2[NV], sc[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
         if (has_o) {
-            load8<WT>(w1[v], static_cast<const W*>(a.w_post), c, D);
-            load8<WT>(sc[v], static_cast<const W*>(a.scale), c, D);
+            load_row<WT>(w1[v], static_cast<const W*>(a.w_post), c, D);
+            load_row<WT>(sc[v], static_cast<const W*>(a.scale), c, D);
         }
-        if (has_y) load8<WT>(w2[v], static_cast<const W*>(a.w_pre), c, D);
+        if (has_y) load_row<WT>(w2[v], static_cast<const W*>(a.w_pre), c, D);
     }
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         float x[NV][8], o[NV][8], z[NV][8];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
-            if (has_o) load8<DT, kStream>(o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D);
-            if (a.act != SDM_ACT_NONE) load8<DT, kStream>(z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D);
+            raw_floats<DT>(o[v], in.o[v]);
+            raw_floats<DT>(z[v], in.z[v]);
             if (has_x) {
-                load8<DT, kStream>(x[v], static_cast<const T*>(a.x) + r * a.ld_x, c, D);
+                raw_floats<DT>(x[v], in.x[v]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[v][i] = 0.f;
             }
         }
+        if (r + gridDim.x < a.rows) fetch(r + gridDim.x);
         float r1 = 0.f, r2 = 0.f;
         if (has_o) {
             float s = 0.f;
@@ -94,12 +119,15 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
             r1 = 1.f / sqrtf(fmaf(row_sum<NT>(s, red, 0), inv, a.eps));
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
+                float w[8], s[8];
+                weight_floats<WT>(w, w1[v]);
+                weight_floats<WT>(s, sc[v]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     float g = 1.f, d;
-                    if (a.act != SDM_ACT_NONE) gate<DT>(z[v][i], a.act, g, d);
+                    if (has_z) gate<DT>(z[v][i], a.act, g, d);
                     // rounded to the residual's type here: the second norm is that of the stored row
-                    x[v][i] = static_cast<float>(static_cast<T>(fmaf(sc[v][i], o[v][i] * r1 * w1[v][i] * g, x[v][i])));
+                    x[v][i] = static_cast<float>(static_cast<T>(fmaf(s[i], o[v][i] * r1 * w[i] * g, x[v][i])));
                 }
                 store8(static_cast<T*>(a.x_new) + r * a.ld_xn, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, x[v]);
             }
@@ -113,8 +141,10 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
             r2 = 1.f / sqrtf(fmaf(row_sum<NT>(s, red, 1), inv, a.eps));
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
+                float w[8];
+                weight_floats<WT>(w, w2[v]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[v][i] = x[v][i] * r2 * w2[v][i];
+                for (int i = 0; i < 8; ++i) x[v][i] = x[v][i] * r2 * w[i];
                 store8(static_cast<T*>(a.y) + r * a.ld_y, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, x[v]);
             }
         }
@@ -332,6 +362,7 @@ hipError_t run_backward(const sdm_nrm_args_t& a, const NrmPlan& p, float* part, 
 
 #define SDM_NRM_SHAPES(F, ...)                                                  \
     if (p.threads == 64) return F<DT, WT, 64, 1>(__VA_ARGS__);                  \
+    if (p.threads == 128) return F<DT, WT, 128, 1>(__VA_ARGS__);                \
     if (p.threads == 256 && p.vecs == 1) return F<DT, WT, 256, 1>(__VA_ARGS__);
 
 template <int DT, int WT>
