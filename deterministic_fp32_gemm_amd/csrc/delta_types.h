@@ -25,16 +25,17 @@ template <int DT>
 struct Raw {
     u32x4 w[DT == 0 ? 2 : 1];
 };
-// From column c, zero past `lim`; only columns < lim are read. STREAM: the caches need not keep what is read.
+// Eight values of a row of `lim`, from column c; only columns < lim are read. A thread whose columns end past the row
+// takes the row's last eight, which move_down puts right when they are used: no branch, so nothing waits for the load
+// here. STREAM: the caches need not keep what is read.
 template <int DT, bool STREAM = false>
 __device__ __forceinline__ void load_row(Raw<DT>& o, const elem_t<DT>* __restrict__ row, int c, int lim) {
-    if (c + 8 <= lim) {
-        const u32x4u* p = reinterpret_cast<const u32x4u*>(row + c);
+    if (lim >= 8) {
+        const u32x4u* p = reinterpret_cast<const u32x4u*>(row + min(c, lim - 8));
         o.w[0] = STREAM ? __builtin_nontemporal_load(p) : p[0];
         if constexpr (DT == 0) o.w[1] = STREAM ? __builtin_nontemporal_load(p + 1) : p[1];
         return;
     }
-    // the row's end: eight single loads, all in flight together, from inside the row
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int k = min(c + i, lim - 1);
@@ -59,11 +60,26 @@ __device__ __forceinline__ void raw_floats(float (&f)[8], const Raw<DT>& r) {
         for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(a[i]);
     }
 }
-template <int DT, bool STREAM = false>
+// The values of a thread whose columns end past the row, moved to their columns; zero past the row. For a row of 8 or
+// more and past = c + 8 - lim > 0.
+__device__ __forceinline__ void move_down(float (&f)[8], int past) {
+#pragma unroll
+    for (int k = 4; k > 0; k >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = i + k < 8 ? f[i + k < 8 ? i + k : i] : 0.f;
+            f[i] = past & k ? x : f[i];
+        }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = past >= 8 ? 0.f : f[i];
+}
+// load_row and its floats in their columns
+template <int DT>
 __device__ __forceinline__ void load8(float (&f)[8], const elem_t<DT>* __restrict__ row, int c, int lim) {
     Raw<DT> r;
-    load_row<DT, STREAM>(r, row, c, lim);
+    load_row<DT>(r, row, c, lim);
     raw_floats<DT>(f, r);
+    if (lim >= 8 && c + 8 > lim) move_down(f, c + 8 - lim);
 }
 
 template <class T>

@@ -8,7 +8,8 @@
 namespace sdm_delta {
 
 struct NrmPlan {
-    int threads;    // of a workgroup, which takes one row at a time
+    int most;       // threads of the kernel's instance at the most: 64, 128, 256 or 512
+    int threads;    // of a workgroup, which takes one row at a time: the wavefronts that have columns
     int vecs;       // groups of 8 columns a thread: threads * vecs * 8 >= D
     int groups;     // workgroups; workgroup i takes rows i, i + groups, ...
 };

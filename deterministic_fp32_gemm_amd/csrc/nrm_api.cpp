@@ -105,10 +105,13 @@ NrmPlan plan(const sdm_nrm_args_t* a, bool backward) {
     // and 250 with 512 of one; backward in bfloat16, which holds two sums a column beside, 340 with 256 of two, 215 with
     // 512 of one
     const bool middle = a->D > 2048 && a->D <= 4096;
-    p.threads = a->D <= 512 ? 64 : a->D <= 1024 ? 128 : a->D <= 2048 || (middle && !backward) ? 256 : 512;
-    p.vecs = static_cast<int>(cdiv(a->D, p.threads * 8));
-    // forward: workgroups for 8 wavefronts a SIMD; backward: each leaves a partial sum, so a quarter of that
-    const int64_t most = (backward ? 2048 : 8192) / (p.threads / 64);
+    p.most = a->D <= 512 ? 64 : a->D <= 1024 ? 128 : a->D <= 2048 || (middle && !backward) ? 256 : 512;
+    p.vecs = static_cast<int>(cdiv(a->D, p.most * 8));
+    // forward: no wavefronts past the row; backward: the sizes whose workgroups fill a CU (20000 rows of 1111 in float32:
+    // 188 us with 4 wavefronts, 246 with the 3 that have columns)
+    p.threads = backward ? p.most : static_cast<int>(cdiv(a->D, p.vecs * 512)) * 64;
+    // forward: workgroups for up to 8 wavefronts a SIMD, whole ones a CU; backward: each leaves a partial sum, so a quarter
+    const int64_t most = (backward ? 8 : 32) / (p.threads / 64) * 256;
     p.groups = static_cast<int>(a->rows < 1 ? 1 : a->rows < most ? a->rows : most);
     return p;
 }

@@ -30,7 +30,8 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[16], int buf) {
         lds_barrier();
         v = 0.f;
 #pragma unroll
-        for (int i = 0; i < NT / 64; ++i) v += red[buf][i];
+        for (int i = 0; i < NT / 64; ++i)
+            if (i < static_cast<int>(blockDim.x >> 6)) v += red[buf][i];
     }
     return v;
 }
@@ -53,8 +54,23 @@ __device__ __forceinline__ void gate(float z, int act, float& a, float& d) {
     }
 }
 
-// A weight's floats as of this use: left to itself the compiler converts 16-bit weights before the row loop and keeps
-// twice the registers.
+// Weights as they lie in memory, and a weight's floats as of this use: left to itself the compiler converts 16-bit weights
+// before the row loop and keeps twice the registers.
+template <int WT>
+__device__ __forceinline__ void load_weights(Raw<WT>& r, const void* w, int c, int D) {
+    float f[8];
+    load8<WT>(f, static_cast<const elem_t<WT>*>(w), c, D);
+    if constexpr (WT == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.w[i / 4][i % 4] = __float_as_uint(f[i]);
+    } else {
+        typedef elem_t<WT> t8 __attribute__((ext_vector_type(8)));
+        t8 a;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = static_cast<elem_t<WT>>(f[i]);
+        r.w[0] = __builtin_bit_cast(u32x4, a);
+    }
+}
 template <int WT>
 __device__ __forceinline__ void weight_floats(float (&f)[8], Raw<WT> r) {
     if constexpr (WT != 0) asm volatile("" : "+v"(r.w[0]));
@@ -62,13 +78,15 @@ __device__ __forceinline__ void weight_floats(float (&f)[8], Raw<WT> r) {
 }
 
 // The next row's loads are in flight while a row is worked on (in bfloat16, inputs in turn: 16384 x 4096 rows 157 -> 109
-// us, 6.2 TB/s; 8192 x 8192 197 -> 119; 2048 x 4096 29.6 -> 21.2).
+// us, 6.2 TB/s; 8192 x 8192 197 -> 119; 2048 x 4096 29.6 -> 21.2). A row's end is loaded without a branch (load_row) and
+// moved once it has come; with a branch its loads would wait for one another and for the row before them (20000 rows of
+// 1111 in bfloat16: forward 109 -> 63 us, with the wavefronts past the row left out, backward 277 -> 143).
 template <int DT, int WT, int NT, int NV>
 __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
     using T = elem_t<DT>;
     using W = elem_t<WT>;
     __shared__ float red[2][16];
-    const int D = static_cast<int>(a.D);
+    const int D = static_cast<int>(a.D), id = static_cast<int>(threadIdx.x), nt = static_cast<int>(blockDim.x);
     const float inv = 1.f / static_cast<float>(D);
     const bool has_o = a.o != nullptr, has_x = a.x != nullptr, has_y = a.w_pre != nullptr;
     const bool has_z = a.act != SDM_ACT_NONE;
@@ -78,7 +96,7 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
     auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
+            const int c = (v * nt + id) * 8;
             if (has_o) load_row<DT, kStream>(in.o[v], static_cast<const T*>(a.o) + r * a.ld_o, c, D);
             if (has_z) load_row<DT, kStream>(in.z[v], static_cast<const T*>(a.z) + r * a.ld_z, c, D);
             if (has_x) load_row<DT, kStream>(in.x[v], static_cast<const T*>(a.x) + r * a.ld_x, c, D);
@@ -88,12 +106,12 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
     Raw<WT> w1[NV], w2[NV], sc[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int c = (v * NT + static_cast<int>(threadIdx.x)) * 8;
+        const int c = (v * nt + id) * 8;
         if (has_o) {
-            load_row<WT>(w1[v], static_cast<const W*>(a.w_post), c, D);
-            load_row<WT>(sc[v], static_cast<const W*>(a.scale), c, D);
+            load_weights<WT>(w1[v], a.w_post, c, D);
+            load_weights<WT>(sc[v], a.scale, c, D);
         }
-        if (has_y) load_row<WT>(w2[v], static_cast<const W*>(a.w_pre), c, D);
+        if (has_y) load_weights<WT>(w2[v], a.w_pre, c, D);
     }
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         float x[NV][8], o[NV][8], z[NV][8];
@@ -106,6 +124,12 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[v][i] = 0.f;
+            }
+            const int past = (v * nt + id) * 8 + 8 - D;
+            if (__builtin_expect(past > 0 && D >= 8, 0)) {
+                move_down(o[v], past);
+                move_down(z[v], past);
+                move_down(x[v], past);
             }
         }
         if (r + gridDim.x < a.rows) fetch(r + gridDim.x);
@@ -129,7 +153,7 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
                     // rounded to the residual's type here: the second norm is that of the stored row
                     x[v][i] = static_cast<float>(static_cast<T>(fmaf(s[i], o[v][i] * r1 * w[i] * g, x[v][i])));
                 }
-                store8(static_cast<T*>(a.x_new) + r * a.ld_xn, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, x[v]);
+                store8(static_cast<T*>(a.x_new) + r * a.ld_xn, (v * nt + id) * 8, D, x[v]);
             }
         }
         if (has_y) {
@@ -145,7 +169,7 @@ __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
                 weight_floats<WT>(w, w2[v]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[v][i] = x[v][i] * r2 * w[i];
-                store8(static_cast<T*>(a.y) + r * a.ld_y, (v * NT + static_cast<int>(threadIdx.x)) * 8, D, x[v]);
+                store8(static_cast<T*>(a.y) + r * a.ld_y, (v * nt + id) * 8, D, x[v]);
             }
         }
         if (threadIdx.x == 0) {
@@ -240,6 +264,16 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dx[v][i] = 0.f;
             }
+            const int past = (v * NT + id) * 8 + 8 - D;
+            if (__builtin_expect(past > 0 && D >= 8, 0)) {
+                move_down(y[v], past);
+                move_down(xn[v], past);
+                move_down(dx[v], past);
+                if (AHEAD) {
+                    move_down(o[v], past);
+                    move_down(z[v], past);
+                }
+            }
         }
         if (AHEAD) {
             const int64_t next = r + gridDim.x < a.rows ? r + gridDim.x : r;    // the last row again: it costs little
@@ -277,6 +311,11 @@ __global__ __launch_bounds__(NT) void nrm_backward(const sdm_nrm_args_t a, float
                 for (int v = 0; v < NV; ++v) {
                     raw_floats<DT>(o[v], in.o[v]);
                     raw_floats<DT>(z[v], in.z[v]);
+                    const int past = (v * NT + id) * 8 + 8 - D;
+                    if (__builtin_expect(past > 0 && D >= 8, 0)) {
+                        move_down(o[v], past);
+                        move_down(z[v], past);
+                    }
                 }
             }
 #pragma unroll
@@ -351,24 +390,24 @@ __global__ __launch_bounds__(256) void nrm_weights(const sdm_nrm_args_t a, const
 
 template <int DT, int WT, int NT, int NV>
 hipError_t run_forward(const sdm_nrm_args_t& a, const NrmPlan& p, hipStream_t s) {
-    nrm_forward<DT, WT, NT, NV><<<p.groups, NT, 0, s>>>(a);
+    nrm_forward<DT, WT, NT, NV><<<p.groups, p.threads, 0, s>>>(a);
     return hipGetLastError();
 }
 template <int DT, int WT, int NT, int NV>
 hipError_t run_backward(const sdm_nrm_args_t& a, const NrmPlan& p, float* part, hipStream_t s) {
-    nrm_backward<DT, WT, NT, NV><<<p.groups, NT, 0, s>>>(a, part);
+    nrm_backward<DT, WT, NT, NV><<<p.groups, p.threads, 0, s>>>(a, part);
     return hipGetLastError();
 }
 
 #define SDM_NRM_SHAPES(F, ...)                                                  \
-    if (p.threads == 64) return F<DT, WT, 64, 1>(__VA_ARGS__);                  \
-    if (p.threads == 128) return F<DT, WT, 128, 1>(__VA_ARGS__);                \
-    if (p.threads == 256 && p.vecs == 1) return F<DT, WT, 256, 1>(__VA_ARGS__);
+    if (p.most == 64) return F<DT, WT, 64, 1>(__VA_ARGS__);                  \
+    if (p.most == 128) return F<DT, WT, 128, 1>(__VA_ARGS__);                \
+    if (p.most == 256 && p.vecs == 1) return F<DT, WT, 256, 1>(__VA_ARGS__);
 
 template <int DT, int WT>
 hipError_t forward_of(const sdm_nrm_args_t& a, const NrmPlan& p, hipStream_t s) {
     SDM_NRM_SHAPES(run_forward, a, p, s)
-    if (p.threads == 256) return run_forward<DT, WT, 256, 2>(a, p, s);
+    if (p.most == 256) return run_forward<DT, WT, 256, 2>(a, p, s);
     return run_forward<DT, WT, 512, 2>(a, p, s);
 }
 template <int DT, int WT>
