@@ -107,9 +107,9 @@ NrmPlan plan(const sdm_nrm_args_t* a, bool backward) {
     const bool middle = a->D > 2048 && a->D <= 4096;
     p.most = a->D <= 512 ? 64 : a->D <= 1024 ? 128 : a->D <= 2048 || (middle && !backward) ? 256 : 512;
     p.vecs = static_cast<int>(cdiv(a->D, p.most * 8));
-    // forward: no wavefronts past the row; backward: the sizes whose workgroups fill a CU (20000 rows of 1111 in float32:
-    // 188 us with 4 wavefronts, 246 with the 3 that have columns)
-    p.threads = backward ? p.most : static_cast<int>(cdiv(a->D, p.vecs * 512)) * 64;
+    // No wavefronts past the row (20000 rows of 2050 in bfloat16: backward 250 us, 268 with all 8); the backward of long
+    // rows keeps its sums by full width.
+    p.threads = backward && p.vecs > 1 ? p.most : static_cast<int>(cdiv(a->D, p.vecs * 512)) * 64;
     // forward: workgroups for up to 8 wavefronts a SIMD, whole ones a CU; backward: each leaves a partial sum, so a quarter
     const int64_t most = (backward ? 8 : 32) / (p.threads / 64) * 256;
     p.groups = static_cast<int>(a->rows < 1 ? 1 : a->rows < most ? a->rows : most);

@@ -80,7 +80,7 @@ __device__ __forceinline__ void weight_floats(float (&f)[8], Raw<WT> r) {
 // The next row's loads are in flight while a row is worked on (in bfloat16, inputs in turn: 16384 x 4096 rows 157 -> 109
 // us, 6.2 TB/s; 8192 x 8192 197 -> 119; 2048 x 4096 29.6 -> 21.2). A row's end is loaded without a branch (load_row) and
 // moved once it has come; with a branch its loads would wait for one another and for the row before them (20000 rows of
-// 1111 in bfloat16: forward 109 -> 63 us, with the wavefronts past the row left out, backward 277 -> 143).
+// 1111 in bfloat16: forward 110 -> 63 us and backward 277 -> 133, the wavefronts past the row left out too).
 template <int DT, int WT, int NT, int NV>
 __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
     using T = elem_t<DT>;
