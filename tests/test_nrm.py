@@ -199,3 +199,13 @@ def test_graph():
         torch.cuda.synchronize()
         for a, b in zip(got, w):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("size,kind", [((2700, 1111), "f32"), ((1700, 2050), "bf16"), ((2100, 4101), "f16"),
+                                       ((4200, 601), "bf16"), ((8300, 17), "f32"), ((8200, 5), "f16")],
+                         ids=lambda s: "x".join(map(str, s)) if isinstance(s, tuple) else s)
+def test_more_rows_than_workgroups(size, kind):
+    """Workgroups that take several rows each, of lengths that end inside a thread's eight columns."""
+    print("rows", size, kind, flush=True)
+    ty = TYPES[kind]
+    check(make(*size, ty, ty, "silu"), "silu", ty, ty)
