@@ -6,7 +6,8 @@
 // Bounded by the state's bytes, once in and once out (2 x 64 KB a head at dk = dv = 128). A workgroup owns 4 CT columns
 // of one stream and head: each thread 4 columns of dk / (256 / CT) rows, held in registers from the load to the store
 // whatever the number of tokens; the sums over dk go through LDS. Columns of S never meet, so small batches take
-// CT = 8 (32 columns a workgroup, four times the workgroups of CT = 32).
+// CT = 8 (32 columns a workgroup, four times the workgroups of CT = 32). 256 streams of 32 heads of 128 x 128 take 209 us,
+// 4.8 TB/s (a copy of 1 GB runs at 5.06); one stream of 16 heads 6 to 7 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -118,13 +119,14 @@ __global__ __launch_bounds__(256) void gdr_step(const sdm_gdr_step_args_t a, con
 template <int DT>
 hipError_t run(const sdm_gdr_step_args_t& a, bool vec, hipStream_t s) {
     const int64_t bh = a.B * a.Hv;
-    const bool narrow = bh * ((a.dv + 127) / 128) < 1024;
+    // 32 columns a workgroup where those of 128 would be at most one a CU (bfloat16, dk = dv = 128, us a step with 32 and
+    // with 128 columns: 16 heads 6.2 and 9.0, 256 10.9 and 14.6, 384 17.7 and 16.1, 2048 70 and 52); for dk = 256, whose
+    // rows fill the registers, 64 always (32: 16 heads 13.9 and 13.6, 128 heads 54 and 18).
+    const bool narrow = a.dk <= 128 && bh * ((a.dv + 127) / 128) <= 256;
     const int cols = narrow ? 32 : a.dk <= 128 ? 128 : 64, slices = static_cast<int>((a.dv + cols - 1) / cols);
     const unsigned grid = static_cast<unsigned>(bh * slices);
-    if (narrow && a.dk <= 128)
+    if (narrow)
         gdr_step<DT, 8, 4><<<grid, 256, 0, s>>>(a, vec, slices);
-    else if (narrow)
-        gdr_step<DT, 8, 8><<<grid, 256, 0, s>>>(a, vec, slices);
     else if (a.dk <= 128)
         gdr_step<DT, 32, 16><<<grid, 256, 0, s>>>(a, vec, slices);
     else
