@@ -41,8 +41,6 @@ struct GdrLaunch {
 
 // bfloat16 parts that hold an element of a type exactly: 3, 1, 2
 inline int parts_of(int dtype) { return dtype == SDM_F32 ? 3 : dtype == SDM_BF16 ? 1 : 2; }
-// bfloat16 parts of P: what the type of o can show
-inline int pm_parts(int dtype) { return dtype == SDM_F32 ? 3 : 2; }
 
 hipError_t launch_gdr_forward(const GdrLaunch& g, hipStream_t stream);
 hipError_t launch_gdr_backward(const GdrLaunch& g, hipStream_t stream);

@@ -178,7 +178,7 @@ int64_t lay_out(const sdm_gdr_args_t* a, bool backward, char* base, GdrWork* w) 
     GdrWork t{};
     t.tok = reinterpret_cast<float*>(take(sv * kTokFields * kChunk * 4));
     t.inv = reinterpret_cast<uint16_t*>(take(sv * kChunk * kChunk * 3 * 2));
-    t.pm = reinterpret_cast<uint16_t*>(take(sv * kChunk * kChunk * (backward ? 3 : pm_parts(a->dtype)) * 2));
+    t.pm = reinterpret_cast<uint16_t*>(take(sv * kChunk * kChunk * 3 * 2));
     t.kf = reinterpret_cast<uint16_t*>(take(sk * dkp * kChunk * in * 2));
     if (!backward) t.qf = reinterpret_cast<uint16_t*>(take(sk * dkp * kChunk * in * 2));
     t.kt = reinterpret_cast<uint16_t*>(take(sk * dkp * kChunk * in * 2));

@@ -27,7 +27,7 @@ constexpr int kLd = 68;     // row of a 64 x 64 float32 matrix in LDS
 
 template <int DT, int DKP, bool BWD>
 __global__ __launch_bounds__(256, DT == 0 && DKP == 128 ? 3 : DKP < 256 || DT == 1 ? 4 : 1) void gdr_chunk(const GdrLaunch g) {
-    constexpr int NP = kParts<DT>, PP = BWD ? 3 : kOutParts<DT>, NKB = DKP / 32;
+    constexpr int NP = kParts<DT>, NKB = DKP / 32;
     using T = elem_t<DT>;
     // K's (or Q's) fragments, then A and the matrix that P, and after it T, are laid out in
     constexpr int kFragBytes = 64 * DKP * NP * 2, kMatBytes = 2 * 64 * kLd * 4;
@@ -114,8 +114,8 @@ __global__ __launch_bounds__(256, DT == 0 && DKP == 128 ? 3 : DKP < 256 || DT ==
         for (int kb = 0; kb < NKB; ++kb) {
             Frag<NP> bf;
             load_frag<NP>(bf, frag_at<NP>(Kf, j, kb, NKB));
-            mma<3>(kk[j], kf[kb], bf);
-            mma<3>(qk[j], qf[kb], bf);
+            mma(kk[j], kf[kb], bf);
+            mma(qk[j], qf[kb], bf);
         }
     }
     // K^T, and Q^T in the backward, once per q/k head: a fragment's eight tokens are eight 2-byte LDS reads
@@ -170,8 +170,8 @@ __global__ __launch_bounds__(256, DT == 0 && DKP == 128 ? 3 : DKP < 256 || DT ==
 
     // P, row tiles in order; the backward's P^T, of columns
     {
-        uint16_t* out = g.w.pm + sv * (PP * 4096);
-        Frag<PP> f;
+        uint16_t* out = g.w.pm + sv * (3 * 4096);
+        Frag<3> f;
         float v[8];
         const int t = wave;
 #pragma unroll
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(256, DT == 0 && DKP == 128 ? 3 : DKP < 256 || DT ==
                 v[e] = BWD ? Ts[k][m] : Ts[m][k];
             }
             split8(f, v);
-            store_frag<PP>(frag_at<PP>(out, t, kb, 2), f);
+            store_frag<3>(frag_at<3>(out, t, kb, 2), f);
         }
     }
     lds_barrier();

@@ -5,7 +5,8 @@
 // the part products whose parts' numbers add up to 2 or less; what is left out is below 2^-25 of the product, so a
 // product costs 6 matrix-core steps and is as exact as float32's own (a quarter of the time of a float32 matrix-core
 // product). Elements that are bfloat16 to begin with are one part (3 steps against a float32 operand), float16 ones
-// two. ORD = 2 leaves out the third parts where only a 16-bit result depends on the product (2^-17).
+// two. Results of 16 bits need them all too: Q S and P U can each be thousands of times their sum, the output, where a key
+// overwrites what the state holds.
 //
 // Fragments. One matrix-core operand of v_mfma_f32_16x16x32_bf16: lane l holds row l % 16, elements
 // 8 (l / 16) .. + 7 of a 32-wide block of the summed axis. Both operands have this layout, each with its summed axis
@@ -24,7 +25,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 template <int DT> constexpr int kParts = DT == 0 ? 3 : DT == 1 ? 1 : 2;
-template <int DT> constexpr int kOutParts = DT == 0 ? 3 : 2;
 
 template <int N>
 struct Frag {
@@ -73,11 +73,11 @@ __device__ __forceinline__ void split4(bf16x4 (&o)[N], const f32x4& f) {
     }
 }
 
-// acc += a b, the part products of order below ORD, smallest first
-template <int ORD, int NA, int NB>
+// acc += a b, the part products of order below 3, smallest first
+template <int NA, int NB>
 __device__ __forceinline__ void mma(f32x4& acc, const Frag<NA>& a, const Frag<NB>& b) {
 #pragma unroll
-    for (int s = ORD - 1; s >= 0; --s)
+    for (int s = 2; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             if (s - i >= 0 && s - i < NB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], acc, 0, 0, 0);

@@ -176,14 +176,14 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g, const int 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     L.s.u.frag(fu, j * 16, kb * 32);
-                    mma<3>(dpa[j], fo, fu);
+                    mma(dpa[j], fo, fu);
                 }
             } else {
                 L.s.r.frag(fr, (wave - 4) * 16, kb * 32);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     L.s.u.frag(fu, j * 16, kb * 32);
-                    mma<3>(dpa[j], fr, fu);
+                    mma(dpa[j], fr, fu);
                 }
             }
             Frag<3> fs[MT];
@@ -202,8 +202,8 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g, const int 
                 L.s.r.frag(fr, (j0 + j) * 16, kb * 32);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    mma<3>(aq[m][j], fo, fs[m]);
-                    mma<3>(ar[m][j], fr, fs[m]);
+                    mma(aq[m][j], fo, fs[m]);
+                    mma(ar[m][j], fr, fs[m]);
                 }
             }
 #pragma unroll
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g, const int 
             for (int j = 0; j < NJ; ++j) {
                 L.s.u.frag(fu, (j0 + j) * 16, kb * 32);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) mma<3>(as[m][j], fu, fs[m]);
+                for (int m = 0; m < MT; ++m) mma(as[m][j], fu, fs[m]);
             }
         }
         lds_barrier();
@@ -294,18 +294,18 @@ __global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g, const int 
             if (NJ < 4 || kb <= j >> 1) {       // a token's row reaches back, its column forward, by blocks of 32
                 L.p.m[0].frag(f, (j0 + j) * 16, kb * 32);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) mma<3>(aq[m][j], f, fk[m][kb]);
+                for (int m = 0; m < MT; ++m) mma(aq[m][j], f, fk[m][kb]);
                 L.p.m[1].frag(f, (j0 + j) * 16, kb * 32);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) mma<3>(ar[m][j], f, fk[m][kb]);
+                for (int m = 0; m < MT; ++m) mma(ar[m][j], f, fk[m][kb]);
             }
             if (NJ < 4 || kb >= j >> 1) {
                 L.p.t[0].frag(f, (j0 + j) * 16, kb * 32);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) mma<3>(as[m][j], f, fq[m][kb]);
+                for (int m = 0; m < MT; ++m) mma(as[m][j], f, fq[m][kb]);
                 L.p.t[1].frag(f, (j0 + j) * 16, kb * 32);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) mma<3>(as[m][j], f, fk[m][kb]);
+                for (int m = 0; m < MT; ++m) mma(as[m][j], f, fk[m][kb]);
             }
         }
 

@@ -61,13 +61,13 @@ __device__ __forceinline__ void put4(T* __restrict__ p, int stride, int t, int n
 
 // Sums of products of fragments over k blocks, in two accumulators that take turns: a product that waits for the one
 // before takes half as long again.
-template <int ORD, int KBS, int NA, int NB>
+template <int KBS, int NA, int NB>
 __device__ __forceinline__ void products(f32x4 (&x)[2], const Frag<NA>* a, const Frag<NB>* b) {
     int i = 0;
 #pragma unroll
     for (int k = 0; k < KBS; ++k)
 #pragma unroll
-        for (int s = ORD - 1; s >= 0; --s)
+        for (int s = 2; s >= 0; --s)
 #pragma unroll
             for (int p = 0; p < NA; ++p)
                 if (s - p >= 0 && s - p < NB) {
@@ -206,13 +206,13 @@ __device__ __forceinline__ void in_turn(int chunks, F step) {
 
 template <int DT, int DKP, int NT, bool STORE>
 __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int total) {
-    constexpr int NP = kParts<DT>, PP = kOutParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
+    constexpr int NP = kParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
     constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kDepth<DT, DKP, NT, false>;
     constexpr bool LATE = kLate<DT, DKP, NT>;
     using T = elem_t<DT>;
     __shared__ Tile<3, COLS, DKP> Sx;           // S, [column][dk]
     __shared__ Tile<3, COLS, 64> Rx, Dx;            // R and exp(G_C - G) U, [column][token]
-    __shared__ Tile<PP, COLS, 64> Ux[STORE ? 1 : 2];    // U, of even and odd chunks
+    __shared__ Tile<3, COLS, 64> Ux[STORE ? 1 : 2];    // U, of even and odd chunks
     const sdm_gdr_args_t& a = g.a;
     Scan w;
     if (!scan_of(w, a, total, COLS)) return;
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 f32x4 y[2] = {S[m][t] * whole, zero};
-                products<3, 2>(y, kt[m], b);
+                products<2>(y, kt[m], b);
                 S[m][t] = y[0] + y[1];
                 Sx.put(t * 16, (Tiles<DKP>::first(w) + m) * 16, S[m][t]);
             }
@@ -304,7 +304,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
                         fetch_u(before, min(chunk + 1, chunks - 1));
                         fetch_s(before, min(chunk + 1, chunks - 1));
                     }
-                    products<3, HALF>(x, f.kf + k0, b);
+                    products<HALF>(x, f.kf + k0, b);
                 }
                 Rx.put(t * 16, tok, f.beta * (floats4<DT>(f.v[t], t4, held(t, n)) - f.eg * (x[0] + x[1])));
             }
@@ -320,7 +320,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
                     else fetch_r(f, next);
                 }
                 f32x4 y[2] = {zero, zero};
-                products<3, KN>(y, f.inv, b);
+                products<KN>(y, f.inv, b);
                 u[t] = y[0] + y[1];
                 Dx.put(t * 16, tok, f.last * u[t]);
             }
@@ -343,25 +343,29 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
         if constexpr (!STORE) lds_barrier();    // the last chunk's U
     };
     auto run_outputs = [&](auto kn) {
-        constexpr int KN = decltype(kn)::value;
+        // Float16 heads of 128 hold two parts of Q and three of P: no more than two k blocks of S beside them, and with two
+        // column tiles Q of the next chunk comes after the update (a lone head of 4096 tokens: 121 us so, 132 with Q late
+        // and four k blocks; neither spills, all four at once with Q early do)
+        constexpr int KN = decltype(kn)::value, OUT = DT == 2 && HALF > 2 ? 2 : HALF;
+        constexpr bool QLATE = DT == 2 && DKP * NT >= 256;
         T* orow = STORE ? nullptr : rows_at<T>(a.o, w.s, hv);
         struct Set {
             Frag<NP> qf[STORE ? 1 : NKB], kt[MT][2];
-            Frag<PP> pm[KN];
+            Frag<3> pm[KN];
             f32x4 eg;
             float whole;
         } set[DEPTH];
         f32x4 o[NT];
         // the outputs of a chunk: P U on top of what Q S left
-        auto finish = [&](int chunk, const Frag<PP>* pm) {
+        auto finish = [&](int chunk, const Frag<3>* pm) {
             const int t0 = chunk * kChunk, n = min(kChunk, w.s.len - t0);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                Frag<PP> b[KN];
+                Frag<3> b[KN];
                 read<KN>(b, Ux[STORE ? 0 : chunk & 1], t * 16, 0);
                 reads_first();
                 f32x4 y[2] = {o[t], zero};
-                products<PP, KN>(y, pm, b);
+                products<KN>(y, pm, b);
                 y[0] += y[1];
                 if (w.c0 + t * 16 + w.row < dv)
                     put4(orow + t0 * a.o.token + w.c0 + t * 16 + w.row, static_cast<int>(a.o.token), t4, n, y[0]);
@@ -402,20 +406,20 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
                 for (int t = 0; t < NT; ++t) {
                     f32x4 x[2] = {zero, zero};
 #pragma unroll
-                    for (int k0 = 0; k0 < NKB; k0 += HALF) {
-                        Frag<PP> b[HALF];
-                        read<HALF>(b, Sx, t * 16, k0 * 32);
+                    for (int k0 = 0; k0 < NKB; k0 += OUT) {
+                        Frag<3> b[OUT];
+                        read<OUT>(b, Sx, t * 16, k0 * 32);
                         reads_first();
-                        products<PP, HALF>(x, f.qf + k0, b);
+                        products<OUT>(x, f.qf + k0, b);
                     }
                     o[t] = (x[0] + x[1]) * (f.eg * a.scale);
                 }
             }
-            if constexpr (!LATE) fetch_q(f, next);
+            if constexpr (!LATE && !QLATE) fetch_q(f, next);
             lds_barrier();
             update(f.kt, f.whole, std::false_type{}, [] {});
-            if constexpr (LATE) fetch_q(f, next);
-            else fetch_s(f, next);
+            if constexpr (LATE || QLATE) fetch_q(f, next);
+            if constexpr (!LATE) fetch_s(f, next);
         });
         if constexpr (!STORE) {
             lds_barrier();
@@ -484,8 +488,8 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 f32x4 y[2] = {S[m][t] * whole, zero};
-                products<3, 2>(y, qt[m], bq);
-                products<3, 2>(y, kt[m], br);
+                products<2>(y, qt[m], bq);
+                products<2>(y, kt[m], br);
                 S[m][t] = y[0] + y[1];
                 Sx.put(t * 16, (Tiles<DKP>::first(w) + m) * 16, S[m][t]);
             }
@@ -545,7 +549,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
                         fetch_r(before, back(i + 1));
                         fetch_s(before, back(i + 1));
                     }
-                    products<3, HALF>(x, f.kf + k0, b);
+                    products<HALF>(x, f.kf + k0, b);
                 }
                 Ux.put(t * 16, tok, (x[0] + x[1]) * f.last + Wx[t][w.part][w.lane]);
             }
@@ -561,7 +565,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
                     else fetch_u(f, next);
                 }
                 f32x4 y[2] = {zero, zero};
-                products<3, KN>(y, f.inv, b);
+                products<KN>(y, f.inv, b);
                 d[t] = y[0] + y[1];
                 Rx.put(t * 16, tok, -(f.beta * f.eg) * d[t]);
             }
@@ -612,7 +616,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
                 read<KN>(b, Ox, t * 16, K0 * 32);
                 reads_first();
                 f32x4 y[2] = {zero, zero};
-                products<3, KN>(y, pm, b);
+                products<KN>(y, pm, b);
                 Wx[t][w.part][w.lane] = y[0] + y[1];
             }
         };
