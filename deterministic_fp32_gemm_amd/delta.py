@@ -181,8 +181,9 @@ def _under(stream, device):
 
 class _Plans(threading.local):
     """Checked argument structs by the layout of a call's tensors, a set for each host thread: a call whose tensors have
-    the layout of an earlier one fills in their addresses and nothing else. Addresses, values and results are never
-    kept."""
+    the layout of an earlier one copies its struct and fills in their addresses. Addresses, values and results are never
+    kept: the copy is the call's own, since a finaliser, a signal handler or an allocator's callback may enter the same
+    function with the same layout before this call's launch."""
 
     MOST = 256
 
@@ -325,7 +326,7 @@ def gdr_forward(q, k, v, g, beta, *, scale=None, initial_state=None, final_state
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _gdr_plan(False, q, k, v, g, beta, scale, initial_state, cu_seqlens, None, None))
-    a, n, state, dev, _ = plan
+    kept, n, state, dev, _ = plan
     if stream is not None:
         with _under(stream, dev):
             return gdr_forward(q, k, v, g, beta, scale=scale, initial_state=initial_state, final_state=final_state,
@@ -336,6 +337,7 @@ def gdr_forward(q, k, v, g, beta, *, scale=None, initial_state=None, final_state
         if s is not None:
             s.zero_() if initial_state is None else s.copy_(initial_state)
         return o, s
+    a = sdm_gdr_args_t.from_buffer_copy(kept)
     keep = _gdr_operands(plan, a, q, k, v, g, beta, initial_state, cu_seqlens)
     ws = _workspace(n, dev)
     a.o.data, a.s_final = o.data_ptr(), 0 if s is None else s.data_ptr()
@@ -359,7 +361,7 @@ def gdr_backward(q, k, v, g, beta, do, *, scale=None, initial_state=None, dfinal
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _gdr_plan(True, q, k, v, g, beta, scale, initial_state, cu_seqlens, do, dfinal_state))
-    a, n, state, dev, copied = plan
+    kept, n, state, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
             return gdr_backward(q, k, v, g, beta, do, scale=scale, initial_state=initial_state,
@@ -370,6 +372,7 @@ def gdr_backward(q, k, v, g, beta, do, *, scale=None, initial_state=None, dfinal
     if not n:
         s.zero_() if dfinal_state is None else s.copy_(dfinal_state)
         return (*outs, s)
+    a = sdm_gdr_args_t.from_buffer_copy(kept)
     keep = _gdr_operands(plan, a, q, k, v, g, beta, initial_state, cu_seqlens)
     if copied:
         do = _inner(do)
@@ -398,17 +401,18 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, out=None, strea
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _step_plan(q, k, v, g, beta, state, slots, scale, out))
-    a, shape, dtype, dev, copied = plan
+    kept, shape, dtype, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
             return gdr_step(q, k, v, g, beta, state, slots=slots, scale=scale, out=out)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=dev)
-    if a is None:
+    if kept is None:
         return out
     if copied:
         q, k, v = _inner(q), _inner(k), _inner(v)
         slots = None if slots is None else slots.contiguous()
+    a = sdm_gdr_step_args_t.from_buffer_copy(kept)
     a.q.data, a.k.data, a.v.data, a.g.data = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr()
     a.beta.data, a.o.data, a.state = beta.data_ptr(), out.data_ptr(), state.data_ptr()
     if slots is not None:
@@ -538,7 +542,7 @@ def norm_forward(x, o, z, w_post, w_pre, scale, *, act="silu", eps=1e-6, stream=
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _norm_plan(False, x, o, z, w_post, w_pre, scale, act, eps))
-    a, _, rows, D, dev, _, copied, shape, dtype = plan
+    kept, _, rows, D, dev, _, copied, shape, dtype = plan
     if stream is not None:
         with _under(stream, dev):
             return norm_forward(x, o, z, w_post, w_pre, scale, act=act, eps=eps)
@@ -550,6 +554,7 @@ def norm_forward(x, o, z, w_post, w_pre, scale, *, act="silu", eps=1e-6, stream=
     if copied:
         x, o, z = _flat(x), _flat(o), _flat(z)
         w_post, w_pre, scale = (None if t is None else t.contiguous() for t in (w_post, w_pre, scale))
+    a = sdm_nrm_args_t.from_buffer_copy(kept)
     a.x, a.o, a.z, a.rstd = _ptr(x), _ptr(o), _ptr(z), rstd.data_ptr()
     a.w_post, a.w_pre, a.scale = _ptr(w_post), _ptr(w_pre), _ptr(scale)
     a.x_new, a.y = 0 if o is None else x_new.data_ptr(), _ptr(y)
@@ -570,7 +575,7 @@ def norm_backward(dx_new, dy, x_new, o, z, w_post, w_pre, scale, rstd, *, act="s
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _norm_plan(True, dx_new, o, z, w_post, w_pre, scale, act, 0.0, dy, x_new, rstd))
-    a, n, rows, D, dev, wd, copied, shape, dtype = plan
+    kept, n, rows, D, dev, wd, copied, shape, dtype = plan
     if stream is not None:
         with _under(stream, dev):
             return norm_backward(dx_new, dy, x_new, o, z, w_post, w_pre, scale, rstd, act=act)
@@ -586,6 +591,7 @@ def norm_backward(dx_new, dy, x_new, o, z, w_post, w_pre, scale, rstd, *, act="s
     if copied:
         dx_new, dy, x_new, o, z = (_flat(t) for t in (dx_new, dy, x_new, o, z))
         w_post, w_pre, scale, rstd = (None if t is None else t.contiguous() for t in (w_post, w_pre, scale, rstd))
+    a = sdm_nrm_args_t.from_buffer_copy(kept)
     a.o, a.z, a.dxn, a.dy, a.rstd = _ptr(o), _ptr(z), _ptr(dx_new), _ptr(dy), rstd.data_ptr()
     a.x_new = 0 if dy is None else x_new.data_ptr()
     a.w_post, a.w_pre, a.scale = _ptr(w_post), _ptr(w_pre), _ptr(scale)
