@@ -216,8 +216,9 @@ int call(const sdm_gdr_args_t* a, bool backward, void* workspace, int64_t bytes,
     if (!workspace) return SDM_GX_ERR_NULL;
     if (!aligned(workspace, 256)) return SDM_GX_ERR_ALIGN;
     if (bytes < lay_out(a, backward, nullptr, nullptr)) return SDM_GX_ERR_LIMIT;
-    const int64_t scans = cdiv(a->dv, 16) * a->Hv * a->nseq;
-    if (slots_of(a) * a->Hv >= (int64_t(1) << 30) || scans >= (int64_t(1) << 30)) return SDM_GX_ERR_LIMIT;
+    const int64_t scans = 8 * cdiv(scan_groups(*a, static_cast<int>(padded_dk(a->dk))), 8);
+    if (slots_of(a) * (backward ? kGradThreads : kChunkThreads) >= kMaxThreads || scans * kScanThreads >= kMaxThreads)
+        return SDM_GX_ERR_LIMIT;
     if ((st = current_gfx950(&dev))) return st;
     const void* both[] = {a->q.data, a->k.data, a->v.data, a->g.data, a->beta.data, a->cu_seqlens, a->s0, workspace};
     const void* fwd[] = {a->o.data, a->s_final};
@@ -285,11 +286,11 @@ int sdm_gdr_step_check(const sdm_gdr_step_args_t* args) { return check_step(args
 int sdm_gdr_step(const sdm_gdr_step_args_t* a, void* stream) {
     int st = check_step(a), dev = 0;
     if (st || a->T == 0) return st;
+    if (step_groups(*a) * kStepThreads >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     if ((st = current_gfx950(&dev))) return st;
     const void* ps[] = {a->q.data, a->k.data, a->v.data, a->g.data, a->beta.data, a->o.data, a->state, a->slots};
     for (const void* p : ps)
         if (p && (st = pointer_on(p, dev))) return st;
-    if (a->B * a->Hv >= (int64_t(1) << 26)) return SDM_GX_ERR_LIMIT;
     const bool vec = a->dv % 4 == 0 && aligned(a->state, 16);
     const hipError_t e = launch_gdr_step(*a, vec, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? SDM_GX_OK : record_hip_error(e);

@@ -26,7 +26,7 @@ namespace {
 constexpr int kLd = 68;     // row of a 64 x 64 float32 matrix in LDS
 
 template <int DT, int DKP, bool BWD>
-__global__ __launch_bounds__(256, DT == 0 && DKP == 128 ? 3 : DKP < 256 || DT == 1 ? 4 : 1) void gdr_chunk(const GdrLaunch g) {
+__global__ __launch_bounds__(kChunkThreads, DT == 0 && DKP == 128 ? 3 : DKP < 256 || DT == 1 ? 4 : 1) void gdr_chunk(const GdrLaunch g) {
     constexpr int NP = kParts<DT>, NKB = DKP / 32;
     using T = elem_t<DT>;
     // K's (or Q's) fragments, then A and the matrix that P, and after it T, are laid out in
@@ -273,11 +273,11 @@ template <int DT, bool BWD>
 hipError_t run(const GdrLaunch& g, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(g.slots), static_cast<unsigned>(g.a.Hv));
     if (g.dkp == 64)
-        gdr_chunk<DT, 64, BWD><<<grid, 256, 0, s>>>(g);
+        gdr_chunk<DT, 64, BWD><<<grid, kChunkThreads, 0, s>>>(g);
     else if (g.dkp == 128)
-        gdr_chunk<DT, 128, BWD><<<grid, 256, 0, s>>>(g);
+        gdr_chunk<DT, 128, BWD><<<grid, kChunkThreads, 0, s>>>(g);
     else
-        gdr_chunk<DT, 256, BWD><<<grid, 256, 0, s>>>(g);
+        gdr_chunk<DT, 256, BWD><<<grid, kChunkThreads, 0, s>>>(g);
     return hipGetLastError();
 }
 

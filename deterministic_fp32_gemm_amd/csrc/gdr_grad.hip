@@ -42,7 +42,7 @@ __device__ __forceinline__ float row_sum16(float x) {
 __device__ __forceinline__ constexpr int token_of(int j, int r) { return 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3); }
 
 template <int DT, int DKP>
-__global__ __launch_bounds__(512, 2) void gdr_grad(const GdrLaunch g, const int heads) {
+__global__ __launch_bounds__(kGradThreads, 2) void gdr_grad(const GdrLaunch g, const int heads) {
     constexpr int NP = kParts<DT>;
     constexpr int MT = 1, PASSES = DKP == 256 ? 2 : 1;  // dk tiles of a wavefront at a time; times
     constexpr int NJ = DKP >= 128 ? 4 : 2;              // its token tiles
@@ -429,11 +429,11 @@ hipError_t run(const GdrLaunch& g, hipStream_t s) {
     const int heads = g.dkp <= 128 && static_cast<int64_t>(g.slots) * g.a.Hk >= 256 ? rr : 1;
     const dim3 grid(static_cast<unsigned>(g.slots), static_cast<unsigned>(g.a.Hv / heads));
     if (g.dkp == 64)
-        gdr_grad<DT, 64><<<grid, 512, 0, s>>>(g, heads);
+        gdr_grad<DT, 64><<<grid, kGradThreads, 0, s>>>(g, heads);
     else if (g.dkp == 128)
-        gdr_grad<DT, 128><<<grid, 512, 0, s>>>(g, heads);
+        gdr_grad<DT, 128><<<grid, kGradThreads, 0, s>>>(g, heads);
     else
-        gdr_grad<DT, 256><<<grid, 512, 0, s>>>(g, heads);
+        gdr_grad<DT, 256><<<grid, kGradThreads, 0, s>>>(g, heads);
     if (heads != rr) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;

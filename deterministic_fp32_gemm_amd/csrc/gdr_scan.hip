@@ -205,7 +205,7 @@ __device__ __forceinline__ void in_turn(int chunks, F step) {
 }
 
 template <int DT, int DKP, int NT, bool STORE>
-__global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int total) {
+__global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
     constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kDepth<DT, DKP, NT, false>;
     constexpr bool LATE = kLate<DT, DKP, NT>;
@@ -448,7 +448,7 @@ __global__ __launch_bounds__(512, 2) void gdr_scan(const GdrLaunch g, const int 
 }
 
 template <int DT, int DKP, int NT>
-__global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const int total) {
+__global__ __launch_bounds__(kScanThreads, 2) void gdr_scan_back(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
     constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kDepth<DT, DKP, NT, true>;
     constexpr bool LATE = kLate<DT, DKP, NT>;
@@ -677,22 +677,19 @@ __global__ __launch_bounds__(512, 2) void gdr_scan_back(const GdrLaunch g, const
 
 template <int DT, int DKP, int NT>
 hipError_t scan(const GdrLaunch& g, int mode, hipStream_t s) {
-    const int total = static_cast<int>((g.a.dv + 16 * NT - 1) / (16 * NT) * g.a.Hv * g.a.nseq), grid = 8 * ((total + 7) / 8);
+    const int total = static_cast<int>(scan_groups(g.a, g.dkp)), grid = 8 * ((total + 7) / 8);
     if (mode == 0)
-        gdr_scan<DT, DKP, NT, false><<<grid, 512, 0, s>>>(g, total);
+        gdr_scan<DT, DKP, NT, false><<<grid, kScanThreads, 0, s>>>(g, total);
     else if (mode == 1)
-        gdr_scan<DT, DKP, NT, true><<<grid, 512, 0, s>>>(g, total);
+        gdr_scan<DT, DKP, NT, true><<<grid, kScanThreads, 0, s>>>(g, total);
     else
-        gdr_scan_back<DT, DKP, NT><<<grid, 512, 0, s>>>(g, total);
+        gdr_scan_back<DT, DKP, NT><<<grid, kScanThreads, 0, s>>>(g, total);
     return hipGetLastError();
 }
 template <int DT, int DKP>
 hipError_t scan(const GdrLaunch& g, int mode, hipStream_t s) {
-    // Workgroups of 32 columns where those of 16 would be more than one a CU: half the operands for 1.45 times the
-    // step (tokens x 32 heads of 128 in bfloat16, forward: 4 x 2048 383 us with 16 columns, 294 with 32; 2 x 2048 180
-    // and 150).
     if constexpr (DKP <= 128)
-        if ((g.a.dv + 15) / 16 * g.a.Hv * g.a.nseq > 256) return scan<DT, DKP, 2>(g, mode, s);
+        if (scan_tiles(g.a, DKP) == 2) return scan<DT, DKP, 2>(g, mode, s);
     return scan<DT, DKP, 1>(g, mode, s);
 }
 

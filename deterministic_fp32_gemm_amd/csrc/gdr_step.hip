@@ -17,9 +17,9 @@ namespace sdm_delta {
 namespace {
 
 template <int DT, int CT, int ROWS>
-__global__ __launch_bounds__(256) void gdr_step(const sdm_gdr_step_args_t a, const bool vec, const int slices) {
+__global__ __launch_bounds__(kStepThreads) void gdr_step(const sdm_gdr_step_args_t a, const bool vec, const int slices) {
     using T = elem_t<DT>;
-    constexpr int RG = 256 / CT, COLS = CT * 4;     // row groups, columns
+    constexpr int RG = kStepThreads / CT, COLS = CT * 4;     // row groups, columns
     __shared__ float K[256], Q[256];
     __shared__ f32x4 red[RG][CT];
     const int dk = static_cast<int>(a.dk), dv = static_cast<int>(a.dv), Hv = static_cast<int>(a.Hv);
@@ -118,19 +118,14 @@ __global__ __launch_bounds__(256) void gdr_step(const sdm_gdr_step_args_t a, con
 
 template <int DT>
 hipError_t run(const sdm_gdr_step_args_t& a, bool vec, hipStream_t s) {
-    const int64_t bh = a.B * a.Hv;
-    // 32 columns a workgroup where those of 128 would be at most one a CU (bfloat16, dk = dv = 128, us a step with 32 and
-    // with 128 columns: 16 heads 6.2 and 9.0, 256 10.9 and 14.6, 384 17.7 and 16.1, 2048 70 and 52); for dk = 256, whose
-    // rows fill the registers, 64 always (32: 16 heads 13.9 and 13.6, 128 heads 54 and 18).
-    const bool narrow = a.dk <= 128 && bh * ((a.dv + 127) / 128) <= 256;
-    const int cols = narrow ? 32 : a.dk <= 128 ? 128 : 64, slices = static_cast<int>((a.dv + cols - 1) / cols);
-    const unsigned grid = static_cast<unsigned>(bh * slices);
-    if (narrow)
-        gdr_step<DT, 8, 4><<<grid, 256, 0, s>>>(a, vec, slices);
-    else if (a.dk <= 128)
-        gdr_step<DT, 32, 16><<<grid, 256, 0, s>>>(a, vec, slices);
+    const int cols = step_columns(a), slices = static_cast<int>((a.dv + cols - 1) / cols);
+    const unsigned grid = static_cast<unsigned>(step_groups(a));
+    if (cols == 32)
+        gdr_step<DT, 8, 4><<<grid, kStepThreads, 0, s>>>(a, vec, slices);
+    else if (cols == 128)
+        gdr_step<DT, 32, 16><<<grid, kStepThreads, 0, s>>>(a, vec, slices);
     else
-        gdr_step<DT, 16, 16><<<grid, 256, 0, s>>>(a, vec, slices);
+        gdr_step<DT, 16, 16><<<grid, kStepThreads, 0, s>>>(a, vec, slices);
     return hipGetLastError();
 }
 

@@ -1,0 +1,51 @@
+"""Sizes past what one launch can hold are refused by the entry points, before any device call (no GPU)."""
+
+import ctypes
+
+import pytest
+
+from deterministic_fp32_gemm_amd import _binding as B
+from deterministic_fp32_gemm_amd import delta as D
+
+FAR = 1 << 44       # made-up addresses, further apart than any operand is long
+
+
+def operands(a, names, T, Hk, Hv, dk, dv):
+    at = FAR
+    for n in names:
+        H, d = {"q": (Hk, dk), "k": (Hk, dk), "d_q": (Hk, dk), "d_k": (Hk, dk), "g": (Hv, 1), "beta": (Hv, 1),
+                "d_g": (Hv, 1), "d_beta": (Hv, 1)}.get(n, (Hv, dv))
+        setattr(a, n, D.sdm_rows_t(at, T * H * d, H * d, d))
+        at += FAR
+    return at
+
+
+@pytest.mark.parametrize("backward", [0, 1])
+@pytest.mark.parametrize("B_,T,Hk,Hv,dk,dv,held", [
+    (1 << 18, 1, 32, 32, 16, 16, False),        # 2^23 scan workgroups of 512 threads
+    ((1 << 18) - 1, 1, 32, 32, 16, 16, True),
+    (1 << 16, 1, 32, 32, 200, 64, False),       # wide heads go 16 columns a workgroup
+    (1, 1 << 30, 1, 1, 16, 16, False),          # 2^24 chunks
+    (1, (1 << 29) - 64, 1, 1, 16, 16, True),    # 2^23 - 1 of them, of 512 threads in the gradient
+])
+def test_sequences(backward, B_, T, Hk, Hv, dk, dv, held):
+    a = D.sdm_gdr_args_t(dtype=1, scale=1.0, B=B_, T=T, Hk=Hk, Hv=Hv, dk=dk, dv=dv, nseq=B_)
+    at = operands(a, ("q", "k", "v", "g", "beta", "o", "d_o", "d_q", "d_k", "d_v", "d_g", "d_beta"), T, Hk, Hv, dk, dv)
+    lib = D.load()
+    n = lib.sdm_gdr_workspace(ctypes.byref(a), backward)
+    assert n > 0
+    call = lib.sdm_gdr_backward if backward else lib.sdm_gdr_forward
+    status = call(ctypes.byref(a), at, n, None)
+    assert (status == B.SDM_GX_ERR_LIMIT) == (not held), status
+    assert status != B.SDM_GX_OK
+
+
+@pytest.mark.parametrize("B_,Hv,dk,dv,held", [(1 << 19, 32, 16, 16, False), ((1 << 19) - 1, 32, 16, 16, True),
+                                              (1 << 17, 32, 256, 256, False), (1 << 17, 31, 256, 256, True)])
+def test_steps(B_, Hv, dk, dv, held):
+    a = D.sdm_gdr_step_args_t(dtype=1, scale=1.0, B=B_, T=1, Hk=1, Hv=Hv, dk=dk, dv=dv, pool=1)
+    at = operands(a, ("q", "k", "v", "g", "beta", "o"), 1, 1, Hv, dk, dv)
+    a.state, a.slots = at, at + FAR
+    status = D.load().sdm_gdr_step(ctypes.byref(a), None)
+    assert (status == B.SDM_GX_ERR_LIMIT) == (not held), status
+    assert status != B.SDM_GX_OK
