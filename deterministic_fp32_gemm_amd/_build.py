@@ -7,6 +7,8 @@ import shutil
 import subprocess
 from concurrent.futures import ThreadPoolExecutor
 
+from . import _code_check
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
@@ -42,8 +44,13 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build libsdm_gx_gemm)")
 
 
-def build(out: str = LIB_PATH, verbose: bool = False, sources=SOURCES) -> str:
-    """Compile every source for gfx950 and link the shared library (always recompiles)."""
+def llvm() -> str:
+    return os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "llvm", "bin")
+
+
+def build(out: str = LIB_PATH, verbose: bool = False, sources=SOURCES, check=None) -> str:
+    """Compile every source for gfx950 and link the shared library (always recompiles). check(path) may refuse the linked
+    library by an exception: then what was at `out` stays."""
     tmpdir = os.path.join(PKG, "_objs")
     os.makedirs(tmpdir, exist_ok=True)
     cc = hipcc()
@@ -63,13 +70,19 @@ def build(out: str = LIB_PATH, verbose: bool = False, sources=SOURCES) -> str:
         objs = list(pool.map(one, sources))
     tmp = out + ".tmp"
     run([cc, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs])
-    os.replace(tmp, out)
+    try:
+        if check is not None:
+            check(tmp)
+        os.replace(tmp, out)
+    finally:
+        if os.path.exists(tmp):
+            os.remove(tmp)
     return out
 
 
-def build_delta(out: str = DELTA_LIB_PATH, verbose: bool = False) -> str:
-    """The same for the gated delta rule and the block norm."""
-    return build(out, verbose, DELTA_SOURCES)
+def build_delta(out: str = DELTA_LIB_PATH, verbose: bool = False, sources=DELTA_SOURCES) -> str:
+    """The same for the gated delta rule and the block norm, whose machine code is checked (_code_check.py)."""
+    return build(out, verbose, sources, lambda path: _code_check.verify(path, llvm()))
 
 
 if __name__ == "__main__":
