@@ -5,6 +5,10 @@ check types and shapes, and call the C ABI of libsdm_delta on torch's current st
 step runs in the library's HIP kernels; there is no other path. A wrong argument raises TypeError or ValueError before
 anything runs. A call with ``stream`` is the call under ``torch.cuda.stream(stream)``: what it allocates is that
 stream's, and tensors made on another stream are the caller's to order and keep alive, as for any torch operation.
+
+Where grad mode is on and a tensor of the call requires a gradient, gdr_forward and norm_forward are part of torch's graph
+(_delta_autograd.py), and a backward pass that reaches gdr_step, which has no gradient, is an error. The gradients that
+gdr_backward and norm_backward return have no graph of their own.
 """
 
 from __future__ import annotations
@@ -160,6 +164,15 @@ def _find_raw_stream():
 _raw_stream = None
 
 
+def _increment_version(tensors):
+    """Counts a write to tensors, by torch's own call without the type checks around it: a graph that has saved one of
+    them must not use it any more."""
+    global _increment_version
+    import torch
+    _increment_version = getattr(torch._C, "_increment_version", torch.autograd.graph.increment_version)
+    _increment_version(tensors)
+
+
 def _stream(device) -> int:
     """The handle of torch's current stream on the device."""
     if _raw_stream is None:
@@ -229,6 +242,24 @@ class _OnDevice:
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
+
+
+def _requires_grad(*tensors) -> bool:
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return True
+    return False
+
+
+def _scale(scale):
+    """scale as a number, also where a tensor holds it; none that torch would differentiate."""
+    if scale is None or type(scale) is float:
+        return scale
+    if getattr(scale, "requires_grad", False):
+        import torch
+        if torch.is_grad_enabled():
+            raise ValueError("scale: a number; no gradient is computed for it (detach it, or scale q)")
+    return float(scale)
 
 
 def _workspace(nbytes: int, device):
@@ -320,7 +351,7 @@ def gdr_forward(q, k, v, g, beta, *, scale=None, initial_state=None, final_state
     sequence get zeros. Any strides; a last axis that is not contiguous is copied first.
     """
     import torch
-    scale = None if scale is None else float(scale)       # a value, also where a tensor holds it
+    scale = _scale(scale)
     key = ("fwd", _layout(q), _layout(k), _layout(v), _layout(g), _layout(beta), _layout(initial_state),
            _layout(cu_seqlens), scale)
     plan = _plans.get(key)
@@ -331,6 +362,9 @@ def gdr_forward(q, k, v, g, beta, *, scale=None, initial_state=None, final_state
         with _under(stream, dev):
             return gdr_forward(q, k, v, g, beta, scale=scale, initial_state=initial_state, final_state=final_state,
                                cu_seqlens=cu_seqlens)
+    if torch.is_grad_enabled() and _requires_grad(q, k, v, g, beta, initial_state):
+        from ._delta_autograd import GatedDeltaRule
+        return GatedDeltaRule.apply(q, k, v, g, beta, initial_state, scale, final_state, cu_seqlens)
     o = (torch.empty if cu_seqlens is None else torch.zeros)(v.shape, dtype=v.dtype, device=dev)
     s = torch.empty(state, dtype=torch.float32, device=dev) if final_state else None
     if not n:
@@ -355,7 +389,7 @@ def gdr_backward(q, k, v, g, beta, do, *, scale=None, initial_state=None, dfinal
     dfinal_state, that of the last state (None: zero). It recomputes the forward's states and needs nothing saved but
     the inputs. Gradients have their tensors' shapes and types; tokens of no sequence get zeros."""
     import torch
-    scale = None if scale is None else float(scale)       # a value, also where a tensor holds it
+    scale = _scale(scale)
     key = ("bwd", _layout(q), _layout(k), _layout(v), _layout(g), _layout(beta), _layout(initial_state),
            _layout(cu_seqlens), _layout(do), _layout(dfinal_state), scale)
     plan = _plans.get(key)
@@ -393,9 +427,10 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, out=None, strea
 
     state [pool, Hv, dk, dv] float32, contiguous. slots: int32 [B] on the GPU, the state each stream uses (None: its
     own number); a stream whose slot is not in the pool, such as -1, is idle: zeros in o, no state touched. No two
-    streams may name one slot. The other tensors as in gdr_forward."""
+    streams may name one slot. The other tensors as in gdr_forward. It has no gradient: a backward pass that reaches o
+    is an error."""
     import torch
-    scale = None if scale is None else float(scale)       # a value, also where a tensor holds it
+    scale = _scale(scale)
     key = ("step", _layout(q), _layout(k), _layout(v), _layout(g), _layout(beta), _layout(state), _layout(slots),
            _layout(out), scale)
     plan = _plans.get(key)
@@ -405,6 +440,8 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, out=None, strea
     if stream is not None:
         with _under(stream, dev):
             return gdr_step(q, k, v, g, beta, state, slots=slots, scale=scale, out=out)
+    recorded = torch.is_grad_enabled() and _requires_grad(q, k, v, g, beta, state)
+    written = (state,) if out is None else (state, out)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=dev)
     if kept is None:
@@ -421,6 +458,10 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, out=None, strea
         status = load().sdm_gdr_step(ctypes.byref(a), _stream(dev))
     if status:
         _raise(status, "gdr_step")
+    _increment_version(written)
+    if recorded:
+        from ._delta_autograd import NoGradient
+        return NoGradient.apply([out], "gdr_step", q, k, v, g, beta, state)
     return out
 
 
@@ -546,6 +587,10 @@ def norm_forward(x, o, z, w_post, w_pre, scale, *, act="silu", eps=1e-6, stream=
     if stream is not None:
         with _under(stream, dev):
             return norm_forward(x, o, z, w_post, w_pre, scale, act=act, eps=eps)
+    if torch.is_grad_enabled() and _requires_grad(x, o, z, w_post, w_pre, scale):
+        from ._delta_autograd import BlockNorm
+        made = BlockNorm.apply(x, o, z, w_post, w_pre, scale, act, eps)
+        return made if o is not None else (x, *made)
     x_new = x if o is None else torch.empty(shape, dtype=dtype, device=dev)
     y = None if w_pre is None else torch.empty(shape, dtype=dtype, device=dev)
     rstd = torch.empty((rows, 2), dtype=torch.float32, device=dev)

@@ -6,8 +6,8 @@ the next block in the same pass:
 
     o = gated_delta_rule(q, k, v, g, beta) W_o;   x = x + scale rms_norm(o) w_post silu(z);   h = rms_norm(x) w_pre
 
-Training takes gdr_forward, gdr_backward, norm_forward and norm_backward; answering takes a prompt with gdr_forward,
-whose last states fill a pool, and goes on with gdr_step on that pool.
+Training takes gdr_forward and norm_forward, whose gradients (gdr_backward, norm_backward) torch's graph calls; answering
+takes a prompt with gdr_forward, whose last states fill a pool, and goes on with gdr_step on that pool.
 
     python examples/delta_block.py [--steps 100] [--dtype bf16|f16|f32]
 """
@@ -23,44 +23,6 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import deterministic_fp32_gemm_amd as sdm  # noqa: E402
 
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
-
-
-class DeltaRule(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, q, k, v, g, beta):
-        ctx.save_for_backward(q, k, v, g, beta)
-        return sdm.gdr_forward(q, k, v, g, beta)
-
-    @staticmethod
-    def backward(ctx, do, ds):
-        return sdm.gdr_backward(*ctx.saved_tensors, do, dfinal_state=ds.contiguous())[:5]
-
-
-class BlockNorm(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, o, z, w_post, w_pre, scale):
-        x_new, y, rstd = sdm.norm_forward(x, o, z, w_post, w_pre, scale)
-        ctx.save_for_backward(x_new, o, z, w_post, w_pre, scale, rstd)
-        return x_new, y
-
-    @staticmethod
-    def backward(ctx, dx_new, dy):
-        dx, do, dz, dw_post, dw_pre, dscale = sdm.norm_backward(dx_new, dy, *ctx.saved_tensors)
-        return dx, do, dz, dw_post, dw_pre, dscale
-
-
-class FirstNorm(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, w):
-        _, y, rstd = sdm.norm_forward(x, None, None, None, w, None, act="none")
-        ctx.save_for_backward(x, w, rstd)
-        return y
-
-    @staticmethod
-    def backward(ctx, dy):
-        x, w, rstd = ctx.saved_tensors
-        dx, _, _, _, dw, _ = sdm.norm_backward(None, dy, x, None, None, None, w, None, rstd, act="none")
-        return dx, dw
 
 
 class Block(torch.nn.Module):
@@ -84,8 +46,9 @@ class Block(torch.nn.Module):
     def forward(self, x, h):
         """Whole sequences: the stream, the next block's input and the states after the last token."""
         q, k, v, g, beta, z = self.operands(h)
-        o, state = DeltaRule.apply(q, k, v, g, beta)
-        x, h = BlockNorm.apply(x, F.linear(o.flatten(2), self.w_out.to(h.dtype)), z, self.w_post, self.w_pre, self.scale)
+        o, state = sdm.gdr_forward(q, k, v, g, beta)
+        x, h, _ = sdm.norm_forward(x, F.linear(o.flatten(2), self.w_out.to(h.dtype)), z, self.w_post, self.w_pre,
+                                   self.scale)
         return x, h, state
 
     def step(self, x, h, pool, slots):
@@ -109,7 +72,7 @@ class Model(torch.nn.Module):
 
     def begin(self, tokens, before):
         x = (self.embed[tokens] * self.near[0] + self.embed[before] * self.near[1]).to(self.dtype)
-        return x, FirstNorm.apply(x, self.w_first)
+        return x, sdm.norm_forward(x, None, None, None, self.w_first, None, act="none")[1]
 
     def forward(self, tokens):
         x, h = self.begin(tokens, F.pad(tokens[:, :-1], (1, 0)))
