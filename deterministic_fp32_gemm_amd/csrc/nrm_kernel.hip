@@ -36,21 +36,26 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[16], int buf) {
     return v;
 }
 
-// act(z) and act'(z). The 16-bit types take the hardware's exponential and reciprocal (1 ulp of float32), float32 the
-// library's.
+// act(z) and act'(z). With e = exp(-|z|) the sigmoid p and 1 - p are 1 / (1 + e) and e / (1 + e), in the order of z's sign:
+// 1 - p taken as a difference would keep nothing of act' from z = 17 on. The 16-bit types take the hardware's exponential
+// and reciprocal (1 ulp of float32), float32 the library's.
 template <int DT>
 __device__ __forceinline__ void gate(float z, int act, float& a, float& d) {
-    float p;
-    if constexpr (DT == 0)
-        p = 1.f / (1.f + expf(-z));
-    else
-        p = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+    float e, large;
+    if constexpr (DT == 0) {
+        e = expf(-fabsf(z));
+        large = 1.f / (1.f + e);
+    } else {
+        e = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(z));
+        large = __builtin_amdgcn_rcpf(1.f + e);
+    }
+    const float small = e * large, p = z < 0.f ? small : large, q = z < 0.f ? large : small;
     if (act == SDM_ACT_SIGMOID) {
         a = p;
-        d = p * (1.f - p);
+        d = p * q;
     } else {
         a = z * p;
-        d = p * (1.f + z * (1.f - p));
+        d = p * (1.f + z * q);
     }
 }
 
@@ -84,7 +89,6 @@ __device__ __forceinline__ void weight_floats(float (&f)[8], Raw<WT> r) {
 template <int DT, int WT, int NT, int NV>
 __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
     using T = elem_t<DT>;
-    using W = elem_t<WT>;
     __shared__ float red[2][16];
     const int D = static_cast<int>(a.D), id = static_cast<int>(threadIdx.x), nt = static_cast<int>(blockDim.x);
     const float inv = 1.f / static_cast<float>(D);
