@@ -14,15 +14,26 @@
  * Types. q, k, v, o and their gradients are float32, bfloat16 or float16 (dtype); g, beta, their gradients and every
  * state are float32. Products run on the matrix cores on operands split into bfloat16 parts that together hold a
  * float32's 24 bits, sums are float32: results carry float32 accuracy before the one rounding to dtype. There are no
- * atomics and the order of every sum is set by the sizes alone, so results are the same bits in every run. Values
- * that are not finite (or within 2^-8 of the largest float32) make what depends on them NaN.
+ * atomics and the order of every sum is set by the sizes alone, so results are the same bits in every run.
+ *
+ * Values that are not finite (or within 2^-8 of the largest float32) make NaN of what depends on them, and of what shares
+ * their head and their chunk of 64 tokens, tokens before them included: zeros above a triangular matrix's diagonal meet
+ * them in a product. One in v stays in its column and one in q in its token's o; the recurrent form has no chunks.
+ * Earlier chunks (in a gradient: none of the sequence), other sequences and other q/k heads keep their bits, and tokens of
+ * no run and states of no stream are not read.
  *
  * Memory. sdm_rows_t: element (b, t, h, c) is data[b*batch + t*token + h*head + c], strides in elements; g and beta
- * have no c. Token and head strides below 2^31, any element
- * alignment; dk and dv that are multiples of 8 are faster. The states are contiguous [sequences][Hv][dk][dv]. Outputs
- * must not overlap inputs or each other. Workspaces are the caller's (sdm_gdr_workspace bytes, 256-byte aligned,
- * contents free to lose after the call). Calls are asynchronous on `stream`, allocate nothing and may be captured into
- * a graph.
+ * have no c. Token and head strides below 2^31, any element alignment; dk and dv that are multiples of 8 are faster. The
+ * states are contiguous [sequences][Hv][dk][dv]. Outputs must not overlap inputs or each other. Calls are asynchronous on
+ * `stream`, allocate nothing and may be captured into a graph.
+ *
+ * Workspaces are the caller's (sdm_gdr_workspace bytes, 256-byte aligned, contents free to lose after the call). With P =
+ * 1, 2 or 3 parts for bfloat16, float16 or float32, dkp = dk up to 64, 128 or 256 and dvp = dv up to a multiple of 8, each
+ * chunk of 64 tokens (of every sequence) takes, in bytes,
+ *     forward:   Hv * 50432 + Hk * 384 P dkp
+ *     gradient:  Hv * (75008 + 8 dvp (dk + 64) + 512 dk where Hv > Hk) + Hk * 384 P dkp
+ * since the gradient holds every chunk's state and its gradient at once: with 16 value heads on 8 of 128 x 128 in bfloat16
+ * 0.74 GB for 8192 tokens, whose q, k and v are 67 MB, and 11.9 GB for 65536 tokens of twice the heads (1.1 GB).
  */
 #ifndef SDM_GDR_H
 #define SDM_GDR_H

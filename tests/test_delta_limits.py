@@ -49,3 +49,14 @@ def test_steps(B_, Hv, dk, dv, held):
     status = D.load().sdm_gdr_step(ctypes.byref(a), None)
     assert (status == B.SDM_GX_ERR_LIMIT) == (not held), status
     assert status != B.SDM_GX_OK
+
+
+@pytest.mark.parametrize("backward", [0, 1])
+@pytest.mark.parametrize("dtype,parts", [(0, 3), (1, 1), (2, 2)])
+@pytest.mark.parametrize("B_,T,Hk,Hv,dk,dv", [(2, 4096, 8, 16, 128, 128), (1, 65, 3, 3, 40, 57), (3, 1, 1, 5, 200, 256)])
+def test_workspace_is_what_the_header_says(B_, T, Hk, Hv, dk, dv, dtype, parts, backward):
+    a = D.sdm_gdr_args_t(dtype=dtype, scale=1.0, B=B_, T=T, Hk=Hk, Hv=Hv, dk=dk, dv=dv, nseq=B_)
+    dkp, dvp = 64 if dk <= 64 else 128 if dk <= 128 else 256, (dv + 7) // 8 * 8
+    head = 75008 + 8 * dvp * (dk + 64) + (512 * dk if Hv > Hk else 0) if backward else 50432
+    want = B_ * -(-T // 64) * (Hv * head + Hk * 384 * parts * dkp)
+    assert 0 <= D.load().sdm_gdr_workspace(ctypes.byref(a), backward) - want < 14 * 256
