@@ -13,7 +13,7 @@
 // chain; four more, the outputs' wavefronts, share their SIMDs and fill their waits with what the chain does not wait
 // for (Q S and P U, a step late; P^T dO, a step early), and all eight share the update of S. S, R and U (16 columns
 // each) pass through LDS as split parts, three barriers a step; everything else (K, Q, T, P and K^T fragments) comes
-// straight from memory in operand layout, one or two chunks ahead of its use. Heads of 128 in bfloat16: a step takes 1.35
+// straight from memory in operand layout, ahead of its use. Heads of 128 in bfloat16: a step takes 1.35
 // us alone and 1.87 us with 256 workgroups, each of which reads some 80 KB of operands a step (16384 tokens of 32 heads:
 // 480 us).
 #include <hip/hip_runtime.h>
@@ -179,16 +179,17 @@ struct Operands {
     __device__ __forceinline__ float whole(int chunk) const { return g.w.tok[(sv(chunk) * kTokFields + kTokEg) * 64 + 63]; }
 };
 
-// How many chunks ahead operands are fetched: a step takes less than a load from memory, so two where the registers
-// hold two chunks (the scans of 2 x 4096 tokens x 16 heads in bfloat16: 160 and 223 us with one, 153 and 212 with two);
-// with wide float32 heads not even one: K^T (and Q^T) come in the middle of their own step.
-template <int DT, int DKP, int NT, bool BACK> constexpr int kDepth = DT == 1 && DKP <= 128 && !(BACK && NT == 2) ? 2 : 1;
+// Operands are fetched one chunk ahead; in the backward scan two where the registers hold two chunks (bfloat16, the whole
+// gradient: 4096 tokens x 2 heads of 128 231 us with one and 222 with two, 2 x 4096 x 16 heads 562 and 566; the forward
+// scans take as long or longer with two, 4 x 2048 tokens x 32 heads 250 us with one and 264); with wide float32 heads not
+// even one: K^T (and Q^T) come in the middle of their own step.
+template <int DT, int DKP, int NT> constexpr int kBackDepth = DT == 1 && DKP <= 128 && NT == 1 ? 2 : 1;
 template <int DT, int DKP, int NT> constexpr bool kLate = (DT != 1 && DKP > 128) || (DT == 0 && DKP * NT >= 256);
 // k blocks of S in registers at once
 template <int DT, int DKP, int NT> constexpr int kHalf = DT == 0 ? (DKP * NT >= 256 ? 1 : 2) : DKP == 128 ? 4 : 2;
 
-// step(chunk, set), sets of operands taking turns. Where two paths meet inside a loop, registers that loads are still on
-// their way to would be moved, and the moves wait: hence no branch in it, and a loop of its own for each kind of
+// step(chunk, set), sets of operands taking turns. Where two paths meet inside a scan's loop, registers that loads are
+// still on their way to would be moved, and the moves wait: hence no branch in it, and a loop of its own for each kind of
 // wavefront.
 template <int DEPTH, class F>
 __device__ __forceinline__ void in_turn(int chunks, F step) {
@@ -207,7 +208,7 @@ __device__ __forceinline__ void in_turn(int chunks, F step) {
 template <int DT, int DKP, int NT, bool STORE>
 __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
-    constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kDepth<DT, DKP, NT, false>;
+    constexpr int HALF = kHalf<DT, DKP, NT>;
     constexpr bool LATE = kLate<DT, DKP, NT>;
     using T = elem_t<DT>;
     __shared__ Tile<3, COLS, DKP> Sx;           // S, [column][dk]
@@ -255,14 +256,14 @@ __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, c
     auto run_chain = [&](auto kn) {
         constexpr int KN = decltype(kn)::value;
         const T* vr = rows_at<const T>(a.v, w.s, hv);
-        struct Set {
+        struct {
             Frag<NP> kf[NKB], kt[MT][2];
             Frag<3> inv[KN];
             Tokens4<DT> v[NT];
             f32x4 eg, last, beta;
             float whole;
-        } set[DEPTH];
-        auto fetch_r = [&](Set& f, int chunk) {
+        } f;
+        auto fetch_r = [&](int chunk) {
             const int t0 = chunk * kChunk, n = min(kChunk, w.s.len - t0);
             from.rows(f.kf, g.w.kf, chunk);
             f.eg = from.token(kTokEg, chunk);
@@ -271,25 +272,21 @@ __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, c
             for (int c = 0; c < NT; ++c)
                 load4<DT>(f.v[c], vr + t0 * a.v.token + min(w.c0 + c * 16 + w.row, dv - 1), static_cast<int>(a.v.token), t4, n);
         };
-        auto fetch_u = [&](Set& f, int chunk) {
+        auto fetch_u = [&](int chunk) {
             from.template square<0, KN>(f.inv, g.w.inv, chunk);
             f.last = from.token(kTokLast, chunk);
         };
-        auto fetch_s = [&](Set& f, int chunk) {
+        auto fetch_s = [&](int chunk) {
             from.template cols<true>(f.kt, g.w.kt, chunk);
             f.whole = from.whole(chunk);
         };
-#pragma unroll
-        for (int i = 0; i < DEPTH; ++i) {
-            fetch_r(set[i], min(i, chunks - 1));
-            fetch_u(set[i], min(i, chunks - 1));
-            if constexpr (!LATE) fetch_s(set[i], min(i, chunks - 1));
-        }
+        fetch_r(0);
+        fetch_u(0);
+        if constexpr (!LATE) fetch_s(0);
         loads_landed();
         __builtin_amdgcn_s_setprio(2);      // over the outputs' wavefronts
-        in_turn<DEPTH>(chunks, [&](int chunk, auto turn, auto other) {
-            Set &f = set[turn], &before = set[other];
-            const int next = min(chunk + DEPTH, chunks - 1), n = min(kChunk, w.s.len - chunk * kChunk);
+        for (int chunk = 0; chunk < chunks; ++chunk) {
+            const int next = min(chunk + 1, chunks - 1), n = min(kChunk, w.s.len - chunk * kChunk);
             keep(chunk, std::true_type{});
             lds_barrier();      // S is in LDS
 #pragma unroll
@@ -300,10 +297,6 @@ __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, c
                     Frag<3> b[HALF];
                     read<HALF>(b, Sx, t * 16, k0 * 32);
                     reads_first();
-                    if (DEPTH == 2 && t == 0 && k0 == 0) {
-                        fetch_u(before, min(chunk + 1, chunks - 1));
-                        fetch_s(before, min(chunk + 1, chunks - 1));
-                    }
                     products<HALF>(x, f.kf + k0, b);
                 }
                 Rx.put(t * 16, tok, f.beta * (floats4<DT>(f.v[t], t4, held(t, n)) - f.eg * (x[0] + x[1])));
@@ -316,8 +309,8 @@ __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, c
                 read<KN>(b, Rx, t * 16, 0);
                 reads_first();
                 if (t == 0) {
-                    if constexpr (LATE) fetch_s(f, chunk);
-                    else fetch_r(f, next);
+                    if constexpr (LATE) fetch_s(chunk);
+                    else fetch_r(next);
                 }
                 f32x4 y[2] = {zero, zero};
                 products<KN>(y, f.inv, b);
@@ -326,7 +319,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, c
             }
             lds_barrier();
             update(f.kt, f.whole, std::true_type{}, [&] {
-                if constexpr (DEPTH == 1) fetch_u(f, next);
+                fetch_u(next);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     if constexpr (!STORE) Ux[chunk & 1].put(t * 16, tok, u[t]);
@@ -337,9 +330,9 @@ __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, c
                     if (w.c0 + t * 16 + w.row < g.dvp)
                         put4(g.w.u + from.sv(chunk) * 64 * g.dvp + w.c0 + t * 16 + w.row, g.dvp, t4, kChunk, u[t]);
             }
-            if constexpr (LATE) fetch_r(f, next);
-            else if constexpr (DEPTH == 1) fetch_s(f, next);
-        });
+            if constexpr (LATE) fetch_r(next);
+            else fetch_s(next);
+        }
         if constexpr (!STORE) lds_barrier();    // the last chunk's U
     };
     auto run_outputs = [&](auto kn) {
@@ -349,15 +342,15 @@ __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, c
         constexpr int KN = decltype(kn)::value, OUT = DT == 2 && HALF > 2 ? 2 : HALF;
         constexpr bool QLATE = DT == 2 && DKP * NT >= 256;
         T* orow = STORE ? nullptr : rows_at<T>(a.o, w.s, hv);
-        struct Set {
+        struct {
             Frag<NP> qf[STORE ? 1 : NKB], kt[MT][2];
             Frag<3> pm[KN];
             f32x4 eg;
             float whole;
-        } set[DEPTH];
+        } f;
         f32x4 o[NT];
         // the outputs of a chunk: P U on top of what Q S left
-        auto finish = [&](int chunk, const Frag<3>* pm) {
+        auto finish = [&](int chunk) {
             const int t0 = chunk * kChunk, n = min(kChunk, w.s.len - t0);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -365,42 +358,38 @@ __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, c
                 read<KN>(b, Ux[STORE ? 0 : chunk & 1], t * 16, 0);
                 reads_first();
                 f32x4 y[2] = {o[t], zero};
-                products<KN>(y, pm, b);
+                products<KN>(y, f.pm, b);
                 y[0] += y[1];
                 if (w.c0 + t * 16 + w.row < dv)
                     put4(orow + t0 * a.o.token + w.c0 + t * 16 + w.row, static_cast<int>(a.o.token), t4, n, y[0]);
             }
         };
-        auto fetch_q = [&](Set& f, int chunk) {
+        auto fetch_q = [&](int chunk) {
             if constexpr (!STORE) {
                 from.rows(f.qf, g.w.qf, chunk);
                 f.eg = from.token(kTokEg, chunk);
             }
         };
-        auto fetch_s = [&](Set& f, int chunk) {
+        auto fetch_s = [&](int chunk) {
             from.template cols<false>(f.kt, g.w.kt, chunk);
             f.whole = from.whole(chunk);
         };
-#pragma unroll
-        for (int i = 0; i < DEPTH; ++i) {
-            fetch_q(set[i], min(i, chunks - 1));
-            if constexpr (!STORE) from.template square<0, KN>(set[i].pm, g.w.pm, min(i, chunks - 1));
-            if constexpr (!LATE) fetch_s(set[i], min(i, chunks - 1));
-        }
+        fetch_q(0);
+        if constexpr (!STORE) from.template square<0, KN>(f.pm, g.w.pm, 0);
+        if constexpr (!LATE) fetch_s(0);
         loads_landed();
-        in_turn<DEPTH>(chunks, [&](int chunk, auto turn, auto other) {
-            Set &f = set[turn], &before = set[other];
-            const int next = min(chunk + DEPTH, chunks - 1);
+        for (int chunk = 0; chunk < chunks; ++chunk) {
+            const int next = min(chunk + 1, chunks - 1);
             keep(chunk, std::false_type{});
             lds_barrier();
             if constexpr (!STORE) {
                 if (chunk) {
-                    finish(chunk - 1, before.pm);
-                    from.template square<0, KN>(before.pm, g.w.pm, min(chunk + DEPTH - 1, chunks - 1));
+                    finish(chunk - 1);
+                    from.template square<0, KN>(f.pm, g.w.pm, chunk);
                 }
             }
             lds_barrier();
-            if constexpr (LATE) fetch_s(f, chunk);
+            if constexpr (LATE) fetch_s(chunk);
             if constexpr (!STORE) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
@@ -415,19 +404,15 @@ __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, c
                     o[t] = (x[0] + x[1]) * (f.eg * a.scale);
                 }
             }
-            if constexpr (!LATE && !QLATE) fetch_q(f, next);
+            if constexpr (!LATE && !QLATE) fetch_q(next);
             lds_barrier();
             update(f.kt, f.whole, std::false_type{}, [] {});
-            if constexpr (LATE || QLATE) fetch_q(f, next);
-            if constexpr (!LATE) fetch_s(f, next);
-        });
+            if constexpr (LATE || QLATE) fetch_q(next);
+            if constexpr (!LATE) fetch_s(next);
+        }
         if constexpr (!STORE) {
             lds_barrier();
-            const int last = chunks - 1;
-            if (DEPTH == 1 || (last & 1) == 0)
-                finish(last, set[0].pm);
-            else
-                finish(last, set[DEPTH - 1].pm);
+            finish(chunks - 1);
         }
     };
     using One = std::integral_constant<int, kSkipZero<DT, DKP> ? 1 : 2>;
@@ -450,7 +435,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan(const GdrLaunch g, c
 template <int DT, int DKP, int NT>
 __global__ __launch_bounds__(kScanThreads, 2) void gdr_scan_back(const GdrLaunch g, const int total) {
     constexpr int NP = kParts<DT>, NKB = DKP / 32, MT = Tiles<DKP>::MT, COLS = 16 * NT;
-    constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kDepth<DT, DKP, NT, true>;
+    constexpr int HALF = kHalf<DT, DKP, NT>, DEPTH = kBackDepth<DT, DKP, NT>;
     constexpr bool LATE = kLate<DT, DKP, NT>;
     using T = elem_t<DT>;
     __shared__ Tile<3, COLS, DKP> Sx;           // dS, [column][dk]
