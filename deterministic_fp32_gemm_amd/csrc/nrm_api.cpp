@@ -61,6 +61,8 @@ int check(const sdm_nrm_args_t* a, bool backward) {
     for (int i = 0; i < ni + no; ++i) {
         const Row& r = i < ni ? in[i] : out[i - ni];
         if (r.ld < a->D || r.ld >= SDM_GX_LD_LIMIT) return SDM_GX_ERR_STRIDE;
+        // before any extent is formed: the product may leave 64 bits
+        if (double(a->rows) * double(r.ld) >= 4e17) return SDM_GX_ERR_STRIDE;
         if (!aligned(r.p, es)) return SDM_GX_ERR_ALIGN;
     }
     const void* w[] = {o ? a->w_post : nullptr, o ? a->scale : nullptr, a->w_pre,

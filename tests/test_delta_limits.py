@@ -60,3 +60,19 @@ def test_workspace_is_what_the_header_says(B_, T, Hk, Hv, dk, dv, dtype, parts, 
     head = 75008 + 8 * dvp * (dk + 64) + (512 * dk if Hv > Hk else 0) if backward else 50432
     want = B_ * -(-T // 64) * (Hv * head + Hk * 384 * parts * dkp)
     assert 0 <= D.load().sdm_gdr_workspace(ctypes.byref(a), backward) - want < 14 * 256
+
+
+@pytest.mark.parametrize("backward", [0, 1])
+@pytest.mark.parametrize("rows,ld,status", [
+    (1 << 39, 1 << 30, B.SDM_GX_ERR_STRIDE),        # 2^69 elements: past what an address holds
+    (1 << 32, (1 << 31) - 1, B.SDM_GX_ERR_STRIDE), (1 << 20, 1 << 20, B.SDM_GX_OK)])
+def test_rows_past_an_address(rows, ld, status, backward):
+    a = D.sdm_nrm_args_t(dtype=1, wtype=1, act=2, eps=1e-6, rows=rows, D=100)
+    at = FAR
+    for n in ("x", "o", "z", "w_post", "w_pre", "scale", "x_new", "y", "rstd", "dxn", "dy", "dx", "d_o", "dz", "dw_post",
+              "dw_pre", "dscale"):
+        setattr(a, n, at)
+        at += FAR
+    for n in ("x", "o", "z", "xn", "y", "dxn", "dy", "dx", "do", "dz"):
+        setattr(a, "ld_" + n, ld)
+    assert D.load().sdm_nrm_check(ctypes.byref(a), backward) == status
