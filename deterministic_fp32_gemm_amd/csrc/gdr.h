@@ -46,8 +46,8 @@ inline int parts_of(int dtype) { return dtype == SDM_F32 ? 3 : dtype == SDM_BF16
 constexpr int64_t kMaxThreads = int64_t(1) << 32;
 constexpr int kChunkThreads = 256, kScanThreads = 512, kGradThreads = 512, kStepThreads = 256;
 // Tiles of 16 state columns that a scan's workgroup owns: two where one each would be more than a workgroup a CU, half
-// the operands for 1.45 times the step (tokens x 32 heads of 128 in bfloat16, forward: 4 x 2048 383 us with one tile, 294
-// with two; 2 x 2048 180 and 150).
+// the operands for 1.6 times the step (forward, dk = 128, bfloat16: a lone head of 16384 tokens 325 us with one tile, 508
+// with two; 32 heads of 4 x 2048 tokens 341 and 250, of 2 x 2048 145 and 119).
 inline int scan_tiles(const sdm_gdr_args_t& a, int dkp) {
     return dkp <= 128 && (a.dv + 15) / 16 * a.Hv * a.nseq > 256 ? 2 : 1;
 }
@@ -55,9 +55,10 @@ inline int64_t scan_groups(const sdm_gdr_args_t& a, int dkp) {
     const int64_t cols = 16 * scan_tiles(a, dkp);
     return (a.dv + cols - 1) / cols * a.Hv * a.nseq;
 }
-// State columns of a step's workgroup: 32 where those of 128 would be at most one a CU (bfloat16, dk = dv = 128, us a step
-// with 32 and with 128 columns: 16 heads 6.2 and 9.0, 256 10.9 and 14.6, 384 17.7 and 16.1, 2048 70 and 52); for dk = 256,
-// whose rows fill the registers, 64 always (32: 16 heads 13.9 and 13.6, 128 heads 54 and 18).
+// State columns of a step's workgroup: 32 where those of 128 would be at most one a CU (bfloat16, dk = dv = 128, us a
+// call with 32 and with 128 columns: 256 heads 11.4 and 14.5, 384 17.1 and 15.6, 512 19.3 and 16.8, 2048 70 and 50; of
+// fewer heads the call on the host shows, not the kernel's 6.2 and 9.0 for 16); for dk = 256, whose rows fill the
+// registers, 64 always (a form of 32 took 54 us for 128 heads that take 18).
 inline int step_columns(const sdm_gdr_step_args_t& a) {
     if (a.dk > 128) return 64;
     return a.B * a.Hv * ((a.dv + 127) / 128) <= 256 ? 32 : 128;

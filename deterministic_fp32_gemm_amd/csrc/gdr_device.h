@@ -5,8 +5,8 @@
 // the part products whose parts' numbers add up to 2 or less; what is left out is below 2^-25 of the product, so a
 // product costs 6 matrix-core steps and is as exact as float32's own (a quarter of the time of a float32 matrix-core
 // product). Elements that are bfloat16 to begin with are one part (3 steps against a float32 operand), float16 ones
-// two. Results of 16 bits need them all too: Q S and P U can each be thousands of times their sum, the output, where a key
-// overwrites what the state holds.
+// two. Results of 16 bits need them all too: Q S and P U can each be thousands of times their sum, the output, where a
+// key overwrites what the state holds.
 //
 // Fragments. One matrix-core operand of v_mfma_f32_16x16x32_bf16: lane l holds row l % 16, elements
 // 8 (l / 16) .. + 7 of a 32-wide block of the summed axis. Both operands have this layout, each with its summed axis

@@ -12,9 +12,10 @@
 //
 // One workgroup per chunk and value head. Each of eight wavefronts owns dk columns of dq and dk for all 64 tokens (half
 // of them for dk <= 64), so S and dE are read and split once; dO, U and dR are staged in LDS by 64 columns of dv at a
-// time. About 18 x 64 dk dv flops on up to six steps each: bounded by the matrix cores and the LDS reads that feed them, which one
-// workgroup a CU (registers) does not overlap: 2 x 4096 tokens of 16 heads of 128 in bfloat16 take 200 us, the matrix
-// cores busy for 24% of it.
+// time. About 18 x 64 dk dv flops on up to six steps each. One workgroup a CU (104 KB of LDS, and some 240 registers at
+// two wavefronts a SIMD; either alone would allow no second) leaves its waits open: for the loads of a block of 64
+// columns, which are used as soon as they are asked for, and for the LDS reads that feed the matrix cores. 2 x 4096 tokens
+// of 16 heads of 128 in bfloat16 take 191 us, 578 MB at 3.0 TB/s, the matrix cores busy for 24% of it.
 //
 // Token order. A result tile's lane holds rows 4 p .. 4 p + 3 (p = lane / 16), a fragment's lane elements 8 p .. 8 p + 7.
 // Row r of token tile j is token 32 (j / 2) + 8 (r / 4) + 4 (j % 2) + r % 4: then the four tokens of a result lane are
@@ -423,8 +424,9 @@ __global__ __launch_bounds__(256) void gdr_shared(const GdrLaunch g) {
 template <int DT>
 hipError_t run(const GdrLaunch& g, hipStream_t s) {
     // One workgroup for all value heads of a q/k head saves their parts of dq and dk a way through memory and a kernel;
-    // few chunks go by one head each, for time (chunks x q/k heads, two value heads each, 128 wide in bfloat16, the whole
-    // gradient: 32: 126 us together, 102 apart; 128: 118 both; 256: 174 and 196; 1024: 586 and 650).
+    // few chunks go by one head each, for time (sequences of one chunk with two q/k heads, two value heads each, 128 wide
+    // in bfloat16, the whole gradient by chunks x q/k heads: 32: 71 us together, 67 apart; 128: 109 and 111; 256: 182 and
+    // 206; 1024: 720 and 775).
     const int rr = static_cast<int>(g.a.Hv / g.a.Hk);
     const int heads = g.dkp <= 128 && static_cast<int64_t>(g.slots) * g.a.Hk >= 256 ? rr : 1;
     const dim3 grid(static_cast<unsigned>(g.slots), static_cast<unsigned>(g.a.Hv / heads));

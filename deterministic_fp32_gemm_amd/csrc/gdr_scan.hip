@@ -13,9 +13,8 @@
 // chain; four more, the outputs' wavefronts, share their SIMDs and fill their waits with what the chain does not wait
 // for (Q S and P U, a step late; P^T dO, a step early), and all eight share the update of S. S, R and U (16 columns
 // each) pass through LDS as split parts, three barriers a step; everything else (K, Q, T, P and K^T fragments) comes
-// straight from memory in operand layout, ahead of its use. Heads of 128 in bfloat16: a step takes 1.35
-// us alone and 1.87 us with 256 workgroups, each of which reads some 80 KB of operands a step (16384 tokens of 32 heads:
-// 480 us).
+// straight from memory in operand layout, ahead of its use. Heads of 128 in bfloat16: a step takes 1.22 us alone and 1.90 us
+// with 256 workgroups, each of which reads some 86 KB of operands a step (16384 tokens of 32 heads: 487 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

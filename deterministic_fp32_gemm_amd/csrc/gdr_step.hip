@@ -7,7 +7,7 @@
 // of one stream and head: each thread 4 columns of dk / (256 / CT) rows, held in registers from the load to the store
 // whatever the number of tokens; the sums over dk go through LDS. Columns of S never meet, so small batches take
 // CT = 8 (32 columns a workgroup, four times the workgroups of CT = 32). 256 streams of 32 heads of 128 x 128 take 209 us,
-// 4.8 TB/s (a copy of 1 GB runs at 5.06); one stream of 16 heads 6 to 7 us.
+// 4.85 TB/s (a copy of 1 GB runs at 5.1); one stream of 16 heads 6 to 7 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -103,13 +103,13 @@ int check(const sdm_nrm_args_t* a, bool backward) {
 
 NrmPlan plan(const sdm_nrm_args_t* a, bool backward) {
     NrmPlan p{};
-    // 16384 rows of 4096: forward 109 us in bfloat16 and 256 in float32 with 256 threads of two groups of columns, 113
-    // and 250 with 512 of one; backward in bfloat16, which holds two sums a column beside, 340 with 256 of two, 215 with
+    // 16384 rows of 4096: forward 111 us in bfloat16 and 260 in float32 with 256 threads of two groups of columns, 113
+    // and 258 with 512 of one; backward in bfloat16, which holds two sums a column beside, 214 with 256 of two, 198 with
     // 512 of one
     const bool middle = a->D > 2048 && a->D <= 4096;
     p.most = a->D <= 512 ? 64 : a->D <= 1024 ? 128 : a->D <= 2048 || (middle && !backward) ? 256 : 512;
     p.vecs = static_cast<int>(cdiv(a->D, p.most * 8));
-    // No wavefronts past the row (20000 rows of 2050 in bfloat16: backward 250 us, 268 with all 8); the backward of long
+    // No wavefronts past the row (20000 rows of 2050 in bfloat16: backward 239 us, 260 with all 8); the backward of long
     // rows keeps its sums by full width.
     p.threads = backward && p.vecs > 1 ? p.most : static_cast<int>(cdiv(a->D, p.vecs * 512)) * 64;
     // forward: workgroups for up to 8 wavefronts a SIMD, whole ones a CU; backward: each leaves a partial sum, so a quarter

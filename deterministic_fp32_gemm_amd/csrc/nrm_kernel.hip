@@ -15,8 +15,8 @@
 namespace sdm_delta {
 namespace {
 
-// Rows are read once: past the caches (16384 x 4096 rows in bfloat16, inputs in turn, before the next row was fetched
-// ahead: forward 169 -> 159 us).
+// Rows are read once: past the caches (16384 x 4096 rows, inputs in turn: in bfloat16 forward 133 -> 111 us, backward 201 ->
+// 198; in float32 forward 247 -> 260, the other way).
 constexpr bool kStream = true;
 
 // The sum of v over the workgroup, in an order set by the lane and wavefront numbers alone. `buf` alternates between
@@ -83,9 +83,9 @@ __device__ __forceinline__ void weight_floats(float (&f)[8], Raw<WT> r) {
 }
 
 // The next row's loads are in flight while a row is worked on (in bfloat16, inputs in turn: 16384 x 4096 rows 157 -> 109
-// us, 6.2 TB/s; 8192 x 8192 197 -> 119; 2048 x 4096 29.6 -> 21.2). A row's end is loaded without a branch (load_row) and
+// us, 6.1 TB/s; 8192 x 8192 197 -> 119; 2048 x 4096 29.6 -> 21.2). A row's end is loaded without a branch (load_row) and
 // moved once it has come; with a branch its loads would wait for one another and for the row before them (20000 rows of
-// 1111 in bfloat16: forward 110 -> 63 us and backward 277 -> 133, the wavefronts past the row left out too).
+// 1111 in bfloat16: forward 110 -> 63 us and backward 277 -> 131, the wavefronts past the row left out too).
 template <int DT, int WT, int NT, int NV>
 __global__ __launch_bounds__(NT) void nrm_forward(const sdm_nrm_args_t a) {
     using T = elem_t<DT>;

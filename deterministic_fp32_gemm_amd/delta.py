@@ -142,7 +142,7 @@ def _tensor(t, name: str, shape, dtype=None, device=None):
 
 
 def _inner(t):
-    """t with its last axis contiguous and no negative or expanded layout the kernels could not address."""
+    """t, copied if its last axis is not contiguous."""
     return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
 
 
