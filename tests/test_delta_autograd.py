@@ -241,3 +241,43 @@ def test_on_a_named_stream():
     assert torch.equal(o, want_o)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_captured():
+    """A block's forward and backward captured through torch's graph, replayed on new inputs with eager passes between."""
+    names = ("q", "k", "v", "g", "beta")
+
+    def both(t, n):
+        o, s = sdm.gdr_forward(*(t[x] for x in names))
+        x_new, y, _ = sdm.norm_forward(n["x"], o.flatten(2).flatten(0, 1)[:, :40], n["z"], n["w_post"], n["w_pre"], n["scale"])
+        need = [*(t[x] for x in names), *n.values()]
+        loss = (x_new * x_new).sum() + (y * n["x"].detach()).sum() + s.square().sum()
+        return x_new, y, s, *torch.autograd.grad(loss, need, allow_unused=True)
+
+    def inputs(seed):
+        n = norm("cuda", seed, rows=140)
+        n.pop("o")
+        return leaves(gdr("cuda", seed)), leaves(n)
+
+    sets = [inputs(i) for i in range(3)]
+    buf = inputs(0)
+    want = [both(*s) for s in sets]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(*buf)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(*buf)
+    for s, w in list(zip(sets, want)) * 2:
+        with torch.no_grad():
+            for to, src in zip(buf, s):
+                for n in to:
+                    to[n].copy_(src[n])
+        graph.replay()
+        both(*s)
+        torch.cuda.synchronize()
+        for a, b in zip(got, w):
+            assert torch.equal(a, b)
