@@ -50,11 +50,12 @@ def code_objects(path: str, llvm: str):
 
 
 def registers(operand: str) -> set:
-    m = re.fullmatch(r"-?\|?([av])(\d+)\|?", operand)
-    if m:
-        return {m[1] + m[2]}
-    m = re.fullmatch(r"-?([av])\[(\d+):(\d+)\]", operand)
-    return {m[1] + str(i) for i in range(int(m[2]), int(m[3]) + 1)} if m else set()
+    """The vector registers that an operand names, with or without a sign, an absolute value or modifiers after it."""
+    m = re.match(r"(?:-|neg\()?(?:\||abs\()?([av])(?:(\d+)\b|\[(\d+):(\d+)\])", operand)
+    if not m:
+        return set()
+    lo, hi = (m[2], m[2]) if m[2] else (m[3], m[4])
+    return {m[1] + str(i) for i in range(int(lo), int(hi) + 1)}
 
 
 def kernels(text: str) -> dict:

@@ -84,6 +84,22 @@ def test_reads(between, early):
     assert bool(_code_check.early_reads(code)) == early
 
 
+@pytest.mark.parametrize("operand,names", [
+    ("v3", {"v3"}), ("-v3", {"v3"}), ("|v3|", {"v3"}), ("-|a12|", {"a12"}), ("v[2:4]", {"v2", "v3", "v4"}), ("s3", set()),
+    ("v[2:3] offset:16", {"v2", "v3"}), ("v3 quad_perm:[1", {"v3"}), ("v3 row_half_mirror row_mask:0xf", {"v3"}),
+    ("neg(v3)", {"v3"}), ("vcc", set()), ("off", set()), ("0x3f", set()), ("vmcnt(0)", set())])
+def test_registers_of_an_operand(operand, names):
+    assert _code_check.registers(operand) == names
+
+
+@pytest.mark.parametrize("read", [step("ds_write_b128", "v30", "v[0:3] offset:16"),
+                                  step("v_mov_b32_dpp", "v9", "v2 quad_perm:[1", "0", "3", "2] row_mask:0xf bank_mask:0xf")])
+def test_reads_with_modifiers(read):
+    product = step("v_mfma_f32_16x16x32_bf16", "v[0:3]", "v[4:7]", "v[8:11]", "v[0:3]")
+    assert _code_check.early_reads([product, read, step("s_endpgm")])
+    assert not _code_check.early_reads([product, step("s_nop", "7"), read, step("s_endpgm")])
+
+
 def test_an_unknown_product_is_refused():
     with pytest.raises(_code_check.CodeError, match="not known"):
         _code_check.early_reads([step("v_mfma_f32_32x32x16_bf16", "v[0:15]", "v[16:19]", "v[20:23]", "v[0:15]")])
