@@ -7,7 +7,9 @@ consumer of the updated d_u (page "... gx_pa2_cuda.py", gx_pa2_kernel), is in th
 include/sdm_gx_gemm.h and include/sdm_gx_pa2.h; the functions below carry the same names and only marshal arguments.
 
 The gated delta rule (gdr_forward, gdr_backward, gdr_step) and the block norm (norm_forward, norm_backward) are in
-libsdm_delta: include/sdm_gdr.h, include/sdm_nrm.h and delta.py.
+libsdm_delta: include/sdm_gdr.h, include/sdm_nrm.h and delta.py. The gated linear recurrence (glr_forward, glr_backward,
+glr_step), rows in 8 bits (norm_quant, quant_rows) and the gated feed-forward product (ffn_forward, ffn_backward) are in
+libsdm_block: include/sdm_glr.h, include/sdm_qnt.h, include/sdm_ffn.h and block.py.
 """
 
 from ._binding import (  # noqa: F401
@@ -71,3 +73,13 @@ from .delta import (  # noqa: F401
     norm_forward,
 )
 from .delta import load as load_delta  # noqa: F401
+from .block import (  # noqa: F401
+    ffn_backward,
+    ffn_forward,
+    glr_backward,
+    glr_forward,
+    glr_step,
+    norm_quant,
+    quant_rows,
+)
+from .block import load as load_block  # noqa: F401

@@ -1,4 +1,4 @@
-"""Ahead-of-time build of libsdm_gx_gemm.so and libsdm_delta.so for gfx950 with hipcc (in-tree, no JIT cache)."""
+"""Ahead-of-time build of libsdm_gx_gemm.so, libsdm_delta.so and libsdm_block.so for gfx950 with hipcc (in-tree, no JIT cache)."""
 
 from __future__ import annotations
 
@@ -18,7 +18,11 @@ SOURCES = ("gx_gemm_kernel.hip", "gx_gemm_mfma.hip", "gx_gemm_api.cpp", "gx_pa2_
 # the gated delta rule and the block norm: a library of their own
 DELTA_LIB_PATH = os.path.join(PKG, "libsdm_delta.so")
 DELTA_SOURCES = ("gdr_chunk.hip", "gdr_scan.hip", "gdr_grad.hip", "gdr_step.hip", "gdr_api.cpp", "nrm_kernel.hip",
-                 "nrm_api.cpp")
+                 "nrm_api.cpp", "delta_host.cpp")
+# the gated linear recurrence, rows in 8 bits and the gated feed-forward product: another
+BLOCK_LIB_PATH = os.path.join(PKG, "libsdm_block.so")
+BLOCK_SOURCES = ("ffn_product.hip", "glr_kernel.hip", "qnt_kernel.hip", "ffn_few.hip", "ffn_lay.hip", "glr_api.cpp",
+                 "qnt_api.cpp", "ffn_api.cpp", "delta_host.cpp")
 JOBS = 6    # compilers at once
 
 # Numerics-relevant flags: no contraction or fast-math (the chain's fmaf and the final add are what runs), f32
@@ -85,6 +89,12 @@ def build_delta(out: str = DELTA_LIB_PATH, verbose: bool = False, sources=DELTA_
     return build(out, verbose, sources, lambda path: _code_check.verify(path, llvm()))
 
 
+def build_block(out: str = BLOCK_LIB_PATH, verbose: bool = False, sources=BLOCK_SOURCES) -> str:
+    """The same for the gated linear recurrence, rows in 8 bits and the gated feed-forward product, with the same check."""
+    return build(out, verbose, sources, lambda path: _code_check.verify(path, llvm(), _code_check.BLOCK_WAITS))
+
+
 if __name__ == "__main__":
     print(build(verbose=True))
     print(build_delta(verbose=True))
+    print(build_block(verbose=True))

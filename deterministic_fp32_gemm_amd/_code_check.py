@@ -1,4 +1,4 @@
-"""Checks of a built library's code objects that no source can promise, made by every build of libsdm_delta.
+"""Checks of a built library's code objects that no source can promise, made by every build of libsdm_delta and libsdm_block.
 
 A matrix-core result may be read only some wait states after its product; the hardware does not wait by itself and the
 compiler puts the wait there. This one counts it along one path where two lead from the product to the read: of
@@ -22,6 +22,9 @@ TARGET = "hipv4-amdgcn-amd-amdhsa--gfx950"
 MAGIC = b"__CLANG_OFFLOAD_BUNDLE__"
 # wait states before a vector instruction may read the result (4 passes: 8; the float32 product of 8 passes: 10)
 WAITS = {"v_mfma_f32_16x16x32_bf16": 8, "v_mfma_f32_16x16x4_f32": 10}
+# libsdm_block's beside them (8 passes: 12; 16 passes: 20)
+BLOCK_WAITS = {**WAITS, "v_mfma_f32_16x16x32_f16": 8, "v_mfma_f32_16x16x32_fp8_fp8": 8, "v_mfma_f32_32x32x16_bf16": 12,
+               "v_mfma_f32_32x32x16_f16": 12, "v_mfma_f32_32x32x64_f8f6f4": 20}
 _STORES = ("ds_", "global_", "buffer_", "scratch_", "flat_")
 
 
@@ -85,15 +88,15 @@ def kernels(text: str) -> dict:
     return found
 
 
-def early_reads(code) -> list:
+def early_reads(code, waits=WAITS) -> list:
     """Reads (or overwrites) of a product's result before its wait is over, on any path."""
     bad = []
     for i, (op, operands, _) in enumerate(code):
         if not op.startswith(("v_mfma", "v_smfmac")):
             continue
-        if op not in WAITS:
+        if op not in waits:
             raise CodeError(f"{op}: its wait states are not known here")
-        need, result = WAITS[op], registers(operands[0])
+        need, result = waits[op], registers(operands[0])
         todo, seen = [(i + 1, 0)], {}
         while todo:
             at, waited = todo.pop()
@@ -122,7 +125,7 @@ def early_reads(code) -> list:
     return bad
 
 
-def verify(path: str, llvm: str) -> int:
+def verify(path: str, llvm: str, waits=WAITS) -> int:
     """The number of matrix products of a library's kernels; raises CodeError for code that must not run."""
     products = 0
     for notes, text in code_objects(path, llvm):
@@ -130,7 +133,7 @@ def verify(path: str, llvm: str) -> int:
             if any(int(n) for n in re.findall(rf"\.{field}:\s*(\d+)", notes)):
                 raise CodeError(f"{path}: a kernel uses scratch memory ({field})")
         for name, code in kernels(text).items():
-            bad = early_reads(code)
+            bad = early_reads(code, waits)
             if bad:
                 raise CodeError(f"{path}: {name} reads a matrix-core result too early: {bad[0]}")
             if any(op.startswith("v_pk_") and "f32" in op for op, _, _ in code):

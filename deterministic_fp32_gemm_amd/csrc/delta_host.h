@@ -1,4 +1,4 @@
-// Host side shared by the delta entry points: device and pointer checks, extents.
+// Host side shared by the entry points of libsdm_delta and libsdm_block: device and pointer checks, extents.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -9,7 +9,9 @@
 
 namespace sdm_delta {
 
-int record_hip_error(hipError_t e);             // keeps e for sdm_delta_last_hip_error, returns SDM_GX_ERR_HIP
+int record_hip_error(hipError_t e);             // keeps e for last_hip_error, returns SDM_GX_ERR_HIP
+int last_hip_error();                           // of this host thread's calls of this library
+const char* status_text(int code);
 int current_gfx950(int* dev);                   // the current device, SDM_GX_ERR_DEVICE if it is not gfx950
 int pointer_on(const void* p, int dev);         // SDM_GX_OK: device memory of dev
 

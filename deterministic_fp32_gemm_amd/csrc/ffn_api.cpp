@@ -1,0 +1,276 @@
+// Host entry points of the gated feed-forward product (sdm_ffn.h): argument checks, workspaces, the order of the launches.
+// The arithmetic is in the ffn_*.hip files.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/sdm_ffn.h"
+#include "delta_host.h"
+#include "ffn.h"
+
+using namespace sdm_delta;
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 21, kMaxWidth = int64_t(1) << 20;    // 256 rows of any operand stay below 2 GB
+constexpr int64_t kMaxThreads = int64_t(1) << 32;
+
+int64_t size_of(int dtype) { return dtype == SDM_E4M3 ? 1 : elem_size(dtype); }
+int64_t up_to(int64_t n, int64_t m) { return cdiv(n, m) * m; }
+
+struct Row {
+    const void* p;
+    int64_t ld, rows, cols, size;
+};
+
+int check(const sdm_ffn_args_t* a, bool backward) {
+    if (!a) return SDM_GX_ERR_ARG;
+    const bool bytes = a->dtype == SDM_E4M3;
+    if (a->dtype < SDM_F32 || a->dtype > SDM_E4M3 || (bytes && backward)) return SDM_GX_ERR_ARG;
+    if (bytes ? a->otype != SDM_BF16 && a->otype != SDM_F16 : a->otype != a->dtype) return SDM_GX_ERR_ARG;
+    if (a->act < SDM_ACT_NONE || a->act > SDM_ACT_GELU) return SDM_GX_ERR_ARG;
+    if (a->M < (backward ? 1 : 0) || a->M > kMaxRows || a->K < 1 || a->K > kMaxWidth || a->F < 1 || a->F > kMaxWidth) return SDM_GX_ERR_SHAPE;
+    if (!a->x || !a->wg || !a->wu) return SDM_GX_ERR_NULL;
+    if (bytes ? !a->sx || !a->sg || !a->su : a->sx || a->sg || a->su) return bytes ? SDM_GX_ERR_NULL : SDM_GX_ERR_ARG;
+    const int64_t es = size_of(a->dtype), os = elem_size(a->otype), M = a->M, K = a->K, F = a->F;
+    Row in[8], out[4];
+    int ni = 0, no = 0;
+    in[ni++] = {a->x, a->ld_x, M, K, es};
+    in[ni++] = {a->wg, a->ld_wg, F, K, es};
+    in[ni++] = {a->wu, a->ld_wu, F, K, es};
+    if (bytes) {
+        in[ni++] = {a->sx, 1, M, 1, 4};
+        in[ni++] = {a->sg, 1, F, 1, 4};
+        in[ni++] = {a->su, 1, F, 1, 4};
+    }
+    if (backward) {
+        if (!a->dh || !a->gate || !a->up || !a->dx || !a->dwg || !a->dwu) return SDM_GX_ERR_NULL;
+        in[ni++] = {a->dh, a->ld_dh, M, F, es};
+        in[ni++] = {a->gate, a->ld_gate, M, F, 4};
+        in[ni++] = {a->up, a->ld_up, M, F, 4};
+        out[no++] = {a->dx, a->ld_dx, M, K, es};
+        out[no++] = {a->dwg, a->ld_dwg, F, K, es};
+        out[no++] = {a->dwu, a->ld_dwu, F, K, es};
+    } else {
+        if (!a->h || !a->gate != !a->up) return SDM_GX_ERR_NULL;
+        out[no++] = {a->h, a->ld_h, M, F, os};
+        if (a->gate) {
+            out[no++] = {a->gate, a->ld_gate, M, F, 4};
+            out[no++] = {a->up, a->ld_up, M, F, 4};
+        }
+    }
+    for (int i = 0; i < ni + no; ++i) {
+        const Row& r = i < ni ? in[i] : out[i - ni];
+        if (r.ld < r.cols || r.ld >= SDM_GX_LD_LIMIT) return SDM_GX_ERR_STRIDE;
+        if (!aligned(r.p, r.size)) return SDM_GX_ERR_ALIGN;
+    }
+    auto span = [](const Row& r) { return extent(r.p, r.rows ? ((r.rows - 1) * r.ld + r.cols) * r.size : 0); };     // below 2^55
+    for (int i = 0; i < no; ++i) {
+        for (int j = i + 1; j < no; ++j)
+            if (overlap(span(out[i]), span(out[j]))) return SDM_GX_ERR_OVERLAP;
+        for (int j = 0; j < ni; ++j)
+            if (overlap(span(out[i]), span(in[j]))) return SDM_GX_ERR_OVERLAP;
+    }
+    return SDM_GX_OK;
+}
+
+// Workspace taken piece by piece; without a base it only counts.
+struct Space {
+    char* base;
+    int64_t used;
+    char* take(int64_t bytes) {
+        char* p = base ? base + used : nullptr;
+        used += up_to(bytes, 256);
+        return p;
+    }
+};
+
+// A product's operand from rows of `src`: where they lie, or laid out anew.
+struct Laid {
+    FfnOperand o;
+    FfnLay lay;
+    bool anew;
+};
+Laid operand(const void* src, int64_t ld, int64_t R, int64_t C, int dtype, Space* s) {
+    const int64_t es = size_of(dtype);
+    Laid l{};
+    l.anew = dtype == SDM_F32 || !aligned(src, 16) || ld * es % 16 || C * es % 16 || ld * es >= (int64_t(1) << 22);
+    if (!l.anew) {
+        l.o = FfnOperand{static_cast<const char*>(src), ld * es, 0};
+        return l;
+    }
+    const int64_t part = dtype == SDM_F32 ? 2 : es, pad = up_to(C, 16 / part), row = pad * part, plane = up_to(R * row, 256);
+    char* p = s->take(plane * (dtype == SDM_F32 ? 3 : 1));
+    l.o = FfnOperand{p, row, plane};
+    l.lay = FfnLay{src, ld, R, C, dtype, p, row, plane, pad};
+    return l;
+}
+
+// Float32's six part products, smallest first; others have one part.
+void segments(FfnProduct* p, int dtype) {
+    constexpr int a[] = {2, 1, 0, 1, 0, 0}, b[] = {0, 1, 2, 0, 1, 0};
+    p->segments = dtype == SDM_F32 ? 6 : 1;
+    for (int i = 0; i < p->segments; ++i) {
+        p->aparts |= static_cast<uint32_t>(dtype == SDM_F32 ? a[i] : 0) << (2 * i);
+        p->bparts |= static_cast<uint32_t>(dtype == SDM_F32 ? b[i] : 0) << (2 * i);
+    }
+    p->type = dtype == SDM_E4M3 ? kE4m3 : dtype == SDM_F16 ? kF16 : kBf16;
+}
+
+// 256 x 256 tiles read half of what 128 x 128 ones do for each product, but two of the latter fit a CU: the large ones where
+// there are enough of them for every CU.
+int tile_for(int64_t M, int64_t N, bool pair) { return cdiv(M, 256) * cdiv(N, pair ? 128 : 256) >= 256 ? 256 : 128; }
+bool too_many(const FfnProduct& p, bool pair) { return cdiv(p.M, p.tile) * cdiv(p.N, pair ? p.tile / 2 : p.tile) * 256 >= kMaxThreads; }
+
+struct Forward {
+    Laid x, wg, wu;
+    int64_t bytes;      // of the workspace
+};
+Forward forward_plan(const sdm_ffn_args_t* a, char* ws) {
+    Space s{ws, 0};
+    Forward f{};
+    if (a->M <= kFfnFewRows) return f;
+    f.x = operand(a->x, a->ld_x, a->M, a->K, a->dtype, &s);
+    f.wg = operand(a->wg, a->ld_wg, a->F, a->K, a->dtype, &s);
+    f.wu = operand(a->wu, a->ld_wu, a->F, a->K, a->dtype, &s);
+    f.bytes = s.used;
+    return f;
+}
+
+struct Backward {
+    FfnGrad grad;
+    FfnLay wg, wu, x;
+    FfnOperand rows, cols, w, xt;
+    int64_t bytes;
+};
+Backward backward_plan(const sdm_ffn_args_t* a, char* ws) {
+    Space s{ws, 0};
+    Backward b{};
+    const int parts = a->dtype == SDM_F32 ? 3 : 1;
+    const int64_t M = a->M, K = a->K, F = a->F, Mp = up_to(M, 8), Fp = up_to(F, 8);
+    auto area = [&](int64_t rows, int64_t cols, FfnOperand* o) {
+        const int64_t plane = up_to(rows * cols * 2, 256);
+        char* p = s.take(plane * parts);
+        *o = FfnOperand{p, cols * 2, plane};
+        return p;
+    };
+    char* rows = area(M, 2 * Fp, &b.rows);
+    char* cols = area(2 * F, Mp, &b.cols);
+    char* w = area(K, 2 * Fp, &b.w);
+    char* xt = area(K, Mp, &b.xt);
+    b.grad = FfnGrad{a->dh, a->gate, a->up, a->ld_dh, a->ld_gate, a->ld_up, M, F, Mp, Fp, a->dtype, a->act, rows, cols, b.rows.plane, b.cols.plane};
+    b.wg = FfnLay{a->wg, a->ld_wg, F, K, a->dtype, w, b.w.ld, b.w.plane, Fp};
+    b.wu = b.wg;
+    b.wu.src = a->wu;
+    b.wu.ld = a->ld_wu;
+    b.wu.dst = w + Fp * 2;
+    b.x = FfnLay{a->x, a->ld_x, M, K, a->dtype, xt, b.xt.ld, b.xt.plane, Mp};
+    b.bytes = s.used;
+    return b;
+}
+
+int prepare(const sdm_ffn_args_t* a, bool backward, int64_t need, void* ws, int64_t ws_bytes) {
+    if (need && !ws) return SDM_GX_ERR_NULL;
+    if (!aligned(ws, 256)) return SDM_GX_ERR_ALIGN;
+    if (ws_bytes < need) return SDM_GX_ERR_LIMIT;
+    int dev = 0, st = current_gfx950(&dev);
+    if (st) return st;
+    const void* ps[] = {a->x, a->wg, a->wu, a->sx, a->sg, a->su, a->gate, a->up, need ? ws : nullptr, backward ? a->dh : a->h,
+                        backward ? a->dx : nullptr, backward ? a->dwg : nullptr, backward ? a->dwu : nullptr};
+    for (const void* p : ps)
+        if (p && (st = pointer_on(p, dev))) return st;
+    return SDM_GX_OK;
+}
+
+int status(hipError_t e) { return e == hipSuccess ? SDM_GX_OK : record_hip_error(e); }
+
+}  // namespace
+
+extern "C" {
+
+int sdm_ffn_check(const sdm_ffn_args_t* args, int32_t backward) { return check(args, backward != 0); }
+
+int64_t sdm_ffn_workspace(const sdm_ffn_args_t* a, int32_t backward) {
+    if (int st = check(a, backward != 0)) return st;
+    return backward ? backward_plan(a, nullptr).bytes : forward_plan(a, nullptr).bytes;
+}
+
+int sdm_ffn_forward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* stream) {
+    int st = check(a, false);
+    if (st || a->M == 0) return st;
+    const Forward f = forward_plan(a, static_cast<char*>(ws));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    FfnProduct p{};
+    p.A = f.x.o;
+    p.B = f.wg.o;
+    p.B2 = f.wu.o;
+    p.M = a->M;
+    p.N = a->F;
+    p.bytes = up_to(a->K * (a->dtype == SDM_F32 ? 2 : size_of(a->dtype)), 16);
+    segments(&p, a->dtype);
+    p.act = a->act;
+    p.otype = a->otype;
+    p.sm = a->sx;
+    p.sn = a->sg;
+    p.sn2 = a->su;
+    p.c = static_cast<char*>(a->h);
+    p.ldc = a->ld_h;
+    p.split = a->M;
+    p.gate = a->gate;
+    p.up = a->up;
+    p.ld_gate = a->ld_gate;
+    p.ld_up = a->ld_up;
+    p.tile = tile_for(p.M, p.N, true);
+    if (too_many(p, true)) return SDM_GX_ERR_LIMIT;
+    for (const Laid* l : {&f.x, &f.wg, &f.wu})
+        if (l->anew && l->lay.R * (l->lay.pad / 8) >= kMaxThreads) return SDM_GX_ERR_LIMIT;
+    if ((st = prepare(a, false, f.bytes, ws, ws_bytes))) return st;
+    if (a->M <= kFfnFewRows) return status(launch_ffn_few(*a, s));
+    for (const Laid* l : {&f.x, &f.wg, &f.wu})
+        if (l->anew)
+            if (const hipError_t e = launch_ffn_lay(l->lay, false, s)) return status(e);
+    return status(launch_ffn_product(p, true, s));
+}
+
+int sdm_ffn_backward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* stream) {
+    int st = check(a, true);
+    if (st) return st;
+    const Backward b = backward_plan(a, static_cast<char*>(ws));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    FfnProduct dx{}, dw{};
+    dx.A = b.rows;
+    dx.B = b.w;
+    dx.M = a->M;
+    dx.N = a->K;
+    dx.bytes = b.rows.ld;
+    dx.c = static_cast<char*>(a->dx);
+    dx.ldc = a->ld_dx;
+    dx.split = a->M;
+    dw.A = b.cols;
+    dw.B = b.xt;
+    dw.M = 2 * a->F;
+    dw.N = a->K;
+    dw.bytes = b.cols.ld;
+    dw.c = static_cast<char*>(a->dwg);
+    dw.c2 = static_cast<char*>(a->dwu);
+    dw.ldc = a->ld_dwg;
+    dw.ldc2 = a->ld_dwu;
+    dw.split = a->F;
+    for (FfnProduct* p : {&dx, &dw}) {
+        segments(p, a->dtype);
+        p->otype = a->otype;
+        p->tile = tile_for(p->M, p->N, false);
+        if (too_many(*p, false)) return SDM_GX_ERR_LIMIT;
+    }
+    if (cdiv(b.grad.Mp, 64) * cdiv(b.grad.Fp, 64) * 256 >= kMaxThreads || cdiv(b.grad.Mp, 64) * cdiv(a->K, 64) * 256 >= kMaxThreads ||
+        cdiv(b.grad.Fp, 64) * cdiv(a->K, 64) * 256 >= kMaxThreads)
+        return SDM_GX_ERR_LIMIT;
+    if ((st = prepare(a, true, b.bytes, ws, ws_bytes))) return st;
+    if (const hipError_t e = launch_ffn_grad(b.grad, s)) return status(e);
+    for (const FfnLay* l : {&b.wg, &b.wu, &b.x})
+        if (const hipError_t e = launch_ffn_lay(*l, true, s)) return status(e);
+    if (const hipError_t e = launch_ffn_product(dx, false, s)) return status(e);
+    return status(launch_ffn_product(dw, false, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,75 @@
+/*
+ * sdm_ffn -- the gated feed-forward product on MI355X (gfx950), C ABI: both projections, the activation and the product in
+ * one kernel, and its gradient. In libsdm_block; status codes are sdm_gx_status (sdm_gx_gemm.h).
+ *
+ * For M rows x of K values and two weights of F rows of K values:
+ *     g = x Wg^T;   u = x Wu^T;   h = act(g) u                         [M][F]
+ * act: none (h = g u), sigmoid, silu (g sigmoid(g)) or gelu (g Phi(g), Phi the normal distribution's). With `gate` and `up`
+ * the products g and u are written too, for the backward call.
+ *
+ * Backward, from dh and the kept g and u:
+ *     dg = dh u act'(g);  du = dh act(g);   dx = dg Wg + du Wu;   dWg = dg^T x;   dWu = du^T x
+ *
+ * Types. float32, bfloat16 or float16 throughout (dtype), or, forward only, SDM_E4M3: x and the weights in OCP e4m3 with a
+ * float32 scale for each of their rows (sx [M], sg and su [F]: the value is the byte's times its row's), h in otype,
+ * bfloat16 or float16; for the other types otype is dtype. Products run on the matrix cores and are summed in float32; h and
+ * the gradients are rounded once, and the kept g and u not at all (rounded to 16 bits they would add as much to the error of
+ * the gradients as the rounding of dg and du does). float32 operands are split into three bfloat16 parts and six part products kept, which
+ * hold float32's 24 bits; few rows take float32 matrix instructions instead. In the backward call of 16-bit types dg and du
+ * are rounded to dtype before their products (dtype's matrix instructions take no more). The order of every sum is set by
+ * the sizes alone and there are no atomics: the same bits in every run.
+ * Values that are not finite make NaN or infinities of the outputs that depend on them; with float32 operands (and, in the
+ * same way, operands within 2^-8 of the largest float32) an infinity may come out as NaN.
+ *
+ * Memory. Rows are contiguous with a row stride `ld_*` in elements, at least the row's length. Any alignment; rows that
+ * begin on 16 bytes (address and stride) are used where they lie, others are laid out in the workspace first. Outputs must not overlap inputs
+ * or each other. Calls are asynchronous on `stream`, allocate nothing and may be captured into a graph. Workspaces are the
+ * caller's (sdm_ffn_workspace bytes, 256-byte aligned, contents free to lose after the call).
+ */
+#ifndef SDM_FFN_H
+#define SDM_FFN_H
+
+#include <stdint.h>
+
+#include "sdm_nrm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+enum { SDM_E4M3 = 3 };      /* after sdm_dtype's */
+enum { SDM_ACT_GELU = 3 };  /* after sdm_act's */
+
+typedef struct sdm_ffn_args {
+    int32_t dtype, otype, act, reserved;
+    int64_t M, K, F;
+    const void *x, *wg, *wu;
+    int64_t ld_x, ld_wg, ld_wu;
+    const float *sx, *sg, *su;   /* SDM_E4M3 */
+    /* forward */
+    void* h;
+    int64_t ld_h;
+    /* the products, float32: forward: written, both or neither NULL; backward: read */
+    float *gate, *up;
+    int64_t ld_gate, ld_up;
+    /* backward */
+    const void* dh;
+    int64_t ld_dh;
+    void *dx, *dwg, *dwu;
+    int64_t ld_dx, ld_dwg, ld_dwu;
+} sdm_ffn_args_t;
+
+SDM_GX_API int sdm_ffn_check(const sdm_ffn_args_t* args, int32_t backward);
+
+/* Workspace bytes of a forward (backward = 0) or backward call: at least 0, or a negative status. They depend on the sizes,
+ * strides and the inputs' alignment (their addresses are read here, not their contents). */
+SDM_GX_API int64_t sdm_ffn_workspace(const sdm_ffn_args_t* args, int32_t backward);
+
+SDM_GX_API int sdm_ffn_forward(const sdm_ffn_args_t* args, void* workspace, int64_t workspace_bytes, void* stream);
+SDM_GX_API int sdm_ffn_backward(const sdm_ffn_args_t* args, void* workspace, int64_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SDM_FFN_H */
