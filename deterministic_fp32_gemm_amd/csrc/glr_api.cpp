@@ -145,7 +145,7 @@ int run(const sdm_glr_args_t* a, bool backward, void* ws, int64_t ws_bytes, void
 int check_step(const sdm_glr_step_args_t* a) {
     if (!a) return SDM_GX_ERR_ARG;
     if (int st = check_sizes(a->dtype, a->gtype, a->act, a->B, a->T, a->D)) return st;
-    if (a->pool < 0 || a->pool >= (int64_t(1) << 31)) return SDM_GX_ERR_SHAPE;
+    if (a->pool < 1 || a->pool >= (int64_t(1) << 31) || (!a->slots && a->pool < a->B)) return SDM_GX_ERR_SHAPE;
     if (!a->state) return SDM_GX_ERR_NULL;
     if (!aligned(a->state, 4) || !aligned(a->slots, 4)) return SDM_GX_ERR_ALIGN;
     const bool z = a->act != SDM_ACT_NONE;
