@@ -6,9 +6,30 @@
 
 namespace sdm_delta {
 
-// act(z) and act'(z). With e = exp(-|z|) the sigmoid p and 1 - p are 1 / (1 + e) and e / (1 + e), in the order of z's sign:
-// 1 - p taken as a difference would keep nothing of act' from z = 17 on. FAST: the hardware's exponential and reciprocal (1
-// ulp of float32), for results of 16 bits. At z = -inf z p is NaN as the formula has it.
+// e^x within 2^-23 of it in 7 instructions: the hardware's 2^t for t = x log2(e), whose rounding (and log2(e)'s own) goes back
+// in as a factor 1 + r. Below -150 it is zero, as float32 has it without its last denormals.
+__device__ __forceinline__ float exp_of(float x) {
+    x = x < -150.f ? -150.f : x;
+    const float t = x * 1.44269504f, e = __builtin_amdgcn_exp2f(t);
+    // log2(e) - 1.44269504f = 1.9259630e-8; times ln 2
+    const float r = 0.69314718f * __builtin_fmaf(x, 1.44269504f, -t) + 1.3349759e-8f * x;
+    return __builtin_fmaf(e, r, e);
+}
+
+// p = 1 / (1 + e^-z) and q = 1 - p = e^-z p, which as a difference would keep nothing of itself from z = 17 on. e^-z is held
+// below 2^116, so that neither is 0 times infinity. FAST: the hardware's exponential and reciprocal (their errors, and 2^-24
+// |z| of the exponent's argument, are far below a rounding to 16 bits), else one more step of Newton's for the reciprocal.
+template <bool FAST>
+__device__ __forceinline__ void sigmoid(float z, float& p, float& q) {
+    float e = FAST ? __builtin_amdgcn_exp2f(-1.44269504f * z) : exp_of(-z);
+    e = z < -80.f ? 5.5406224e34f : e;
+    const float d = 1.f + e;
+    p = __builtin_amdgcn_rcpf(d);
+    if constexpr (!FAST) p = __builtin_fmaf(__builtin_fmaf(-d, p, 1.f), p, p);
+    q = e * p;
+}
+
+// act(z) and act'(z). At z = -inf z p is NaN as the formula has it.
 template <bool FAST>
 __device__ __forceinline__ void gate(float z, int act, float& a, float& d) {
     if (act == SDM_ACT_NONE) {
@@ -24,21 +45,14 @@ __device__ __forceinline__ void gate(float z, int act, float& a, float& d) {
         d = __builtin_fmaf(0.39894228f * e, z, p);
         return;
     }
-    float e, large;
-    if constexpr (FAST) {
-        e = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(z));
-        large = __builtin_amdgcn_rcpf(1.f + e);
-    } else {
-        e = expf(-fabsf(z));
-        large = 1.f / (1.f + e);
-    }
-    const float small = e * large, p = z < 0.f ? small : large, q = z < 0.f ? large : small;
+    float p, q;
+    sigmoid<FAST>(z, p, q);
     if (act == SDM_ACT_SIGMOID) {
         a = p;
         d = p * q;
     } else {
         a = z * p;
-        d = p * (1.f + z * q);
+        d = p * __builtin_fmaf(z, q, 1.f);
     }
 }
 

@@ -114,7 +114,7 @@ GlrPlan plan(const sdm_glr_args_t* a) {
     GlrPlan p{};
     p.cblocks = static_cast<int>(cdiv(a->D, 64));
     const int64_t have = a->nseq * p.cblocks, each = cdiv(a->T * a->B, a->nseq);
-    p.segs = static_cast<int>(std::max<int64_t>(1, std::min(512 / have, each / 512)));
+    p.segs = static_cast<int>(std::max<int64_t>(1, std::min(256 / have, each / 512)));
     return p;
 }
 int64_t workspace(const sdm_glr_args_t* a) {

@@ -15,6 +15,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "block_device.h"
 #include "glr.h"
 
@@ -47,30 +49,49 @@ __device__ __forceinline__ Run run_of(const sdm_glr_args_t& a, int i) {
     return r;
 }
 
-// One token row's element of this lane's channel; `t` is the same for the whole wavefront.
+// The rows of a run, one token after the other; which token is the same for the whole wavefront.
 template <class T>
-__device__ __forceinline__ T at(const sdm_seq_t& s, int64_t row, int64_t t, int c) {
-    return (static_cast<const T*>(s.data) + row * s.batch + t * s.token)[c];
-}
+struct Rows {
+    T* p;
+    int64_t step;
+};
 template <class T>
-__device__ __forceinline__ void put(const sdm_seq_t& s, int64_t row, int64_t t, int c, float v) {
-    (static_cast<T*>(s.data) + row * s.batch + t * s.token)[c] = static_cast<T>(v);
+__device__ __forceinline__ Rows<T> rows_of(const sdm_seq_t& s, const Run& r) {
+    return Rows<T>{static_cast<T*>(s.data) + r.row * s.batch + r.start * s.token, s.token};
 }
 // A h + H; from no state nothing comes, also where a growing A has left float32.
 __device__ __forceinline__ float enter(float A, float H, float h) { return h == 0.f ? H : __builtin_fmaf(A, h, H); }
 
-// The wavefront's KT tokens from t, read from inside the run whatever t is.
+// A lane's element of a row: the row's address is the wavefront's, the byte offset the lane's.
 template <class T>
-__device__ __forceinline__ void fetch(T (&o)[KT], const sdm_seq_t& s, const Run& r, int t, int c) {
+__device__ __forceinline__ T get(const T* row, uint32_t off) {
+    return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) + off);
+}
+template <class T>
+__device__ __forceinline__ void put(T* row, uint32_t off, float v) {
+    *reinterpret_cast<T*>(reinterpret_cast<char*>(row) + off) = static_cast<T>(v);
+}
+
+// The wavefront's KT tokens from t: all of them in the run, or read from inside it whatever t is. (One form for both would
+// have the compiler merge them and take an address register for each load.)
+template <class T>
+__device__ __forceinline__ void fetch(std::true_type, T (&o)[KT], const Rows<T>& s, int t, int, uint32_t c) {
+    const T* p = s.p + t * s.step;
 #pragma unroll
-    for (int i = 0; i < KT; ++i) o[i] = at<T>(s, r.row, r.start + min(t + i, r.len - 1), c);
+    for (int i = 0; i < KT; ++i, p += s.step) o[i] = get(p, c * static_cast<uint32_t>(sizeof(T)));
+}
+template <class T>
+__device__ __forceinline__ void fetch(std::false_type, T (&o)[KT], const Rows<T>& s, int t, int len, uint32_t c) {
+#pragma unroll
+    for (int i = 0; i < KT; ++i) o[i] = get(s.p + min(t + i, len - 1) * s.step, c * static_cast<uint32_t>(sizeof(T)));
 }
 
 // The map of each part of a run: BACK that of D's recurrence, from right to left, else that of the states.
-template <int DT, int GT, bool Z, bool BACK>
+template <int DT, int GT, int ACT, bool BACK>
 __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a, const int cblocks, const int segs, float* __restrict__ part) {
     using T = elem_t<DT>;
     using G = elem_t<GT>;
+    constexpr bool Z = ACT != SDM_ACT_NONE;
     __shared__ float ex[NW][2][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cb = blockIdx.x % cblocks, rs = blockIdx.x / cblocks, seg = rs % segs, run = rs / segs;
@@ -84,29 +105,28 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
     float A = 1.f, H = 0.f;
     T x[KT], z[KT];
     G g[KT];
+    const Rows<T> xs = rows_of<T>(BACK ? a.dy : a.x, r), zs = rows_of<T>(a.z, r);
+    const Rows<G> gs = rows_of<G>(a.g, r);
     const int n = hi > lo ? (hi - lo + KT - 1) / KT : 0;
-    auto first = [&](int i) { return lo + (BACK ? i : n - 1 - i) * KT; };
-    auto load = [&](int t) {
-        fetch<T>(x, BACK ? a.dy : a.x, r, t, cc);
-        fetch<G>(g, a.g, r, t, cc);
-        if constexpr (BACK && Z) fetch<T>(z, a.z, r, t, cc);
+    auto load = [&](auto whole, int t) __attribute__((always_inline)) {
+        fetch(whole, x, xs, t, r.len, cc);
+        fetch(whole, g, gs, t, r.len, cc);
+        if constexpr (BACK && Z) fetch(whole, z, zs, t, r.len, cc);
     };
-    if (n > 0) load(first(0));
-    for (int i = 0; i < n; ++i) {
-        const int t = first(i);
+    auto work = [&](auto whole, int t, int next) __attribute__((always_inline)) {
         float e[KT], u[KT];
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            const bool in = t + k < hi;
-            e[k] = in ? expf(static_cast<float>(g[k])) : 1.f;
+            const bool in = whole.value || t + k < hi;
+            e[k] = in ? exp_of(static_cast<float>(g[k])) : 1.f;
             u[k] = in ? static_cast<float>(x[k]) : 0.f;
             if constexpr (BACK && Z) {
                 float f, d;
-                gate<DT != 0>(static_cast<float>(z[k]), a.act, f, d);
+                gate<DT != 0>(static_cast<float>(z[k]), ACT, f, d);
                 u[k] = in ? u[k] * f : 0.f;
             }
         }
-        if (i + 1 < n) load(first(i + 1));
+        if (next >= 0) load(std::true_type{}, next);
         float P = 1.f, h = 0.f;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
@@ -117,6 +137,20 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
         // the new stretch is on the far side of those before it
         H = enter(A, H, h);
         A *= P;
+    };
+    // the wavefront's last block may not be whole: it comes first, or last
+    const int whole = hi > lo ? (hi - lo) / KT : 0, rest = n > whole ? lo + whole * KT : -1;
+    auto at = [&](int i) { return i < whole ? lo + (BACK ? i : whole - 1 - i) * KT : -1; };
+    if (!BACK && rest >= 0) {
+        load(std::false_type{}, rest);
+        work(std::false_type{}, rest, at(0));
+    } else if (whole > 0) {
+        load(std::true_type{}, at(0));
+    }
+    for (int i = 0; i < whole; ++i) work(std::true_type{}, at(i), at(i + 1));
+    if (BACK && rest >= 0) {
+        load(std::false_type{}, rest);
+        work(std::false_type{}, rest, -1);
     }
     ex[w][0][lane] = A;
     ex[w][1][lane] = H;
@@ -136,10 +170,11 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
     }
 }
 
-template <int DT, int GT, bool Z>
+template <int DT, int GT, int ACT>
 __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t a, const int cblocks, const int segs, const float* __restrict__ part) {
     using T = elem_t<DT>;
     using G = elem_t<GT>;
+    constexpr bool Z = ACT != SDM_ACT_NONE;
     __shared__ float ex[2][NW][2][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cb = blockIdx.x % cblocks, rs = blockIdx.x / cblocks, seg = rs % segs, run = rs / segs;
@@ -155,32 +190,35 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
     const int t0 = static_cast<int>(s0), t1 = min(r.len, t0 + seglen);
     T x[KT], z[KT];
     G g[KT];
-    auto load = [&](int t) {
-        fetch<T>(x, a.x, r, t, cc);
-        fetch<G>(g, a.g, r, t, cc);
-        if constexpr (Z) fetch<T>(z, a.z, r, t, cc);
+    const Rows<T> xs = rows_of<T>(a.x, r), zs = rows_of<T>(a.z, r), ys = rows_of<T>(a.y, r);
+    const Rows<G> gs = rows_of<G>(a.g, r);
+    auto load = [&](auto whole, int t) __attribute__((always_inline)) {
+        fetch(whole, x, xs, t, r.len, cc);
+        fetch(whole, g, gs, t, r.len, cc);
+        if constexpr (Z) fetch(whole, z, zs, t, r.len, cc);
     };
-    load(t0 + w * KT);
+    const int end = t0 + (t1 - t0) / TILE * TILE;       // of the whole tiles
+    if (end > t0) load(std::true_type{}, t0 + w * KT);
     for (int s = 0; s < seg; ++s) {
         const float* p = part + (static_cast<int64_t>(run) * segs + s) * 2 * a.D + cc;
         h0 = enter(p[0], p[a.D], h0);
     }
     int buf = 0;
-    for (int tile = t0; tile < t1; tile += TILE, buf ^= 1) {
+    auto work = [&](auto whole, int tile) __attribute__((always_inline)) {
         const int t = tile + w * KT;
         float e[KT], u[KT];
         T zz[KT];
         float A = 1.f, H = 0.f;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            const bool in = t + k < t1;
-            e[k] = in ? expf(static_cast<float>(g[k])) : 1.f;
+            const bool in = whole.value || t + k < t1;
+            e[k] = in ? exp_of(static_cast<float>(g[k])) : 1.f;
             u[k] = in ? static_cast<float>(x[k]) : 0.f;
             H = __builtin_fmaf(e[k], H, u[k]);
             A *= e[k];
             if constexpr (Z) zz[k] = z[k];
         }
-        if (tile + TILE < t1) load(t + TILE);
+        if (whole.value && tile + TILE < end) load(std::true_type{}, t + TILE);
         ex[buf][w][0][lane] = A;
         ex[buf][w][1][lane] = H;
         lds_barrier();      // the other buffer is written again only after the next one
@@ -192,25 +230,33 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
         }
         if (w == 0 && a.marks && c < D) a.marks[(r.mark + tile / TILE) * a.D + c] = h0;
         h0 = next;
+        if (c >= D) return;
+        T* yp = ys.p + t * ys.step;
 #pragma unroll
-        for (int k = 0; k < KT; ++k) {
+        for (int k = 0; k < KT; ++k, yp += ys.step) {
             h = __builtin_fmaf(e[k], h, u[k]);
             float y = h;
             if constexpr (Z) {
                 float f, d;
-                gate<DT != 0>(static_cast<float>(zz[k]), a.act, f, d);
+                gate<DT != 0>(static_cast<float>(zz[k]), ACT, f, d);
                 y *= f;
             }
-            if (t + k < t1 && c < D) put<T>(a.y, r.row, r.start + t + k, c, y);
+            if (whole.value || t + k < t1) put(yp, c * sizeof(T), y);
         }
+    };
+    for (int tile = t0; tile < end; tile += TILE, buf ^= 1) work(std::true_type{}, tile);
+    if (end < t1) {
+        load(std::false_type{}, end + w * KT);
+        work(std::false_type{}, end);
     }
     if (t1 == r.len && w == 0 && c < D && a.h_final) a.h_final[run * a.D + c] = h0;
 }
 
-template <int DT, int GT, bool Z>
+template <int DT, int GT, int ACT>
 __global__ __launch_bounds__(kGlrThreads) void glr_backward(const sdm_glr_args_t a, const int cblocks, const int segs, const float* __restrict__ part) {
     using T = elem_t<DT>;
     using G = elem_t<GT>;
+    constexpr bool Z = ACT != SDM_ACT_NONE;
     __shared__ float ex[2][NW][3][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cb = blockIdx.x % cblocks, rs = blockIdx.x / cblocks, seg = rs % segs, run = rs / segs;
@@ -227,36 +273,41 @@ __global__ __launch_bounds__(kGlrThreads) void glr_backward(const sdm_glr_args_t
     T x[KT], z[KT], dy[KT];
     G g[KT];
     float m;
-    auto load = [&](int tile) {
+    const Rows<T> xs = rows_of<T>(a.x, r), zs = rows_of<T>(a.z, r), dys = rows_of<T>(a.dy, r), dxs = rows_of<T>(a.dx, r), dzs = rows_of<T>(a.dz, r);
+    const Rows<G> gs = rows_of<G>(a.g, r), dgs = rows_of<G>(a.dg, r);
+    auto load = [&](auto whole, int tile) __attribute__((always_inline)) {
         const int t = tile + w * KT;
-        fetch<T>(x, a.x, r, t, cc);
-        fetch<G>(g, a.g, r, t, cc);
-        fetch<T>(dy, a.dy, r, t, cc);
-        if constexpr (Z) fetch<T>(z, a.z, r, t, cc);
+        fetch(whole, x, xs, t, r.len, cc);
+        fetch(whole, g, gs, t, r.len, cc);
+        fetch(whole, dy, dys, t, r.len, cc);
+        if constexpr (Z) fetch(whole, z, zs, t, r.len, cc);
         m = a.marks[(r.mark + tile / TILE) * a.D + cc];
     };
-    const int last = t0 + (t1 - t0 - 1) / TILE * TILE;
-    load(last);
+    const int end = t0 + (t1 - t0) / TILE * TILE;       // of the whole tiles
+    if (end < t1)
+        load(std::false_type{}, end);
+    else
+        load(std::true_type{}, end - TILE);
     const int used = (r.len - 1) / seglen;      // the last part that has tokens
     for (int s = used; s > seg; --s) {
         const float* p = part + (static_cast<int64_t>(run) * segs + s) * 2 * a.D + cc;
         e0 = enter(p[0], p[a.D], e0);
     }
     int buf = 0;
-    for (int tile = last; tile >= t0; tile -= TILE, buf ^= 1) {
+    auto work = [&](auto whole, int tile) __attribute__((always_inline)) {
         const int t = tile + w * KT;
         float e[KT], u[KT], f[KT], v[KT], df[KT];     // a, x, dy act(z), and dy act'(z)
         float A = 1.f, H = 0.f, E = 0.f;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            const bool in = t + k < t1;
-            e[k] = in ? expf(static_cast<float>(g[k])) : 1.f;
+            const bool in = whole.value || t + k < t1;
+            e[k] = in ? exp_of(static_cast<float>(g[k])) : 1.f;
             u[k] = in ? static_cast<float>(x[k]) : 0.f;
             v[k] = in ? static_cast<float>(dy[k]) : 0.f;
             f[k] = v[k];
             if constexpr (Z) {
                 float q, d;
-                gate<DT != 0>(static_cast<float>(z[k]), a.act, q, d);
+                gate<DT != 0>(static_cast<float>(z[k]), ACT, q, d);
                 f[k] = in ? v[k] * q : 0.f;
                 df[k] = v[k] * d;
             }
@@ -266,7 +317,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_backward(const sdm_glr_args_t
 #pragma unroll
         for (int k = KT - 1; k >= 0; --k) E = e[k] * (f[k] + E);
         float h = m;
-        if (tile > t0) load(tile - TILE);
+        if (tile > t0) load(std::true_type{}, tile - TILE);
         ex[buf][w][0][lane] = A;
         ex[buf][w][1][lane] = H;
         ex[buf][w][2][lane] = E;
@@ -281,83 +332,93 @@ __global__ __launch_bounds__(kGlrThreads) void glr_backward(const sdm_glr_args_t
             next = enter(ex[buf][i][0][lane], ex[buf][i][2][lane], next);
         }
         e0 = next;
+        if (c >= D) return;
         float met[KT];
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
             met[k] = h;
             h = __builtin_fmaf(e[k], h, u[k]);
         }
+        T *dxp = dxs.p + (t + KT - 1) * dxs.step, *dzp = dzs.p + (t + KT - 1) * dzs.step;
+        G* dgp = dgs.p + (t + KT - 1) * dgs.step;
 #pragma unroll
-        for (int k = KT - 1; k >= 0; --k) {
+        for (int k = KT - 1; k >= 0; --k, dxp -= dxs.step, dgp -= dgs.step, dzp -= dzs.step) {
             const float d = f[k] + q;
             q = e[k] * d;
-            if (t + k < t1 && c < D) {
-                const int64_t at = r.start + t + k;
-                put<T>(a.dx, r.row, at, c, d);
-                put<G>(a.dg, r.row, at, c, q * met[k]);
-                if constexpr (Z) put<T>(a.dz, r.row, at, c, df[k] * __builtin_fmaf(e[k], met[k], u[k]));
+            if (whole.value || t + k < t1) {
+                put(dxp, c * sizeof(T), d);
+                put(dgp, c * sizeof(G), q * met[k]);
+                if constexpr (Z) put(dzp, c * sizeof(T), df[k] * __builtin_fmaf(e[k], met[k], u[k]));
             }
         }
+    };
+    if (end < t1) {
+        work(std::false_type{}, end);
+        buf ^= 1;
     }
+    for (int tile = end - TILE; tile >= t0; tile -= TILE, buf ^= 1) work(std::true_type{}, tile);
     if (seg == 0 && w == 0 && c < D && a.dh0) a.dh0[run * a.D + c] = e0;
 }
 
 // A thread has one channel of one stream.
-template <int DT, int GT, bool Z>
+template <int DT, int GT, int ACT>
 __global__ __launch_bounds__(kGlrStepThreads) void glr_step(const sdm_glr_step_args_t a, const int cblocks) {
     using T = elem_t<DT>;
     using G = elem_t<GT>;
+    constexpr bool Z = ACT != SDM_ACT_NONE;
     const int64_t b = blockIdx.x / cblocks;
     const int c = blockIdx.x % cblocks * kGlrStepThreads + threadIdx.x;
     if (c >= a.D) return;
     const int64_t slot = a.slots ? a.slots[b] : b;
+    const T *x = static_cast<const T*>(a.x.data) + b * a.x.batch + c, *z = Z ? static_cast<const T*>(a.z.data) + b * a.z.batch + c : nullptr;
+    const G* g = static_cast<const G*>(a.g.data) + b * a.g.batch + c;
+    T* y = static_cast<T*>(a.y.data) + b * a.y.batch + c;
     if (slot < 0 || slot >= a.pool) {
-        for (int64_t t = 0; t < a.T; ++t) put<T>(a.y, b, t, c, 0.f);
+        for (int64_t t = 0; t < a.T; ++t) y[t * a.y.token] = static_cast<T>(0.f);
         return;
     }
     float h = a.state[slot * a.D + c];
     for (int64_t t = 0; t < a.T; ++t) {
-        h = __builtin_fmaf(expf(static_cast<float>(at<G>(a.g, b, t, c))), h, static_cast<float>(at<T>(a.x, b, t, c)));
-        float y = h;
-        if constexpr (Z) {
-            float f, d;
-            gate<DT != 0>(static_cast<float>(at<T>(a.z, b, t, c)), a.act, f, d);
-            y *= f;
-        }
-        put<T>(a.y, b, t, c, y);
+        h = __builtin_fmaf(exp_of(static_cast<float>(g[t * a.g.token])), h, static_cast<float>(x[t * a.x.token]));
+        float f = 1.f, d;
+        if constexpr (Z) gate<DT != 0>(static_cast<float>(z[t * a.z.token]), ACT, f, d);
+        y[t * a.y.token] = static_cast<T>(h * f);
     }
     a.state[slot * a.D + c] = h;
 }
 
-template <int DT, int GT, bool Z>
+template <int DT, int GT, int ACT>
 hipError_t forward_of(const sdm_glr_args_t& a, const GlrPlan& p, float* part, hipStream_t s) {
     const unsigned grid = static_cast<unsigned>(a.nseq * p.segs * p.cblocks);
-    if (p.segs > 1) glr_parts<DT, GT, Z, false><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
-    glr_forward<DT, GT, Z><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
+    if (p.segs > 1) glr_parts<DT, GT, ACT, false><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
+    glr_forward<DT, GT, ACT><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
     return hipGetLastError();
 }
-template <int DT, int GT, bool Z>
+template <int DT, int GT, int ACT>
 hipError_t backward_of(const sdm_glr_args_t& a, const GlrPlan& p, float* part, hipStream_t s) {
     const unsigned grid = static_cast<unsigned>(a.nseq * p.segs * p.cblocks);
-    if (p.segs > 1) glr_parts<DT, GT, Z, true><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
-    glr_backward<DT, GT, Z><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
+    if (p.segs > 1) glr_parts<DT, GT, ACT, true><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
+    glr_backward<DT, GT, ACT><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
     return hipGetLastError();
 }
-template <int DT, int GT, bool Z>
+template <int DT, int GT, int ACT>
 hipError_t step_of(const sdm_glr_step_args_t& a, hipStream_t s) {
     const int cblocks = static_cast<int>((a.D + kGlrStepThreads - 1) / kGlrStepThreads);
-    glr_step<DT, GT, Z><<<static_cast<unsigned>(a.B * cblocks), kGlrStepThreads, 0, s>>>(a, cblocks);
+    glr_step<DT, GT, ACT><<<static_cast<unsigned>(a.B * cblocks), kGlrStepThreads, 0, s>>>(a, cblocks);
     return hipGetLastError();
 }
 
 // gtype is dtype or float32 (the host checks)
+#define SDM_GLR_ACTS(F, DT, GT, ...)                                                                            \
+    return a.act == SDM_ACT_NONE      ? F<DT, GT, SDM_ACT_NONE>(__VA_ARGS__)                                    \
+           : a.act == SDM_ACT_SIGMOID ? F<DT, GT, SDM_ACT_SIGMOID>(__VA_ARGS__)                                 \
+                                      : F<DT, GT, SDM_ACT_SILU>(__VA_ARGS__);
 #define SDM_GLR_TYPES(F, ...)                                                                                   \
-    const bool z = a.act != SDM_ACT_NONE, wide = a.gtype == SDM_F32;                                            \
-    if (a.dtype == SDM_F32) return z ? F<0, 0, true>(__VA_ARGS__) : F<0, 0, false>(__VA_ARGS__);                \
-    if (a.dtype == SDM_BF16 && wide) return z ? F<1, 0, true>(__VA_ARGS__) : F<1, 0, false>(__VA_ARGS__);       \
-    if (a.dtype == SDM_BF16) return z ? F<1, 1, true>(__VA_ARGS__) : F<1, 1, false>(__VA_ARGS__);               \
-    if (wide) return z ? F<2, 0, true>(__VA_ARGS__) : F<2, 0, false>(__VA_ARGS__);                              \
-    return z ? F<2, 2, true>(__VA_ARGS__) : F<2, 2, false>(__VA_ARGS__);
+    if (a.dtype == SDM_F32) SDM_GLR_ACTS(F, 0, 0, __VA_ARGS__)                                                  \
+    if (a.dtype == SDM_BF16 && a.gtype == SDM_F32) SDM_GLR_ACTS(F, 1, 0, __VA_ARGS__)                           \
+    if (a.dtype == SDM_BF16) SDM_GLR_ACTS(F, 1, 1, __VA_ARGS__)                                                 \
+    if (a.gtype == SDM_F32) SDM_GLR_ACTS(F, 2, 0, __VA_ARGS__)                                                  \
+    SDM_GLR_ACTS(F, 2, 2, __VA_ARGS__)
 
 }  // namespace
 
