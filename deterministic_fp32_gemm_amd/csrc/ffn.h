@@ -29,12 +29,13 @@ struct FfnProduct {
     int64_t ldc, ldc2, split;   // elements
     float *gate, *up;           // the pair's products, or NULL
     int64_t ld_gate, ld_up;
-    int tile;                   // rows and columns of a workgroup's tile: 128 or 256
 };
-hipError_t launch_ffn_product(const FfnProduct& p, bool pair, hipStream_t stream);
+// tile: rows and columns of a workgroup's tile, 64, 128 or 256. Two products of one type go in one launch.
+hipError_t launch_ffn_pair(const FfnProduct& p, int tile, hipStream_t stream);
+hipError_t launch_ffn_products(const FfnProduct (&p)[2], int tile, hipStream_t stream);
 
-// Few rows: weights straight from memory, at any alignment. joint: wavefronts that share a workgroup's rows of weights.
-constexpr int kFfnFewRows = 64;
+// Few rows: weights straight from memory, at any alignment.
+constexpr int kFfnFewRows = 32;
 hipError_t launch_ffn_few(const sdm_ffn_args_t& a, hipStream_t stream);
 
 // dst[part][r][c] = src[r][c] for c < C, zero up to `pad` columns; turned: dst[part][c][r], pad rows of src. float32 sources
@@ -47,7 +48,7 @@ struct FfnLay {
     int64_t ldd, plane;         // bytes
     int64_t pad;                // elements
 };
-hipError_t launch_ffn_lay(const FfnLay& l, bool turned, hipStream_t stream);
+hipError_t launch_ffn_lay(const FfnLay (&l)[3], bool turned, hipStream_t stream);     // one launch; without rows: none
 
 // dg and du from dh, g and u: rows[part][m] = dg, zeros to Fp, du, zeros to 2 Fp; cols[part][f] = dg's column f, zeros to Mp,
 // and du's at row F + f.

@@ -117,10 +117,15 @@ void segments(FfnProduct* p, int dtype) {
     p->type = dtype == SDM_E4M3 ? kE4m3 : dtype == SDM_F16 ? kF16 : kBf16;
 }
 
-// 256 x 256 tiles read half of what 128 x 128 ones do for each product, but two of the latter fit a CU: the large ones where
-// there are enough of them for every CU.
-int tile_for(int64_t M, int64_t N, bool pair) { return cdiv(M, 256) * cdiv(N, pair ? 128 : 256) >= 256 ? 256 : 128; }
-bool too_many(const FfnProduct& p, bool pair) { return cdiv(p.M, p.tile) * cdiv(p.N, pair ? p.tile / 2 : p.tile) * 256 >= kMaxThreads; }
+// 256 x 256 tiles read half of what 128 x 128 ones do for each product, and these half of 64 x 64 ones: the largest of which
+// there are enough for every CU.
+int64_t tiles(const FfnProduct& p, int tile, bool pair) { return cdiv(p.M, tile) * cdiv(p.N, pair ? tile / 2 : tile); }
+int pair_tile(const FfnProduct& p) { return tiles(p, 256, true) >= 256 ? 256 : tiles(p, 128, true) >= 256 ? 128 : 64; }
+int products_tile(const FfnProduct (&p)[2]) {
+    for (int tile : {256, 128})
+        if (tiles(p[0], tile, false) + tiles(p[1], tile, false) >= 256) return tile;
+    return 64;
+}
 
 struct Forward {
     Laid x, wg, wu;
@@ -220,16 +225,17 @@ int sdm_ffn_forward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* s
     p.up = a->up;
     p.ld_gate = a->ld_gate;
     p.ld_up = a->ld_up;
-    p.tile = tile_for(p.M, p.N, true);
-    if (too_many(p, true)) return SDM_GX_ERR_LIMIT;
-    for (const Laid* l : {&f.x, &f.wg, &f.wu})
-        if (l->anew && l->lay.R * (l->lay.pad / 8) >= kMaxThreads) return SDM_GX_ERR_LIMIT;
+    const int tile = pair_tile(p);
+    if (tiles(p, tile, true) * 256 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
+    int64_t threads = 0;
+    for (const Laid* l : {&f.x, &f.wg, &f.wu}) threads += l->lay.R * (l->lay.pad / 8) + 256;
+    if (threads >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     if ((st = prepare(a, false, f.bytes, ws, ws_bytes))) return st;
     if (a->M <= kFfnFewRows) return status(launch_ffn_few(*a, s));
-    for (const Laid* l : {&f.x, &f.wg, &f.wu})
-        if (l->anew)
-            if (const hipError_t e = launch_ffn_lay(l->lay, false, s)) return status(e);
-    return status(launch_ffn_product(p, true, s));
+    // an operand used where it lies has no rows to lay out
+    const FfnLay lay[3] = {f.x.lay, f.wg.lay, f.wu.lay};
+    if (const hipError_t e = launch_ffn_lay(lay, false, s)) return status(e);
+    return status(launch_ffn_pair(p, tile, s));
 }
 
 int sdm_ffn_backward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* stream) {
@@ -237,7 +243,7 @@ int sdm_ffn_backward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* 
     if (st) return st;
     const Backward b = backward_plan(a, static_cast<char*>(ws));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    FfnProduct dx{}, dw{};
+    FfnProduct both[2] = {}, &dx = both[0], &dw = both[1];
     dx.A = b.rows;
     dx.B = b.w;
     dx.M = a->M;
@@ -259,18 +265,16 @@ int sdm_ffn_backward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* 
     for (FfnProduct* p : {&dx, &dw}) {
         segments(p, a->dtype);
         p->otype = a->otype;
-        p->tile = tile_for(p->M, p->N, false);
-        if (too_many(*p, false)) return SDM_GX_ERR_LIMIT;
     }
-    if (cdiv(b.grad.Mp, 64) * cdiv(b.grad.Fp, 64) * 256 >= kMaxThreads || cdiv(b.grad.Mp, 64) * cdiv(a->K, 64) * 256 >= kMaxThreads ||
-        cdiv(b.grad.Fp, 64) * cdiv(a->K, 64) * 256 >= kMaxThreads)
-        return SDM_GX_ERR_LIMIT;
+    const int tile = products_tile(both);
+    if ((tiles(dx, tile, false) + tiles(dw, tile, false)) * 256 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
+    const int64_t gm = cdiv(b.grad.Mp, 64), gf = cdiv(b.grad.Fp, 64), gk = cdiv(a->K, 64);
+    if (gm * gf * 256 >= kMaxThreads || (gm + 2 * gf) * gk * 256 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     if ((st = prepare(a, true, b.bytes, ws, ws_bytes))) return st;
     if (const hipError_t e = launch_ffn_grad(b.grad, s)) return status(e);
-    for (const FfnLay* l : {&b.wg, &b.wu, &b.x})
-        if (const hipError_t e = launch_ffn_lay(*l, true, s)) return status(e);
-    if (const hipError_t e = launch_ffn_product(dx, false, s)) return status(e);
-    return status(launch_ffn_product(dw, false, s));
+    const FfnLay lay[3] = {b.wg, b.wu, b.x};
+    if (const hipError_t e = launch_ffn_lay(lay, true, s)) return status(e);
+    return status(launch_ffn_products(both, tile, s));
 }
 
 }  // extern "C"

@@ -1,8 +1,9 @@
 // The gated feed-forward product of few rows (sdm_ffn.h): one token, or a batch of streams' next ones, for gfx950.
 //
-// Bounded by the weights' bytes, each read once. A workgroup owns 16 rows of either weight: its four wavefronts take
+// Bounded by the weights' bytes, each read once. A workgroup owns 16 rows of either weight: its eight wavefronts take
 // blocks of 256 bytes of them in turn, straight from memory into the matrix cores' operands (lane l: 16 bytes of row l % 16
-// for each 64 bytes), against the same bytes of up to 64 rows of x, which stay in the caches. The wavefronts' sums meet in
+// for each 64 bytes), against the same bytes of up to 32 rows of x, which stay in the caches. The next block's loads are in
+// flight while a block is multiplied. The wavefronts' sums meet in
 // LDS and are added in order. Which element meets which place of an instruction's summed axis does not matter as long as
 // both operands agree. float32 takes float32 matrix instructions: their rate is enough for what memory brings.
 #include <hip/hip_runtime.h>
@@ -19,7 +20,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef long i64x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1)));
 
-constexpr int kWaves = 4, kDepth = 4;       // wavefronts that share the rows, 64-byte steps in flight
+constexpr int kWaves = 8, kDepth = 4;       // wavefronts that share the rows, 64-byte steps of a block
 
 // DT: sdm_dtype or SDM_E4M3; a 16-byte piece of a weight's 16 rows against that of 16 rows of x
 template <int DT>
@@ -89,20 +90,31 @@ __global__ __launch_bounds__(kWaves * 64) void ffn_few(const sdm_ffn_args_t a) {
     for (int i = 0; i < MT; ++i) ag[i] = au[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     constexpr int kBlock = kDepth * 64;
     const int64_t whole = n / kBlock * kBlock;
-    for (int64_t c = w * kBlock; c < whole; c += kWaves * kBlock) {
-        u32x4 pg[kDepth], pu[kDepth];
+    u32x4 pg[kDepth], pu[kDepth];
+    auto fetch = [&](int64_t c) {
 #pragma unroll
         for (int k = 0; k < kDepth; ++k) {
             pg[k] = *reinterpret_cast<const u32x4b*>(g + c + k * 64 + part * 16);
             pu[k] = *reinterpret_cast<const u32x4b*>(u + c + k * 64 + part * 16);
         }
+    };
+    if (w * kBlock < whole) fetch(w * kBlock);
+    for (int64_t c = w * kBlock; c < whole; c += kWaves * kBlock) {
+        u32x4 qg[kDepth], qu[kDepth], px[kDepth][MT];
+#pragma unroll
+        for (int k = 0; k < kDepth; ++k) {
+            qg[k] = pg[k];
+            qu[k] = pu[k];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) px[k][i] = *reinterpret_cast<const u32x4b*>(x[i] + c + k * 64 + part * 16);
+        }
+        if (c + kWaves * kBlock < whole) fetch(c + kWaves * kBlock);
 #pragma unroll
         for (int k = 0; k < kDepth; ++k)
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                const u32x4 px = *reinterpret_cast<const u32x4b*>(x[i] + c + k * 64 + part * 16);
-                mma<DT>(ag[i], pg[k], px);
-                mma<DT>(au[i], pu[k], px);
+                mma<DT>(ag[i], qg[k], px[k][i]);
+                mma<DT>(au[i], qu[k], px[k][i]);
             }
     }
     // what is left of the rows, a step a wavefront
@@ -153,10 +165,8 @@ hipError_t run(const sdm_ffn_args_t& a, hipStream_t s) {
     const unsigned grid = static_cast<unsigned>((a.F + 15) / 16);
     if (a.M <= 16)
         ffn_few<DT, 1><<<grid, kWaves * 64, 0, s>>>(a);
-    else if (a.M <= 32)
-        ffn_few<DT, 2><<<grid, kWaves * 64, 0, s>>>(a);
     else
-        ffn_few<DT, 4><<<grid, kWaves * 64, 0, s>>>(a);
+        ffn_few<DT, 2><<<grid, kWaves * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 

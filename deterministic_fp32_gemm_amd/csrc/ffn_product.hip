@@ -66,9 +66,11 @@ __device__ __forceinline__ u32x4 resource(const Buffer& b) {
 __device__ __forceinline__ void load_lds(const u32x4& r, uint32_t lds, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r) : "memory");
 }
-// Every load of this wavefront has landed, every read of LDS has come back; then all wavefronts meet.
+// All but this wavefront's last N loads have landed, every read of LDS has come back; then all wavefronts meet.
+template <int N>
 __device__ __forceinline__ void meet() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    static_assert(N < 64, "the counter's 6 bits");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // The workgroup's tile: workgroups go to the XCDs in turn, so each XCD takes a contiguous stretch of tiles, and a stretch
@@ -108,15 +110,27 @@ __device__ __forceinline__ void store4(int otype, char* base, int64_t at, int64_
         store4(reinterpret_cast<_Float16*>(base) + at, n, v);
 }
 
+struct Both {
+    FfnProduct p[2];
+    int tm[2], tn[2], first;       // tiles of each; workgroups of the first
+};
+
 // Tiles of T x T (as a pair: T rows and T / 2 columns of either product), four wavefronts of T/2 x T/2. A wavefront's part of
-// B's tile is its columns of Bg, then the same of Bu.
-template <int ET, int T, bool PAIR>
-__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void ffn_product(const FfnProduct p, const int tm, const int tn) {
-    constexpr int W = T / 2, NB = W / 32, LOADS = 2 * T / 32;       // a wavefront's rows, blocks of 32, loads a step
-    __shared__ __attribute__((aligned(1024))) char lds[2][2 * T * kStep];
+// B's tile is its columns of Bg, then the same of Bu. S steps of LDS: S - 1 of them in flight, or one and a half where S is 2.
+// P parts of each operand a step: 3 for the small tiles of float32, whose six products then come from one step's reads (a
+// sixth of the steps, half of the loads; 333 rows of 1111 to 777: 39 -> 17 us); the large tiles take a part of each a step.
+template <int ET, int T, int S, int P, bool PAIR>
+__global__ __launch_bounds__(256, T == 256 || P > 1 ? 1 : 2) void ffn_product(const Both both) {
+    constexpr int W = T / 2, NB = W / 32, LOADS = 2 * T / 32;       // a wavefront's rows, blocks of 32, loads a step and part
+    constexpr int PLACE = 2 * T * kStep;        // bytes of a step's part
+    __shared__ __attribute__((aligned(1024))) char lds[S][P * PLACE];
+    const int second = static_cast<int>(blockIdx.x) >= both.first ? 1 : 0;
+    const FfnProduct& p = both.p[second];
+    const int tm = both.tm[second], tn = both.tn[second];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w >> 1, wn = w & 1;
+    __builtin_assume(w >= 0 && w < 4);
     int ti, tj;
-    tile_of(blockIdx.x, tm, tn, ti, tj);
+    tile_of(static_cast<int>(blockIdx.x) - (second ? both.first : 0), tm, tn, ti, tj);
     const int64_t m0 = static_cast<int64_t>(ti) * T, n0 = static_cast<int64_t>(tj) * (PAIR ? W : T);
     constexpr int BR = PAIR ? W : T;            // rows of a B that the tile takes
     auto rows_of = [&](const FfnOperand& o, int64_t first, int64_t all, int most) {
@@ -139,60 +153,70 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void ffn_product(const FfnPr
             off[j] = static_cast<uint32_t>(r * p.B.ld) + piece * 16;
     }
     const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)&lds[0][0]));
-    const int steps = static_cast<int>((p.bytes + kStep - 1) / kStep), total = steps * p.segments;
+    const int segments = P > 1 ? 1 : p.segments, steps = static_cast<int>((p.bytes + kStep - 1) / kStep), total = steps * segments;
     // The next step's buffers; past the last step nothing is read.
     int seg = 0, at = 0;
-    u32x4 ra, rb, rc;
+    u32x4 ra[P], rb[P], rc[P];
     uint32_t none;
     auto next_step = [&]() {
         const int64_t from = static_cast<int64_t>(at) * kStep;
-        auto part = [&](const Buffer& b, int64_t plane, uint32_t parts) {
-            return resource(Buffer{b.p + plane * (parts >> (2 * seg) & 3) + from, b.n - static_cast<uint32_t>(from)});
+        auto part = [&](const Buffer& b, int64_t plane, uint32_t which) {
+            return resource(Buffer{b.p + plane * which + from, b.n - static_cast<uint32_t>(from)});
         };
-        ra = part(ba, p.A.plane, p.aparts);
-        rb = part(bb, p.B.plane, p.bparts);
-        rc = PAIR ? part(bc, p.B2.plane, p.bparts) : rb;
-        none = seg >= p.segments || from + piece * 16 >= p.bytes ? kNowhere : 0u;       // the row has ended
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const uint32_t ia = P > 1 ? i : p.aparts >> (2 * seg) & 3, ib = P > 1 ? i : p.bparts >> (2 * seg) & 3;
+            ra[i] = part(ba, p.A.plane, ia);
+            rb[i] = part(bb, p.B.plane, ib);
+            rc[i] = PAIR ? part(bc, p.B2.plane, ib) : rb[i];
+        }
+        none = seg >= segments || from + piece * 16 >= p.bytes ? kNowhere : 0u;       // the row has ended
         if (++at == steps) {
             at = 0;
             ++seg;
         }
     };
-    auto load = [&](int buf, int j) {
-        const uint32_t to = base + buf * (2 * T * kStep) + (j * 4 + w) * 1024;
+    auto load = [&](int buf, int n) {
+        const int i = n / LOADS, j = n % LOADS;
+        const uint32_t to = base + buf * (P * PLACE) + i * PLACE + (j * 4 + w) * 1024;
         if (j < LOADS / 2)
-            load_lds(ra, to, off[j] | none);
-        else if (PAIR && (j - LOADS / 2) * 32 / (W / 2) % 2)     // the same for all four wavefronts
-            load_lds(rc, to, off[j] | none);
+            load_lds(ra[i], to, off[j] | none);
         else
-            load_lds(rb, to, off[j] | none);
+            load_lds(PAIR && (j - LOADS / 2) * 32 + w * 8 & W / 2 ? rc[i] : rb[i], to, off[j] | none);
     };
     f32x16 acc[NB][NB];                         // [columns][rows]
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[i][j] = (f32x16){0};
-    Piece fa[2][NB], fb[2][NB];
+    Piece fa[2][P][NB], fb[2][P][NB];
     const int lr = lane & 31, lh = lane >> 5, sw = lr & 7;
-    constexpr int READS = 4 * NB, BLOCKS = NB * NB;
-    // Read k of a half step, in the order in which the products want them: B's first block, A's, B's others.
-    auto read = [&](int buf, int half, int k) {
-        const int c = ((half * 4 + lh * 2 + k % 2) ^ sw) * 16, i = k / 2;
-        const char* a = &lds[buf][(wm * W + lr) * kStep + c];
-        const char* b = &lds[buf][(T + wn * W + lr) * kStep + c];
+    constexpr int READS = 4 * NB * P, BLOCKS = NB * NB, AHEAD = BLOCKS > 1 ? BLOCKS / 2 : 1;
+    // Read n of a half step, in the order in which the products want them: B's first block, A's, B's others.
+    auto read = [&](int buf, int half, int n) {
+        const int part = P - 1 - n / (4 * NB), k = n % (4 * NB), c = ((half * 4 + lh * 2 + k % 2) ^ sw) * 16, i = k / 2;
+        const char* a = &lds[buf][part * PLACE + (wm * W + lr) * kStep + c];
+        const char* b = &lds[buf][part * PLACE + (T + wn * W + lr) * kStep + c];
         if (i >= 1 && i <= NB)
-            fa[half][i - 1].w[k % 2] = *reinterpret_cast<const u32x4*>(a + (i - 1) * 32 * kStep);
+            fa[half][part][i - 1].w[k % 2] = *reinterpret_cast<const u32x4*>(a + (i - 1) * 32 * kStep);
         else
-            fb[half][i ? i - NB : 0].w[k % 2] = *reinterpret_cast<const u32x4*>(b + (i ? i - NB : 0) * 32 * kStep);
+            fb[half][part][i ? i - NB : 0].w[k % 2] = *reinterpret_cast<const u32x4*>(b + (i ? i - NB : 0) * 32 * kStep);
+    };
+    // the part products of a block, smallest first
+    auto products = [&](int half, int i, int j) {
+#pragma unroll
+        for (int order = P - 1; order >= 0; --order)
+#pragma unroll
+            for (int x = order; x >= 0; --x) mma<ET>(acc[i][j], fb[half][order - x][i], fa[half][x][j]);
     };
     // A step's second half is read while its first is multiplied, and the next step's first half while the second is. Between
-    // the two the wavefronts meet: all reads of this step are back, so its place takes the loads of the step after the next,
-    // which have a whole step to land. Blocks of 64 clocks of products, with the reads behind the first half of them and the
+    // the two the wavefronts meet: all reads of this step are back, so its place takes the loads of the step S later, which
+    // have S - 1 whole steps to land. Blocks of 64 clocks of products, with the reads behind the first half of them and the
     // loads spread over all, in the order written here (the compiler would gather the products behind the barrier).
     auto blocks = [&](int half, int from, bool loads, int to) {
 #pragma unroll
         for (int n = 0; n < BLOCKS; ++n) {
-            constexpr int kReads = 2 * READS / BLOCKS, kLoads = LOADS / BLOCKS;
+            constexpr int kReads = READS / AHEAD, kLoads = P * LOADS / BLOCKS;
 #pragma unroll
             for (int k = 0; k < kReads; ++k)
                 if (n * kReads + k < READS) read(from, 1 - half, n * kReads + k);
@@ -200,31 +224,31 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void ffn_product(const FfnPr
 #pragma unroll
                 for (int k = 0; k < kLoads; ++k) load(to, n * kLoads + k);
             }
-            mma<ET>(acc[n / NB][n % NB], fb[half][n / NB], fa[half][n % NB]);
+            products(half, n / NB, n % NB);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    next_step();
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) load(0, j);
-    meet();
-    next_step();
+    for (int s = 0; s < S; ++s) {
+        next_step();
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) load(1, j);
+        for (int j = 0; j < P * LOADS; ++j) load(s, j);
+    }
+    meet<(S - 1) * P * LOADS>();
 #pragma unroll
     for (int k = 0; k < READS; ++k) read(0, 0, k);
     for (int t = 0; t < total; ++t) {
-        const int buf = t & 1;
+        const int buf = t % S;
         blocks(0, buf, false, 0);
         next_step();
-        meet();
+        meet<(S - 2) * P * LOADS>();
         __builtin_amdgcn_sched_barrier(0);
-        blocks(1, buf ^ 1, true, buf);
+        blocks(1, (t + 1) % S, true, buf);
     }
 
     // Lane l holds columns 8 (i / 4) + 4 (l / 32) + i % 4 of row l % 32 of each block. 32 rows at a time go through the
     // wavefront's own part of LDS, so that its lanes store whole stretches of a row; rows there are 4 banks apart.
-    meet();
+    meet<0>();
     constexpr int kRow = W * 4 + 16, kLanes = (PAIR ? W / 2 : W) / 4, kRows = 64 / kLanes;
     static_assert(4 * 32 * kRow <= sizeof(lds), "the wavefronts' rows fit");
     char* mine = &lds[0][0] + w * 32 * kRow;
@@ -288,24 +312,38 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void ffn_product(const FfnPr
     }
 }
 
-template <int ET, int T, bool PAIR>
-hipError_t run(const FfnProduct& p, hipStream_t s) {
-    const int64_t tm = (p.M + T - 1) / T, tn = (p.N + (PAIR ? T / 2 : T) - 1) / (PAIR ? T / 2 : T);
-    ffn_product<ET, T, PAIR><<<static_cast<unsigned>(tm * tn), 256, 0, s>>>(p, static_cast<int>(tm), static_cast<int>(tn));
+template <int ET, int T, int S, int P, bool PAIR>
+hipError_t run(const FfnProduct* p, int n, hipStream_t s) {
+    Both b{};
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) {
+        b.p[i] = p[i];
+        b.tm[i] = static_cast<int>((p[i].M + T - 1) / T);
+        b.tn[i] = static_cast<int>((p[i].N + (PAIR ? T / 2 : T) - 1) / (PAIR ? T / 2 : T));
+        total += static_cast<int64_t>(b.tm[i]) * b.tn[i];
+        if (i == 0) b.first = static_cast<int>(total);
+    }
+    ffn_product<ET, T, S, P, PAIR><<<static_cast<unsigned>(total), 256, 0, s>>>(b);
     return hipGetLastError();
 }
 template <int ET, bool PAIR>
-hipError_t tiled(const FfnProduct& p, hipStream_t s) {
-    return p.tile == 256 ? run<ET, 256, PAIR>(p, s) : run<ET, 128, PAIR>(p, s);
+hipError_t tiled(const FfnProduct* p, int n, int tile, hipStream_t s) {
+    if (tile == 256) return run<ET, 256, 2, 1, PAIR>(p, n, s);
+    if (tile == 128) return run<ET, 128, 2, 1, PAIR>(p, n, s);
+    if constexpr (ET == kBf16)
+        if (p[0].segments > 1) return run<ET, 64, 3, 3, PAIR>(p, n, s);
+    return run<ET, 64, 4, 1, PAIR>(p, n, s);
 }
 
 }  // namespace
 
 // 8-bit operands come as a pair only (the host has no other call)
-hipError_t launch_ffn_product(const FfnProduct& p, bool pair, hipStream_t s) {
-    if (p.type == kE4m3) return tiled<kE4m3, true>(p, s);
-    if (p.type == kBf16) return pair ? tiled<kBf16, true>(p, s) : tiled<kBf16, false>(p, s);
-    return pair ? tiled<kF16, true>(p, s) : tiled<kF16, false>(p, s);
+hipError_t launch_ffn_pair(const FfnProduct& p, int tile, hipStream_t s) {
+    if (p.type == kE4m3) return tiled<kE4m3, true>(&p, 1, tile, s);
+    return p.type == kBf16 ? tiled<kBf16, true>(&p, 1, tile, s) : tiled<kF16, true>(&p, 1, tile, s);
+}
+hipError_t launch_ffn_products(const FfnProduct (&p)[2], int tile, hipStream_t s) {
+    return p[0].type == kBf16 ? tiled<kBf16, false>(p, 2, tile, s) : tiled<kF16, false>(p, 2, tile, s);
 }
 
 }  // namespace sdm_delta
