@@ -8,21 +8,20 @@
 namespace sdm_delta {
 
 // What the matrix cores are given: element types of a product's operands.
-enum FfnType { kBf16 = 0, kF16 = 1, kE4m3 = 2, kTypes = 3 };
+enum FfnType { kBf16, kF16, kE4m3, kF32 };
 
-// Rows of `bytes` each, 16-byte aligned, `bytes` a multiple of 16; `plane` bytes from one part of the values to the next.
+// Rows of `bytes` each, 16-byte aligned, `bytes` a multiple of 16.
 struct FfnOperand {
     const char* p;
-    int64_t ld, plane;      // bytes
+    int64_t ld;     // bytes
 };
 
-// C[m][n] = sum over segments s and k of A[part a(s)][m][k] B[part b(s)][n][k]. A pair of B's is gate and up: C is h.
+// C[m][n] = sum over k of A[m][k] B[n][k]. A pair of B's is gate and up: C is h.
 struct FfnProduct {
     FfnOperand A, B, B2;
     int64_t M, N;
-    int64_t bytes;              // of a row of each segment
-    int segments, type, act, otype;
-    uint32_t aparts, bparts;    // two bits a segment
+    int64_t bytes;              // of a row of A and of B
+    int type, act, otype;       // FfnType, sdm_act or SDM_ACT_GELU, sdm_dtype
     const float *sm, *sn, *sn2; // kE4m3: scales of A's, B's and B2's rows
     char* c;                    // rows below `split`
     char* c2;                   // rows from `split` on, numbered from 0
@@ -34,31 +33,30 @@ struct FfnProduct {
 hipError_t launch_ffn_pair(const FfnProduct& p, int tile, hipStream_t stream);
 hipError_t launch_ffn_products(const FfnProduct (&p)[2], int tile, hipStream_t stream);
 
-// Few rows: weights straight from memory, at any alignment.
-constexpr int kFfnFewRows = 32;
+// Few rows: weights straight from memory, at any alignment. 16-bit and 8-bit rows from 17 on are faster in tiles (4096 to 8192,
+// 32 rows: bfloat16 40 us here and 36 in tiles, 8 bits 21 and 15); float32 ones from 33 on.
+constexpr int kFfnFewRows = 16, kFfnFewFloatRows = 32;
 hipError_t launch_ffn_few(const sdm_ffn_args_t& a, hipStream_t stream);
 
-// dst[part][r][c] = src[r][c] for c < C, zero up to `pad` columns; turned: dst[part][c][r], pad rows of src. float32 sources
-// become three bfloat16 parts, others are copied.
+// dst[r][c] = src[r][c] for c < C, zero up to `pad` columns; turned: dst[c][r], pad rows of src.
 struct FfnLay {
     const void* src;
     int64_t ld, R, C;           // elements
     int dtype;                  // sdm_dtype or SDM_E4M3
     char* dst;
-    int64_t ldd, plane;         // bytes
+    int64_t ldd;                // bytes
     int64_t pad;                // elements
 };
 hipError_t launch_ffn_lay(const FfnLay (&l)[3], bool turned, hipStream_t stream);     // one launch; without rows: none
 
-// dg and du from dh, g and u: rows[part][m] = dg, zeros to Fp, du, zeros to 2 Fp; cols[part][f] = dg's column f, zeros to Mp,
-// and du's at row F + f.
+// dg and du from dh, g and u: rows[m] = dg, zeros to Fp, du, zeros to 2 Fp; cols[f] = dg's column f, zeros to Mp, and du's at
+// row F + f.
 struct FfnGrad {
     const void* dh;
     const float *gate, *up;
     int64_t ld_dh, ld_gate, ld_up, M, F, Mp, Fp;
     int dtype, act;
     char *rows, *cols;
-    int64_t rows_plane, cols_plane;     // bytes
 };
 hipError_t launch_ffn_grad(const FfnGrad& g, hipStream_t stream);
 

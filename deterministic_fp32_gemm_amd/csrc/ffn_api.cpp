@@ -94,47 +94,45 @@ struct Laid {
 Laid operand(const void* src, int64_t ld, int64_t R, int64_t C, int dtype, Space* s) {
     const int64_t es = size_of(dtype);
     Laid l{};
-    l.anew = dtype == SDM_F32 || !aligned(src, 16) || ld * es % 16 || C * es % 16 || ld * es >= (int64_t(1) << 22);
+    l.anew = !aligned(src, 16) || ld * es % 16 || C * es % 16 || ld * es >= (int64_t(1) << 22);
     if (!l.anew) {
-        l.o = FfnOperand{static_cast<const char*>(src), ld * es, 0};
+        l.o = FfnOperand{static_cast<const char*>(src), ld * es};
         return l;
     }
-    const int64_t part = dtype == SDM_F32 ? 2 : es, pad = up_to(C, 16 / part), row = pad * part, plane = up_to(R * row, 256);
-    char* p = s->take(plane * (dtype == SDM_F32 ? 3 : 1));
-    l.o = FfnOperand{p, row, plane};
-    l.lay = FfnLay{src, ld, R, C, dtype, p, row, plane, pad};
+    const int64_t pad = up_to(C, 16 / es), row = pad * es;
+    char* p = s->take(R * row);
+    l.o = FfnOperand{p, row};
+    l.lay = FfnLay{src, ld, R, C, dtype, p, row, pad};
     return l;
 }
 
-// Float32's six part products, smallest first; others have one part.
-void segments(FfnProduct* p, int dtype) {
-    constexpr int a[] = {2, 1, 0, 1, 0, 0}, b[] = {0, 1, 2, 0, 1, 0};
-    p->segments = dtype == SDM_F32 ? 6 : 1;
-    for (int i = 0; i < p->segments; ++i) {
-        p->aparts |= static_cast<uint32_t>(dtype == SDM_F32 ? a[i] : 0) << (2 * i);
-        p->bparts |= static_cast<uint32_t>(dtype == SDM_F32 ? b[i] : 0) << (2 * i);
-    }
-    p->type = dtype == SDM_E4M3 ? kE4m3 : dtype == SDM_F16 ? kF16 : kBf16;
-}
+int product_type(int dtype) { return dtype == SDM_E4M3 ? kE4m3 : dtype == SDM_F32 ? kF32 : dtype == SDM_F16 ? kF16 : kBf16; }
 
 // 256 x 256 tiles read half of what 128 x 128 ones do for each product, and these half of 64 x 64 ones: the largest of which
-// there are enough for every CU.
-int64_t tiles(const FfnProduct& p, int tile, bool pair) { return cdiv(p.M, tile) * cdiv(p.N, pair ? tile / 2 : tile); }
-int pair_tile(const FfnProduct& p) { return tiles(p, 256, true) >= 256 ? 256 : tiles(p, 128, true) >= 256 ? 128 : 64; }
-int products_tile(const FfnProduct (&p)[2]) {
-    for (int tile : {256, 128})
-        if (tiles(p[0], tile, false) + tiles(p[1], tile, false) >= 256) return tile;
-    return 64;
+// there are enough for every CU. float32's six products a value are enough for 128 x 128 ones; their parts and the sums of
+// larger ones would not fit the registers.
+int64_t pair_tiles(int64_t M, int64_t F, int tile) { return cdiv(M, tile) * cdiv(F, tile / 2); }
+int pair_tile(int64_t M, int64_t F, int dtype) {
+    return dtype != SDM_F32 && pair_tiles(M, F, 256) >= 256 ? 256 : pair_tiles(M, F, 128) >= 256 ? 128 : 64;
+}
+// dx and both weights' gradients
+int64_t gradient_tiles(int64_t M, int64_t K, int64_t F, int tile) { return (cdiv(M, tile) + cdiv(2 * F, tile)) * cdiv(K, tile); }
+int gradient_tile(int64_t M, int64_t K, int64_t F, int dtype) {
+    return dtype != SDM_F32 && gradient_tiles(M, K, F, 256) >= 256 ? 256 : gradient_tiles(M, K, F, 128) >= 256 ? 128 : 64;
 }
 
+bool few(const sdm_ffn_args_t* a) { return a->M <= (a->dtype == SDM_F32 ? kFfnFewFloatRows : kFfnFewRows); }
+
 struct Forward {
+    int tile;
     Laid x, wg, wu;
     int64_t bytes;      // of the workspace
 };
 Forward forward_plan(const sdm_ffn_args_t* a, char* ws) {
     Space s{ws, 0};
     Forward f{};
-    if (a->M <= kFfnFewRows) return f;
+    if (few(a)) return f;
+    f.tile = pair_tile(a->M, a->F, a->dtype);
     f.x = operand(a->x, a->ld_x, a->M, a->K, a->dtype, &s);
     f.wg = operand(a->wg, a->ld_wg, a->F, a->K, a->dtype, &s);
     f.wu = operand(a->wu, a->ld_wu, a->F, a->K, a->dtype, &s);
@@ -143,6 +141,7 @@ Forward forward_plan(const sdm_ffn_args_t* a, char* ws) {
 }
 
 struct Backward {
+    int tile;
     FfnGrad grad;
     FfnLay wg, wu, x;
     FfnOperand rows, cols, w, xt;
@@ -151,25 +150,25 @@ struct Backward {
 Backward backward_plan(const sdm_ffn_args_t* a, char* ws) {
     Space s{ws, 0};
     Backward b{};
-    const int parts = a->dtype == SDM_F32 ? 3 : 1;
-    const int64_t M = a->M, K = a->K, F = a->F, Mp = up_to(M, 8), Fp = up_to(F, 8);
+    b.tile = gradient_tile(a->M, a->K, a->F, a->dtype);
+    const int64_t es = size_of(a->dtype);
+    const int64_t M = a->M, K = a->K, F = a->F, Mp = up_to(M, 16 / es), Fp = up_to(F, 16 / es);
     auto area = [&](int64_t rows, int64_t cols, FfnOperand* o) {
-        const int64_t plane = up_to(rows * cols * 2, 256);
-        char* p = s.take(plane * parts);
-        *o = FfnOperand{p, cols * 2, plane};
+        char* p = s.take(rows * cols * es);
+        *o = FfnOperand{p, cols * es};
         return p;
     };
     char* rows = area(M, 2 * Fp, &b.rows);
     char* cols = area(2 * F, Mp, &b.cols);
     char* w = area(K, 2 * Fp, &b.w);
     char* xt = area(K, Mp, &b.xt);
-    b.grad = FfnGrad{a->dh, a->gate, a->up, a->ld_dh, a->ld_gate, a->ld_up, M, F, Mp, Fp, a->dtype, a->act, rows, cols, b.rows.plane, b.cols.plane};
-    b.wg = FfnLay{a->wg, a->ld_wg, F, K, a->dtype, w, b.w.ld, b.w.plane, Fp};
+    b.grad = FfnGrad{a->dh, a->gate, a->up, a->ld_dh, a->ld_gate, a->ld_up, M, F, Mp, Fp, a->dtype, a->act, rows, cols};
+    b.wg = FfnLay{a->wg, a->ld_wg, F, K, a->dtype, w, b.w.ld, Fp};
     b.wu = b.wg;
     b.wu.src = a->wu;
     b.wu.ld = a->ld_wu;
-    b.wu.dst = w + Fp * 2;
-    b.x = FfnLay{a->x, a->ld_x, M, K, a->dtype, xt, b.xt.ld, b.xt.plane, Mp};
+    b.wu.dst = w + Fp * es;
+    b.x = FfnLay{a->x, a->ld_x, M, K, a->dtype, xt, b.xt.ld, Mp};
     b.bytes = s.used;
     return b;
 }
@@ -211,8 +210,8 @@ int sdm_ffn_forward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* s
     p.B2 = f.wu.o;
     p.M = a->M;
     p.N = a->F;
-    p.bytes = up_to(a->K * (a->dtype == SDM_F32 ? 2 : size_of(a->dtype)), 16);
-    segments(&p, a->dtype);
+    p.bytes = up_to(a->K * size_of(a->dtype), 16);
+    p.type = product_type(a->dtype);
     p.act = a->act;
     p.otype = a->otype;
     p.sm = a->sx;
@@ -225,17 +224,16 @@ int sdm_ffn_forward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* s
     p.up = a->up;
     p.ld_gate = a->ld_gate;
     p.ld_up = a->ld_up;
-    const int tile = pair_tile(p);
-    if (tiles(p, tile, true) * 256 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
+    if (!few(a) && pair_tiles(a->M, a->F, f.tile) * 512 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     int64_t threads = 0;
-    for (const Laid* l : {&f.x, &f.wg, &f.wu}) threads += l->lay.R * (l->lay.pad / 8) + 256;
+    for (const Laid* l : {&f.x, &f.wg, &f.wu}) threads += l->lay.R * cdiv(l->lay.pad * size_of(a->dtype), 16) + 256;
     if (threads >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     if ((st = prepare(a, false, f.bytes, ws, ws_bytes))) return st;
-    if (a->M <= kFfnFewRows) return status(launch_ffn_few(*a, s));
+    if (few(a)) return status(launch_ffn_few(*a, s));
     // an operand used where it lies has no rows to lay out
     const FfnLay lay[3] = {f.x.lay, f.wg.lay, f.wu.lay};
     if (const hipError_t e = launch_ffn_lay(lay, false, s)) return status(e);
-    return status(launch_ffn_pair(p, tile, s));
+    return status(launch_ffn_pair(p, f.tile, s));
 }
 
 int sdm_ffn_backward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* stream) {
@@ -263,18 +261,17 @@ int sdm_ffn_backward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* 
     dw.ldc2 = a->ld_dwu;
     dw.split = a->F;
     for (FfnProduct* p : {&dx, &dw}) {
-        segments(p, a->dtype);
+        p->type = product_type(a->dtype);
         p->otype = a->otype;
     }
-    const int tile = products_tile(both);
-    if ((tiles(dx, tile, false) + tiles(dw, tile, false)) * 256 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
+    if (gradient_tiles(a->M, a->K, a->F, b.tile) * 512 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     const int64_t gm = cdiv(b.grad.Mp, 64), gf = cdiv(b.grad.Fp, 64), gk = cdiv(a->K, 64);
     if (gm * gf * 256 >= kMaxThreads || (gm + 2 * gf) * gk * 256 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     if ((st = prepare(a, true, b.bytes, ws, ws_bytes))) return st;
     if (const hipError_t e = launch_ffn_grad(b.grad, s)) return status(e);
     const FfnLay lay[3] = {b.wg, b.wu, b.x};
     if (const hipError_t e = launch_ffn_lay(lay, true, s)) return status(e);
-    return status(launch_ffn_products(both, tile, s));
+    return status(launch_ffn_products(both, b.tile, s));
 }
 
 }  // extern "C"

@@ -2,7 +2,7 @@
 //
 // Bounded by the weights' bytes, each read once. A workgroup owns 16 rows of either weight: its eight wavefronts take
 // blocks of 256 bytes of them in turn, straight from memory into the matrix cores' operands (lane l: 16 bytes of row l % 16
-// for each 64 bytes), against the same bytes of up to 32 rows of x, which stay in the caches. The next block's loads are in
+// for each 64 bytes), against the same bytes of x's rows, which stay in the caches. The next block's loads are in
 // flight while a block is multiplied. The wavefronts' sums meet in
 // LDS and are added in order. Which element meets which place of an instruction's summed axis does not matter as long as
 // both operands agree. float32 takes float32 matrix instructions: their rate is enough for what memory brings.
@@ -163,10 +163,11 @@ __global__ __launch_bounds__(kWaves * 64) void ffn_few(const sdm_ffn_args_t a) {
 template <int DT>
 hipError_t run(const sdm_ffn_args_t& a, hipStream_t s) {
     const unsigned grid = static_cast<unsigned>((a.F + 15) / 16);
-    if (a.M <= 16)
-        ffn_few<DT, 1><<<grid, kWaves * 64, 0, s>>>(a);
-    else
-        ffn_few<DT, 2><<<grid, kWaves * 64, 0, s>>>(a);
+    if constexpr (DT == SDM_F32) {
+        if (a.M > 16)
+            ffn_few<DT, 2><<<grid, kWaves * 64, 0, s>>>(a);
+    }
+    if (a.M <= 16) ffn_few<DT, 1><<<grid, kWaves * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -5,15 +5,18 @@
 // alike, by bytes: a step takes 128 bytes of each row, of which a lane holds 32 of row l % 32 for each half of the step
 // (lanes 0 .. 31 the first 32 bytes of 64, lanes 32 .. 63 the other), two 16-byte pieces. Which element of a row meets which
 // place of the instruction's summed axis does not matter as long as A and B agree, so the same pieces feed two
-// v_mfma_f32_32x32x16 of 16-bit elements or one v_mfma_f32_32x32x64 of 8-bit ones, 64 clocks either way.
+// v_mfma_f32_32x32x16 of 16-bit elements or one v_mfma_f32_32x32x64 of 8-bit ones, 64 clocks either way. Eight float32 are
+// split into bfloat16 parts on their way from LDS and take six v_mfma_f32_32x32x16, 192 clocks, where float32's own matrix
+// instructions would take 512; the vector instructions of the split run beside another wavefront's products.
 //
 // 8-bit products: the instruction aligns 8 adjacent elements' products and cuts each off below 2^-13 of the largest (measured;
 // the groups' sums have float32's bits). 16-bit instructions would not, at half the rate; for operands rounded to 2^-4 and a
 // result of 16 bits the full rate is taken.
 //
 // Memory to LDS by buffer_load_dwordx4 ... lds, no registers between: 16 bytes of a lane go to 16 consecutive bytes a lane,
-// so the order that keeps reads off one another's banks (piece c of row r at place c ^ (r % 8)) is made by the choice of each
-// lane's source. Rows past M or N and pieces past the row's end read as zero by the buffer's bounds.
+// so the order that keeps reads off one another's banks is made by the choice of each lane's source: piece c of row r is at
+// place c ^ (r / 2 % 8). A 16-byte read serves 16 lanes at once from 64 banks, two rows' worth, and not 16 neighbouring lanes:
+// with c ^ (r % 8) half of all LDS cycles were conflicts. Rows past M or N and pieces past the row's end read as zero by the buffer's bounds.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -49,6 +52,40 @@ __device__ __forceinline__ void mma(f32x16& acc, const Piece& a, const Piece& b)
             else
                 acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a.w[i]), __builtin_bit_cast(f16x8, b.w[i]), acc, 0, 0, 0);
     }
+}
+
+// Eight float32 in three bfloat16 parts each: x = h + m + l with h = bf16(x), m = bf16(x - h), l = bf16(x - h - m), every
+// difference exact: 24 bits. Products whose parts' numbers add up to 2 or less are kept, smallest first; what is left out is
+// below 2^-25 of the product.
+struct Parts {
+    bf16x8 p[3];
+};
+__device__ __forceinline__ Parts split(const Piece& a) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    u32x4 w[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x = __uint_as_float(a.w[i / 2][i % 2 * 2]), y = __uint_as_float(a.w[i / 2][i % 2 * 2 + 1]);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            const f32x2 v = {x, y};
+            const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+            w[n][i] = b;
+            x -= __uint_as_float(b << 16);
+            y -= __uint_as_float(b & 0xffff0000u);
+        }
+    }
+    Parts o;
+#pragma unroll
+    for (int n = 0; n < 3; ++n) o.p[n] = __builtin_bit_cast(bf16x8, w[n]);
+    return o;
+}
+__device__ __forceinline__ void mma(f32x16& acc, const Parts& a, const Parts& b) {
+#pragma unroll
+    for (int order = 2; order >= 0; --order)
+#pragma unroll
+        for (int i = order; i >= 0; --i) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[order - i], b.p[i], acc, 0, 0, 0);
 }
 
 struct Buffer {
@@ -115,108 +152,91 @@ struct Both {
     int tm[2], tn[2], first;       // tiles of each; workgroups of the first
 };
 
-// Tiles of T x T (as a pair: T rows and T / 2 columns of either product), four wavefronts of T/2 x T/2. A wavefront's part of
-// B's tile is its columns of Bg, then the same of Bu. S steps of LDS: S - 1 of them in flight, or one and a half where S is 2.
-// P parts of each operand a step: 3 for the small tiles of float32, whose six products then come from one step's reads (a
-// sixth of the steps, half of the loads; 333 rows of 1111 to 777: 39 -> 17 us); the large tiles take a part of each a step.
-template <int ET, int T, int S, int P, bool PAIR>
-__global__ __launch_bounds__(256, T == 256 || P > 1 ? 1 : 2) void ffn_product(const Both both) {
-    constexpr int W = T / 2, NB = W / 32, LOADS = 2 * T / 32;       // a wavefront's rows, blocks of 32, loads a step and part
-    constexpr int PLACE = 2 * T * kStep;        // bytes of a step's part
-    __shared__ __attribute__((aligned(1024))) char lds[S][P * PLACE];
+// Tiles of T x T (as a pair: T rows and T / 2 columns of either product); a wavefront has NM blocks of 32 rows by NN of 32
+// columns, of which a pair's first half is Bg's and the second Bu's. S steps of LDS: S - 1 of them in flight, or one and a half
+// where S is 2.
+template <int T, int NM, int NN> constexpr int kWaves = (T / (32 * NM)) * (T / (32 * NN));
+template <int ET, int T, int NM, int NN, int S, bool PAIR>
+__global__ __launch_bounds__((64 * kWaves<T, NM, NN>), (T == 256 ? 1 : 2)) void ffn_product(const Both both) {
+    constexpr int WM = 32 * NM, WN = 32 * NN, WAVES = kWaves<T, NM, NN>, ACROSS = T / WN;
+    constexpr int LOADS = 2 * T / (8 * WAVES);  // a wavefront's loads a step, of 8 rows each
+    __shared__ __attribute__((aligned(1024))) char lds[S][2 * T * kStep];
     const int second = static_cast<int>(blockIdx.x) >= both.first ? 1 : 0;
     const FfnProduct& p = both.p[second];
-    const int tm = both.tm[second], tn = both.tn[second];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w >> 1, wn = w & 1;
-    __builtin_assume(w >= 0 && w < 4);
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w / ACROSS, wn = w % ACROSS;
+    __builtin_assume(w >= 0 && w < WAVES);
     int ti, tj;
-    tile_of(static_cast<int>(blockIdx.x) - (second ? both.first : 0), tm, tn, ti, tj);
-    const int64_t m0 = static_cast<int64_t>(ti) * T, n0 = static_cast<int64_t>(tj) * (PAIR ? W : T);
-    constexpr int BR = PAIR ? W : T;            // rows of a B that the tile takes
+    tile_of(static_cast<int>(blockIdx.x) - (second ? both.first : 0), both.tm[second], both.tn[second], ti, tj);
+    constexpr int BR = PAIR ? T / 2 : T;        // rows of a B that the tile takes
+    const int64_t m0 = static_cast<int64_t>(ti) * T, n0 = static_cast<int64_t>(tj) * BR;
     auto rows_of = [&](const FfnOperand& o, int64_t first, int64_t all, int most) {
         const int64_t n = min(all - first, static_cast<int64_t>(most));
         return Buffer{o.p + first * o.ld, static_cast<uint32_t>((n - 1) * o.ld + p.bytes)};
     };
     const Buffer ba = rows_of(p.A, m0, p.M, T), bb = rows_of(p.B, n0, p.N, BR), bc = PAIR ? rows_of(p.B2, n0, p.N, BR) : bb;
 
-    // Load j of wavefront w fills rows (4 j + w) 8 .. + 7 of the tile's A, then B: a lane's row and piece.
-    const int r8 = lane >> 3, piece = (lane & 7) ^ r8;
+    // Load j of wavefront w fills rows (WAVES j + w) 8 .. + 7 of the tile's A, then B: a lane's row and piece.
+    const int r8 = lane >> 3, piece = (lane & 7) ^ ((w & 1) << 2 | r8 >> 1);
     uint32_t off[LOADS];
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-        const int r = ((j % (LOADS / 2)) * 4 + w) * 8 + r8;
+        const int r = (j % (LOADS / 2) * WAVES + w) * 8 + r8;
         if (j < LOADS / 2)
             off[j] = static_cast<uint32_t>(r * p.A.ld) + piece * 16;
         else if constexpr (PAIR)
-            off[j] = static_cast<uint32_t>((r / W * (W / 2) + r % (W / 2)) * (r / (W / 2) % 2 ? p.B2.ld : p.B.ld)) + piece * 16;
+            off[j] = static_cast<uint32_t>((r / WN * (WN / 2) + r % (WN / 2)) * (r & WN / 2 ? p.B2.ld : p.B.ld)) + piece * 16;
         else
             off[j] = static_cast<uint32_t>(r * p.B.ld) + piece * 16;
     }
     const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)&lds[0][0]));
-    const int segments = P > 1 ? 1 : p.segments, steps = static_cast<int>((p.bytes + kStep - 1) / kStep), total = steps * segments;
-    // The next step's buffers; past the last step nothing is read.
-    int seg = 0, at = 0;
-    u32x4 ra[P], rb[P], rc[P];
+    const int steps = static_cast<int>((p.bytes + kStep - 1) / kStep), total = steps;
+    // The next step's buffers. Past the last step they are empty, since their bounds less what is behind would wrap around:
+    // every load of such a step reads nothing.
+    int at = 0;
+    u32x4 ra, rb, rc;
     uint32_t none;
     auto next_step = [&]() {
         const int64_t from = static_cast<int64_t>(at) * kStep;
-        auto part = [&](const Buffer& b, int64_t plane, uint32_t which) {
-            return resource(Buffer{b.p + plane * which + from, b.n - static_cast<uint32_t>(from)});
-        };
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const uint32_t ia = P > 1 ? i : p.aparts >> (2 * seg) & 3, ib = P > 1 ? i : p.bparts >> (2 * seg) & 3;
-            ra[i] = part(ba, p.A.plane, ia);
-            rb[i] = part(bb, p.B.plane, ib);
-            rc[i] = PAIR ? part(bc, p.B2.plane, ib) : rb[i];
-        }
-        none = seg >= segments || from + piece * 16 >= p.bytes ? kNowhere : 0u;       // the row has ended
-        if (++at == steps) {
-            at = 0;
-            ++seg;
-        }
+        const bool past = at >= steps;
+        auto from_here = [&](const Buffer& b) { return resource(Buffer{b.p + (past ? 0 : from), past ? 0u : b.n - static_cast<uint32_t>(from)}); };
+        ra = from_here(ba);
+        rb = from_here(bb);
+        rc = PAIR ? from_here(bc) : rb;
+        none = from + piece * 16 >= p.bytes ? kNowhere : 0u;       // the row has ended
+        ++at;
     };
-    auto load = [&](int buf, int n) {
-        const int i = n / LOADS, j = n % LOADS;
-        const uint32_t to = base + buf * (P * PLACE) + i * PLACE + (j * 4 + w) * 1024;
+    auto load = [&](int buf, int j) {
+        const uint32_t to = base + buf * (2 * T * kStep) + (j * WAVES + w) * 1024;
         if (j < LOADS / 2)
-            load_lds(ra[i], to, off[j] | none);
+            load_lds(ra, to, off[j] | none);
         else
-            load_lds(PAIR && (j - LOADS / 2) * 32 + w * 8 & W / 2 ? rc[i] : rb[i], to, off[j] | none);
+            load_lds(PAIR && ((j - LOADS / 2) * WAVES + w) * 8 & WN / 2 ? rc : rb, to, off[j] | none);
     };
-    f32x16 acc[NB][NB];                         // [columns][rows]
+    f32x16 acc[NN][NM];                         // [columns][rows]
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < NN; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = (f32x16){0};
-    Piece fa[2][P][NB], fb[2][P][NB];
-    const int lr = lane & 31, lh = lane >> 5, sw = lr & 7;
-    constexpr int READS = 4 * NB * P, BLOCKS = NB * NB, AHEAD = BLOCKS > 1 ? BLOCKS / 2 : 1;
+        for (int j = 0; j < NM; ++j) acc[i][j] = (f32x16){0};
+    Piece fa[2][NM], fb[2][NN];
+    const int lr = lane & 31, lh = lane >> 5, sw = lr >> 1 & 7;
+    constexpr int READS = 2 * (NM + NN), BLOCKS = NM * NN, AHEAD = BLOCKS > 1 ? BLOCKS / 2 : 1;
     // Read n of a half step, in the order in which the products want them: B's first block, A's, B's others.
     auto read = [&](int buf, int half, int n) {
-        const int part = P - 1 - n / (4 * NB), k = n % (4 * NB), c = ((half * 4 + lh * 2 + k % 2) ^ sw) * 16, i = k / 2;
-        const char* a = &lds[buf][part * PLACE + (wm * W + lr) * kStep + c];
-        const char* b = &lds[buf][part * PLACE + (T + wn * W + lr) * kStep + c];
-        if (i >= 1 && i <= NB)
-            fa[half][part][i - 1].w[k % 2] = *reinterpret_cast<const u32x4*>(a + (i - 1) * 32 * kStep);
+        const int i = n / 2, k = n % 2, c = ((half * 4 + lh * 2 + k) ^ sw) * 16;
+        if (i >= 1 && i <= NM)
+            fa[half][i - 1].w[k] = *reinterpret_cast<const u32x4*>(&lds[buf][(wm * WM + (i - 1) * 32 + lr) * kStep + c]);
         else
-            fb[half][part][i ? i - NB : 0].w[k % 2] = *reinterpret_cast<const u32x4*>(b + (i ? i - NB : 0) * 32 * kStep);
-    };
-    // the part products of a block, smallest first
-    auto products = [&](int half, int i, int j) {
-#pragma unroll
-        for (int order = P - 1; order >= 0; --order)
-#pragma unroll
-            for (int x = order; x >= 0; --x) mma<ET>(acc[i][j], fb[half][order - x][i], fa[half][x][j]);
+            fb[half][i ? i - NM : 0].w[k] = *reinterpret_cast<const u32x4*>(&lds[buf][(T + wn * WN + (i ? i - NM : 0) * 32 + lr) * kStep + c]);
     };
     // A step's second half is read while its first is multiplied, and the next step's first half while the second is. Between
     // the two the wavefronts meet: all reads of this step are back, so its place takes the loads of the step S later, which
     // have S - 1 whole steps to land. Blocks of 64 clocks of products, with the reads behind the first half of them and the
     // loads spread over all, in the order written here (the compiler would gather the products behind the barrier).
     auto blocks = [&](int half, int from, bool loads, int to) {
+        Parts pa[NM], pb[NN];       // of float32
 #pragma unroll
         for (int n = 0; n < BLOCKS; ++n) {
-            constexpr int kReads = READS / AHEAD, kLoads = P * LOADS / BLOCKS;
+            constexpr int kReads = READS / AHEAD, kLoads = LOADS / BLOCKS;
 #pragma unroll
             for (int k = 0; k < kReads; ++k)
                 if (n * kReads + k < READS) read(from, 1 - half, n * kReads + k);
@@ -224,7 +244,14 @@ __global__ __launch_bounds__(256, T == 256 || P > 1 ? 1 : 2) void ffn_product(co
 #pragma unroll
                 for (int k = 0; k < kLoads; ++k) load(to, n * kLoads + k);
             }
-            products(half, n / NB, n % NB);
+            const int i = n / NM, j = n % NM;
+            if constexpr (ET == kF32) {
+                if (j == 0) pb[i] = split(fb[half][i]);
+                if (i == 0) pa[j] = split(fa[half][j]);
+                mma(acc[i][j], pb[i], pa[j]);
+            } else {
+                mma<ET>(acc[i][j], fb[half][i], fa[half][j]);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -232,16 +259,16 @@ __global__ __launch_bounds__(256, T == 256 || P > 1 ? 1 : 2) void ffn_product(co
     for (int s = 0; s < S; ++s) {
         next_step();
 #pragma unroll
-        for (int j = 0; j < P * LOADS; ++j) load(s, j);
+        for (int j = 0; j < LOADS; ++j) load(s, j);
     }
-    meet<(S - 1) * P * LOADS>();
+    meet<(S - 1) * LOADS>();
 #pragma unroll
     for (int k = 0; k < READS; ++k) read(0, 0, k);
     for (int t = 0; t < total; ++t) {
         const int buf = t % S;
         blocks(0, buf, false, 0);
         next_step();
-        meet<(S - 2) * P * LOADS>();
+        meet<(S - 2) * LOADS>();
         __builtin_amdgcn_sched_barrier(0);
         blocks(1, (t + 1) % S, true, buf);
     }
@@ -249,11 +276,11 @@ __global__ __launch_bounds__(256, T == 256 || P > 1 ? 1 : 2) void ffn_product(co
     // Lane l holds columns 8 (i / 4) + 4 (l / 32) + i % 4 of row l % 32 of each block. 32 rows at a time go through the
     // wavefront's own part of LDS, so that its lanes store whole stretches of a row; rows there are 4 banks apart.
     meet<0>();
-    constexpr int kRow = W * 4 + 16, kLanes = (PAIR ? W / 2 : W) / 4, kRows = 64 / kLanes;
-    static_assert(4 * 32 * kRow <= sizeof(lds), "the wavefronts' rows fit");
+    constexpr int kRow = WN * 4 + 16, kLanes = (PAIR ? WN / 2 : WN) / 4, kRows = 64 / kLanes;
+    static_assert(WAVES * 32 * kRow <= static_cast<int>(sizeof(lds)), "the wavefronts' rows fit");
     char* mine = &lds[0][0] + w * 32 * kRow;
     const int col = lane % kLanes * 4;
-    const int64_t n = n0 + wn * (PAIR ? W / 2 : W) + col, left = p.N - n;
+    const int64_t n = n0 + wn * (PAIR ? WN / 2 : WN) + col, left = p.N - n;
     float sg[4], su[4];
     if constexpr (ET == kE4m3) {
 #pragma unroll
@@ -264,16 +291,16 @@ __global__ __launch_bounds__(256, T == 256 || P > 1 ? 1 : 2) void ffn_product(co
         }
     }
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
+    for (int j = 0; j < NM; ++j) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < NN; ++i)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 *reinterpret_cast<f32x4*>(mine + lr * kRow + (i * 32 + q * 8 + lh * 4) * 4) =
                     f32x4{acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
         for (int r = lane / kLanes; r < 32; r += kRows) {
-            const int64_t m = m0 + wm * W + j * 32 + r;
+            const int64_t m = m0 + wm * WM + j * 32 + r;
             const f32x4* from = reinterpret_cast<const f32x4*>(mine + r * kRow + col * 4);
             if (m >= p.M || left <= 0) continue;
             const f32x4 x = from[0];
@@ -282,7 +309,7 @@ __global__ __launch_bounds__(256, T == 256 || P > 1 ? 1 : 2) void ffn_product(co
                 char* c = m < p.split ? p.c : p.c2;
                 store4(p.otype, c, (m < p.split ? m * p.ldc : (m - p.split) * p.ldc2) + n, left, g);
             } else {
-                const f32x4 y = from[W / 8];
+                const f32x4 y = from[WN / 8];
                 float u[4] = {y[0], y[1], y[2], y[3]}, h[4];
                 if constexpr (ET == kE4m3) {
                     const float sm = p.sm[m];
@@ -312,7 +339,7 @@ __global__ __launch_bounds__(256, T == 256 || P > 1 ? 1 : 2) void ffn_product(co
     }
 }
 
-template <int ET, int T, int S, int P, bool PAIR>
+template <int ET, int T, int NM, int NN, int S, bool PAIR>
 hipError_t run(const FfnProduct* p, int n, hipStream_t s) {
     Both b{};
     int64_t total = 0;
@@ -323,26 +350,27 @@ hipError_t run(const FfnProduct* p, int n, hipStream_t s) {
         total += static_cast<int64_t>(b.tm[i]) * b.tn[i];
         if (i == 0) b.first = static_cast<int>(total);
     }
-    ffn_product<ET, T, S, P, PAIR><<<static_cast<unsigned>(total), 256, 0, s>>>(b);
+    ffn_product<ET, T, NM, NN, S, PAIR><<<static_cast<unsigned>(total), 64 * kWaves<T, NM, NN>, 0, s>>>(b);
     return hipGetLastError();
 }
 template <int ET, bool PAIR>
 hipError_t tiled(const FfnProduct* p, int n, int tile, hipStream_t s) {
-    if (tile == 256) return run<ET, 256, 2, 1, PAIR>(p, n, s);
-    if (tile == 128) return run<ET, 128, 2, 1, PAIR>(p, n, s);
-    if constexpr (ET == kBf16)
-        if (p[0].segments > 1) return run<ET, 64, 3, 3, PAIR>(p, n, s);
-    return run<ET, 64, 4, 1, PAIR>(p, n, s);
+    if constexpr (ET != kF32)
+        if (tile == 256) return run<ET, 256, 4, 2, 2, PAIR>(p, n, s);
+    if (tile == 128) return run<ET, 128, 2, 2, 2, PAIR>(p, n, s);
+    return run<ET, 64, 1, 1, 4, PAIR>(p, n, s);
 }
 
 }  // namespace
 
-// 8-bit operands come as a pair only (the host has no other call)
+// 8-bit operands come as a pair only, float32 ones in tiles of 128 at the most (the host has no other call)
 hipError_t launch_ffn_pair(const FfnProduct& p, int tile, hipStream_t s) {
     if (p.type == kE4m3) return tiled<kE4m3, true>(&p, 1, tile, s);
+    if (p.type == kF32) return tiled<kF32, true>(&p, 1, tile, s);
     return p.type == kBf16 ? tiled<kBf16, true>(&p, 1, tile, s) : tiled<kF16, true>(&p, 1, tile, s);
 }
 hipError_t launch_ffn_products(const FfnProduct (&p)[2], int tile, hipStream_t s) {
+    if (p[0].type == kF32) return tiled<kF32, false>(p, 2, tile, s);
     return p[0].type == kBf16 ? tiled<kBf16, false>(p, 2, tile, s) : tiled<kF16, false>(p, 2, tile, s);
 }
 

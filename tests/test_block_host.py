@@ -206,8 +206,9 @@ def test_ffn_backward_checks(change, status):
 def test_ffn_workspaces():
     lib, r = L.load(), ctypes.byref
     size = lambda **kw: lib.sdm_ffn_workspace(r(ffn(**kw)), 0)  # noqa: E731
-    assert size() == 0 and size(M=3, dtype=0, otype=0) == 0        # rows where they lie; few rows
-    assert size(x=(1 << 25) + 2) > 0 and size(ld_wg=73) > 0 and size(K=71) > 0 and size(dtype=0, otype=0) > 0
+    # rows where they lie; few rows
+    assert size() == 0 and size(dtype=0, otype=0) == 0 and size(M=3, x=(1 << 25) + 2) == 0
+    assert size(x=(1 << 25) + 2) > 0 and size(ld_wg=73) > 0 and size(K=71) > 0
     n = lib.sdm_ffn_workspace(r(ffn()), 1)
     assert n > 0 and lib.sdm_ffn_workspace(r(ffn(F=0)), 1) == SHAPE
     odd = ffn(K=71)
