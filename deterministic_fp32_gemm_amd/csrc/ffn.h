@@ -47,7 +47,7 @@ struct FfnLay {
     int64_t ldd;                // bytes
     int64_t pad;                // elements
 };
-hipError_t launch_ffn_lay(const FfnLay (&l)[3], bool turned, hipStream_t stream);     // one launch; without rows: none
+hipError_t launch_ffn_lay(const FfnLay (&l)[3], hipStream_t stream);     // one launch; without rows: none
 
 // dg and du from dh, g and u: rows[m] = dg, zeros to Fp, du, zeros to 2 Fp; cols[f] = dg's column f, zeros to Mp, and du's at
 // row F + f.
@@ -58,6 +58,7 @@ struct FfnGrad {
     int dtype, act;
     char *rows, *cols;
 };
-hipError_t launch_ffn_grad(const FfnGrad& g, hipStream_t stream);
+// One launch, with the three operands turned.
+hipError_t launch_ffn_grad(const FfnGrad& g, const FfnLay (&l)[3], hipStream_t stream);
 
 }  // namespace sdm_delta

@@ -232,7 +232,7 @@ int sdm_ffn_forward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* s
     if (few(a)) return status(launch_ffn_few(*a, s));
     // an operand used where it lies has no rows to lay out
     const FfnLay lay[3] = {f.x.lay, f.wg.lay, f.wu.lay};
-    if (const hipError_t e = launch_ffn_lay(lay, false, s)) return status(e);
+    if (const hipError_t e = launch_ffn_lay(lay, s)) return status(e);
     return status(launch_ffn_pair(p, f.tile, s));
 }
 
@@ -266,11 +266,10 @@ int sdm_ffn_backward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* 
     }
     if (gradient_tiles(a->M, a->K, a->F, b.tile) * 512 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     const int64_t gm = cdiv(b.grad.Mp, 64), gf = cdiv(b.grad.Fp, 64), gk = cdiv(a->K, 64);
-    if (gm * gf * 256 >= kMaxThreads || (gm + 2 * gf) * gk * 256 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
+    if ((gm * gf + (gm + 2 * gf) * gk) * 256 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     if ((st = prepare(a, true, b.bytes, ws, ws_bytes))) return st;
-    if (const hipError_t e = launch_ffn_grad(b.grad, s)) return status(e);
     const FfnLay lay[3] = {b.wg, b.wu, b.x};
-    if (const hipError_t e = launch_ffn_lay(lay, true, s)) return status(e);
+    if (const hipError_t e = launch_ffn_grad(b.grad, lay, s)) return status(e);
     return status(launch_ffn_products(both, b.tile, s));
 }
 

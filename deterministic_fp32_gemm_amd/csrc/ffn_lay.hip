@@ -109,10 +109,8 @@ __device__ __forceinline__ void four(uint16_t (&o)[4], const uint16_t* row, int6
 
 // dst[c][r]: a tile of 64 rows and 64 columns.
 template <int N>
-__global__ __launch_bounds__(256) void lay_turned(const Three three) {
+__device__ __forceinline__ void lay_turned(const Three& three, unsigned b, bits_t<N> (&tile)[64][kAcross<N>]) {
     using B = bits_t<N>;
-    __shared__ B tile[64][kAcross<N>];
-    unsigned b = blockIdx.x;
     const FfnLay& l = three.l[which(three, b)];
     const unsigned across = static_cast<unsigned>((l.C + 63) / 64);
     const int64_t r0 = static_cast<int64_t>(b / across) * 64, c0 = static_cast<int64_t>(b % across) * 64;
@@ -139,13 +137,18 @@ __device__ __forceinline__ float value(uint32_t b, float) { return __uint_as_flo
 __device__ __forceinline__ float value(uint16_t b, __bf16) { return static_cast<float>(__builtin_bit_cast(__bf16, b)); }
 __device__ __forceinline__ float value(uint16_t b, _Float16) { return static_cast<float>(__builtin_bit_cast(_Float16, b)); }
 
-// 16-bit types: dg and du are rounded to dtype, as their products take them.
+// dg and du, and, in the workgroups from `first` on, the operands to be turned: one launch for all that the gradient's products
+// read. 16-bit types: dg and du are rounded to dtype, as their products take them.
 template <int DT>
-__global__ __launch_bounds__(256) void ffn_grad(const FfnGrad a, const int across) {
+__global__ __launch_bounds__(256) void ffn_grad(const FfnGrad a, const int across, const Three three, const unsigned first) {
     using T = elem_t<DT>;
     constexpr int N = sizeof(T);
     using B = bits_t<N>;
     __shared__ B tile[2][64][kAcross<N>];
+    if (blockIdx.x >= first) {
+        lay_turned<N>(three, blockIdx.x - first, tile[0]);
+        return;
+    }
     const int64_t m0 = static_cast<int64_t>(blockIdx.x / across) * 64, f0 = static_cast<int64_t>(blockIdx.x % across) * 64;
     const int r16 = threadIdx.x / 16, c = threadIdx.x % 16 * 4;
     B dh[4][4];
@@ -191,41 +194,43 @@ __global__ __launch_bounds__(256) void ffn_grad(const FfnGrad a, const int acros
 int64_t tiles(int64_t n) { return (n + 63) / 64; }
 
 template <int N>
-hipError_t lay(const FfnLay (&l)[3], bool turned, hipStream_t s) {
+hipError_t lay(const FfnLay (&l)[3], hipStream_t s) {
     Three t{};
     unsigned n = 0;
     for (int i = 0; i < 3; ++i) {
         t.l[i] = l[i];
-        if (l[i].R) n += static_cast<unsigned>(turned ? tiles(l[i].pad) * tiles(l[i].C) : (l[i].R * (l[i].pad * N / 16) + 255) / 256);
+        n += static_cast<unsigned>((l[i].R * (l[i].pad * N / 16) + 255) / 256);
         t.upto[i] = n;
     }
-    if (!n) return hipSuccess;
-    if (!turned)
-        lay_rows<N><<<n, 256, 0, s>>>(t);
-    else if constexpr (N > 1)
-        lay_turned<N><<<n, 256, 0, s>>>(t);
+    if (n) lay_rows<N><<<n, 256, 0, s>>>(t);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t grad(const FfnGrad& g, const FfnLay (&l)[3], hipStream_t s) {
+    const unsigned first = static_cast<unsigned>(tiles(g.Mp) * tiles(g.Fp));
+    Three t{};
+    unsigned n = 0;
+    for (int i = 0; i < 3; ++i) {
+        t.l[i] = l[i];
+        n += static_cast<unsigned>(tiles(l[i].pad) * tiles(l[i].C));
+        t.upto[i] = n;
+    }
+    ffn_grad<DT><<<first + n, 256, 0, s>>>(g, static_cast<int>(tiles(g.Fp)), t, first);
     return hipGetLastError();
 }
 
 }  // namespace
 
-// All three of one type; 8-bit ones are never turned (they have no gradient).
-hipError_t launch_ffn_lay(const FfnLay (&l)[3], bool turned, hipStream_t s) {
+// All three of one type; without rows: none
+hipError_t launch_ffn_lay(const FfnLay (&l)[3], hipStream_t s) {
     const int dtype = l[0].R ? l[0].dtype : l[1].R ? l[1].dtype : l[2].dtype;
-    if (dtype == SDM_F32) return lay<4>(l, turned, s);
-    return dtype == SDM_E4M3 ? lay<1>(l, turned, s) : lay<2>(l, turned, s);
+    return dtype == SDM_F32 ? lay<4>(l, s) : dtype == SDM_E4M3 ? lay<1>(l, s) : lay<2>(l, s);
 }
 
-hipError_t launch_ffn_grad(const FfnGrad& g, hipStream_t s) {
-    const unsigned grid = static_cast<unsigned>(tiles(g.Mp) * tiles(g.Fp));
-    const int across = static_cast<int>(tiles(g.Fp));
-    if (g.dtype == SDM_F32)
-        ffn_grad<SDM_F32><<<grid, 256, 0, s>>>(g, across);
-    else if (g.dtype == SDM_BF16)
-        ffn_grad<SDM_BF16><<<grid, 256, 0, s>>>(g, across);
-    else
-        ffn_grad<SDM_F16><<<grid, 256, 0, s>>>(g, across);
-    return hipGetLastError();
+hipError_t launch_ffn_grad(const FfnGrad& g, const FfnLay (&l)[3], hipStream_t s) {
+    if (g.dtype == SDM_F32) return grad<SDM_F32>(g, l, s);
+    return g.dtype == SDM_BF16 ? grad<SDM_BF16>(g, l, s) : grad<SDM_F16>(g, l, s);
 }
 
 }  // namespace sdm_delta

@@ -154,17 +154,19 @@ struct Both {
 
 // Tiles of T x T (as a pair: T rows and T / 2 columns of either product); a wavefront has NM blocks of 32 rows by NN of 32
 // columns, of which a pair's first half is Bg's and the second Bu's. S steps of LDS: S - 1 of them in flight, or one and a half
-// where S is 2.
-template <int T, int NM, int NN> constexpr int kWaves = (T / (32 * NM)) * (T / (32 * NN));
-template <int ET, int T, int NM, int NN, int S, bool PAIR>
-__global__ __launch_bounds__((64 * kWaves<T, NM, NN>), (T == 256 ? 1 : 2)) void ffn_product(const Both both) {
-    constexpr int WM = 32 * NM, WN = 32 * NN, WAVES = kWaves<T, NM, NN>, ACROSS = T / WN;
+// where S is 2. HALVES: two wavefronts share a part of the tile, one for each half of every step, and add up at the end: small
+// tiles are there for calls with few of them, whose steps are chains of a read, a split and products that nothing else hides.
+template <int T, int NM, int NN, bool HALVES> constexpr int kWaves = (T / (32 * NM)) * (T / (32 * NN)) * (HALVES ? 2 : 1);
+template <int ET, int T, int NM, int NN, int S, bool HALVES, bool PAIR>
+__global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2)) void ffn_product(const Both both) {
+    constexpr int WM = 32 * NM, WN = 32 * NN, WAVES = kWaves<T, NM, NN, HALVES>, ACROSS = T / WN, OWNERS = HALVES ? WAVES / 2 : WAVES;
     constexpr int LOADS = 2 * T / (8 * WAVES);  // a wavefront's loads a step, of 8 rows each
     __shared__ __attribute__((aligned(1024))) char lds[S][2 * T * kStep];
     const int second = static_cast<int>(blockIdx.x) >= both.first ? 1 : 0;
     const FfnProduct& p = both.p[second];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w / ACROSS, wn = w % ACROSS;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     __builtin_assume(w >= 0 && w < WAVES);
+    const int wm = w % OWNERS / ACROSS, wn = w % ACROSS, mine_half = w / OWNERS;
     int ti, tj;
     tile_of(static_cast<int>(blockIdx.x) - (second ? both.first : 0), both.tm[second], both.tn[second], ti, tj);
     constexpr int BR = PAIR ? T / 2 : T;        // rows of a B that the tile takes
@@ -221,36 +223,36 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN>), (T == 256 ? 1 : 2)) void 
     const int lr = lane & 31, lh = lane >> 5, sw = lr >> 1 & 7;
     constexpr int READS = 2 * (NM + NN), BLOCKS = NM * NN, AHEAD = BLOCKS > 1 ? BLOCKS / 2 : 1;
     // Read n of a half step, in the order in which the products want them: B's first block, A's, B's others.
-    auto read = [&](int buf, int half, int n) {
+    auto read = [&](int buf, int to, int half, int n) {
         const int i = n / 2, k = n % 2, c = ((half * 4 + lh * 2 + k) ^ sw) * 16;
         if (i >= 1 && i <= NM)
-            fa[half][i - 1].w[k] = *reinterpret_cast<const u32x4*>(&lds[buf][(wm * WM + (i - 1) * 32 + lr) * kStep + c]);
+            fa[to][i - 1].w[k] = *reinterpret_cast<const u32x4*>(&lds[buf][(wm * WM + (i - 1) * 32 + lr) * kStep + c]);
         else
-            fb[half][i ? i - NM : 0].w[k] = *reinterpret_cast<const u32x4*>(&lds[buf][(T + wn * WN + (i ? i - NM : 0) * 32 + lr) * kStep + c]);
+            fb[to][i ? i - NM : 0].w[k] = *reinterpret_cast<const u32x4*>(&lds[buf][(T + wn * WN + (i ? i - NM : 0) * 32 + lr) * kStep + c]);
     };
     // A step's second half is read while its first is multiplied, and the next step's first half while the second is. Between
     // the two the wavefronts meet: all reads of this step are back, so its place takes the loads of the step S later, which
     // have S - 1 whole steps to land. Blocks of 64 clocks of products, with the reads behind the first half of them and the
     // loads spread over all, in the order written here (the compiler would gather the products behind the barrier).
-    auto blocks = [&](int half, int from, bool loads, int to) {
+    auto blocks = [&](int slot, int from, int half, bool loads, int to) {
         Parts pa[NM], pb[NN];       // of float32
 #pragma unroll
         for (int n = 0; n < BLOCKS; ++n) {
             constexpr int kReads = READS / AHEAD, kLoads = LOADS / BLOCKS;
 #pragma unroll
             for (int k = 0; k < kReads; ++k)
-                if (n * kReads + k < READS) read(from, 1 - half, n * kReads + k);
+                if (n * kReads + k < READS) read(from, 1 - slot, half, n * kReads + k);
             if (loads) {
 #pragma unroll
                 for (int k = 0; k < kLoads; ++k) load(to, n * kLoads + k);
             }
             const int i = n / NM, j = n % NM;
             if constexpr (ET == kF32) {
-                if (j == 0) pb[i] = split(fb[half][i]);
-                if (i == 0) pa[j] = split(fa[half][j]);
+                if (j == 0) pb[i] = split(fb[slot][i]);
+                if (i == 0) pa[j] = split(fa[slot][j]);
                 mma(acc[i][j], pb[i], pa[j]);
             } else {
-                mma<ET>(acc[i][j], fb[half][i], fa[half][j]);
+                mma<ET>(acc[i][j], fb[slot][i], fa[slot][j]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -263,21 +265,51 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN>), (T == 256 ? 1 : 2)) void 
     }
     meet<(S - 1) * LOADS>();
 #pragma unroll
-    for (int k = 0; k < READS; ++k) read(0, 0, k);
-    for (int t = 0; t < total; ++t) {
-        const int buf = t % S;
-        blocks(0, buf, false, 0);
-        next_step();
-        meet<(S - 2) * LOADS>();
-        __builtin_amdgcn_sched_barrier(0);
-        blocks(1, (t + 1) % S, true, buf);
+    for (int k = 0; k < READS; ++k) read(0, 0, HALVES ? mine_half : 0, k);
+    if constexpr (HALVES) {
+        // the next step's half is read behind this one's products
+        auto step = [&](int slot, int t) {
+            next_step();
+            meet<(S - 2) * LOADS>();
+            __builtin_amdgcn_sched_barrier(0);
+            blocks(slot, (t + 1) % S, mine_half, true, t % S);
+        };
+        for (int t = 0; t < total; t += 2) {
+            step(0, t);
+            if (t + 1 < total) step(1, t + 1);
+        }
+    } else {
+        for (int t = 0; t < total; ++t) {
+            const int buf = t % S;
+            blocks(0, buf, 1, false, 0);
+            next_step();
+            meet<(S - 2) * LOADS>();
+            __builtin_amdgcn_sched_barrier(0);
+            blocks(1, (t + 1) % S, 0, true, buf);
+        }
     }
 
     // Lane l holds columns 8 (i / 4) + 4 (l / 32) + i % 4 of row l % 32 of each block. 32 rows at a time go through the
     // wavefront's own part of LDS, so that its lanes store whole stretches of a row; rows there are 4 banks apart.
     meet<0>();
     constexpr int kRow = WN * 4 + 16, kLanes = (PAIR ? WN / 2 : WN) / 4, kRows = 64 / kLanes;
-    static_assert(WAVES * 32 * kRow <= static_cast<int>(sizeof(lds)), "the wavefronts' rows fit");
+    static_assert(OWNERS * 32 * kRow + (HALVES ? OWNERS * 4096 : 0) <= static_cast<int>(sizeof(lds)), "the wavefronts' rows fit");
+    if constexpr (HALVES) {
+        static_assert(NM == 1 && NN == 1, "one block a wavefront");
+        f32x4* other = reinterpret_cast<f32x4*>(&lds[0][0] + OWNERS * 32 * kRow + w % OWNERS * 4096) + lane;
+        if (mine_half) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) other[q * 64] = f32x4{acc[0][0][q * 4], acc[0][0][q * 4 + 1], acc[0][0][q * 4 + 2], acc[0][0][q * 4 + 3]};
+        }
+        meet<0>();
+        if (mine_half) return;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const f32x4 x = other[q * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[0][0][q * 4 + e] += x[e];
+        }
+    }
     char* mine = &lds[0][0] + w * 32 * kRow;
     const int col = lane % kLanes * 4;
     const int64_t n = n0 + wn * (PAIR ? WN / 2 : WN) + col, left = p.N - n;
@@ -339,7 +371,7 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN>), (T == 256 ? 1 : 2)) void 
     }
 }
 
-template <int ET, int T, int NM, int NN, int S, bool PAIR>
+template <int ET, int T, int NM, int NN, int S, bool HALVES, bool PAIR>
 hipError_t run(const FfnProduct* p, int n, hipStream_t s) {
     Both b{};
     int64_t total = 0;
@@ -350,15 +382,15 @@ hipError_t run(const FfnProduct* p, int n, hipStream_t s) {
         total += static_cast<int64_t>(b.tm[i]) * b.tn[i];
         if (i == 0) b.first = static_cast<int>(total);
     }
-    ffn_product<ET, T, NM, NN, S, PAIR><<<static_cast<unsigned>(total), 64 * kWaves<T, NM, NN>, 0, s>>>(b);
+    ffn_product<ET, T, NM, NN, S, HALVES, PAIR><<<static_cast<unsigned>(total), 64 * kWaves<T, NM, NN, HALVES>, 0, s>>>(b);
     return hipGetLastError();
 }
 template <int ET, bool PAIR>
 hipError_t tiled(const FfnProduct* p, int n, int tile, hipStream_t s) {
     if constexpr (ET != kF32)
-        if (tile == 256) return run<ET, 256, 4, 2, 2, PAIR>(p, n, s);
-    if (tile == 128) return run<ET, 128, 2, 2, 2, PAIR>(p, n, s);
-    return run<ET, 64, 1, 1, 4, PAIR>(p, n, s);
+        if (tile == 256) return run<ET, 256, 4, 2, 2, false, PAIR>(p, n, s);
+    if (tile == 128) return run<ET, 128, 2, 2, 2, false, PAIR>(p, n, s);
+    return run<ET, 64, 1, 1, 4, true, PAIR>(p, n, s);
 }
 
 }  // namespace
