@@ -153,15 +153,15 @@ struct Both {
 };
 
 // Tiles of T x T (as a pair: T rows and T / 2 columns of either product); a wavefront has NM blocks of 32 rows by NN of 32
-// columns, of which a pair's first half is Bg's and the second Bu's. S steps of LDS: S - 1 of them in flight, or one and a half
-// where S is 2. HALVES: two wavefronts share a part of the tile, one for each half of every step, and add up at the end: small
+// columns, of which a pair's first half is Bg's and the second Bu's. LDS is a ring of U places, each for A's or B's rows of one
+// step, A and B in turn. HALVES: two wavefronts share a part of the tile, one for each half of every step, and add up at the end: small
 // tiles are there for calls with few of them, whose steps are chains of a read, a split and products that nothing else hides.
 template <int T, int NM, int NN, bool HALVES> constexpr int kWaves = (T / (32 * NM)) * (T / (32 * NN)) * (HALVES ? 2 : 1);
-template <int ET, int T, int NM, int NN, int S, bool HALVES, bool PAIR>
+template <int ET, int T, int NM, int NN, int U, bool HALVES, bool PAIR>
 __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2)) void ffn_product(const Both both) {
     constexpr int WM = 32 * NM, WN = 32 * NN, WAVES = kWaves<T, NM, NN, HALVES>, ACROSS = T / WN, OWNERS = HALVES ? WAVES / 2 : WAVES;
-    constexpr int LOADS = 2 * T / (8 * WAVES);  // a wavefront's loads a step, of 8 rows each
-    __shared__ __attribute__((aligned(1024))) char lds[S][2 * T * kStep];
+    constexpr int LOADS = T / (8 * WAVES), PLACE = T * kStep;   // a wavefront's loads of a place, of 8 rows each; its bytes
+    __shared__ __attribute__((aligned(1024))) char lds[U][PLACE];
     const int second = static_cast<int>(blockIdx.x) >= both.first ? 1 : 0;
     const FfnProduct& p = both.p[second];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -177,21 +177,20 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
     };
     const Buffer ba = rows_of(p.A, m0, p.M, T), bb = rows_of(p.B, n0, p.N, BR), bc = PAIR ? rows_of(p.B2, n0, p.N, BR) : bb;
 
-    // Load j of wavefront w fills rows (WAVES j + w) 8 .. + 7 of the tile's A, then B: a lane's row and piece.
+    // Load j of wavefront w fills rows (WAVES j + w) 8 .. + 7 of a place: a lane's row and piece, and their offsets in A and B.
     const int r8 = lane >> 3, piece = (lane & 7) ^ ((w & 1) << 2 | r8 >> 1);
-    uint32_t off[LOADS];
+    uint32_t off_a[LOADS], off_b[LOADS];
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-        const int r = (j % (LOADS / 2) * WAVES + w) * 8 + r8;
-        if (j < LOADS / 2)
-            off[j] = static_cast<uint32_t>(r * p.A.ld) + piece * 16;
-        else if constexpr (PAIR)
-            off[j] = static_cast<uint32_t>((r / WN * (WN / 2) + r % (WN / 2)) * (r & WN / 2 ? p.B2.ld : p.B.ld)) + piece * 16;
+        const int r = (j * WAVES + w) * 8 + r8;
+        off_a[j] = static_cast<uint32_t>(r * p.A.ld) + piece * 16;
+        if constexpr (PAIR)
+            off_b[j] = static_cast<uint32_t>((r / WN * (WN / 2) + r % (WN / 2)) * (r & WN / 2 ? p.B2.ld : p.B.ld)) + piece * 16;
         else
-            off[j] = static_cast<uint32_t>(r * p.B.ld) + piece * 16;
+            off_b[j] = static_cast<uint32_t>(r * p.B.ld) + piece * 16;
     }
     const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)&lds[0][0]));
-    const int steps = static_cast<int>((p.bytes + kStep - 1) / kStep), total = steps;
+    const int steps = static_cast<int>((p.bytes + kStep - 1) / kStep);
     // The next step's buffers. Past the last step they are empty, since their bounds less what is behind would wrap around:
     // every load of such a step reads nothing.
     int at = 0;
@@ -207,12 +206,9 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
         none = from + piece * 16 >= p.bytes ? kNowhere : 0u;       // the row has ended
         ++at;
     };
-    auto load = [&](int buf, int j) {
-        const uint32_t to = base + buf * (2 * T * kStep) + (j * WAVES + w) * 1024;
-        if (j < LOADS / 2)
-            load_lds(ra, to, off[j] | none);
-        else
-            load_lds(PAIR && ((j - LOADS / 2) * WAVES + w) * 8 & WN / 2 ? rc : rb, to, off[j] | none);
+    auto load_a = [&](int place, int j) { load_lds(ra, base + place * PLACE + (j * WAVES + w) * 1024, off_a[j] | none); };
+    auto load_b = [&](int place, int j) {
+        load_lds(PAIR && (j * WAVES + w) * 8 & WN / 2 ? rc : rb, base + place * PLACE + (j * WAVES + w) * 1024, off_b[j] | none);
     };
     f32x16 acc[NN][NM];                         // [columns][rows]
 #pragma unroll
@@ -223,69 +219,81 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
     const int lr = lane & 31, lh = lane >> 5, sw = lr >> 1 & 7;
     constexpr int READS = 2 * (NM + NN), BLOCKS = NM * NN, AHEAD = BLOCKS > 1 ? BLOCKS / 2 : 1;
     // Read n of a half step, in the order in which the products want them: B's first block, A's, B's others.
-    auto read = [&](int buf, int to, int half, int n) {
+    auto read = [&](int pa, int pb, int to, int half, int n) {
         const int i = n / 2, k = n % 2, c = ((half * 4 + lh * 2 + k) ^ sw) * 16;
         if (i >= 1 && i <= NM)
-            fa[to][i - 1].w[k] = *reinterpret_cast<const u32x4*>(&lds[buf][(wm * WM + (i - 1) * 32 + lr) * kStep + c]);
+            fa[to][i - 1].w[k] = *reinterpret_cast<const u32x4*>(&lds[pa][(wm * WM + (i - 1) * 32 + lr) * kStep + c]);
         else
-            fb[to][i ? i - NM : 0].w[k] = *reinterpret_cast<const u32x4*>(&lds[buf][(T + wn * WN + (i ? i - NM : 0) * 32 + lr) * kStep + c]);
+            fb[to][i ? i - NM : 0].w[k] = *reinterpret_cast<const u32x4*>(&lds[pb][(wn * WN + (i ? i - NM : 0) * 32 + lr) * kStep + c]);
     };
-    // A step's second half is read while its first is multiplied, and the next step's first half while the second is. Between
-    // the two the wavefronts meet: all reads of this step are back, so its place takes the loads of the step S later, which
-    // have S - 1 whole steps to land. Blocks of 64 clocks of products, with the reads behind the first half of them and the
-    // loads spread over all, in the order written here (the compiler would gather the products behind the barrier).
-    auto blocks = [&](int slot, int from, int half, bool loads, int to) {
-        Parts pa[NM], pb[NN];       // of float32
+    // Blocks of 64 clocks of products (float32: 192) of the pieces in `slot`, with the reads of the other slot's pieces behind the
+    // first half of them and loads spread over all, in the order written here (the compiler would gather the products behind the
+    // barrier). Loads: `a` A's, `b` B's.
+    auto blocks = [&](int slot, int pa, int pb, int half, bool a, bool b, int to_a, int to_b) {
+        Parts sa[NM], sb[NN];       // of float32
 #pragma unroll
         for (int n = 0; n < BLOCKS; ++n) {
-            constexpr int kReads = READS / AHEAD, kLoads = LOADS / BLOCKS;
+            constexpr int kReads = READS / AHEAD;
 #pragma unroll
             for (int k = 0; k < kReads; ++k)
-                if (n * kReads + k < READS) read(from, 1 - slot, half, n * kReads + k);
-            if (loads) {
+                if (n * kReads + k < READS) read(pa, pb, 1 - slot, half, n * kReads + k);
 #pragma unroll
-                for (int k = 0; k < kLoads; ++k) load(to, n * kLoads + k);
+            for (int k = n * LOADS / BLOCKS; k < (n + 1) * LOADS / BLOCKS; ++k) {
+                if (a) load_a(to_a, k);
+                if (b) load_b(to_b, k);
             }
             const int i = n / NM, j = n % NM;
             if constexpr (ET == kF32) {
-                if (j == 0) pb[i] = split(fb[slot][i]);
-                if (i == 0) pa[j] = split(fa[slot][j]);
-                mma(acc[i][j], pb[i], pa[j]);
+                if (j == 0) sb[i] = split(fb[slot][i]);
+                if (i == 0) sa[j] = split(fa[slot][j]);
+                mma(acc[i][j], sb[i], sa[j]);
             } else {
                 mma<ET>(acc[i][j], fb[slot][i], fa[slot][j]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    // two steps, A's and B's rows in turn
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < (HALVES ? U / 2 : 2); ++s) {
         next_step();
 #pragma unroll
-        for (int j = 0; j < LOADS; ++j) load(s, j);
-    }
-    meet<(S - 1) * LOADS>();
+        for (int j = 0; j < LOADS; ++j) load_a(2 * s, j);
 #pragma unroll
-    for (int k = 0; k < READS; ++k) read(0, 0, HALVES ? mine_half : 0, k);
+        for (int j = 0; j < LOADS; ++j) load_b(2 * s + 1, j);
+    }
+    meet<(HALVES ? U - 2 : 2) * LOADS>();
+#pragma unroll
+    for (int k = 0; k < READS; ++k) read(0, 1, 0, HALVES ? mine_half : 0, k);
     if constexpr (HALVES) {
-        // the next step's half is read behind this one's products
+        // Between two steps the wavefronts meet: the next one has landed and is read behind this one's products, and all reads of
+        // this one are back, so its places take the loads of the step U / 2 later.
         auto step = [&](int slot, int t) {
             next_step();
-            meet<(S - 2) * LOADS>();
+            meet<(U - 4) * LOADS>();
             __builtin_amdgcn_sched_barrier(0);
-            blocks(slot, (t + 1) % S, mine_half, true, t % S);
+            const int here = t % (U / 2) * 2, next = (t + 1) % (U / 2) * 2;
+            blocks(slot, next, next + 1, mine_half, true, true, here, here + 1);
         };
-        for (int t = 0; t < total; t += 2) {
+        for (int t = 0; t < steps; t += 2) {
             step(0, t);
-            if (t + 1 < total) step(1, t + 1);
+            if (t + 1 < steps) step(1, t + 1);
         }
     } else {
-        for (int t = 0; t < total; ++t) {
-            const int buf = t % S;
-            blocks(0, buf, 1, false, 0);
+        // A step's second half is read while its first is multiplied, and the next step's first half while the second is. Between
+        // the two the wavefronts meet: the next step has landed, and all reads of this one are back. Loads never pause: A's rows
+        // of the step after the next go behind the first half, where the fifth place is free, and B's behind the second, to this
+        // step's place for A (LDS is full: a burst of both behind the second half takes as long as a step, and the products wait).
+        static_assert(U == 5, "A's and B's rows of two steps and a half");
+        int at_a = 0;       // the place of this step's A; B's is the next one
+        auto after = [](int place, int n) { return place + n < U ? place + n : place + n - U; };
+        for (int t = 0; t < steps; ++t) {
             next_step();
-            meet<(S - 2) * LOADS>();
+            blocks(0, at_a, after(at_a, 1), 1, true, false, after(at_a, 4), 0);
+            meet<LOADS>();
             __builtin_amdgcn_sched_barrier(0);
-            blocks(1, (t + 1) % S, 0, true, buf);
+            blocks(1, after(at_a, 2), after(at_a, 3), 0, false, true, 0, at_a);
+            at_a = after(at_a, 2);
         }
     }
 
@@ -371,7 +379,7 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
     }
 }
 
-template <int ET, int T, int NM, int NN, int S, bool HALVES, bool PAIR>
+template <int ET, int T, int NM, int NN, int U, bool HALVES, bool PAIR>
 hipError_t run(const FfnProduct* p, int n, hipStream_t s) {
     Both b{};
     int64_t total = 0;
@@ -382,15 +390,15 @@ hipError_t run(const FfnProduct* p, int n, hipStream_t s) {
         total += static_cast<int64_t>(b.tm[i]) * b.tn[i];
         if (i == 0) b.first = static_cast<int>(total);
     }
-    ffn_product<ET, T, NM, NN, S, HALVES, PAIR><<<static_cast<unsigned>(total), 64 * kWaves<T, NM, NN, HALVES>, 0, s>>>(b);
+    ffn_product<ET, T, NM, NN, U, HALVES, PAIR><<<static_cast<unsigned>(total), 64 * kWaves<T, NM, NN, HALVES>, 0, s>>>(b);
     return hipGetLastError();
 }
 template <int ET, bool PAIR>
 hipError_t tiled(const FfnProduct* p, int n, int tile, hipStream_t s) {
     if constexpr (ET != kF32)
-        if (tile == 256) return run<ET, 256, 4, 2, 2, false, PAIR>(p, n, s);
-    if (tile == 128) return run<ET, 128, 2, 2, 2, false, PAIR>(p, n, s);
-    return run<ET, 64, 1, 1, 4, true, PAIR>(p, n, s);
+        if (tile == 256) return run<ET, 256, 4, 2, 5, false, PAIR>(p, n, s);
+    if (tile == 128) return run<ET, 128, 2, 2, 5, false, PAIR>(p, n, s);
+    return run<ET, 64, 1, 1, 8, true, PAIR>(p, n, s);
 }
 
 }  // namespace
