@@ -21,7 +21,7 @@ import threading
 from . import delta
 from ._binding import SDM_GX_ERR_HIP, SDM_GX_OK
 from ._build import BLOCK_LIB_PATH
-from .delta import (SDM_BF16, SDM_F16, SDM_F32, _ARG_ERRORS, _dtype, _flat, _inner, _layout, _ld, _OnDevice, _Plans, _ptr,
+from .delta import (SDM_BF16, SDM_F16, SDM_F32, _ARG_ERRORS, _dtype, _flat, _inner, _layout, _ld, _Plans, _ptr,
                     _requires_grad, _tensor, _under, _workspace)
 
 SDM_E4M3 = 3
@@ -123,6 +123,36 @@ _plans = _Plans()
 _stream = delta._stream
 
 
+def _call(fn, what, dev, *args):
+    """fn's call on the device's current stream, with the device made current where it is not; raises for a refusal."""
+    import torch
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(dev))
+    if status:
+        _raise(status, what)
+
+
+class _New:
+    """New contiguous tensors of one shape (torch makes them fastest from sizes and strides)."""
+
+    __slots__ = ("shape", "strides", "device")
+
+    def __init__(self, shape, device):
+        self.shape, strides, n = tuple(shape), [], 1
+        for s in reversed(self.shape):
+            strides.append(n)
+            n *= max(s, 1)
+        self.strides, self.device = tuple(strides[::-1]), device
+
+    def __call__(self, dtype, zero=False):
+        import torch
+        t = torch.empty_strided(self.shape, self.strides, dtype=dtype, device=self.device)
+        return t.zero_() if zero else t
+
+
 # ---- the gated linear recurrence ------------------------------------------------------------------------------------
 def _seq(t) -> sdm_seq_t:
     return sdm_seq_t(0, t.stride(0), t.stride(1))
@@ -196,7 +226,7 @@ def _glr_plan(backward, x, g, z, act, h0, cu, dy=None, dh=None, marks=None):
         a.cu_seqlens = 0
     if backward:
         _tensor(marks, "marks", (rows, D), torch.float32, dev)
-    return a, n, (rows, D), (nseq, D), dev, copied
+    return a, n, _New(x.shape, dev), _New((rows, D), dev), _New((nseq, D), dev), dev, copied
 
 
 def _glr_operands(copied, a, x, g, z, h0, cu):
@@ -222,16 +252,14 @@ def glr_forward(x, g, z=None, *, act="none", initial_state=None, cu_seqlens=None
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _glr_plan(False, x, g, z, act, initial_state, cu_seqlens))
-    kept, n, marks, states, dev, copied = plan
+    kept, n, whole, marks, states, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
             return glr_forward(x, g, z, act=act, initial_state=initial_state, cu_seqlens=cu_seqlens)
     if torch.is_grad_enabled() and _requires_grad(x, g, z, initial_state):
         from ._block_autograd import GatedLinearRecurrence
         return GatedLinearRecurrence.apply(x, g, z, initial_state, act, cu_seqlens)
-    y = (torch.empty if cu_seqlens is None else torch.zeros)(x.shape, dtype=x.dtype, device=dev)
-    h = torch.empty(states, dtype=torch.float32, device=dev)
-    marks = torch.empty(marks, dtype=torch.float32, device=dev)
+    y, h, marks = whole(x.dtype, cu_seqlens is not None), states(torch.float32), marks(torch.float32)
     if not y.numel():
         h.zero_() if initial_state is None else h.copy_(initial_state)
         return y, h, marks
@@ -239,11 +267,8 @@ def glr_forward(x, g, z=None, *, act="none", initial_state=None, cu_seqlens=None
     keep = _glr_operands(copied, a, x, g, z, initial_state, cu_seqlens)
     a.y.data, a.h_final, a.marks = y.data_ptr(), h.data_ptr(), marks.data_ptr()
     ws = _workspace(n, dev) if n else None
-    with _OnDevice(dev):
-        status = load().sdm_glr_forward(ctypes.byref(a), _ptr(ws), n, _stream(dev))
+    _call(load().sdm_glr_forward, "glr_forward", dev, ctypes.byref(a), _ptr(ws), n)
     del keep
-    if status:
-        _raise(status, "glr_forward")
     return y, h, marks
 
 
@@ -257,15 +282,14 @@ def glr_backward(x, g, z, dy, marks, *, act="none", initial_state=None, dfinal_s
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _glr_plan(True, x, g, z, act, initial_state, cu_seqlens, dy, dfinal_state, marks))
-    kept, n, _, states, dev, copied = plan
+    kept, n, whole, _, states, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
             return glr_backward(x, g, z, dy, marks, act=act, initial_state=initial_state, dfinal_state=dfinal_state,
                                 cu_seqlens=cu_seqlens)
-    make = torch.empty if cu_seqlens is None else torch.zeros
-    dx, dg = make(x.shape, dtype=x.dtype, device=dev), make(x.shape, dtype=g.dtype, device=dev)
-    dz = None if z is None else make(x.shape, dtype=x.dtype, device=dev)
-    dh0 = torch.empty(states, dtype=torch.float32, device=dev)
+    zero = cu_seqlens is not None
+    dx, dg, dz = whole(x.dtype, zero), whole(g.dtype, zero), None if z is None else whole(x.dtype, zero)
+    dh0 = states(torch.float32)
     if not dx.numel():
         dh0.zero_() if dfinal_state is None else dh0.copy_(dfinal_state)
         return dx, dg, dz, dh0
@@ -277,11 +301,8 @@ def glr_backward(x, g, z, dy, marks, *, act="none", initial_state=None, dfinal_s
     a.dy.data, a.marks, a.dh_final = dy.data_ptr(), marks.data_ptr(), _ptr(dfinal_state)
     a.dx.data, a.dg.data, a.dz.data, a.dh0 = dx.data_ptr(), dg.data_ptr(), _ptr(dz), dh0.data_ptr()
     ws = _workspace(n, dev) if n else None
-    with _OnDevice(dev):
-        status = load().sdm_glr_backward(ctypes.byref(a), _ptr(ws), n, _stream(dev))
+    _call(load().sdm_glr_backward, "glr_backward", dev, ctypes.byref(a), _ptr(ws), n)
     del keep
-    if status:
-        _raise(status, "glr_backward")
     return dx, dg, dz, dh0
 
 
@@ -296,12 +317,12 @@ def glr_step(x, g, z, state, *, act="none", slots=None, stream=None):
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _glr_step_plan(x, g, z, state, act, slots))
-    kept, dev, copied = plan
+    kept, whole, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
             return glr_step(x, g, z, state, act=act, slots=slots)
     recorded = torch.is_grad_enabled() and _requires_grad(x, g, z, state)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    y = whole(x.dtype)
     if not y.numel():
         return y
     if copied:
@@ -310,10 +331,7 @@ def glr_step(x, g, z, state, *, act="none", slots=None, stream=None):
     a = sdm_glr_step_args_t.from_buffer_copy(kept)
     a.x.data, a.g.data, a.z.data, a.y.data = x.data_ptr(), g.data_ptr(), _ptr(z), y.data_ptr()
     a.state, a.slots = state.data_ptr(), _ptr(slots)
-    with _OnDevice(dev):
-        status = load().sdm_glr_step(ctypes.byref(a), _stream(dev))
-    if status:
-        _raise(status, "glr_step")
+    _call(load().sdm_glr_step, "glr_step", dev, ctypes.byref(a))
     delta._increment_version((state,))
     if recorded:
         from ._block_autograd import NoGradient
@@ -340,7 +358,7 @@ def _glr_step_plan(x, g, z, state, act, slots):
                             y=_whole(x))
     if z is not None:
         a.z = _seq(z)
-    return a, dev, copied
+    return a, _New(x.shape, dev), dev, copied
 
 
 # ---- rows in 8 bits -------------------------------------------------------------------------------------------------
@@ -364,7 +382,7 @@ def _qnt_plan(what, x, r, w, eps):
     fx, fr = _flat(x), _flat(r)
     copied = fx is not x or fr is not r or (w is not None and not w.is_contiguous())
     a = sdm_qnt_args_t(dtype=dt, wtype=wt, eps=eps, rows=rows, D=D, ld_x=_ld(fx), ld_r=_ld(fr), ld_xn=D, ld_q=D)
-    return a, dev, copied
+    return a, _New(x.shape, dev), _New(x.shape[:-1], dev), dev, copied
 
 
 def _qnt(what, x, r, w, eps, stream):
@@ -374,25 +392,20 @@ def _qnt(what, x, r, w, eps, stream):
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _qnt_plan(what, x, r, w, eps))
-    kept, dev, copied = plan
+    kept, whole, by_row, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
             return _qnt(what, x, r, w, eps, None)
     recorded = torch.is_grad_enabled() and _requires_grad(x, r, w)
-    shape, inputs = x.shape, (x, r, w)
-    q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
-    scale = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    x_new = x if r is None else torch.empty(shape, dtype=x.dtype, device=dev)
+    inputs = (x, r, w)
+    q, scale, x_new = whole(torch.float8_e4m3fn), by_row(torch.float32), x if r is None else whole(x.dtype)
     if kept.rows:
         if copied:
             x, r, w = _flat(x), _flat(r), None if w is None else w.contiguous()
         a = sdm_qnt_args_t.from_buffer_copy(kept)
         a.x, a.r, a.w, a.q, a.scale = x.data_ptr(), _ptr(r), _ptr(w), q.data_ptr(), scale.data_ptr()
         a.x_new = 0 if r is None else x_new.data_ptr()
-        with _OnDevice(dev):
-            status = load().sdm_qnt_rows(ctypes.byref(a), _stream(dev))
-        if status:
-            _raise(status, what)
+        _call(load().sdm_qnt_rows, what, dev, ctypes.byref(a))
     if recorded:
         from ._block_autograd import NoGradient
         scale = NoGradient.apply([scale], what, *inputs)
@@ -423,7 +436,7 @@ def quant_rows(x, *, stream=None):
 
 # ---- the gated feed-forward product ---------------------------------------------------------------------------------
 def _ffn_plan(x, wg, wu, act, scales, dtype, dh=None, kept=None):
-    """(argument struct without addresses, h's shape, its type, device, whether an operand is copied first)"""
+    """(argument struct without addresses, what makes h, its type, device, whether an operand is copied first)"""
     import torch
     for t, name in ((x, "x"), (wg, "w_gate"), (wu, "w_up")):
         if not isinstance(t, torch.Tensor):
@@ -470,7 +483,7 @@ def _ffn_plan(x, wg, wu, act, scales, dtype, dh=None, kept=None):
         fd, f0, f1 = _flat(dh), _flat(kept[0]), _flat(kept[1])
         copied = copied or fd is not dh or f0 is not kept[0] or f1 is not kept[1]
         a.ld_dh, a.ld_gate, a.ld_up = _ld(fd), _ld(f0), _ld(f1)
-    return a, (*lead, F), dtype, dev, copied
+    return a, _New((*lead, F), dev), dtype, dev, copied
 
 
 def ffn_forward(x, w_gate, w_up, *, act="silu", keep=False, x_scale=None, gate_scale=None, up_scale=None, dtype=None,
@@ -489,7 +502,7 @@ def ffn_forward(x, w_gate, w_up, *, act="silu", keep=False, x_scale=None, gate_s
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _ffn_plan(x, w_gate, w_up, act, scales, dtype))
-    struct, shape, otype, dev, copied = plan
+    struct, whole, otype, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
             return ffn_forward(x, w_gate, w_up, act=act, keep=keep, x_scale=x_scale, gate_scale=gate_scale, up_scale=up_scale,
@@ -499,8 +512,7 @@ def ffn_forward(x, w_gate, w_up, *, act="silu", keep=False, x_scale=None, gate_s
         from ._block_autograd import GatedFeedForward
         h, *kept = GatedFeedForward.apply(x, w_gate, w_up, act)
         return (h, tuple(kept)) if keep else h
-    h = torch.empty(shape, dtype=otype, device=dev)
-    kept = tuple(torch.empty(shape, dtype=torch.float32, device=dev) for _ in range(2)) if keep else (None, None)
+    h, kept = whole(otype), (whole(torch.float32), whole(torch.float32)) if keep else (None, None)
     inputs = (x, w_gate, w_up, *scales)
     if struct.M:
         if copied:
@@ -513,10 +525,7 @@ def ffn_forward(x, w_gate, w_up, *, act="silu", keep=False, x_scale=None, gate_s
         if n < 0:
             _raise(n, "ffn_forward")
         ws = _workspace(n, dev) if n else None
-        with _OnDevice(dev):
-            status = load().sdm_ffn_forward(ctypes.byref(a), _ptr(ws), n, _stream(dev))
-        if status:
-            _raise(status, "ffn_forward")
+        _call(load().sdm_ffn_forward, "ffn_forward", dev, ctypes.byref(a), _ptr(ws), n)
     if recorded:
         from ._block_autograd import NoGradient
         h = NoGradient.apply([h], "ffn_forward of 8-bit operands", *inputs)
@@ -554,8 +563,5 @@ def ffn_backward(dh, x, w_gate, w_up, kept, *, act="silu", stream=None):
     if n < 0:
         _raise(n, "ffn_backward")
     ws = _workspace(n, dev)
-    with _OnDevice(dev):
-        status = load().sdm_ffn_backward(ctypes.byref(a), ws.data_ptr(), n, _stream(dev))
-    if status:
-        _raise(status, "ffn_backward")
+    _call(load().sdm_ffn_backward, "ffn_backward", dev, ctypes.byref(a), ws.data_ptr(), n)
     return dx, dwg, dwu

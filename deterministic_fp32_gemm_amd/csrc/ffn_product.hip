@@ -217,7 +217,7 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
         for (int j = 0; j < NM; ++j) acc[i][j] = (f32x16){0};
     Piece fa[2][NM], fb[2][NN];
     const int lr = lane & 31, lh = lane >> 5, sw = lr >> 1 & 7;
-    constexpr int READS = 2 * (NM + NN), BLOCKS = NM * NN, AHEAD = BLOCKS > 1 ? BLOCKS / 2 : 1;
+    constexpr int READS = 2 * (NM + NN), BLOCKS = NM * NN, AHEAD = BLOCKS > 4 ? BLOCKS * 3 / 4 : BLOCKS > 1 ? BLOCKS / 2 : 1;
     // Read n of a half step, in the order in which the products want them: B's first block, A's, B's others.
     auto read = [&](int pa, int pb, int to, int half, int n) {
         const int i = n / 2, k = n % 2, c = ((half * 4 + lh * 2 + k) ^ sw) * 16;
@@ -227,7 +227,7 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
             fb[to][i ? i - NM : 0].w[k] = *reinterpret_cast<const u32x4*>(&lds[pb][(wn * WN + (i ? i - NM : 0) * 32 + lr) * kStep + c]);
     };
     // Blocks of 64 clocks of products (float32: 192) of the pieces in `slot`, with the reads of the other slot's pieces behind the
-    // first half of them and loads spread over all, in the order written here (the compiler would gather the products behind the
+    // first of them and loads spread over all, in the order written here (the compiler would gather the products behind the
     // barrier). Loads: `a` A's, `b` B's.
     auto blocks = [&](int slot, int pa, int pb, int half, bool a, bool b, int to_a, int to_b) {
         Parts sa[NM], sb[NN];       // of float32

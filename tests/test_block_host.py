@@ -1,7 +1,6 @@
 """Host tests of libsdm_block (no GPU): exports, struct layouts, every refusal of the C ABI's checks and of the Python entry
 points, workspaces, the machine code, and the entry points in torch's graph with a library that computes nothing."""
 
-import contextlib
 import ctypes
 import os
 import re
@@ -261,8 +260,7 @@ def no_library(monkeypatch):
         return t
 
     monkeypatch.setattr(L, "_tensor", tensor)
-    monkeypatch.setattr(L, "_OnDevice", lambda device: contextlib.nullcontext())
-    monkeypatch.setattr(L, "_stream", lambda device: 0)
+    monkeypatch.setattr(L, "_call", lambda fn, what, dev, *args: None)
     monkeypatch.setattr(L, "_plans", L._Plans())
     monkeypatch.setattr(L.delta, "_increment_version", lambda tensors: None)
 
