@@ -52,8 +52,8 @@ int check_seq(const Operand& o, int64_t B, int64_t T, int64_t D, Extent* e) {
     return SDM_GX_OK;
 }
 
-int64_t mark_rows(const sdm_glr_args_t* a) {
-    return a->cu_seqlens ? a->T / SDM_GLR_TILE + a->nseq : a->nseq * cdiv(a->T, SDM_GLR_TILE);
+int64_t mark_rows(const sdm_glr_args_t* a, bool packed) {
+    return packed ? a->T / SDM_GLR_TILE + a->nseq : a->nseq * cdiv(a->T, SDM_GLR_TILE);
 }
 
 int check(const sdm_glr_args_t* a, bool backward) {
@@ -90,7 +90,7 @@ int check(const sdm_glr_args_t* a, bool backward) {
     auto plain = [](const void* p, int64_t bytes) { return extent(p, p ? bytes : 0); };
     in[ni++] = plain(a->cu_seqlens, (a->nseq + 1) * 4);
     in[ni++] = plain(a->h0, state);
-    const Extent marks = plain(a->marks, mark_rows(a) * a->D * 4);
+    const Extent marks = plain(a->marks, mark_rows(a, a->cu_seqlens != nullptr) * a->D * 4);
     if (backward) {
         in[ni++] = marks;
         in[ni++] = plain(a->dh_final, state);
@@ -108,29 +108,32 @@ int check(const sdm_glr_args_t* a, bool backward) {
     return SDM_GX_OK;
 }
 
-// Runs are cut until there are two workgroups a CU, into parts of 512 tokens at the least: a part's map costs another
-// reading of its inputs.
-GlrPlan plan(const sdm_glr_args_t* a) {
+// Backward: runs are cut until there is a workgroup a CU, into parts of 512 tokens at the least: a part's map costs another
+// reading of its inputs. Forward: one workgroup a run and 64 channels where that is a workgroup a CU and all runs are alike, or
+// no run has more than 4 tiles; else the queue.
+GlrPlan plan(const sdm_glr_args_t* a, bool packed, bool backward) {
     GlrPlan p{};
     p.cblocks = static_cast<int>(cdiv(a->D, 64));
     const int64_t have = a->nseq * p.cblocks, each = cdiv(a->T * a->B, a->nseq);
-    p.segs = static_cast<int>(std::max<int64_t>(1, std::min(256 / have, each / 512)));
+    p.segs = backward ? static_cast<int>(std::max<int64_t>(1, std::min(256 / have, each / 512))) : 1;
+    if (!backward && a->T > 4 * SDM_GLR_TILE && (packed || have < 256)) p.rows = mark_rows(a, packed);
     return p;
 }
-int64_t workspace(const sdm_glr_args_t* a) {
-    const GlrPlan p = plan(a);
-    return p.segs > 1 ? a->nseq * p.segs * 2 * a->D * 4 : 0;
+int64_t workspace(const sdm_glr_args_t* a, bool packed, bool backward) {
+    const GlrPlan p = plan(a, packed, backward);
+    return backward ? (p.segs > 1 ? a->nseq * p.segs * 2 * a->D * 4 : 0) : glr_chain_words(*a, p) * 8;
 }
 
 int run(const sdm_glr_args_t* a, bool backward, void* ws, int64_t ws_bytes, void* stream) {
     int st = check(a, backward), dev = 0;
     if (st) return st;
-    const int64_t need = workspace(a);
+    const bool packed = a->cu_seqlens != nullptr;
+    const int64_t need = workspace(a, packed, backward);
     if (need && !ws) return SDM_GX_ERR_NULL;
     if (!aligned(ws, 16)) return SDM_GX_ERR_ALIGN;
     if (ws_bytes < need) return SDM_GX_ERR_LIMIT;
-    const GlrPlan p = plan(a);
-    if (a->nseq * p.segs * p.cblocks * kGlrThreads >= kMaxThreads) return SDM_GX_ERR_LIMIT;
+    const GlrPlan p = plan(a, packed, backward);
+    if (a->nseq * p.segs * p.cblocks * kGlrThreads >= kMaxThreads || glr_chain_words(*a, p) / 2 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     if ((st = current_gfx950(&dev))) return st;
     const void* ps[] = {a->x.data, a->g.data, a->act ? a->z.data : nullptr, a->cu_seqlens, a->h0, a->marks, need ? ws : nullptr,
                         backward ? a->dy.data : a->y.data, backward ? a->dh_final : a->h_final, backward ? a->dx.data : nullptr,
@@ -138,7 +141,7 @@ int run(const sdm_glr_args_t* a, bool backward, void* ws, int64_t ws_bytes, void
     for (const void* q : ps)
         if (q && a->T && (st = pointer_on(q, dev))) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = backward ? launch_glr_backward(*a, p, static_cast<float*>(ws), s) : launch_glr_forward(*a, p, static_cast<float*>(ws), s);
+    const hipError_t e = backward ? launch_glr_backward(*a, p, ws, s) : launch_glr_forward(*a, p, ws, s);
     return e == hipSuccess ? SDM_GX_OK : record_hip_error(e);
 }
 
@@ -171,14 +174,14 @@ int64_t sdm_glr_marks(const sdm_glr_args_t* args) {
     if (!args) return SDM_GX_ERR_ARG;
     const int st = check_sizes(args->dtype, args->gtype, args->act, args->B, args->T, args->D);
     if (st || args->nseq < 1 || args->nseq >= (int64_t(1) << 20)) return st ? st : SDM_GX_ERR_SHAPE;
-    return mark_rows(args);
+    return mark_rows(args, args->cu_seqlens != nullptr);
 }
 
-int64_t sdm_glr_workspace(const sdm_glr_args_t* args, int32_t) {
+int64_t sdm_glr_workspace(const sdm_glr_args_t* args, int32_t backward) {
     if (!args) return SDM_GX_ERR_ARG;
     const int st = check_sizes(args->dtype, args->gtype, args->act, args->B, args->T, args->D);
     if (st || args->nseq < 1 || args->nseq >= (int64_t(1) << 20)) return st ? st : SDM_GX_ERR_SHAPE;
-    return workspace(args);
+    return workspace(args, args->cu_seqlens != nullptr, backward != 0);
 }
 
 int sdm_glr_forward(const sdm_glr_args_t* args, void* ws, int64_t ws_bytes, void* stream) { return run(args, false, ws, ws_bytes, stream); }

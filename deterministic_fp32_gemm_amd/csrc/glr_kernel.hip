@@ -9,9 +9,10 @@
 // The next tile's loads are in flight meanwhile. The gradient walks the tiles from the last to the first: the states come
 // from the tile's mark and the same maps, and D's recurrence, e -> a_t (u_t + e) from right to left, has the same A.
 //
-// Runs are cut into parts where 64 channels a workgroup give too few workgroups: a first kernel finds each part's map,
-// which reads x and g (or dy, z and g) once more. It walks its part away from the end at which the second kernel starts, so
-// that what it read last is what is wanted first and may still be in the last-level cache.
+// Where 64 channels of a run give too few workgroups, or runs of unlike lengths uneven ones, the forward takes tiles from one
+// queue instead (glr_chain below): still one pass. The gradient cuts runs into parts there: a first kernel finds each part's
+// map, which reads dy, z and g once more. It walks its part away from the end at which the second kernel starts, so that what
+// it read last is what is wanted first and may still be in the last-level cache.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -86,8 +87,8 @@ __device__ __forceinline__ void fetch(std::false_type, T (&o)[KT], const Rows<T>
     for (int i = 0; i < KT; ++i) o[i] = get(s.p + min(t + i, len - 1) * s.step, c * static_cast<uint32_t>(sizeof(T)));
 }
 
-// The map of each part of a run: BACK that of D's recurrence, from right to left, else that of the states.
-template <int DT, int GT, int ACT, bool BACK>
+// The map of D's recurrence, from right to left, over each part of a run.
+template <int DT, int GT, int ACT>
 __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a, const int cblocks, const int segs, float* __restrict__ part) {
     using T = elem_t<DT>;
     using G = elem_t<GT>;
@@ -103,15 +104,15 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
     const int t0 = static_cast<int>(s0), t1 = min(r.len, t0 + seglen), each = seglen / NW;     // a multiple of KT
     const int lo = t0 + w * each, hi = min(t1, lo + each);
     float A = 1.f, H = 0.f;
-    T x[KT], z[KT];
+    T dy[KT], z[KT];
     G g[KT];
-    const Rows<T> xs = rows_of<T>(BACK ? a.dy : a.x, r), zs = rows_of<T>(a.z, r);
+    const Rows<T> dys = rows_of<T>(a.dy, r), zs = rows_of<T>(a.z, r);
     const Rows<G> gs = rows_of<G>(a.g, r);
     const int n = hi > lo ? (hi - lo + KT - 1) / KT : 0;
     auto load = [&](auto whole, int t) __attribute__((always_inline)) {
-        fetch(whole, x, xs, t, r.len, cc);
+        fetch(whole, dy, dys, t, r.len, cc);
         fetch(whole, g, gs, t, r.len, cc);
-        if constexpr (BACK && Z) fetch(whole, z, zs, t, r.len, cc);
+        if constexpr (Z) fetch(whole, z, zs, t, r.len, cc);
     };
     auto work = [&](auto whole, int t, int next) __attribute__((always_inline)) {
         float e[KT], u[KT];
@@ -119,8 +120,8 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
         for (int k = 0; k < KT; ++k) {
             const bool in = whole.value || t + k < hi;
             e[k] = in ? exp_of(static_cast<float>(g[k])) : 1.f;
-            u[k] = in ? static_cast<float>(x[k]) : 0.f;
-            if constexpr (BACK && Z) {
+            u[k] = in ? static_cast<float>(dy[k]) : 0.f;
+            if constexpr (Z) {
                 float f, d;
                 gate<DT != 0>(static_cast<float>(z[k]), ACT, f, d);
                 u[k] = in ? u[k] * f : 0.f;
@@ -129,28 +130,21 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
         if (next >= 0) load(std::true_type{}, next);
         float P = 1.f, h = 0.f;
 #pragma unroll
-        for (int k = 0; k < KT; ++k) {
-            const int j = BACK ? KT - 1 - k : k;
-            h = BACK ? e[j] * (u[j] + h) : __builtin_fmaf(e[j], h, u[j]);
-            P *= e[j];
+        for (int k = KT - 1; k >= 0; --k) {
+            h = e[k] * (u[k] + h);
+            P *= e[k];
         }
-        // the new stretch is on the far side of those before it
+        // the new stretch is to the right of those before it
         H = enter(A, H, h);
         A *= P;
     };
-    // the wavefront's last block may not be whole: it comes first, or last
-    const int whole = hi > lo ? (hi - lo) / KT : 0, rest = n > whole ? lo + whole * KT : -1;
-    auto at = [&](int i) { return i < whole ? lo + (BACK ? i : whole - 1 - i) * KT : -1; };
-    if (!BACK && rest >= 0) {
-        load(std::false_type{}, rest);
-        work(std::false_type{}, rest, at(0));
-    } else if (whole > 0) {
-        load(std::true_type{}, at(0));
-    }
-    for (int i = 0; i < whole; ++i) work(std::true_type{}, at(i), at(i + 1));
-    if (BACK && rest >= 0) {
-        load(std::false_type{}, rest);
-        work(std::false_type{}, rest, -1);
+    // the wavefront's last block may not be whole
+    const int whole = hi > lo ? (hi - lo) / KT : 0;
+    if (whole > 0) load(std::true_type{}, lo);
+    for (int i = 0; i < whole; ++i) work(std::true_type{}, lo + i * KT, i + 1 < whole ? lo + (i + 1) * KT : -1);
+    if (n > whole) {
+        load(std::false_type{}, lo + whole * KT);
+        work(std::false_type{}, lo + whole * KT, -1);
     }
     ex[w][0][lane] = A;
     ex[w][1][lane] = H;
@@ -160,9 +154,8 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
         H = 0.f;
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-            const int j = BACK ? i : NW - 1 - i;
-            H = enter(A, H, ex[j][1][lane]);
-            A *= ex[j][0][lane];
+            H = enter(A, H, ex[i][1][lane]);
+            A *= ex[i][0][lane];
         }
         float* p = part + (static_cast<int64_t>(run) * segs + seg) * 2 * a.D + c;
         p[0] = A;
@@ -171,23 +164,16 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
 }
 
 template <int DT, int GT, int ACT>
-__global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t a, const int cblocks, const int segs, const float* __restrict__ part) {
+__global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t a, const int cblocks) {
     using T = elem_t<DT>;
     using G = elem_t<GT>;
     constexpr bool Z = ACT != SDM_ACT_NONE;
     __shared__ float ex[2][NW][2][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int cb = blockIdx.x % cblocks, rs = blockIdx.x / cblocks, seg = rs % segs, run = rs / segs;
+    const int cb = blockIdx.x % cblocks, run = blockIdx.x / cblocks;
     const Run r = run_of(a, run);
     const int D = static_cast<int>(a.D), c = cb * 64 + lane, cc = min(c, D - 1);
-    const int seglen = ((r.len + segs - 1) / segs + TILE - 1) / TILE * TILE;
-    const int64_t s0 = static_cast<int64_t>(seg) * seglen;
     float h0 = a.h0 ? a.h0[run * a.D + cc] : 0.f;
-    if (s0 >= r.len) {
-        if (r.len == 0 && seg == 0 && w == 0 && c < D && a.h_final) a.h_final[run * a.D + c] = h0;
-        return;
-    }
-    const int t0 = static_cast<int>(s0), t1 = min(r.len, t0 + seglen);
     T x[KT], z[KT];
     G g[KT];
     const Rows<T> xs = rows_of<T>(a.x, r), zs = rows_of<T>(a.z, r), ys = rows_of<T>(a.y, r);
@@ -197,12 +183,8 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
         fetch(whole, g, gs, t, r.len, cc);
         if constexpr (Z) fetch(whole, z, zs, t, r.len, cc);
     };
-    const int end = t0 + (t1 - t0) / TILE * TILE;       // of the whole tiles
-    if (end > t0) load(std::true_type{}, t0 + w * KT);
-    for (int s = 0; s < seg; ++s) {
-        const float* p = part + (static_cast<int64_t>(run) * segs + s) * 2 * a.D + cc;
-        h0 = enter(p[0], p[a.D], h0);
-    }
+    const int end = r.len / TILE * TILE;       // of the whole tiles
+    if (end > 0) load(std::true_type{}, w * KT);
     int buf = 0;
     auto work = [&](auto whole, int tile) __attribute__((always_inline)) {
         const int t = tile + w * KT;
@@ -211,7 +193,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
         float A = 1.f, H = 0.f;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            const bool in = whole.value || t + k < t1;
+            const bool in = whole.value || t + k < r.len;
             e[k] = in ? exp_of(static_cast<float>(g[k])) : 1.f;
             u[k] = in ? static_cast<float>(x[k]) : 0.f;
             H = __builtin_fmaf(e[k], H, u[k]);
@@ -241,15 +223,256 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
                 gate<DT != 0>(static_cast<float>(zz[k]), ACT, f, d);
                 y *= f;
             }
-            if (whole.value || t + k < t1) put(yp, c * sizeof(T), y);
+            if (whole.value || t + k < r.len) put(yp, c * sizeof(T), y);
         }
     };
-    for (int tile = t0; tile < end; tile += TILE, buf ^= 1) work(std::true_type{}, tile);
-    if (end < t1) {
+    for (int tile = 0; tile < end; tile += TILE, buf ^= 1) work(std::true_type{}, tile);
+    if (end < r.len) {
         load(std::false_type{}, end + w * KT);
         work(std::false_type{}, end);
     }
-    if (t1 == r.len && w == 0 && c < D && a.h_final) a.h_final[run * a.D + c] = h0;
+    if (w == 0 && c < D && a.h_final) a.h_final[run * a.D + c] = h0;
+}
+
+// Tiles from a queue. Workgroups take tickets in order: which tile is which ticket's follows from the sizes and bounds alone, so
+// who takes it does not change a bit of the result. Beside the eight wavefronts that hold the tile, a ninth takes the tickets and
+// joins the tile to those before it in its run. When the eight have found the tile's map it publishes it, waits for the state
+// after the last tile of the group of 8 before and for the maps of the tiles of its own group before it, composes them in
+// order, publishes the state after its tile and hands the eight the one that enters; their loads of the next tile are in flight
+// meanwhile. A run's states thus pass from group to group, and maps within one.
+//
+// What is published goes as words of 8 bytes, a float32 and a mark that it is there, by relaxed atomics of device scope: a
+// word is there or not, and needs no order with others. All words are cleared by a kernel before. No wait goes unended: a
+// ticket waits for lower ones only, which running workgroups hold, each of which publishes whatever its tile is; after some
+// seconds of waiting, which nothing but a fault explains, a tile goes on with NaN.
+constexpr int kGroup = 8;
+constexpr int kPolls = 1 << 22;
+
+struct Ticket {
+    int64_t row, start, mark;       // b, the run's first token, the tile's row of marks
+    int run, tile, len, cb;         // the run and its length, the tile's number in it, the block of channels
+    int state;                      // 0: no more; 1: a row of marks that has no tile; 2: a tile
+};
+
+__device__ __forceinline__ uint64_t word(float v) { return uint64_t(1) << 32 | __float_as_uint(v); }
+__device__ __forceinline__ void publish(uint64_t* p, float v) { __hip_atomic_store(p, word(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ uint64_t look(const uint64_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// The ticket's tile, found by one wavefront.
+__device__ __forceinline__ Ticket ticket_of(const sdm_glr_args_t& a, int64_t id, int64_t rows, int cblocks) {
+    Ticket t{};
+    if (id >= rows * cblocks) return t;
+    const int64_t r = id / cblocks;
+    t.cb = static_cast<int>(id % cblocks);
+    t.state = 2;
+    if (a.cu_seqlens == nullptr) {
+        // all rows' first tiles, then all second ones
+        t.run = static_cast<int>(r % a.nseq);
+        t.tile = static_cast<int>(r / a.nseq);
+        const Run run = run_of(a, t.run);
+        t.row = run.row;
+        t.len = run.len;
+        t.mark = run.mark + t.tile;
+        return t;
+    }
+    // the last run whose first row of marks is not past r: 64 of them at a time
+    const int T = static_cast<int>(a.T), lane = threadIdx.x & 63;
+    int lo = 0, n = static_cast<int>(a.nseq);
+    while (n > 1) {
+        const int step = (n + 63) / 64, i = lo + min(lane * step, n - 1);
+        const bool in = lane * step < n && min(max(a.cu_seqlens[i], 0), T) / TILE + i <= r;
+        const int k = max(static_cast<int>(__popcll(__ballot(in))) - 1, 0), at = min(k * step, n - 1);
+        n = min(step, n - at);
+        lo += at;
+    }
+    const Run run = run_of(a, lo);
+    const int64_t tile = r - run.mark;
+    t.run = lo;
+    t.start = run.start;
+    t.len = run.len;
+    t.mark = r;
+    t.tile = static_cast<int>(max(tile, int64_t(0)));
+    if (tile < 0 || tile * TILE >= run.len) t.state = 1;
+    return t;
+}
+
+template <int DT, int GT, int ACT>
+__global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args_t a, const int cblocks, const int64_t rows, uint64_t* __restrict__ words) {
+    using T = elem_t<DT>;
+    using G = elem_t<GT>;
+    constexpr bool Z = ACT != SDM_ACT_NONE;
+    __shared__ float ex[NW][2][64], entering[64];
+    __shared__ int tickets[2][sizeof(Ticket) / 4];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = static_cast<int>(a.D);
+    // the first words: the queue's counter; then, of each tile, 64 A's, 64 H's and 64 states
+    unsigned long long* counter = reinterpret_cast<unsigned long long*>(words);
+    auto words_of = [&](int64_t mark, int cb) { return words + 64 + (mark * cblocks + cb) * 192 + lane; };
+    auto take = [&](int slot) {
+        unsigned long long id = 0;
+        if (lane == 0) id = __hip_atomic_fetch_add(counter, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        id = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(id)) | static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(id >> 32))) << 32;
+        const Ticket t = ticket_of(a, static_cast<int64_t>(id), rows, cblocks);
+        if (lane == 0) __builtin_memcpy(tickets[slot], &t, sizeof(t));
+    };
+    // a ticket from LDS, the same for the whole wavefront
+    auto ticket = [&](int slot) {
+        int of[sizeof(Ticket) / 4];
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(Ticket) / 4); ++i) of[i] = __builtin_amdgcn_readfirstlane(tickets[slot][i]);
+        Ticket t;
+        __builtin_memcpy(&t, of, sizeof(t));
+        return t;
+    };
+    // runs without tokens have no tile
+    for (int64_t i = blockIdx.x; i < a.nseq && a.cu_seqlens && a.h_final; i += gridDim.x)
+        if (run_of(a, static_cast<int>(i)).len == 0)
+            for (int c = threadIdx.x; c < D; c += kGlrChainThreads) a.h_final[i * D + c] = a.h0 ? a.h0[i * D + c] : 0.f;
+
+    if (w == NW) {
+        take(0);
+        lds_barrier();                                          // the first ticket
+        for (int slot = 0;; slot ^= 1) {
+            const Ticket t = ticket(slot);
+            if (t.state == 0) break;
+            const int c = t.cb * 64 + lane, cc = min(c, D - 1);
+            const int64_t at = static_cast<int64_t>(t.run) * D + cc;
+            const int group = t.tile - t.tile % kGroup;
+            float h = group == 0 && a.h0 && t.state == 2 ? a.h0[at] : 0.f;
+            take(slot ^ 1);
+            lds_barrier();                                      // the tile's maps, the next ticket
+            float A = 1.f, H = 0.f;
+            if (t.state == 2) {
+#pragma unroll
+                for (int i = 0; i < NW; ++i) {
+                    H = enter(ex[i][0][lane], ex[i][1][lane], H);
+                    A *= ex[i][0][lane];
+                }
+            }
+            uint64_t* own = words_of(t.mark, t.cb);
+            publish(own, A);
+            publish(own + 64, H);
+            if (t.state == 2) {
+                const int before = t.tile - group;              // tiles of the group before this one
+                uint64_t m[kGroup - 1][2], s = word(h);
+                bool missing = true;
+                for (int polls = 0; missing && polls < kPolls; ++polls) {
+                    if (polls) __builtin_amdgcn_s_sleep(1);
+                    if (group) s = look(words_of(t.mark - before - 1, t.cb) + 128);
+#pragma unroll
+                    for (int i = 0; i < kGroup - 1; ++i)
+                        if (i < before) {
+                            const uint64_t* p = words_of(t.mark - before + i, t.cb);
+                            m[i][0] = look(p);
+                            m[i][1] = look(p + 64);
+                        }
+                    bool there = s >> 32;
+#pragma unroll
+                    for (int i = 0; i < kGroup - 1; ++i)
+                        if (i < before) there = there && m[i][0] >> 32 && m[i][1] >> 32;
+                    missing = !__all(there);
+                }
+                h = __uint_as_float(static_cast<uint32_t>(s));
+#pragma unroll
+                for (int i = 0; i < kGroup - 1; ++i)
+                    if (i < before) h = enter(__uint_as_float(static_cast<uint32_t>(m[i][0])), __uint_as_float(static_cast<uint32_t>(m[i][1])), h);
+                if (missing) h = __uint_as_float(0x7fc00000u);
+            }
+            const float after = enter(A, H, h);
+            publish(own + 128, after);
+            entering[lane] = h;
+            lds_barrier();                                      // the state that enters
+            lds_barrier();                                      // it and the maps have been read
+            if (t.state == 2 && c < D) {
+                if (a.marks) a.marks[t.mark * D + c] = h;
+                if (a.h_final && (t.tile + 1) * static_cast<int64_t>(TILE) >= t.len) a.h_final[at] = after;
+            }
+        }
+        return;
+    }
+
+    T x[KT], z[KT];
+    G g[KT];
+    auto whole_tile = [](const Ticket& t) { return t.state == 2 && (t.tile + 1) * static_cast<int64_t>(TILE) <= t.len; };
+    auto load = [&](auto whole, const Ticket& t) __attribute__((always_inline)) {
+        Run r;
+        r.row = t.row;
+        r.start = t.start;
+        const uint32_t cc = min(t.cb * 64 + lane, D - 1);
+        const int first = t.tile * TILE + w * KT;
+        fetch(whole, x, rows_of<T>(a.x, r), first, t.len, cc);
+        fetch(whole, g, rows_of<G>(a.g, r), first, t.len, cc);
+        if constexpr (Z) fetch(whole, z, rows_of<T>(a.z, r), first, t.len, cc);
+    };
+    auto work = [&](auto whole, const Ticket& t, int slot) __attribute__((always_inline)) {
+        const int first = t.tile * TILE + w * KT, c = t.cb * 64 + lane;
+        float e[KT], u[KT];
+        T zz[KT];
+        float A = 1.f, H = 0.f;
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            const bool in = whole.value || first + k < t.len;
+            e[k] = in ? exp_of(static_cast<float>(g[k])) : 1.f;
+            u[k] = in ? static_cast<float>(x[k]) : 0.f;
+            H = __builtin_fmaf(e[k], H, u[k]);
+            A *= e[k];
+            if constexpr (Z) zz[k] = z[k];
+        }
+        ex[w][0][lane] = A;
+        ex[w][1][lane] = H;
+        lds_barrier();
+        const Ticket next = ticket(slot ^ 1);
+        if (whole_tile(next)) load(std::true_type{}, next);
+        lds_barrier();
+        float h = entering[lane];
+#pragma unroll
+        for (int i = 0; i < NW - 1; ++i)
+            if (i < w) h = enter(ex[i][0][lane], ex[i][1][lane], h);
+        lds_barrier();      // before the next tile's maps
+        if (c >= D) return;
+        Run r;
+        r.row = t.row;
+        r.start = t.start;
+        const Rows<T> ys = rows_of<T>(a.y, r);
+        T* yp = ys.p + first * ys.step;
+#pragma unroll
+        for (int k = 0; k < KT; ++k, yp += ys.step) {
+            h = __builtin_fmaf(e[k], h, u[k]);
+            float y = h;
+            if constexpr (Z) {
+                float f, d;
+                gate<DT != 0>(static_cast<float>(zz[k]), ACT, f, d);
+                y *= f;
+            }
+            if (whole.value || first + k < t.len) put(yp, c * sizeof(T), y);
+        }
+    };
+    lds_barrier();                                              // the first ticket
+    {
+        const Ticket t = ticket(0);
+        if (whole_tile(t)) load(std::true_type{}, t);
+    }
+    for (int slot = 0;; slot ^= 1) {
+        const Ticket t = ticket(slot);
+        if (t.state == 0) break;
+        if (t.state == 1) {
+            lds_barrier();
+            const Ticket next = ticket(slot ^ 1);
+            if (whole_tile(next)) load(std::true_type{}, next);
+            lds_barrier();
+            lds_barrier();
+        } else if (whole_tile(t)) {
+            work(std::true_type{}, t, slot);
+        } else {
+            load(std::false_type{}, t);
+            work(std::false_type{}, t, slot);
+        }
+    }
+}
+
+// a thread clears 16 bytes
+__global__ __launch_bounds__(256) void glr_clear(u32x4* __restrict__ p, const int64_t n) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) p[i] = u32x4{0u, 0u, 0u, 0u};
 }
 
 template <int DT, int GT, int ACT>
@@ -388,16 +611,23 @@ __global__ __launch_bounds__(kGlrStepThreads) void glr_step(const sdm_glr_step_a
 }
 
 template <int DT, int GT, int ACT>
-hipError_t forward_of(const sdm_glr_args_t& a, const GlrPlan& p, float* part, hipStream_t s) {
-    const unsigned grid = static_cast<unsigned>(a.nseq * p.segs * p.cblocks);
-    if (p.segs > 1) glr_parts<DT, GT, ACT, false><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
-    glr_forward<DT, GT, ACT><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
+hipError_t forward_of(const sdm_glr_args_t& a, const GlrPlan& p, void* ws, hipStream_t s) {
+    if (p.rows) {
+        const int64_t n = glr_chain_words(a, p) / 2;
+        glr_clear<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(static_cast<u32x4*>(ws), n);
+        const int64_t tickets = p.rows * p.cblocks;
+        glr_chain<DT, GT, ACT><<<static_cast<unsigned>(tickets < kGlrChainGroups ? tickets : kGlrChainGroups), kGlrChainThreads, 0, s>>>(
+            a, p.cblocks, p.rows, static_cast<uint64_t*>(ws));
+    } else {
+        glr_forward<DT, GT, ACT><<<static_cast<unsigned>(a.nseq * p.cblocks), kGlrThreads, 0, s>>>(a, p.cblocks);
+    }
     return hipGetLastError();
 }
 template <int DT, int GT, int ACT>
-hipError_t backward_of(const sdm_glr_args_t& a, const GlrPlan& p, float* part, hipStream_t s) {
+hipError_t backward_of(const sdm_glr_args_t& a, const GlrPlan& p, void* ws, hipStream_t s) {
     const unsigned grid = static_cast<unsigned>(a.nseq * p.segs * p.cblocks);
-    if (p.segs > 1) glr_parts<DT, GT, ACT, true><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
+    float* part = static_cast<float*>(ws);
+    if (p.segs > 1) glr_parts<DT, GT, ACT><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
     glr_backward<DT, GT, ACT><<<grid, kGlrThreads, 0, s>>>(a, p.cblocks, p.segs, part);
     return hipGetLastError();
 }
@@ -422,12 +652,8 @@ hipError_t step_of(const sdm_glr_step_args_t& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_glr_forward(const sdm_glr_args_t& a, const GlrPlan& p, float* part, hipStream_t s) {
-    SDM_GLR_TYPES(forward_of, a, p, part, s)
-}
-hipError_t launch_glr_backward(const sdm_glr_args_t& a, const GlrPlan& p, float* part, hipStream_t s) {
-    SDM_GLR_TYPES(backward_of, a, p, part, s)
-}
+hipError_t launch_glr_forward(const sdm_glr_args_t& a, const GlrPlan& p, void* ws, hipStream_t s) { SDM_GLR_TYPES(forward_of, a, p, ws, s) }
+hipError_t launch_glr_backward(const sdm_glr_args_t& a, const GlrPlan& p, void* ws, hipStream_t s) { SDM_GLR_TYPES(backward_of, a, p, ws, s) }
 hipError_t launch_glr_step(const sdm_glr_step_args_t& a, hipStream_t s) { SDM_GLR_TYPES(step_of, a, s) }
 
 }  // namespace sdm_delta

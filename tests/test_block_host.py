@@ -115,7 +115,7 @@ def test_glr_sizes():
     assert lib.sdm_glr_workspace(r(glr()), 0) == 0
     big = glr(T=1 << 20)
     n = lib.sdm_glr_workspace(r(big), 0)
-    assert n > 0 and n == lib.sdm_glr_workspace(r(big), 1)
+    assert n > 0 and lib.sdm_glr_workspace(r(big), 1) > 0
     for f in (lib.sdm_glr_marks, lambda a: lib.sdm_glr_workspace(a, 0)):
         assert f(None) == ARG and f(r(glr(D=0))) == SHAPE and f(r(glr(nseq=0))) == SHAPE
     for n_, v in (("x", 1), ("g", 2), ("z", 3), ("y", 4)):
