@@ -109,19 +109,19 @@ int check(const sdm_glr_args_t* a, bool backward) {
 }
 
 // Backward: runs are cut until there is a workgroup a CU, into parts of 512 tokens at the least: a part's map costs another
-// reading of its inputs. Forward: one workgroup a run and 64 channels where that is a workgroup a CU and all runs are alike, or
-// no run has more than 4 tiles; else the queue.
+// reading of its inputs. Forward: the queue where it is faster than one workgroup a run and 64 channels; of packed runs the GPU
+// finds out, but where none can have more than 4 tiles.
 GlrPlan plan(const sdm_glr_args_t* a, bool packed, bool backward) {
     GlrPlan p{};
     p.cblocks = static_cast<int>(cdiv(a->D, 64));
-    const int64_t have = a->nseq * p.cblocks, each = cdiv(a->T * a->B, a->nseq);
+    const int64_t have = a->nseq * p.cblocks, each = cdiv(a->T * a->B, a->nseq), tiles = cdiv(a->T, SDM_GLR_TILE);
     p.segs = backward ? static_cast<int>(std::max<int64_t>(1, std::min(256 / have, each / 512))) : 1;
-    if (!backward && a->T > 4 * SDM_GLR_TILE && (packed || have < 256)) p.rows = mark_rows(a, packed);
+    if (!backward && (packed ? tiles > 4 : !glr_walks(tiles, tiles * have))) p.rows = mark_rows(a, packed);
     return p;
 }
 int64_t workspace(const sdm_glr_args_t* a, bool packed, bool backward) {
     const GlrPlan p = plan(a, packed, backward);
-    return backward ? (p.segs > 1 ? a->nseq * p.segs * 2 * a->D * 4 : 0) : glr_chain_words(*a, p) * 8;
+    return backward ? (p.segs > 1 ? a->nseq * p.segs * 2 * a->D * 4 : 0) : glr_chain_words(p) * 8;
 }
 
 int run(const sdm_glr_args_t* a, bool backward, void* ws, int64_t ws_bytes, void* stream) {
@@ -133,7 +133,7 @@ int run(const sdm_glr_args_t* a, bool backward, void* ws, int64_t ws_bytes, void
     if (!aligned(ws, 16)) return SDM_GX_ERR_ALIGN;
     if (ws_bytes < need) return SDM_GX_ERR_LIMIT;
     const GlrPlan p = plan(a, packed, backward);
-    if (a->nseq * p.segs * p.cblocks * kGlrThreads >= kMaxThreads || glr_chain_words(*a, p) / 2 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
+    if (a->nseq * p.segs * p.cblocks * kGlrThreads >= kMaxThreads || glr_chain_words(p) / 2 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     if ((st = current_gfx950(&dev))) return st;
     const void* ps[] = {a->x.data, a->g.data, a->act ? a->z.data : nullptr, a->cu_seqlens, a->h0, a->marks, need ? ws : nullptr,
                         backward ? a->dy.data : a->y.data, backward ? a->dh_final : a->h_final, backward ? a->dx.data : nullptr,

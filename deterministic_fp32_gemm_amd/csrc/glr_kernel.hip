@@ -9,8 +9,8 @@
 // The next tile's loads are in flight meanwhile. The gradient walks the tiles from the last to the first: the states come
 // from the tile's mark and the same maps, and D's recurrence, e -> a_t (u_t + e) from right to left, has the same A.
 //
-// Where 64 channels of a run give too few workgroups, or runs of unlike lengths uneven ones, the forward takes tiles from one
-// queue instead (glr_chain below): still one pass. The gradient cuts runs into parts there: a first kernel finds each part's
+// Where 64 channels of a run give too few workgroups, or one run is much longer than the others, the forward takes tiles from
+// one queue instead (glr_chain below): still one pass. The gradient cuts runs into parts there: a first kernel finds each part's
 // map, which reads dy, z and g once more. It walks its part away from the end at which the second kernel starts, so that what
 // it read last is what is wanted first and may still be in the last-level cache.
 #include <hip/hip_runtime.h>
@@ -71,6 +71,14 @@ __device__ __forceinline__ T get(const T* row, uint32_t off) {
 template <class T>
 __device__ __forceinline__ void put(T* row, uint32_t off, float v) {
     *reinterpret_cast<T*>(reinterpret_cast<char*>(row) + off) = static_cast<T>(v);
+}
+
+// A first token of which the compiler does not know that it is zero: else it makes the multiples of every stride before the
+// loop, more than the scalar registers hold, and reads them back from lanes of vector registers (4 x 4096 tokens of 4096
+// channels in 150 us instead of 127).
+__device__ __forceinline__ int unknown(int t) {
+    asm volatile("" : "+s"(t));
+    return t;
 }
 
 // The wavefront's KT tokens from t: all of them in the run, or read from inside it whatever t is. (One form for both would
@@ -164,12 +172,13 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
 }
 
 template <int DT, int GT, int ACT>
-__global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t a, const int cblocks) {
+__global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t a, const int cblocks, const uint64_t* __restrict__ words) {
     using T = elem_t<DT>;
     using G = elem_t<GT>;
     constexpr bool Z = ACT != SDM_ACT_NONE;
     __shared__ float ex[2][NW][2][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (words && words[1] == 0) return;        // the queue's
     const int cb = blockIdx.x % cblocks, run = blockIdx.x / cblocks;
     const Run r = run_of(a, run);
     const int D = static_cast<int>(a.D), c = cb * 64 + lane, cc = min(c, D - 1);
@@ -184,7 +193,8 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
         if constexpr (Z) fetch(whole, z, zs, t, r.len, cc);
     };
     const int end = r.len / TILE * TILE;       // of the whole tiles
-    if (end > 0) load(std::true_type{}, w * KT);
+    const int t0 = unknown(0);
+    if (end > t0) load(std::true_type{}, t0 + w * KT);
     int buf = 0;
     auto work = [&](auto whole, int tile) __attribute__((always_inline)) {
         const int t = tile + w * KT;
@@ -226,7 +236,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
             if (whole.value || t + k < r.len) put(yp, c * sizeof(T), y);
         }
     };
-    for (int tile = 0; tile < end; tile += TILE, buf ^= 1) work(std::true_type{}, tile);
+    for (int tile = t0; tile < end; tile += TILE, buf ^= 1) work(std::true_type{}, tile);
     if (end < r.len) {
         load(std::false_type{}, end + w * KT);
         work(std::false_type{}, end);
@@ -238,13 +248,18 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
 // who takes it does not change a bit of the result. Beside the eight wavefronts that hold the tile, a ninth takes the tickets and
 // joins the tile to those before it in its run. When the eight have found the tile's map it publishes it, waits for the state
 // after the last tile of the group of 8 before and for the maps of the tiles of its own group before it, composes them in
-// order, publishes the state after its tile and hands the eight the one that enters; their loads of the next tile are in flight
-// meanwhile. A run's states thus pass from group to group, and maps within one.
+// order, publishes the state after its tile and hands the eight the one that enters. They load the next tile and find this
+// one's gates meanwhile. A run's states thus pass from group to group, and maps within one. (Groups of 4 took 149 us where 8
+// take 155, and 46 where 8 take 45; 16: 172 and 43. Two workgroups a CU without loads ahead took 184.)
 //
-// What is published goes as words of 8 bytes, a float32 and a mark that it is there, by relaxed atomics of device scope: a
-// word is there or not, and needs no order with others. All words are cleared by a kernel before. No wait goes unended: a
-// ticket waits for lower ones only, which running workgroups hold, each of which publishes whatever its tile is; after some
-// seconds of waiting, which nothing but a fault explains, a tile goes on with NaN.
+// What is published goes as words of 8 bytes, a map or a state, with a bit that says that it is there, by relaxed atomics of
+// device scope: a word is there or not, and needs no order with others. All words are cleared by a kernel before. No wait goes
+// unended: a ticket waits for lower ones only, which running workgroups hold, each of which publishes whatever its tile is;
+// after some seconds of waiting, which nothing but a fault explains, a tile goes on with NaN.
+//
+// One run of 16384 tokens and 4096 channels, bfloat16 with float32 g and z: 155 us, 4.3 TB/s (walking it in four parts, whose
+// maps a kernel before has to find: 215). A tile takes its workgroup 4.7 us, of which the exponentials and the last walk are
+// half and the join the rest; the loads are hidden.
 constexpr int kGroup = 8;
 constexpr int kPolls = 1 << 22;
 
@@ -254,8 +269,10 @@ struct Ticket {
     int state;                      // 0: no more; 1: a row of marks that has no tile; 2: a tile
 };
 
-__device__ __forceinline__ uint64_t word(float v) { return uint64_t(1) << 32 | __float_as_uint(v); }
-__device__ __forceinline__ void publish(uint64_t* p, float v) { __hip_atomic_store(p, word(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+// a map's A is never below zero: its sign marks that the word is there
+__device__ __forceinline__ uint64_t map_word(float A, float H) { return static_cast<uint64_t>(__float_as_uint(A) | 0x80000000u) << 32 | __float_as_uint(H); }
+__device__ __forceinline__ uint64_t state_word(float h) { return uint64_t(1) << 63 | __float_as_uint(h); }
+__device__ __forceinline__ void publish(uint64_t* p, uint64_t v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ uint64_t look(const uint64_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
 // The ticket's tile, found by one wavefront.
@@ -304,9 +321,10 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
     __shared__ float ex[NW][2][64], entering[64];
     __shared__ int tickets[2][sizeof(Ticket) / 4];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = static_cast<int>(a.D);
-    // the first words: the queue's counter; then, of each tile, 64 A's, 64 H's and 64 states
+    // the first words: the queue's counter, whether runs are walked; then, of each tile, 64 maps and 64 states
+    if (words[1] != 0) return;
     unsigned long long* counter = reinterpret_cast<unsigned long long*>(words);
-    auto words_of = [&](int64_t mark, int cb) { return words + 64 + (mark * cblocks + cb) * 192 + lane; };
+    auto words_of = [&](int64_t mark, int cb) { return words + 64 + (mark * cblocks + cb) * 128 + lane; };
     auto take = [&](int slot) {
         unsigned long long id = 0;
         if (lane == 0) id = __hip_atomic_fetch_add(counter, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -349,36 +367,31 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
                 }
             }
             uint64_t* own = words_of(t.mark, t.cb);
-            publish(own, A);
-            publish(own + 64, H);
+            publish(own, map_word(A, H));
             if (t.state == 2) {
                 const int before = t.tile - group;              // tiles of the group before this one
-                uint64_t m[kGroup - 1][2], s = word(h);
-                bool missing = true;
+                uint64_t m[kGroup - 1], s = state_word(h);
+                // what is still missing, a bit each: the maps and, in the last one, the state; what is there is not read again
+                uint32_t missing = ((1u << before) - 1) | (group ? 1u << (kGroup - 1) : 0u);
                 for (int polls = 0; missing && polls < kPolls; ++polls) {
                     if (polls) __builtin_amdgcn_s_sleep(1);
-                    if (group) s = look(words_of(t.mark - before - 1, t.cb) + 128);
+                    if (missing >> (kGroup - 1)) s = look(words_of(t.mark - before - 1, t.cb) + 64);
 #pragma unroll
                     for (int i = 0; i < kGroup - 1; ++i)
-                        if (i < before) {
-                            const uint64_t* p = words_of(t.mark - before + i, t.cb);
-                            m[i][0] = look(p);
-                            m[i][1] = look(p + 64);
-                        }
-                    bool there = s >> 32;
+                        if (missing >> i & 1) m[i] = look(words_of(t.mark - before + i, t.cb));
+                    if (missing >> (kGroup - 1) && __all(s >> 63)) missing &= (1u << (kGroup - 1)) - 1;
 #pragma unroll
                     for (int i = 0; i < kGroup - 1; ++i)
-                        if (i < before) there = there && m[i][0] >> 32 && m[i][1] >> 32;
-                    missing = !__all(there);
+                        if (missing >> i & 1 && __all(m[i] >> 63)) missing &= ~(1u << i);
                 }
                 h = __uint_as_float(static_cast<uint32_t>(s));
 #pragma unroll
                 for (int i = 0; i < kGroup - 1; ++i)
-                    if (i < before) h = enter(__uint_as_float(static_cast<uint32_t>(m[i][0])), __uint_as_float(static_cast<uint32_t>(m[i][1])), h);
+                    if (i < before) h = enter(__uint_as_float(static_cast<uint32_t>(m[i] >> 32) & 0x7fffffffu), __uint_as_float(static_cast<uint32_t>(m[i])), h);
                 if (missing) h = __uint_as_float(0x7fc00000u);
             }
             const float after = enter(A, H, h);
-            publish(own + 128, after);
+            publish(own + 64, state_word(after));
             entering[lane] = h;
             lds_barrier();                                      // the state that enters
             lds_barrier();                                      // it and the maps have been read
@@ -405,9 +418,8 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
     };
     auto work = [&](auto whole, const Ticket& t, int slot) __attribute__((always_inline)) {
         const int first = t.tile * TILE + w * KT, c = t.cb * 64 + lane;
-        float e[KT], u[KT];
+        float e[KT], u[KT], f[KT], A = 1.f, H = 0.f;
         T zz[KT];
-        float A = 1.f, H = 0.f;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
             const bool in = whole.value || first + k < t.len;
@@ -422,6 +434,15 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
         lds_barrier();
         const Ticket next = ticket(slot ^ 1);
         if (whole_tile(next)) load(std::true_type{}, next);
+        // the gates, while the ninth waits; not to be moved behind the barrier
+        if constexpr (Z) {
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                float d;
+                gate<DT != 0>(static_cast<float>(zz[k]), ACT, f[k], d);
+                asm volatile("" : "+v"(f[k]));
+            }
+        }
         lds_barrier();
         float h = entering[lane];
 #pragma unroll
@@ -437,13 +458,7 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
 #pragma unroll
         for (int k = 0; k < KT; ++k, yp += ys.step) {
             h = __builtin_fmaf(e[k], h, u[k]);
-            float y = h;
-            if constexpr (Z) {
-                float f, d;
-                gate<DT != 0>(static_cast<float>(zz[k]), ACT, f, d);
-                y *= f;
-            }
-            if (whole.value || first + k < t.len) put(yp, c * sizeof(T), y);
+            if (whole.value || first + k < t.len) put(yp, c * sizeof(T), Z ? h * f[k] : h);
         }
     };
     lds_barrier();                                              // the first ticket
@@ -469,10 +484,22 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
     }
 }
 
-// a thread clears 16 bytes
-__global__ __launch_bounds__(256) void glr_clear(u32x4* __restrict__ p, const int64_t n) {
+// Clears the words, 16 bytes a thread, and for packed runs decides between the queue and walking (glr_walks), since only here
+// their lengths are known.
+__global__ __launch_bounds__(256) void glr_clear(const sdm_glr_args_t a, const int cblocks, const int64_t rows, u32x4* __restrict__ p, const int64_t n) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i < n) p[i] = u32x4{0u, 0u, 0u, 0u};
+    uint32_t walk = 0;
+    if (blockIdx.x == 0 && a.cu_seqlens) {
+        __shared__ int longest;
+        if (threadIdx.x == 0) longest = 0;
+        __syncthreads();
+        int l = 0;
+        for (int64_t r = threadIdx.x; r < a.nseq; r += 256) l = max(l, run_of(a, static_cast<int>(r)).len);
+        atomicMax(&longest, l);
+        __syncthreads();
+        walk = glr_walks((longest + TILE - 1) / TILE, rows * cblocks);
+    }
+    if (i < n) p[i] = u32x4{0u, 0u, i == 0 ? walk : 0u, 0u};
 }
 
 template <int DT, int GT, int ACT>
@@ -613,14 +640,15 @@ __global__ __launch_bounds__(kGlrStepThreads) void glr_step(const sdm_glr_step_a
 template <int DT, int GT, int ACT>
 hipError_t forward_of(const sdm_glr_args_t& a, const GlrPlan& p, void* ws, hipStream_t s) {
     if (p.rows) {
-        const int64_t n = glr_chain_words(a, p) / 2;
-        glr_clear<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(static_cast<u32x4*>(ws), n);
+        const int64_t n = glr_chain_words(p) / 2;
+        glr_clear<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(a, p.cblocks, p.rows, static_cast<u32x4*>(ws), n);
         const int64_t tickets = p.rows * p.cblocks;
         glr_chain<DT, GT, ACT><<<static_cast<unsigned>(tickets < kGlrChainGroups ? tickets : kGlrChainGroups), kGlrChainThreads, 0, s>>>(
             a, p.cblocks, p.rows, static_cast<uint64_t*>(ws));
-    } else {
-        glr_forward<DT, GT, ACT><<<static_cast<unsigned>(a.nseq * p.cblocks), kGlrThreads, 0, s>>>(a, p.cblocks);
     }
+    if (!p.rows || a.cu_seqlens)
+        glr_forward<DT, GT, ACT><<<static_cast<unsigned>(a.nseq * p.cblocks), kGlrThreads, 0, s>>>(
+            a, p.cblocks, p.rows ? static_cast<const uint64_t*>(ws) : nullptr);
     return hipGetLastError();
 }
 template <int DT, int GT, int ACT>

@@ -57,6 +57,43 @@ def test_packed(T, cu, ty, act):
     check(inputs(ty, "f32", 1, T, 37, act, len(cu) - 1), act, cu)
 
 
+@pytest.mark.parametrize("ty,gty,B,T,D,act", [
+    ("bf16", "f32", 1, 20001, 70, "silu"),      # tiles from the queue, many groups of them
+    ("f16", "f16", 3, 2500, 66, "sigmoid"), ("f32", "f32", 2, 1280, 1, "none"), ("bf16", "bf16", 1, 1024, 4100, "silu"),
+])
+def test_long_rows(ty, gty, B, T, D, act):
+    say("glr long", ty, gty, B, T, D, act)
+    check(inputs(ty, gty, B, T, D, act), act)
+
+
+@pytest.mark.parametrize("ty,act", [("f32", "silu"), ("bf16", "none")])
+@pytest.mark.parametrize("lens", [
+    [5000] + [30, 0, 1] * 43, [0] * 70 + [3000, 0, 129] + [0] * 70, [128] * 9 + [4096], [100, 4100, 0], [700] * 3])
+def test_packed_long_runs(lens, ty, act):
+    """Runs taken from the queue and runs walked, with more of them than a wavefront has lanes and empty ones at every place."""
+    say("glr packed long", len(lens), sum(lens), ty, act)
+    cu = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    check(inputs(ty, "f32", 1, cu[-1], 65, act, len(lens)), act, cu)
+
+
+def test_bad_bounds_of_long_runs_stay_inside():
+    """As below, where tiles come from the queue: the call ends."""
+    t = inputs("f32", "f32", 1, 3000, 12, "silu", 4)
+    cu = torch.tensor([-5, 1500, 90, 100000, 7], dtype=torch.int32, device="cuda")
+    y, h, marks = sdm.glr_forward(t["x"], t["g"], t["z"], act="silu", initial_state=t["h0"], cu_seqlens=cu)
+    sdm.glr_backward(t["x"], t["g"], t["z"], t["dy"], marks, act="silu", initial_state=t["h0"], dfinal_state=t["dh"], cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert y.shape == t["x"].shape and marks.shape[1] == 12
+
+
+def test_the_same_bits_from_the_queue():
+    t, cu = inputs("bf16", "f32", 1, 9000, 300, "silu", 3), [0, 8000, 8100, 9000]
+    want = run(t, "silu", cu)
+    for _ in range(5):
+        got = run(t, "silu", cu)
+        assert all(torch.equal(got[k], want[k]) for k in want)
+
+
 def test_tokens_of_no_run_are_zero():
     t = inputs("f32", "f32", 1, 300, 20, "silu", 2)
     got = run(t, "silu", [10, 150, 290])
