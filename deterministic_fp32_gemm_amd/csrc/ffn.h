@@ -46,16 +46,17 @@ struct FfnLay {
     char* dst;
     int64_t ldd;                // bytes
     int64_t pad;                // elements
+    int64_t again;              // turned: bytes from dst to a second copy; 0: none
 };
 hipError_t launch_ffn_lay(const FfnLay (&l)[3], hipStream_t stream);     // one launch; without rows: none
 
 // dg and du from dh, g and u: rows[m] = dg, zeros to Fp, du, zeros to 2 Fp; cols[f] = dg's column f, zeros to Mp, and du's at
-// row F + f.
+// row F + f. Two parts: behind them, in rows of twice the length, what dg and du lost by their rounding.
 struct FfnGrad {
     const void* dh;
     const float *gate, *up;
     int64_t ld_dh, ld_gate, ld_up, M, F, Mp, Fp;
-    int dtype, act;
+    int dtype, act, parts;
     char *rows, *cols;
 };
 // One launch, with the three operands turned.

@@ -1,5 +1,6 @@
 // Host entry points of the gated feed-forward product (sdm_ffn.h): argument checks, workspaces, the order of the launches.
 // The arithmetic is in the ffn_*.hip files.
+#include <algorithm>
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -102,7 +103,7 @@ Laid operand(const void* src, int64_t ld, int64_t R, int64_t C, int dtype, Space
     const int64_t pad = up_to(C, 16 / es), row = pad * es;
     char* p = s->take(R * row);
     l.o = FfnOperand{p, row};
-    l.lay = FfnLay{src, ld, R, C, dtype, p, row, pad};
+    l.lay = FfnLay{src, ld, R, C, dtype, p, row, pad, 0};
     return l;
 }
 
@@ -140,6 +141,11 @@ Forward forward_plan(const sdm_ffn_args_t* a, char* ws) {
     return f;
 }
 
+// What rounding dg and du to 16 bits adds to the error of a sum of many of them is as large as what rounding the result adds,
+// and for few of them now and then more. There they come in two parts, and what they meet in the products twice: 5 rows of 64
+// to 128 in bfloat16 had 1.5 times the error of the rounded result alone, now 1.0; two rows of 2048 to 8192 would pay XX us.
+int gradient_parts(const sdm_ffn_args_t* a) { return a->dtype != SDM_F32 && a->M * std::min(a->K, a->F) <= 4096 ? 2 : 1; }
+
 struct Backward {
     int tile;
     FfnGrad grad;
@@ -152,23 +158,23 @@ Backward backward_plan(const sdm_ffn_args_t* a, char* ws) {
     Backward b{};
     b.tile = gradient_tile(a->M, a->K, a->F, a->dtype);
     const int64_t es = size_of(a->dtype);
-    const int64_t M = a->M, K = a->K, F = a->F, Mp = up_to(M, 16 / es), Fp = up_to(F, 16 / es);
+    const int64_t M = a->M, K = a->K, F = a->F, Mp = up_to(M, 16 / es), Fp = up_to(F, 16 / es), parts = gradient_parts(a);
     auto area = [&](int64_t rows, int64_t cols, FfnOperand* o) {
         char* p = s.take(rows * cols * es);
         *o = FfnOperand{p, cols * es};
         return p;
     };
-    char* rows = area(M, 2 * Fp, &b.rows);
-    char* cols = area(2 * F, Mp, &b.cols);
-    char* w = area(K, 2 * Fp, &b.w);
-    char* xt = area(K, Mp, &b.xt);
-    b.grad = FfnGrad{a->dh, a->gate, a->up, a->ld_dh, a->ld_gate, a->ld_up, M, F, Mp, Fp, a->dtype, a->act, rows, cols};
-    b.wg = FfnLay{a->wg, a->ld_wg, F, K, a->dtype, w, b.w.ld, Fp};
+    char* rows = area(M, 2 * parts * Fp, &b.rows);
+    char* cols = area(2 * F, parts * Mp, &b.cols);
+    char* w = area(K, 2 * parts * Fp, &b.w);
+    char* xt = area(K, parts * Mp, &b.xt);
+    b.grad = FfnGrad{a->dh, a->gate, a->up, a->ld_dh, a->ld_gate, a->ld_up, M, F, Mp, Fp, a->dtype, a->act, static_cast<int>(parts), rows, cols};
+    b.wg = FfnLay{a->wg, a->ld_wg, F, K, a->dtype, w, b.w.ld, Fp, parts == 2 ? 2 * Fp * es : 0};
     b.wu = b.wg;
     b.wu.src = a->wu;
     b.wu.ld = a->ld_wu;
     b.wu.dst = w + Fp * es;
-    b.x = FfnLay{a->x, a->ld_x, M, K, a->dtype, xt, b.xt.ld, Mp};
+    b.x = FfnLay{a->x, a->ld_x, M, K, a->dtype, xt, b.xt.ld, Mp, parts == 2 ? Mp * es : 0};
     b.bytes = s.used;
     return b;
 }

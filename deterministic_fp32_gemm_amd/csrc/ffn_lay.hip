@@ -129,7 +129,10 @@ __device__ __forceinline__ void lay_turned(const Three& three, unsigned b, bits_
 #pragma unroll
     for (int i = 0; i < L / 4; ++i) {
         const int c = i * (256 / L) + threadIdx.x / L, r = threadIdx.x % L * E;
-        if (c0 + c < l.C && r0 + r < l.pad) *reinterpret_cast<u32x4*>(l.dst + (c0 + c) * l.ldd + (r0 + r) * N) = column(tile, r, c);
+        if (c0 + c >= l.C || r0 + r >= l.pad) continue;
+        char* p = l.dst + (c0 + c) * l.ldd + (r0 + r) * N;
+        *reinterpret_cast<u32x4*>(p) = column(tile, r, c);
+        if (l.again) *reinterpret_cast<u32x4*>(p + l.again) = column(tile, r, c);
     }
 }
 
@@ -138,8 +141,8 @@ __device__ __forceinline__ float value(uint16_t b, __bf16) { return static_cast<
 __device__ __forceinline__ float value(uint16_t b, _Float16) { return static_cast<float>(__builtin_bit_cast(_Float16, b)); }
 
 // dg and du, and, in the workgroups from `first` on, the operands to be turned: one launch for all that the gradient's products
-// read. 16-bit types: dg and du are rounded to dtype, as their products take them.
-template <int DT>
+// read. 16-bit types: dg and du are rounded to dtype, as their products take them, in PARTS parts.
+template <int DT, int PARTS>
 __global__ __launch_bounds__(256) void ffn_grad(const FfnGrad a, const int across, const Three three, const unsigned first) {
     using T = elem_t<DT>;
     constexpr int N = sizeof(T);
@@ -151,7 +154,7 @@ __global__ __launch_bounds__(256) void ffn_grad(const FfnGrad a, const int acros
     }
     const int64_t m0 = static_cast<int64_t>(blockIdx.x / across) * 64, f0 = static_cast<int64_t>(blockIdx.x % across) * 64;
     const int r16 = threadIdx.x / 16, c = threadIdx.x % 16 * 4;
-    B dh[4][4];
+    B dh[4][4], lost[PARTS == 2 ? 4 : 1][2][4];
     uint32_t g[4][4], u[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -170,24 +173,46 @@ __global__ __launch_bounds__(256) void ffn_grad(const FfnGrad a, const int acros
             gate<DT != SDM_F32>(__uint_as_float(g[i][k]), a.act, act, d);
             const bool in = m0 + r < a.M && f0 + c + k < a.F;
             const float h = value(dh[i][k], T{});
-            x[0][k] = __builtin_bit_cast(B, static_cast<T>(in ? h * __uint_as_float(u[i][k]) * d : 0.f));
-            x[1][k] = __builtin_bit_cast(B, static_cast<T>(in ? h * act : 0.f));
+            const float v[2] = {in ? h * __uint_as_float(u[i][k]) * d : 0.f, in ? h * act : 0.f};
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const T first_part = static_cast<T>(v[s]);
+                x[s][k] = __builtin_bit_cast(B, first_part);
+                // nothing is lost of what is not finite
+                if constexpr (PARTS == 2)
+                    lost[i][s][k] = __builtin_bit_cast(B, static_cast<T>(__builtin_isfinite(static_cast<float>(first_part)) ? v[s] - static_cast<float>(first_part) : 0.f));
+            }
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             put4(&tile[s][r][c], x[s]);
             // c and a row's padded length are multiples of 4
-            if (m0 + r < a.M && f0 + c < a.Fp) store4(a.rows + ((m0 + r) * 2 * a.Fp + s * a.Fp + f0 + c) * N, x[s]);
+            if (m0 + r < a.M && f0 + c < a.Fp) {
+                char* p = a.rows + ((m0 + r) * 2 * PARTS * a.Fp + s * a.Fp + f0 + c) * N;
+                store4(p, x[s]);
+                if constexpr (PARTS == 2) store4(p + 2 * a.Fp * N, lost[i][s]);
+            }
         }
     }
-    __syncthreads();
     constexpr int E = 16 / N, L = 64 / E;
 #pragma unroll
-    for (int i = 0; i < L / 4; ++i) {
-        const int f = i * (256 / L) + threadIdx.x / L, m = threadIdx.x % L * E;
-        if (f0 + f >= a.F || m0 + m >= a.Mp) continue;
+    for (int part = 0; part < PARTS; ++part) {
+        __syncthreads();
+        if (part) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) *reinterpret_cast<u32x4*>(a.cols + ((s * a.F + f0 + f) * a.Mp + m0 + m) * N) = column(tile[s], m, f);
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) put4(&tile[s][i * 16 + r16][c], lost[i][s]);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < L / 4; ++i) {
+            const int f = i * (256 / L) + threadIdx.x / L, m = threadIdx.x % L * E;
+            if (f0 + f >= a.F || m0 + m >= a.Mp) continue;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                *reinterpret_cast<u32x4*>(a.cols + ((s * a.F + f0 + f) * PARTS * a.Mp + part * a.Mp + m0 + m) * N) = column(tile[s], m, f);
+        }
     }
 }
 
@@ -216,7 +241,10 @@ hipError_t grad(const FfnGrad& g, const FfnLay (&l)[3], hipStream_t s) {
         n += static_cast<unsigned>(tiles(l[i].pad) * tiles(l[i].C));
         t.upto[i] = n;
     }
-    ffn_grad<DT><<<first + n, 256, 0, s>>>(g, static_cast<int>(tiles(g.Fp)), t, first);
+    if (g.parts == 1)
+        ffn_grad<DT, 1><<<first + n, 256, 0, s>>>(g, static_cast<int>(tiles(g.Fp)), t, first);
+    else if constexpr (DT != SDM_F32)
+        ffn_grad<DT, 2><<<first + n, 256, 0, s>>>(g, static_cast<int>(tiles(g.Fp)), t, first);
     return hipGetLastError();
 }
 

@@ -117,7 +117,7 @@ def cut8(X, W):
     return 7 * 2.0 ** -13 * lost
 
 
-def ffn(x, wg, wu, act, otype, scales=(None, None, None), dh=None):
+def ffn(x, wg, wu, act, otype, scales=(None, None, None), dh=None, parts=1):
     """{name: (value, bound)} of the gated feed-forward product, and with dh of its gradient. On x's device.
 
     A sum of K products in float32 is off by at most (K + 8) 2^-23 of the sum of their absolute values (a rounding or a cut-off
@@ -142,7 +142,7 @@ def ffn(x, wg, wu, act, otype, scales=(None, None, None), dh=None):
     ty, DH = x.dtype, dh.double()
     edf = gate + dd * eg * (1 + (1 if act == "none" else 2) * eg)
     dg, du = DH * u * df, DH * f
-    rough = half(ty) if ty != torch.float32 else 4 * U      # dg and du as the products take them
+    rough = half(ty) ** parts if ty != torch.float32 else 4 * U     # dg and du as the products take them
     # a value under the type's range rounds to a multiple of its smallest step
     edg = DH.abs() * (eu * (df.abs() + edf) + u.abs() * edf) + (rough + 2 * U) * dg.abs() * 1.01 + tiny(ty)
     edu = DH.abs() * ef + (rough + 2 * U) * du.abs() * 1.01 + tiny(ty)

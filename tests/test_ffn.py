@@ -41,6 +41,18 @@ def test_against_the_definition(ty, act, M, K, F):
     check(*inputs(ty, M, K, F), act)
 
 
+@pytest.mark.parametrize("M,K,F", [(1, 2048, 70), (5, 64, 128), (2, 128, 1856), (26, 157, 130), (70, 58, 300)])
+@pytest.mark.parametrize("ty", ["bf16", "f16"])
+def test_gradients_of_few_values(ty, M, K, F):
+    """dg and du come in two parts there, each of which is off by half a step: half a step squared is left of their rounding."""
+    say("ffn few values", ty, M, K, F)
+    x, wg, wu, dh = inputs(ty, M, K, F)
+    grads = sdm.ffn_backward(dh, x, wg, wu, sdm.ffn_forward(x, wg, wu, act="gelu", keep=True)[1], act="gelu")
+    want = ffn(x, wg, wu, "gelu", x.dtype, dh=dh, parts=2)
+    for name, got in zip(("dx", "dwg", "dwu"), grads):
+        within(got, *want[name], name)
+
+
 @pytest.mark.parametrize("ty", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("act", ["none", "sigmoid", "silu", "gelu"])
 def test_activations(ty, act):
