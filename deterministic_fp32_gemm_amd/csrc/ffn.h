@@ -28,10 +28,23 @@ struct FfnProduct {
     int64_t ldc, ldc2, split;   // elements
     float *gate, *up;           // the pair's products, or NULL
     int64_t ld_gate, ld_up;
+    // No pair: the sum in `parts` parts of `part` bytes of each row (a multiple of 128), float32 sums of part i in rows i M and on
+    int64_t part;
+    int parts;
 };
 // tile: rows and columns of a workgroup's tile, 64, 128 or 256. Two products of one type go in one launch.
 hipError_t launch_ffn_pair(const FfnProduct& p, int tile, hipStream_t stream);
 hipError_t launch_ffn_products(const FfnProduct (&p)[2], int tile, hipStream_t stream);
+
+// Sums of parts, in order, into a product's rows: c, and c2 from `split` on.
+struct FfnJoin {
+    const float* from;          // [parts][M][ld], 16-byte aligned, ld a multiple of 4
+    int64_t M, N, ld;
+    int parts, otype;
+    char *c, *c2;
+    int64_t ldc, ldc2, split;
+};
+hipError_t launch_ffn_join(const FfnJoin (&j)[2], hipStream_t stream);      // one launch; without parts: none
 
 // Few rows: weights straight from memory, at any alignment. 16-bit and 8-bit rows from 17 on are faster in tiles (4096 to 8192,
 // 32 rows: bfloat16 40 us here and 36 in tiles, 8 bits 21 and 15); float32 ones from 33 on.

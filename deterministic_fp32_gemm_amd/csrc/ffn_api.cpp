@@ -143,11 +143,30 @@ Forward forward_plan(const sdm_ffn_args_t* a, char* ws) {
 
 // What rounding dg and du to 16 bits adds to the error of a sum of many of them is as large as what rounding the result adds,
 // and for few of them now and then more. There they come in two parts, and what they meet in the products twice: 5 rows of 64
-// to 128 in bfloat16 had 1.5 times the error of the rounded result alone, now 1.0; two rows of 2048 to 8192 would pay XX us.
+// to 128 in bfloat16 had 1.5 times the error of the rounded result alone, now 1.0. Above, the sums are long enough for 1.42.
 int gradient_parts(const sdm_ffn_args_t* a) { return a->dtype != SDM_F32 && a->M * std::min(a->K, a->F) <= 4096 ? 2 : 1; }
+
+// A product of few tiles and a long sum is cut into parts along the sum, up to two workgroups a CU (tiles of 256: one), of 8
+// steps of 128 bytes at the least, where that saves 32 steps: joining them is one more launch, about as long as 8 to 16 steps.
+// bfloat16 training steps in parts and without: 100 rows of 1024 to 8192 73 and 281 us, 64 of 4096 to 8192 199 and 446, 8192 of
+// 64 to 128 36 and 54.
+struct Cut {
+    int64_t part;
+    int parts;
+};
+Cut cut(int64_t M, int64_t N, int64_t bytes, int tile) {
+    const int64_t steps = cdiv(bytes, 128), have = cdiv(M, tile) * cdiv(N, tile);
+    const int64_t most = std::min(steps / 8, (tile == 256 ? 256 : 512) / have);
+    if (most < 2) return {up_to(bytes, 128), 1};
+    const int64_t each = cdiv(steps, most);
+    if (steps - each < 32) return {up_to(bytes, 128), 1};
+    return {each * 128, static_cast<int>(cdiv(steps, each))};
+}
 
 struct Backward {
     int tile;
+    Cut dx, dw;
+    float *dx_parts, *dw_parts;
     FfnGrad grad;
     FfnLay wg, wu, x;
     FfnOperand rows, cols, w, xt;
@@ -175,6 +194,11 @@ Backward backward_plan(const sdm_ffn_args_t* a, char* ws) {
     b.wu.ld = a->ld_wu;
     b.wu.dst = w + Fp * es;
     b.x = FfnLay{a->x, a->ld_x, M, K, a->dtype, xt, b.xt.ld, Mp, parts == 2 ? Mp * es : 0};
+    const int64_t wide = up_to(K, 4);
+    b.dx = cut(M, K, b.rows.ld, b.tile);
+    b.dw = cut(2 * F, K, b.cols.ld, b.tile);
+    if (b.dx.parts > 1) b.dx_parts = reinterpret_cast<float*>(s.take(b.dx.parts * M * wide * 4));
+    if (b.dw.parts > 1) b.dw_parts = reinterpret_cast<float*>(s.take(b.dw.parts * 2 * F * wide * 4));
     b.bytes = s.used;
     return b;
 }
@@ -266,17 +290,30 @@ int sdm_ffn_backward(const sdm_ffn_args_t* a, void* ws, int64_t ws_bytes, void* 
     dw.ldc = a->ld_dwg;
     dw.ldc2 = a->ld_dwu;
     dw.split = a->F;
-    for (FfnProduct* p : {&dx, &dw}) {
-        p->type = product_type(a->dtype);
-        p->otype = a->otype;
+    FfnJoin join[2] = {};
+    const Cut cuts[2] = {b.dx, b.dw};
+    float* const areas[2] = {b.dx_parts, b.dw_parts};
+    for (int i = 0; i < 2; ++i) {
+        FfnProduct& p = both[i];
+        p.type = product_type(a->dtype);
+        p.otype = a->otype;
+        p.part = cuts[i].part;
+        p.parts = cuts[i].parts;
+        if (p.parts == 1) continue;
+        join[i] = FfnJoin{areas[i], p.M, p.N, up_to(p.N, 4), p.parts, p.otype, p.c, p.c2, p.ldc, p.ldc2, p.split};
+        p.otype = SDM_F32;
+        p.c = reinterpret_cast<char*>(areas[i]);
+        p.ldc = join[i].ld;
+        p.split = p.M;
     }
-    if (gradient_tiles(a->M, a->K, a->F, b.tile) * 512 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
+    if ((gradient_tiles(a->M, a->K, a->F, b.tile) + 1024) * 512 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     const int64_t gm = cdiv(b.grad.Mp, 64), gf = cdiv(b.grad.Fp, 64), gk = cdiv(a->K, 64);
     if ((gm * gf + (gm + 2 * gf) * gk) * 256 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     if ((st = prepare(a, true, b.bytes, ws, ws_bytes))) return st;
     const FfnLay lay[3] = {b.wg, b.wu, b.x};
     if (const hipError_t e = launch_ffn_grad(b.grad, lay, s)) return status(e);
-    return status(launch_ffn_products(both, b.tile, s));
+    if (const hipError_t e = launch_ffn_products(both, b.tile, s)) return status(e);
+    return status(launch_ffn_join(join, s));
 }
 
 }  // extern "C"

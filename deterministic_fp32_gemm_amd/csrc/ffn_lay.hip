@@ -216,6 +216,31 @@ __global__ __launch_bounds__(256) void ffn_grad(const FfnGrad a, const int acros
     }
 }
 
+struct Joins {
+    FfnJoin j[2];
+    int64_t first;      // threads of the first
+};
+// A thread has four columns of a row.
+__global__ __launch_bounds__(256) void ffn_join(const Joins joins, const int64_t all) {
+    int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (id >= all) return;
+    const FfnJoin& j = joins.j[id >= joins.first];
+    id -= id >= joins.first ? joins.first : 0;
+    const int64_t m = id / (j.ld / 4), n = id % (j.ld / 4) * 4;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < j.parts; ++i) sum += *reinterpret_cast<const f32x4*>(j.from + (i * j.M + m) * j.ld + n);
+    char* c = m < j.split ? j.c : j.c2;
+    const int64_t at = (m < j.split ? m * j.ldc : (m - j.split) * j.ldc2) + n;
+    for (int e = 0; e < 4 && n + e < j.N; ++e) {
+        if (j.otype == SDM_F32)
+            reinterpret_cast<float*>(c)[at + e] = sum[e];
+        else if (j.otype == SDM_BF16)
+            reinterpret_cast<__bf16*>(c)[at + e] = static_cast<__bf16>(sum[e]);
+        else
+            reinterpret_cast<_Float16*>(c)[at + e] = static_cast<_Float16>(sum[e]);
+    }
+}
+
 int64_t tiles(int64_t n) { return (n + 63) / 64; }
 
 template <int N>
@@ -254,6 +279,13 @@ hipError_t grad(const FfnGrad& g, const FfnLay (&l)[3], hipStream_t s) {
 hipError_t launch_ffn_lay(const FfnLay (&l)[3], hipStream_t s) {
     const int dtype = l[0].R ? l[0].dtype : l[1].R ? l[1].dtype : l[2].dtype;
     return dtype == SDM_F32 ? lay<4>(l, s) : dtype == SDM_E4M3 ? lay<1>(l, s) : lay<2>(l, s);
+}
+
+hipError_t launch_ffn_join(const FfnJoin (&j)[2], hipStream_t s) {
+    Joins joins{{j[0], j[1]}, j[0].parts > 1 ? j[0].M * (j[0].ld / 4) : 0};
+    const int64_t all = joins.first + (j[1].parts > 1 ? j[1].M * (j[1].ld / 4) : 0);
+    if (all) ffn_join<<<static_cast<unsigned>((all + 255) / 256), 256, 0, s>>>(joins, all);
+    return hipGetLastError();
 }
 
 hipError_t launch_ffn_grad(const FfnGrad& g, const FfnLay (&l)[3], hipStream_t s) {

@@ -149,7 +149,7 @@ __device__ __forceinline__ void store4(int otype, char* base, int64_t at, int64_
 
 struct Both {
     FfnProduct p[2];
-    int tm[2], tn[2], first;       // tiles of each; workgroups of the first
+    int tm[2], tn[2], first;       // tiles of each, in all parts; workgroups of the first
 };
 
 // Tiles of T x T (as a pair: T rows and T / 2 columns of either product); a wavefront has NM blocks of 32 rows by NN of 32
@@ -169,11 +169,20 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
     const int wm = w % OWNERS / ACROSS, wn = w % ACROSS, mine_half = w / OWNERS;
     int ti, tj;
     tile_of(static_cast<int>(blockIdx.x) - (second ? both.first : 0), both.tm[second], both.tn[second], ti, tj);
+    int part = 0;
+    int64_t bytes = p.bytes, begin = 0;
+    if constexpr (!PAIR) {
+        const int down = both.tm[second] / p.parts;
+        part = ti / down;
+        ti -= part * down;
+        begin = part * p.part;
+        bytes = min(p.part, bytes - begin);
+    }
     constexpr int BR = PAIR ? T / 2 : T;        // rows of a B that the tile takes
     const int64_t m0 = static_cast<int64_t>(ti) * T, n0 = static_cast<int64_t>(tj) * BR;
     auto rows_of = [&](const FfnOperand& o, int64_t first, int64_t all, int most) {
         const int64_t n = min(all - first, static_cast<int64_t>(most));
-        return Buffer{o.p + first * o.ld, static_cast<uint32_t>((n - 1) * o.ld + p.bytes)};
+        return Buffer{o.p + first * o.ld + begin, static_cast<uint32_t>((n - 1) * o.ld + bytes)};
     };
     const Buffer ba = rows_of(p.A, m0, p.M, T), bb = rows_of(p.B, n0, p.N, BR), bc = PAIR ? rows_of(p.B2, n0, p.N, BR) : bb;
 
@@ -190,7 +199,7 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
             off_b[j] = static_cast<uint32_t>(r * p.B.ld) + piece * 16;
     }
     const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)&lds[0][0]));
-    const int steps = static_cast<int>((p.bytes + kStep - 1) / kStep);
+    const int steps = static_cast<int>((bytes + kStep - 1) / kStep);
     // The next step's buffers. Past the last step they are empty, since their bounds less what is behind would wrap around:
     // every load of such a step reads nothing.
     int at = 0;
@@ -203,7 +212,7 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
         ra = from_here(ba);
         rb = from_here(bb);
         rc = PAIR ? from_here(bc) : rb;
-        none = from + piece * 16 >= p.bytes ? kNowhere : 0u;       // the row has ended
+        none = from + piece * 16 >= bytes ? kNowhere : 0u;       // the row has ended
         ++at;
     };
     auto load_a = [&](int place, int j) { load_lds(ra, base + place * PLACE + (j * WAVES + w) * 1024, off_a[j] | none); };
@@ -346,8 +355,9 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
             const f32x4 x = from[0];
             float g[4] = {x[0], x[1], x[2], x[3]};
             if constexpr (!PAIR) {
+                // parts: no second area
                 char* c = m < p.split ? p.c : p.c2;
-                store4(p.otype, c, (m < p.split ? m * p.ldc : (m - p.split) * p.ldc2) + n, left, g);
+                store4(p.otype, c, (m < p.split ? (part * p.M + m) * p.ldc : (m - p.split) * p.ldc2) + n, left, g);
             } else {
                 const f32x4 y = from[WN / 8];
                 float u[4] = {y[0], y[1], y[2], y[3]}, h[4];
@@ -385,7 +395,7 @@ hipError_t run(const FfnProduct* p, int n, hipStream_t s) {
     int64_t total = 0;
     for (int i = 0; i < n; ++i) {
         b.p[i] = p[i];
-        b.tm[i] = static_cast<int>((p[i].M + T - 1) / T);
+        b.tm[i] = static_cast<int>((p[i].M + T - 1) / T) * (PAIR ? 1 : p[i].parts);
         b.tn[i] = static_cast<int>((p[i].N + (PAIR ? T / 2 : T) - 1) / (PAIR ? T / 2 : T));
         total += static_cast<int64_t>(b.tm[i]) * b.tn[i];
         if (i == 0) b.first = static_cast<int>(total);

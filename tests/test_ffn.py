@@ -41,6 +41,14 @@ def test_against_the_definition(ty, act, M, K, F):
     check(*inputs(ty, M, K, F), act)
 
 
+@pytest.mark.parametrize("ty,M,K,F", [("bf16", 3, 200, 5000), ("f32", 40, 130, 4100), ("f16", 5001, 65, 72), ("bf16", 64, 1030, 8200),
+                                      ("f32", 3001, 33, 30)])
+def test_long_sums_of_the_gradient(ty, M, K, F):
+    """Few tiles with long sums: cut into parts that are joined."""
+    say("ffn long", ty, M, K, F)
+    check(*inputs(ty, M, K, F), "silu")
+
+
 @pytest.mark.parametrize("M,K,F", [(1, 2048, 70), (5, 64, 128), (2, 128, 1856), (26, 157, 130), (70, 58, 300)])
 @pytest.mark.parametrize("ty", ["bf16", "f16"])
 def test_gradients_of_few_values(ty, M, K, F):
