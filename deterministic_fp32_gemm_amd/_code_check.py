@@ -24,7 +24,7 @@ MAGIC = b"__CLANG_OFFLOAD_BUNDLE__"
 WAITS = {"v_mfma_f32_16x16x32_bf16": 8, "v_mfma_f32_16x16x4_f32": 10}
 # libsdm_block's beside them (8 passes: 12; 16 passes: 20, of float32 18)
 BLOCK_WAITS = {**WAITS, "v_mfma_f32_16x16x32_f16": 8, "v_mfma_f32_16x16x32_fp8_fp8": 8, "v_mfma_f32_32x32x16_bf16": 12,
-               "v_mfma_f32_32x32x16_f16": 12, "v_mfma_f32_32x32x64_f8f6f4": 20, "v_mfma_f32_32x32x2_f32": 18}
+               "v_mfma_f32_32x32x16_f16": 12, "v_mfma_f32_32x32x64_f8f6f4": 20}
 _STORES = ("ds_", "global_", "buffer_", "scratch_", "flat_")
 
 

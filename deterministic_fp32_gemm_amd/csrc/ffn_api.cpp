@@ -147,8 +147,8 @@ Forward forward_plan(const sdm_ffn_args_t* a, char* ws) {
 int gradient_parts(const sdm_ffn_args_t* a) { return a->dtype != SDM_F32 && a->M * std::min(a->K, a->F) <= 4096 ? 2 : 1; }
 
 // A product of few tiles and a long sum is cut into parts along the sum, up to two workgroups a CU (tiles of 256: one), of 8
-// steps of 128 bytes at the least, where that saves 32 steps: joining them is one more launch, about as long as 8 to 16 steps.
-// bfloat16 training steps in parts and without: 100 rows of 1024 to 8192 73 and 281 us, 64 of 4096 to 8192 199 and 446, 8192 of
+// steps of 128 bytes at the least, where that saves 40 steps: joining them is one more launch (333 rows of 1111 to 777 in
+// float32, 36 steps saved: 80 us in parts and 78 without). bfloat16 training steps in parts and without: 100 rows of 1024 to 8192 73 and 281 us, 64 of 4096 to 8192 199 and 446, 8192 of
 // 64 to 128 36 and 54.
 struct Cut {
     int64_t part;
@@ -159,7 +159,7 @@ Cut cut(int64_t M, int64_t N, int64_t bytes, int tile) {
     const int64_t most = std::min(steps / 8, (tile == 256 ? 256 : 512) / have);
     if (most < 2) return {up_to(bytes, 128), 1};
     const int64_t each = cdiv(steps, most);
-    if (steps - each < 32) return {up_to(bytes, 128), 1};
+    if (steps - each < 40) return {up_to(bytes, 128), 1};
     return {each * 128, static_cast<int>(cdiv(steps, each))};
 }
 
