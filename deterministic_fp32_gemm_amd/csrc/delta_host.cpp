@@ -52,7 +52,7 @@ const char* status_text(int code) {
         case SDM_GX_OK: return "ok";
         case SDM_GX_ERR_NULL: return "a required pointer is NULL";
         case SDM_GX_ERR_SHAPE: return "sizes out of range (see the header's limits)";
-        case SDM_GX_ERR_ALIGN: return "a pointer is not aligned to its elements, or a workspace to 256 (norm: 16) bytes";
+        case SDM_GX_ERR_ALIGN: return "a pointer is not aligned to its elements, or a workspace to 256 (norm, linear recurrence: 16) bytes";
         case SDM_GX_ERR_OVERLAP: return "an output overlaps an input or another output";
         case SDM_GX_ERR_STRIDE: return "stride out of range, or rows of an output that overlap each other";
         case SDM_GX_ERR_LIMIT: return "workspace too small, or the launch exceeds a device limit";

@@ -494,6 +494,7 @@ __global__ __launch_bounds__(256) void glr_clear(const sdm_glr_args_t a, const i
         if (threadIdx.x == 0) longest = 0;
         __syncthreads();
         int l = 0;
+#pragma unroll 8
         for (int64_t r = threadIdx.x; r < a.nseq; r += 256) l = max(l, run_of(a, static_cast<int>(r)).len);
         atomicMax(&longest, l);
         __syncthreads();

@@ -86,6 +86,23 @@ def test_bad_bounds_of_long_runs_stay_inside():
     assert y.shape == t["x"].shape and marks.shape[1] == 12
 
 
+def test_two_calls_at_once():
+    """Each call has its own queue: two at once on two streams, with strides that are not a tensor's own, give what one gives."""
+    base = inputs("bf16", "f32", 2, 6000, 200, "silu")
+    t = {k: v.transpose(0, 1).contiguous().transpose(0, 1) if v is not None and v.dim() == 3 else v for k, v in base.items()}
+    want = run(base, "silu")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        for s in streams:
+            got.append(sdm.glr_forward(t["x"], t["g"], t["z"], act="silu", initial_state=t["h0"], stream=s)[:2])
+    torch.cuda.synchronize()
+    for y, h in got:
+        assert torch.equal(y, want["y"]) and torch.equal(h, want["state"])
+
+
 def test_the_same_bits_from_the_queue():
     t, cu = inputs("bf16", "f32", 1, 9000, 300, "silu", 3), [0, 8000, 8100, 9000]
     want = run(t, "silu", cu)
