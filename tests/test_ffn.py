@@ -244,3 +244,43 @@ def test_a_block_as_it_is_used():
         h8 = sdm.ffn_forward(q, wg, wu, x_scale=sx, gate_scale=sg, up_scale=su)
         ref = ffn(q.flatten(0, 1), wg, wu, "silu", h8.dtype, (sx.flatten(), sg, su))["h"]
         within(h8.flatten(0, 1), *ref, "served")
+
+
+def test_captured():
+    """The recurrence and the product captured forward and backward through torch's graph, replayed on new inputs with eager
+    passes between."""
+    T, D, F = 1500, 72, 104
+
+    def made(seed):
+        gen = torch.Generator().manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+        t = dict(x=r(1, T, D), g=-r(1, T, D).abs(), z=r(1, T, D), h0=r(1, D), wg=r(F, D) * D ** -0.5, wu=r(F, D) * D ** -0.5)
+        dh, ds = r(1, T, F), r(1, D)
+        return {k: v.cuda().requires_grad_() for k, v in t.items()}, dh.cuda(), ds.cuda()
+
+    def both(t, dh, ds):
+        y, s, _ = sdm.glr_forward(t["x"], t["g"], t["z"], act="silu", initial_state=t["h0"])
+        h = sdm.ffn_forward(y, t["wg"], t["wu"], act="gelu")
+        return (h, s, *torch.autograd.grad((h, s), list(t.values()), (dh, ds)))
+
+    sets, buf = [made(i) for i in range(3)], made(0)
+    want = [both(*s) for s in sets]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(*buf)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(*buf)
+    for s, w in list(zip(sets, want)) * 2:
+        with torch.no_grad():
+            for k, v in s[0].items():
+                buf[0][k].copy_(v)
+            buf[1].copy_(s[1])
+            buf[2].copy_(s[2])
+        graph.replay()
+        both(*s)
+        torch.cuda.synchronize()
+        for a, b in zip(got, w):
+            assert torch.equal(a, b)
