@@ -16,20 +16,21 @@ __device__ __forceinline__ float exp_of(float x) {
     return __builtin_fmaf(e, r, e);
 }
 
-// p = 1 / (1 + e^-z) and q = 1 - p = e^-z p, which as a difference would keep nothing of itself from z = 17 on. e^-z is held
-// below 2^116, so that neither is 0 times infinity. FAST: the hardware's exponential and reciprocal (their errors, and 2^-24
-// |z| of the exponent's argument, are far below a rounding to 16 bits), else one more step of Newton's for the reciprocal.
+// p = 1 / (1 + e^-z) and q = 1 - p. With e = e^-|z| they are 1 / (1 + e) and e / (1 + e), in the order of z's sign: as a
+// difference q would keep nothing of itself from z = 17 on, and neither is ever 0 times infinity. FAST: the hardware's
+// exponential and reciprocal (their errors, and 2^-24 |z| of the exponent's argument, are far below a rounding to 16 bits), else
+// one more step of Newton's for the reciprocal. What is below 2^-126 may be zero.
 template <bool FAST>
 __device__ __forceinline__ void sigmoid(float z, float& p, float& q) {
-    float e = FAST ? __builtin_amdgcn_exp2f(-1.44269504f * z) : exp_of(-z);
-    e = z < -80.f ? 5.5406224e34f : e;
-    const float d = 1.f + e;
-    p = __builtin_amdgcn_rcpf(d);
-    if constexpr (!FAST) p = __builtin_fmaf(__builtin_fmaf(-d, p, 1.f), p, p);
-    q = e * p;
+    const float e = FAST ? __builtin_amdgcn_exp2f(-1.44269504f * fabsf(z)) : exp_of(-fabsf(z)), d = 1.f + e;
+    float large = __builtin_amdgcn_rcpf(d);
+    if constexpr (!FAST) large = __builtin_fmaf(__builtin_fmaf(-d, large, 1.f), large, large);
+    const float small = e * large;
+    p = z < 0.f ? small : large;
+    q = z < 0.f ? large : small;
 }
 
-// act(z) and act'(z). At z = -inf z p is NaN as the formula has it.
+// act(z) and act'(z). Far below zero z p and its derivative are zero, since p is; at z = -inf they are NaN, -inf times 0.
 template <bool FAST>
 __device__ __forceinline__ void gate(float z, int act, float& a, float& d) {
     if (act == SDM_ACT_NONE) {
