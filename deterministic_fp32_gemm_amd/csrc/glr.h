@@ -26,7 +26,7 @@ __host__ __device__ inline bool glr_walks(int64_t longest, int64_t tickets) { re
 // and channel.
 inline int64_t glr_chain_words(const GlrPlan& p) { return p.rows ? 64 + p.rows * p.cblocks * 128 : 0; }
 
-// ws: forward: glr_chain_words; backward: float [nseq][segs][2][D], what each part makes of what enters it (segs > 1)
+// ws: forward: glr_chain_words; backward: float [nseq][segs][3][D], what each part makes of what enters it (segs > 1)
 hipError_t launch_glr_forward(const sdm_glr_args_t& a, const GlrPlan& p, void* ws, hipStream_t stream);
 hipError_t launch_glr_backward(const sdm_glr_args_t& a, const GlrPlan& p, void* ws, hipStream_t stream);
 hipError_t launch_glr_step(const sdm_glr_step_args_t& a, hipStream_t stream);

@@ -121,7 +121,7 @@ GlrPlan plan(const sdm_glr_args_t* a, bool packed, bool backward) {
 }
 int64_t workspace(const sdm_glr_args_t* a, bool packed, bool backward) {
     const GlrPlan p = plan(a, packed, backward);
-    return backward ? (p.segs > 1 ? a->nseq * p.segs * 2 * a->D * 4 : 0) : glr_chain_words(p) * 8;
+    return backward ? (p.segs > 1 ? a->nseq * p.segs * 3 * a->D * 4 : 0) : glr_chain_words(p) * 8;
 }
 
 int run(const sdm_glr_args_t* a, bool backward, void* ws, int64_t ws_bytes, void* stream) {

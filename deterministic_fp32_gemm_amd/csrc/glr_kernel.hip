@@ -3,7 +3,8 @@
 //     h_t = a_t h_{t-1} + x_t,  a_t = exp(g_t);   y_t = h_t act(z_t)
 //
 // What bounds it is memory: x, g and z are read and y written once. A stretch of tokens maps the state that enters it as
-// h -> A h + H, and two stretches after one another as A = A2 A1, H = A2 H1 + H2. A workgroup owns 64 channels (a lane
+// h -> A h + H, and two stretches after one another as A = A2 A1, H = A2 H1 + H2 (A with its exponent apart: where gates grow and
+// fall it may leave float32 though no state does). A workgroup owns 64 channels (a lane
 // each) of one run and walks it in tiles of 128 tokens: each of 8 wavefronts holds 16 of them in registers, finds its (A,
 // H), and after one barrier each composes the maps before it, in order, and runs its own tokens from the state that enters.
 // The next tile's loads are in flight meanwhile. The gradient walks the tiles from the last to the first: the states come
@@ -60,8 +61,41 @@ template <class T>
 __device__ __forceinline__ Rows<T> rows_of(const sdm_seq_t& s, const Run& r) {
     return Rows<T>{static_cast<T*>(s.data) + r.row * s.batch + r.start * s.token, s.token};
 }
-// A h + H; from no state nothing comes, also where a growing A has left float32.
-__device__ __forceinline__ float enter(float A, float H, float h) { return h == 0.f ? H : __builtin_fmaf(A, h, H); }
+// A stretch's A, m 2^x: a product of decays that grow and fall may leave float32 where no state does. m is in [1, 2), so
+// that 2^x h stays below the product and rounds only where that does, or 0 with x 0.
+struct Decay {
+    float m;
+    int x;
+};
+constexpr int kFar = 1 << 20;       // exponents past it mean the same
+__device__ __forceinline__ Decay decay(float m, int x) {
+    x = min(max(x + __builtin_amdgcn_frexp_expf(m) - 1, -kFar), kFar);
+    return Decay{2.f * __builtin_amdgcn_frexp_mantf(m), m == 0.f ? 0 : x};
+}
+// A h + H; from no state nothing comes, also where A has left float32.
+__device__ __forceinline__ float enter(const Decay& A, float H, float h) { return h == 0.f ? H : __builtin_fmaf(A.m, __builtin_amdgcn_ldexpf(h, A.x), H); }
+// The product of a wavefront's decays, from their plain product and the largest. Where none is above 1 and the product is far
+// from float32's smallest, no product on the way has lost anything; elsewhere it is made again, with its exponent apart.
+__device__ __forceinline__ Decay product(const float (&e)[KT], float plain, float top) {
+    int x = 0;
+    if (__builtin_expect(!__all(top <= 1.f && plain >= 0x1p-100f), 0)) {
+        plain = 1.f;
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            plain *= e[k];
+            x += __builtin_amdgcn_frexp_expf(plain);
+            plain = __builtin_amdgcn_frexp_mantf(plain);
+        }
+    }
+    return decay(plain, x);
+}
+// A map in LDS: m, H, x
+__device__ __forceinline__ void keep(float (&ex)[3][64], int lane, const Decay& A, float H) {
+    ex[0][lane] = A.m;
+    ex[1][lane] = H;
+    ex[2][lane] = __int_as_float(A.x);
+}
+__device__ __forceinline__ Decay kept(const float (&ex)[3][64], int lane) { return Decay{ex[0][lane], __float_as_int(ex[2][lane])}; }
 
 // A lane's element of a row: the row's address is the wavefront's, the byte offset the lane's.
 template <class T>
@@ -101,7 +135,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
     using T = elem_t<DT>;
     using G = elem_t<GT>;
     constexpr bool Z = ACT != SDM_ACT_NONE;
-    __shared__ float ex[NW][2][64];
+    __shared__ float ex[NW][3][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cb = blockIdx.x % cblocks, rs = blockIdx.x / cblocks, seg = rs % segs, run = rs / segs;
     const Run r = run_of(a, run);
@@ -111,7 +145,8 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
     if (s0 >= r.len) return;                                        // never asked for
     const int t0 = static_cast<int>(s0), t1 = min(r.len, t0 + seglen), each = seglen / NW;     // a multiple of KT
     const int lo = t0 + w * each, hi = min(t1, lo + each);
-    float A = 1.f, H = 0.f;
+    Decay A{1.f, 0};
+    float H = 0.f;
     T dy[KT], z[KT];
     G g[KT];
     const Rows<T> dys = rows_of<T>(a.dy, r), zs = rows_of<T>(a.z, r);
@@ -136,15 +171,17 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
             }
         }
         if (next >= 0) load(std::true_type{}, next);
-        float P = 1.f, h = 0.f;
+        float P = 1.f, top = 0.f, h = 0.f;
 #pragma unroll
         for (int k = KT - 1; k >= 0; --k) {
             h = e[k] * (u[k] + h);
             P *= e[k];
+            top = fmaxf(top, e[k]);
         }
         // the new stretch is to the right of those before it
         H = enter(A, H, h);
-        A *= P;
+        const Decay right = product(e, P, top);
+        A = decay(A.m * right.m, A.x + right.x);
     };
     // the wavefront's last block may not be whole
     const int whole = hi > lo ? (hi - lo) / KT : 0;
@@ -154,20 +191,21 @@ __global__ __launch_bounds__(kGlrThreads) void glr_parts(const sdm_glr_args_t a,
         load(std::false_type{}, lo + whole * KT);
         work(std::false_type{}, lo + whole * KT, -1);
     }
-    ex[w][0][lane] = A;
-    ex[w][1][lane] = H;
+    keep(ex[w], lane, A, H);
     __syncthreads();
     if (w == 0 && c < D) {
-        A = 1.f;
+        A = Decay{1.f, 0};
         H = 0.f;
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
+            const Decay right = kept(ex[i], lane);
             H = enter(A, H, ex[i][1][lane]);
-            A *= ex[i][0][lane];
+            A = decay(A.m * right.m, A.x + right.x);
         }
-        float* p = part + (static_cast<int64_t>(run) * segs + seg) * 2 * a.D + c;
-        p[0] = A;
+        float* p = part + (static_cast<int64_t>(run) * segs + seg) * 3 * a.D + c;
+        p[0] = A.m;
         p[a.D] = H;
+        p[2 * a.D] = __int_as_float(A.x);
     }
 }
 
@@ -176,7 +214,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
     using T = elem_t<DT>;
     using G = elem_t<GT>;
     constexpr bool Z = ACT != SDM_ACT_NONE;
-    __shared__ float ex[2][NW][2][64];
+    __shared__ float ex[2][NW][3][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (words && words[1] == 0) return;        // the queue's
     const int cb = blockIdx.x % cblocks, run = blockIdx.x / cblocks;
@@ -200,7 +238,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
         const int t = tile + w * KT;
         float e[KT], u[KT];
         T zz[KT];
-        float A = 1.f, H = 0.f;
+        float A = 1.f, top = 0.f, H = 0.f;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
             const bool in = whole.value || t + k < r.len;
@@ -208,17 +246,17 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
             u[k] = in ? static_cast<float>(x[k]) : 0.f;
             H = __builtin_fmaf(e[k], H, u[k]);
             A *= e[k];
+            top = fmaxf(top, e[k]);
             if constexpr (Z) zz[k] = z[k];
         }
         if (whole.value && tile + TILE < end) load(std::true_type{}, t + TILE);
-        ex[buf][w][0][lane] = A;
-        ex[buf][w][1][lane] = H;
+        keep(ex[buf][w], lane, product(e, A, top), H);
         lds_barrier();      // the other buffer is written again only after the next one
         float h = h0, next = h0;
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
             h = i == w ? next : h;
-            next = enter(ex[buf][i][0][lane], ex[buf][i][1][lane], next);
+            next = enter(kept(ex[buf][i], lane), ex[buf][i][1][lane], next);
         }
         if (w == 0 && a.marks && c < D) a.marks[(r.mark + tile / TILE) * a.D + c] = h0;
         h0 = next;
@@ -257,8 +295,8 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
 // unended: a ticket waits for lower ones only, which running workgroups hold, each of which publishes whatever its tile is;
 // after some seconds of waiting, which nothing but a fault explains, a tile goes on with NaN.
 //
-// One run of 16384 tokens and 4096 channels, bfloat16 with float32 g and z: 155 us, 4.3 TB/s (walking it in four parts, whose
-// maps a kernel before has to find: 215). A tile takes its workgroup 4.7 us, of which the exponentials and the last walk are
+// One run of 16384 tokens and 4096 channels, bfloat16 with float32 g and z: 162 us, 4.1 TB/s (walking it in four parts, whose
+// maps a kernel before has to find: 215). A tile takes its workgroup 4.9 us, of which the exponentials and the last walk are
 // half and the join the rest; the loads are hidden.
 constexpr int kGroup = 8;
 constexpr int kPolls = 1 << 22;
@@ -269,8 +307,24 @@ struct Ticket {
     int state;                      // 0: no more; 1: a row of marks that has no tile; 2: a tile
 };
 
-// a map's A is never below zero: its sign marks that the word is there
-__device__ __forceinline__ uint64_t map_word(float A, float H) { return static_cast<uint64_t>(__float_as_uint(A) | 0x80000000u) << 32 | __float_as_uint(H); }
+// A map's word: a bit that says that it is there, 31 for A and 32 for H. Of A in [2^-126, 2) or zero, which is any product of
+// decays but the smallest, they are its own bits, the first of which is clear. Where it is set, 10 of the others are an exponent
+// and 20 a fraction rounded to 2^-21: what a state brings through a tile that all but forgets it, or multiplies it. Below 2^-511
+// no float32 leaves anything, from 2^511 on every one becomes infinite; where A itself is not finite, H is not either.
+__device__ __forceinline__ uint64_t map_word(const Decay& A, float H) {
+    const bool there = A.m < 2.f;
+    const int x = there ? min(A.x, 511) : 511;
+    uint32_t c = __float_as_uint(__builtin_amdgcn_ldexpf(A.m, A.x));
+    if (x > 0 || x < -126)
+        c = x < -511 ? 0u : 0x40000000u + (static_cast<uint32_t>(x + 512) << 20) + min(((__float_as_uint(there ? A.m : 1.f) + 4u) >> 3) - (0x3f800000u >> 3), x == 511 ? 0u : 0x100000u);
+    return static_cast<uint64_t>(c | 0x80000000u) << 32 | __float_as_uint(H);
+}
+__device__ __forceinline__ float enter(uint64_t word, float h) {
+    const uint32_t c = static_cast<uint32_t>(word >> 32);
+    const bool far = c >> 30 & 1;
+    const Decay A{__uint_as_float(far ? 0x3f800000u | (c & 0xfffffu) << 3 : c & 0x7fffffffu), far ? static_cast<int>(c >> 20 & 0x3ff) - 512 : 0};
+    return enter(A, __uint_as_float(static_cast<uint32_t>(word)), h);
+}
 __device__ __forceinline__ uint64_t state_word(float h) { return uint64_t(1) << 63 | __float_as_uint(h); }
 __device__ __forceinline__ void publish(uint64_t* p, uint64_t v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ uint64_t look(const uint64_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
@@ -318,7 +372,7 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
     using T = elem_t<DT>;
     using G = elem_t<GT>;
     constexpr bool Z = ACT != SDM_ACT_NONE;
-    __shared__ float ex[NW][2][64], entering[64];
+    __shared__ float ex[NW][3][64], entering[64];
     __shared__ int tickets[2][sizeof(Ticket) / 4];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = static_cast<int>(a.D);
     // the first words: the queue's counter, whether runs are walked; then, of each tile, 64 maps and 64 states
@@ -358,13 +412,18 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
             float h = group == 0 && a.h0 && t.state == 2 ? a.h0[at] : 0.f;
             take(slot ^ 1);
             lds_barrier();                                      // the tile's maps, the next ticket
-            float A = 1.f, H = 0.f;
+            Decay A{1.f, 0};
+            float H = 0.f;
             if (t.state == 2) {
+                // eight factors below 2
 #pragma unroll
                 for (int i = 0; i < NW; ++i) {
-                    H = enter(ex[i][0][lane], ex[i][1][lane], H);
-                    A *= ex[i][0][lane];
+                    const Decay next = kept(ex[i], lane);
+                    H = enter(next, ex[i][1][lane], H);
+                    A.m *= next.m;
+                    A.x += next.x;
                 }
+                A = decay(A.m, A.x);
             }
             uint64_t* own = words_of(t.mark, t.cb);
             publish(own, map_word(A, H));
@@ -387,7 +446,7 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
                 h = __uint_as_float(static_cast<uint32_t>(s));
 #pragma unroll
                 for (int i = 0; i < kGroup - 1; ++i)
-                    if (i < before) h = enter(__uint_as_float(static_cast<uint32_t>(m[i] >> 32) & 0x7fffffffu), __uint_as_float(static_cast<uint32_t>(m[i])), h);
+                    if (i < before) h = enter(m[i], h);
                 if (missing) h = __uint_as_float(0x7fc00000u);
             }
             const float after = enter(A, H, h);
@@ -418,7 +477,7 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
     };
     auto work = [&](auto whole, const Ticket& t, int slot) __attribute__((always_inline)) {
         const int first = t.tile * TILE + w * KT, c = t.cb * 64 + lane;
-        float e[KT], u[KT], f[KT], A = 1.f, H = 0.f;
+        float e[KT], u[KT], f[KT], A = 1.f, top = 0.f, H = 0.f;
         T zz[KT];
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
@@ -427,10 +486,10 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
             u[k] = in ? static_cast<float>(x[k]) : 0.f;
             H = __builtin_fmaf(e[k], H, u[k]);
             A *= e[k];
+            top = fmaxf(top, e[k]);
             if constexpr (Z) zz[k] = z[k];
         }
-        ex[w][0][lane] = A;
-        ex[w][1][lane] = H;
+        keep(ex[w], lane, product(e, A, top), H);
         lds_barrier();
         const Ticket next = ticket(slot ^ 1);
         if (whole_tile(next)) load(std::true_type{}, next);
@@ -447,7 +506,7 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
         float h = entering[lane];
 #pragma unroll
         for (int i = 0; i < NW - 1; ++i)
-            if (i < w) h = enter(ex[i][0][lane], ex[i][1][lane], h);
+            if (i < w) h = enter(kept(ex[i], lane), ex[i][1][lane], h);
         lds_barrier();      // before the next tile's maps
         if (c >= D) return;
         Run r;
@@ -508,7 +567,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_backward(const sdm_glr_args_t
     using T = elem_t<DT>;
     using G = elem_t<GT>;
     constexpr bool Z = ACT != SDM_ACT_NONE;
-    __shared__ float ex[2][NW][3][64];
+    __shared__ float ex[2][NW][3][64], ends[2][NW][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cb = blockIdx.x % cblocks, rs = blockIdx.x / cblocks, seg = rs % segs, run = rs / segs;
     const Run r = run_of(a, run);
@@ -541,14 +600,14 @@ __global__ __launch_bounds__(kGlrThreads) void glr_backward(const sdm_glr_args_t
         load(std::true_type{}, end - TILE);
     const int used = (r.len - 1) / seglen;      // the last part that has tokens
     for (int s = used; s > seg; --s) {
-        const float* p = part + (static_cast<int64_t>(run) * segs + s) * 2 * a.D + cc;
-        e0 = enter(p[0], p[a.D], e0);
+        const float* p = part + (static_cast<int64_t>(run) * segs + s) * 3 * a.D + cc;
+        e0 = enter(Decay{p[0], __float_as_int(p[2 * a.D])}, p[a.D], e0);
     }
     int buf = 0;
     auto work = [&](auto whole, int tile) __attribute__((always_inline)) {
         const int t = tile + w * KT;
         float e[KT], u[KT], f[KT], v[KT], df[KT];     // a, x, dy act(z), and dy act'(z)
-        float A = 1.f, H = 0.f, E = 0.f;
+        float A = 1.f, top = 0.f, H = 0.f, E = 0.f;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
             const bool in = whole.value || t + k < t1;
@@ -564,23 +623,23 @@ __global__ __launch_bounds__(kGlrThreads) void glr_backward(const sdm_glr_args_t
             }
             H = __builtin_fmaf(e[k], H, u[k]);
             A *= e[k];
+            top = fmaxf(top, e[k]);
         }
 #pragma unroll
         for (int k = KT - 1; k >= 0; --k) E = e[k] * (f[k] + E);
         float h = m;
         if (tile > t0) load(std::true_type{}, tile - TILE);
-        ex[buf][w][0][lane] = A;
-        ex[buf][w][1][lane] = H;
-        ex[buf][w][2][lane] = E;
+        keep(ex[buf][w], lane, product(e, A, top), H);
+        ends[buf][w][lane] = E;
         lds_barrier();      // the other buffer is written again only after the next one
 #pragma unroll
         for (int i = 0; i < NW - 1; ++i)
-            if (i < w) h = enter(ex[buf][i][0][lane], ex[buf][i][1][lane], h);
+            if (i < w) h = enter(kept(ex[buf][i], lane), ex[buf][i][1][lane], h);
         float q = e0, next = e0;
 #pragma unroll
         for (int i = NW - 1; i >= 0; --i) {
             q = i == w ? next : q;
-            next = enter(ex[buf][i][0][lane], ex[buf][i][2][lane], next);
+            next = enter(kept(ex[buf][i], lane), ends[buf][i][lane], next);
         }
         e0 = next;
         if (c >= D) return;

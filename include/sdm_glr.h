@@ -19,6 +19,7 @@
  * Types. x, y, z and their gradients are float32, bfloat16 or float16 (dtype); g and dg that or float32 (gtype); states
  * float32, and so is every sum. No atomics in sums and an order of operations set by the sizes and the sequences' lengths: the
  * same bits in every run.
+ * Gates may grow (g > 0) and fall as far as the states stay in float32: products of decays over many tokens need not.
  * Values that are not finite stay in their channel and sequence; what they make of later tokens is not finite or NaN.
  *
  * Memory. sdm_seq_t: element (b, t, c) is data[b*batch + t*token + c], strides in elements; token strides below 2^31, any
