@@ -285,20 +285,22 @@ __global__ __launch_bounds__(kGlrThreads) void glr_forward(const sdm_glr_args_t 
 // Tiles from a queue. Workgroups take tickets in order: which tile is which ticket's follows from the sizes and bounds alone, so
 // who takes it does not change a bit of the result. Beside the eight wavefronts that hold the tile, a ninth takes the tickets and
 // joins the tile to those before it in its run. When the eight have found the tile's map it publishes it, waits for the state
-// after the last tile of the group of 8 before and for the maps of the tiles of its own group before it, composes them in
+// after the last tile of the group before and for the maps of the tiles of its own group before it, composes them in
 // order, publishes the state after its tile and hands the eight the one that enters. They load the next tile and find this
-// one's gates meanwhile. A run's states thus pass from group to group, and maps within one. (Groups of 4 took 149 us where 8
-// take 155, and 46 where 8 take 45; 16: 172 and 43. Two workgroups a CU without loads ahead took 184.)
+// one's gates meanwhile. A run's states thus pass from group to group, and maps within one. Groups are of 4 tiles, or of 8 where
+// few runs and channels leave a tile little but waiting (bfloat16, groups of 2, 4 and 8: 16384 tokens of 4096 channels 150, 154
+// and 162 us; 2 x 4096 of 4096 79, 81 and 85; one run of 6784 and 22 of 64, 2048 channels, 70, 70 and 71; 3 packed of 3000, 1024
+// channels, 45, 42 and 43; 32768 tokens of 512 91, 65 and 59). Two workgroups a CU without loads ahead took 184 for the first.
 //
 // What is published goes as words of 8 bytes, a map or a state, with a bit that says that it is there, by relaxed atomics of
 // device scope: a word is there or not, and needs no order with others. All words are cleared by a kernel before. No wait goes
 // unended: a ticket waits for lower ones only, which running workgroups hold, each of which publishes whatever its tile is;
 // after some seconds of waiting, which nothing but a fault explains, a tile goes on with NaN.
 //
-// One run of 16384 tokens and 4096 channels, bfloat16 with float32 g and z: 162 us, 4.1 TB/s (walking it in four parts, whose
-// maps a kernel before has to find: 215). A tile takes its workgroup 4.9 us, of which the exponentials and the last walk are
+// One run of 16384 tokens and 4096 channels, bfloat16 with float32 g and z: 156 us, 4.3 TB/s (walking it in four parts, whose
+// maps a kernel before has to find: 215). A tile takes its workgroup 4.7 us, of which the exponentials and the last walk are
 // half and the join the rest; the loads are hidden.
-constexpr int kGroup = 8;
+constexpr int kGroup = 8;       // at the most
 constexpr int kPolls = 1 << 22;
 
 struct Ticket {
@@ -368,7 +370,7 @@ __device__ __forceinline__ Ticket ticket_of(const sdm_glr_args_t& a, int64_t id,
 }
 
 template <int DT, int GT, int ACT>
-__global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args_t a, const int cblocks, const int64_t rows, uint64_t* __restrict__ words) {
+__global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args_t a, const int cblocks, const int64_t rows, const int groups, uint64_t* __restrict__ words) {
     using T = elem_t<DT>;
     using G = elem_t<GT>;
     constexpr bool Z = ACT != SDM_ACT_NONE;
@@ -408,7 +410,7 @@ __global__ __launch_bounds__(kGlrChainThreads) void glr_chain(const sdm_glr_args
             if (t.state == 0) break;
             const int c = t.cb * 64 + lane, cc = min(c, D - 1);
             const int64_t at = static_cast<int64_t>(t.run) * D + cc;
-            const int group = t.tile - t.tile % kGroup;
+            const int group = t.tile & -groups;
             float h = group == 0 && a.h0 && t.state == 2 ? a.h0[at] : 0.f;
             take(slot ^ 1);
             lds_barrier();                                      // the tile's maps, the next ticket
@@ -704,7 +706,7 @@ hipError_t forward_of(const sdm_glr_args_t& a, const GlrPlan& p, void* ws, hipSt
         glr_clear<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(a, p.cblocks, p.rows, static_cast<u32x4*>(ws), n);
         const int64_t tickets = p.rows * p.cblocks;
         glr_chain<DT, GT, ACT><<<static_cast<unsigned>(tickets < kGlrChainGroups ? tickets : kGlrChainGroups), kGlrChainThreads, 0, s>>>(
-            a, p.cblocks, p.rows, static_cast<uint64_t*>(ws));
+            a, p.cblocks, p.rows, a.nseq * p.cblocks <= 8 ? 8 : 4, static_cast<uint64_t*>(ws));
     }
     if (!p.rows || a.cu_seqlens)
         glr_forward<DT, GT, ACT><<<static_cast<unsigned>(a.nseq * p.cblocks), kGlrThreads, 0, s>>>(
