@@ -135,10 +135,13 @@ int run(const sdm_glr_args_t* a, bool backward, void* ws, int64_t ws_bytes, void
     const GlrPlan p = plan(a, packed, backward);
     if (a->nseq * p.segs * p.cblocks * kGlrThreads >= kMaxThreads || glr_chain_words(p) / 2 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     if ((st = current_gfx950(&dev))) return st;
-    const void* ps[] = {a->x.data, a->g.data, a->act ? a->z.data : nullptr, a->cu_seqlens, a->h0, a->marks, need ? ws : nullptr,
-                        backward ? a->dy.data : a->y.data, backward ? a->dh_final : a->h_final, backward ? a->dx.data : nullptr,
-                        backward ? a->dg.data : nullptr, backward && a->act ? a->dz.data : nullptr, backward ? a->dh0 : nullptr};
-    for (const void* q : ps)
+    // without tokens the kernels still read and write the states
+    const void* always[] = {a->cu_seqlens, need ? ws : nullptr, backward ? a->dh_final : a->h0, backward ? a->dh0 : a->h_final};
+    for (const void* q : always)
+        if (q && (st = pointer_on(q, dev))) return st;
+    const void* tokens[] = {a->x.data, a->g.data, a->act ? a->z.data : nullptr, a->marks, backward ? a->dy.data : a->y.data, backward ? a->h0 : nullptr,
+                            backward ? a->dx.data : nullptr, backward ? a->dg.data : nullptr, backward && a->act ? a->dz.data : nullptr};
+    for (const void* q : tokens)
         if (q && a->T && (st = pointer_on(q, dev))) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = backward ? launch_glr_backward(*a, p, ws, s) : launch_glr_forward(*a, p, ws, s);
