@@ -9,7 +9,7 @@ other path. A wrong argument raises TypeError or ValueError before anything runs
 Where grad mode is on and a tensor of the call requires a gradient, glr_forward and ffn_forward are part of torch's graph
 (_block_autograd.py), and a backward pass that reaches glr_step, norm_quant, quant_rows or a feed-forward product of 8-bit
 operands, which have no gradient, is an error. The gradients that glr_backward and ffn_backward return have no graph of
-their own.
+their own. There are no forward-mode derivatives: a tensor that carries a tangent is an error.
 """
 
 from __future__ import annotations
@@ -21,8 +21,8 @@ import threading
 from . import delta
 from ._binding import SDM_GX_ERR_HIP, SDM_GX_OK
 from ._build import BLOCK_LIB_PATH
-from .delta import (SDM_BF16, SDM_F16, SDM_F32, _ARG_ERRORS, _dtype, _flat, _inner, _layout, _ld, _Plans, _ptr,
-                    _requires_grad, _tensor, _under, _workspace)
+from .delta import (SDM_BF16, SDM_F16, SDM_F32, _ARG_ERRORS, _dtype, _flat, _inner, _layout, _ld, _no_tangents, _Plans,
+                    _ptr, _requires_grad, _tensor, _under, _workspace)
 
 SDM_E4M3 = 3
 GATES = {"none": 0, "sigmoid": 1, "silu": 2}
@@ -252,6 +252,7 @@ def glr_forward(x, g, z=None, *, act="none", initial_state=None, cu_seqlens=None
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _glr_plan(False, x, g, z, act, initial_state, cu_seqlens))
+    _no_tangents("glr_forward", x, g, z, initial_state)
     kept, n, whole, marks, states, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
@@ -282,6 +283,7 @@ def glr_backward(x, g, z, dy, marks, *, act="none", initial_state=None, dfinal_s
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _glr_plan(True, x, g, z, act, initial_state, cu_seqlens, dy, dfinal_state, marks))
+    _no_tangents("glr_backward", x, g, z, dy, marks, initial_state, dfinal_state)
     kept, n, whole, _, states, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
@@ -317,6 +319,7 @@ def glr_step(x, g, z, state, *, act="none", slots=None, stream=None):
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _glr_step_plan(x, g, z, state, act, slots))
+    _no_tangents("glr_step", x, g, z, state)
     kept, whole, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
@@ -392,6 +395,7 @@ def _qnt(what, x, r, w, eps, stream):
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _qnt_plan(what, x, r, w, eps))
+    _no_tangents(what, x, r, w)
     kept, whole, by_row, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
@@ -502,6 +506,7 @@ def ffn_forward(x, w_gate, w_up, *, act="silu", keep=False, x_scale=None, gate_s
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _ffn_plan(x, w_gate, w_up, act, scales, dtype))
+    _no_tangents("ffn_forward", x, w_gate, w_up, *scales)
     struct, whole, otype, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
@@ -544,6 +549,7 @@ def ffn_backward(dh, x, w_gate, w_up, kept, *, act="silu", stream=None):
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _ffn_plan(x, w_gate, w_up, act, (None,) * 3, None, dh, kept))
+    _no_tangents("ffn_backward", dh, x, w_gate, w_up, *kept)
     struct, _, otype, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):

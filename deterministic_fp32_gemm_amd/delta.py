@@ -8,7 +8,8 @@ stream's, and tensors made on another stream are the caller's to order and keep 
 
 Where grad mode is on and a tensor of the call requires a gradient, gdr_forward and norm_forward are part of torch's graph
 (_delta_autograd.py), and a backward pass that reaches gdr_step, which has no gradient, is an error. The gradients that
-gdr_backward and norm_backward return have no graph of their own.
+gdr_backward and norm_backward return have no graph of their own. There are no forward-mode derivatives: a tensor that carries
+a tangent is an error.
 """
 
 from __future__ import annotations
@@ -251,6 +252,18 @@ def _requires_grad(*tensors) -> bool:
     return False
 
 
+def _no_tangents(what, *tensors):
+    """Refuses a tensor that carries a tangent of torch's forward mode, which the outputs would lose in silence (such a tensor
+    need not require a gradient)."""
+    import torch
+    forward = torch.autograd.forward_ad
+    if getattr(forward, "_current_level", 0) < 0:       # outside of every dual_level: no tensor has one
+        return
+    for t in tensors:
+        if t is not None and forward.unpack_dual(t).tangent is not None:
+            raise RuntimeError(f"{what} has no forward-mode derivative: call it on the primal tensors")
+
+
 def _scale(scale):
     """scale as a number, also where a tensor holds it; none that torch would differentiate."""
     if scale is None or type(scale) is float:
@@ -357,6 +370,7 @@ def gdr_forward(q, k, v, g, beta, *, scale=None, initial_state=None, final_state
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _gdr_plan(False, q, k, v, g, beta, scale, initial_state, cu_seqlens, None, None))
+    _no_tangents("gdr_forward", q, k, v, g, beta, initial_state)
     kept, n, state, dev, _ = plan
     if stream is not None:
         with _under(stream, dev):
@@ -395,6 +409,7 @@ def gdr_backward(q, k, v, g, beta, do, *, scale=None, initial_state=None, dfinal
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _gdr_plan(True, q, k, v, g, beta, scale, initial_state, cu_seqlens, do, dfinal_state))
+    _no_tangents("gdr_backward", q, k, v, g, beta, do, initial_state, dfinal_state)
     kept, n, state, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
@@ -436,6 +451,7 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, out=None, strea
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _step_plan(q, k, v, g, beta, state, slots, scale, out))
+    _no_tangents("gdr_step", q, k, v, g, beta, state, out)
     kept, shape, dtype, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
@@ -583,6 +599,7 @@ def norm_forward(x, o, z, w_post, w_pre, scale, *, act="silu", eps=1e-6, stream=
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _norm_plan(False, x, o, z, w_post, w_pre, scale, act, eps))
+    _no_tangents("norm_forward", x, o, z, w_post, w_pre, scale)
     kept, _, rows, D, dev, _, copied, shape, dtype = plan
     if stream is not None:
         with _under(stream, dev):
@@ -620,6 +637,7 @@ def norm_backward(dx_new, dy, x_new, o, z, w_post, w_pre, scale, rstd, *, act="s
     plan = _plans.get(key)
     if plan is None:
         plan = _plans.put(key, _norm_plan(True, dx_new, o, z, w_post, w_pre, scale, act, 0.0, dy, x_new, rstd))
+    _no_tangents("norm_backward", dx_new, dy, x_new, o, z, w_post, w_pre, scale, rstd)
     kept, n, rows, D, dev, wd, copied, shape, dtype = plan
     if stream is not None:
         with _under(stream, dev):
