@@ -110,13 +110,17 @@ int check(const sdm_glr_args_t* a, bool backward) {
 
 // Backward: runs are cut until there is a workgroup a CU, into parts of 512 tokens at the least: a part's map costs another
 // reading of its inputs. Forward: the queue where it is faster than one workgroup a run and 64 channels; of packed runs the GPU
-// finds out, but where none can have more than 4 tiles.
+// finds out, but where a run of all tokens would be walked. So the queue's words, 1 KB a tile and 64 channels, stay below 1.3 KB a
+// token however many runs there are (4096 runs in 16384 tokens of 4096 channels would have 277 MB of them). More than a launch
+// clears: walked.
 GlrPlan plan(const sdm_glr_args_t* a, bool packed, bool backward) {
     GlrPlan p{};
     p.cblocks = static_cast<int>(cdiv(a->D, 64));
     const int64_t have = a->nseq * p.cblocks, each = cdiv(a->T * a->B, a->nseq), tiles = cdiv(a->T, SDM_GLR_TILE);
     p.segs = backward ? static_cast<int>(std::max<int64_t>(1, std::min(256 / have, each / 512))) : 1;
-    if (!backward && (packed ? tiles > 4 : !glr_walks(tiles, tiles * have))) p.rows = mark_rows(a, packed);
+    const int64_t rows = mark_rows(a, packed);
+    if (!backward && !(packed && tiles <= 4) && !glr_walks(tiles, rows * p.cblocks)) p.rows = rows;
+    if (glr_chain_words(p) / 2 >= kMaxThreads) p.rows = 0;
     return p;
 }
 int64_t workspace(const sdm_glr_args_t* a, bool packed, bool backward) {
@@ -133,7 +137,7 @@ int run(const sdm_glr_args_t* a, bool backward, void* ws, int64_t ws_bytes, void
     if (!aligned(ws, 16)) return SDM_GX_ERR_ALIGN;
     if (ws_bytes < need) return SDM_GX_ERR_LIMIT;
     const GlrPlan p = plan(a, packed, backward);
-    if (a->nseq * p.segs * p.cblocks * kGlrThreads >= kMaxThreads || glr_chain_words(p) / 2 >= kMaxThreads) return SDM_GX_ERR_LIMIT;
+    if (a->nseq * p.segs * p.cblocks * kGlrThreads >= kMaxThreads) return SDM_GX_ERR_LIMIT;
     if ((st = current_gfx950(&dev))) return st;
     // without tokens the kernels still read and write the states
     const void* always[] = {a->cu_seqlens, need ? ws : nullptr, backward ? a->dh_final : a->h0, backward ? a->dh0 : a->h_final};

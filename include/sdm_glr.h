@@ -80,7 +80,8 @@ SDM_GX_API int sdm_glr_check(const sdm_glr_args_t* args, int32_t backward);
 SDM_GX_API int sdm_glr_step_check(const sdm_glr_step_args_t* args);
 
 /* Rows of `marks`, and workspace bytes of a forward (backward = 0) or backward call: at least 0, or a negative status.
- * They depend on the sizes and on whether cu_seqlens is NULL. */
+ * They depend on the sizes and on whether cu_seqlens is NULL. Calls of 2^23 workgroups or more (runs times D / 64, rounded up)
+ * are refused. */
 SDM_GX_API int64_t sdm_glr_marks(const sdm_glr_args_t* args);
 SDM_GX_API int64_t sdm_glr_workspace(const sdm_glr_args_t* args, int32_t backward);
 
