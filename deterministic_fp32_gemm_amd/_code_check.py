@@ -125,6 +125,28 @@ def early_reads(code, waits=WAITS) -> list:
     return bad
 
 
+# what reads m0 without naming it, beside loads into LDS
+_M0_READERS = ("v_movrel", "s_movrel", "s_sendmsg", "s_set_gpr_idx", "v_interp", "ds_gws", "ds_ordered", "ds_append", "ds_consume")
+
+
+def m0_uses(code) -> list:
+    """Uses of m0 other than writing it for a load into LDS that follows at once. Such loads are written in assembly, which cannot
+    say that it overwrites m0 (a register that the compiler keeps for itself): nothing else of a kernel may rely on it."""
+    written, targets = set(), {to for _, _, to in code if to is not None}
+    bad = []
+    for i, (op, operands, _) in enumerate(code):
+        if any(re.search(r"\blds\b", x) for x in operands) and op.startswith(("buffer_load", "global_load")):
+            before = [(o, b[:1]) for o, b, _ in code[max(i - 2, 0):i]]
+            if before == [("s_mov_b32", ["m0"]), ("s_nop", ["0"])] and not targets & {i - 1, i}:
+                written.add(i - 2)
+            else:
+                bad.append((i, op, operands))
+    for i, (op, operands, _) in enumerate(code):
+        if (any(re.search(r"\bm0\b", x) for x in operands) or op.startswith(_M0_READERS)) and i not in written:
+            bad.append((i, op, operands))
+    return bad
+
+
 def verify(path: str, llvm: str, waits=WAITS) -> int:
     """The number of matrix products of a library's kernels; raises CodeError for code that must not run."""
     products = 0
@@ -136,6 +158,9 @@ def verify(path: str, llvm: str, waits=WAITS) -> int:
             bad = early_reads(code, waits)
             if bad:
                 raise CodeError(f"{path}: {name} reads a matrix-core result too early: {bad[0]}")
+            bad = m0_uses(code)
+            if bad:
+                raise CodeError(f"{path}: {name} uses m0, or does not set it for a load into LDS: {bad[0]}")
             if any(op.startswith("v_pk_") and "f32" in op for op, _, _ in code):
                 raise CodeError(f"{path}: {name} holds packed float32 instructions")
             products += sum(op.startswith("v_mfma") for op, _, _ in code)

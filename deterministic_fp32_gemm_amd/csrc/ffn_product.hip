@@ -104,7 +104,8 @@ __device__ __forceinline__ u32x4 resource(const Buffer& b) {
                  static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(b.n))), kBufferWord};
 }
 // 16 bytes a lane from offset `off` into LDS at `lds` + 16 lane. In assembly, since the compiler would otherwise wait for
-// every load in flight before each read of LDS; wait_loads() below counts them.
+// every load in flight before each read of LDS; meet() below counts them. m0 is the compiler's own and cannot be named as
+// overwritten: the build refuses code where anything else uses it (_code_check.py).
 __device__ __forceinline__ void load_lds(const u32x4& r, uint32_t lds, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r) : "memory");
 }
