@@ -22,6 +22,10 @@
  * Gates may grow (g > 0) and fall as far as the states stay in float32: products of decays over many tokens need not.
  * Values that are not finite stay in their channel and sequence; what they make of later tokens is not finite or NaN.
  *
+ * Where few runs are long, the forward call's workgroups wait on the GPU for one another's states. Each of those waits ends by
+ * itself; one of 2^22 looks (some seconds, which nothing but a fault of the machine explains) is given up, and the outputs, marks and
+ * states that come after it in its run are NaN. The status, that of the launch, does not tell.
+ *
  * Memory. sdm_seq_t: element (b, t, c) is data[b*batch + t*token + c], strides in elements; token strides below 2^31, any
  * element alignment. The states are contiguous [sequences][D], marks [sdm_glr_marks rows][D]. Outputs must not overlap
  * inputs or each other. Calls are asynchronous on `stream`, allocate nothing and may be captured into a graph.
