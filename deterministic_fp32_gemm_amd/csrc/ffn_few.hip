@@ -147,8 +147,9 @@ __global__ __launch_bounds__(kWaves * 64) void ffn_few(const sdm_ffn_args_t a) {
             x1 += sums[k][1][m][c];
         }
         if constexpr (DT == SDM_E4M3) {
-            x0 *= a.sx[m] * a.sg[col];
-            x1 *= a.sx[m] * a.su[col];
+            const Scale sm = scale_of(a.sx[m]);
+            x0 = scaled(x0, sm, scale_of(a.sg[col]));
+            x1 = scaled(x1, sm, scale_of(a.su[col]));
         }
         float h, d;
         gate<DT != SDM_F32>(x0, a.act, h, d);

@@ -336,13 +336,13 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
     char* mine = &lds[0][0] + w * 32 * kRow;
     const int col = lane % kLanes * 4;
     const int64_t n = n0 + wn * (PAIR ? WN / 2 : WN) + col, left = p.N - n;
-    float sg[4], su[4];
+    Scale sg[4], su[4];
     if constexpr (ET == kE4m3) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int64_t c = min(n + e, p.N - 1);
-            sg[e] = p.sn[c];
-            su[e] = p.sn2[c];
+            sg[e] = scale_of(p.sn[c]);
+            su[e] = scale_of(p.sn2[c]);
         }
     }
 #pragma unroll
@@ -368,11 +368,11 @@ __global__ __launch_bounds__((64 * kWaves<T, NM, NN, HALVES>), (T == 256 ? 1 : 2
                 const f32x4 y = from[WN / 8];
                 float u[4] = {y[0], y[1], y[2], y[3]}, h[4];
                 if constexpr (ET == kE4m3) {
-                    const float sm = p.sm[m];
+                    const Scale sm = scale_of(p.sm[m]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        g[e] *= sm * sg[e];
-                        u[e] *= sm * su[e];
+                        g[e] = scaled(g[e], sm, sg[e]);
+                        u[e] = scaled(u[e], sm, su[e]);
                     }
                 }
 #pragma unroll
