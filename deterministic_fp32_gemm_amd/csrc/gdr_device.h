@@ -2,7 +2,7 @@
 //
 // Split operands. The bfloat16 matrix cores run 16 times the float32 ones' rate. A float32 x is h + m + l with
 // h = bf16(x), m = bf16(x - h), l = bf16(x - h - m), each difference exact: 24 bits. A product of two such sums keeps
-// the part products whose parts' numbers add up to 2 or less; what is left out is below 2^-25 of the product, so a
+// the part products whose parts' numbers add up to 2 or less; what is left out is below 2^-24 of the product, so a
 // product costs 6 matrix-core steps and is as exact as float32's own (a quarter of the time of a float32 matrix-core
 // product). Elements that are bfloat16 to begin with are one part (3 steps against a float32 operand), float16 ones
 // two. Results of 16 bits need them all too: Q S and P U can each be thousands of times their sum, the output, where a
