@@ -110,13 +110,17 @@ Laid operand(const void* src, int64_t ld, int64_t R, int64_t C, int dtype, Space
 int product_type(int dtype) { return dtype == SDM_E4M3 ? kE4m3 : dtype == SDM_F32 ? kF32 : dtype == SDM_F16 ? kF16 : kBf16; }
 
 // 256 x 256 tiles read half of what 128 x 128 ones do for each product, and these half of 64 x 64 ones: the largest of which
-// there are enough for every CU. float32's six products a value are enough for 128 x 128 ones; their parts and the sums of
-// larger ones would not fit the registers.
+// there are enough for every CU, but where a second round of 256 x 256 ones would be half empty (one a CU, where two of 128 x 128
+// fit). 4096 values a row, bfloat16 and 8 bits, tiles of 256 and of 128 in us: 256 tiles of 256 119 and 139, 65 and 75; 261 of
+// them 187 and 162, 106 and 91; 320 194 and 172, 108 and 94; 416 205 and 230, 114 and 125; 512 231 and 267, 126 and 143. Tiles of
+// 64 instead of 256 of 128: 69 and 42 (2048 rows of 2048 to 2048), instead of fewer 21 and 22 (1024 of 2048 to 1024). float32's six
+// products a value are enough for 128 x 128 ones; their parts and the sums of larger ones would not fit the registers.
 int64_t pair_tiles(int64_t M, int64_t F, int tile) { return cdiv(M, tile) * cdiv(F, tile / 2); }
 int pair_tile(int64_t M, int64_t F, int dtype) {
-    return dtype != SDM_F32 && pair_tiles(M, F, 256) >= 256 ? 256 : pair_tiles(M, F, 128) >= 256 ? 128 : 64;
+    const int64_t large = dtype == SDM_F32 ? 0 : pair_tiles(M, F, 256);
+    return large == 256 || large >= 384 ? 256 : pair_tiles(M, F, 128) >= 256 ? 128 : 64;
 }
-// dx and both weights' gradients
+// dx and both weights' gradients: 400 tiles of 256 and more of 128 198 and 202 us, 608 319 and 348, 768 562 and 631
 int64_t gradient_tiles(int64_t M, int64_t K, int64_t F, int tile) { return (cdiv(M, tile) + cdiv(2 * F, tile)) * cdiv(K, tile); }
 int gradient_tile(int64_t M, int64_t K, int64_t F, int dtype) {
     return dtype != SDM_F32 && gradient_tiles(M, K, F, 256) >= 256 ? 256 : gradient_tiles(M, K, F, 128) >= 256 ? 128 : 64;

@@ -17,7 +17,8 @@ KIND = {"bf16": 0, "f16": 1, "e4m3": 2, "f32": 3}          # of the matrix cores
 DTYPE = {"f32": 0, "bf16": 1, "f16": 2, "e4m3": 3}
 
 # forward: rows, lengths, weights' rows, and the tile; 0: few rows
-FORWARD = [(m, 100, 41, 0) for m in (1, 15, 16)] + [(17, 100, 41, 64), (1100, 90, 1900, 128), (4010, 70, 2010, 256)]
+FORWARD = [(m, 100, 41, 0) for m in (1, 15, 16)] + [(17, 100, 41, 64), (1100, 90, 1900, 128), (4010, 70, 2010, 256),
+                                                           (4200, 70, 2010, 128), (6010, 70, 2010, 256)]
 FORWARD_F32 = [(m, 100, 41, 0) for m in (16, 17, 31, 32)] + [(33, 100, 41, 64), (1100, 90, 1900, 128), (4010, 70, 2010, 128)]
 # gradient: rows, lengths, weights' rows, the tile, the parts of dx's sums and of the weights'
 GRADIENT = [(130, 90, 70, 64, 1, 1), (3, 200, 3001, 64, 21, 1), (4001, 66, 70, 64, 1, 7), (300, 1801, 1003, 128, 1, 1), (100, 1301, 1801, 128, 7, 1),
