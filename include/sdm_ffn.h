@@ -25,8 +25,11 @@
  * Values that are not finite make NaN or infinities of the outputs that depend on them; with float32 operands (and, in the
  * same way, operands within 2^-8 of the largest float32) an infinity may come out as NaN.
  *
- * Memory. Rows are contiguous with a row stride `ld_*` in elements, at least the row's length. Any alignment; rows that
- * begin on 16 bytes (address and stride) are used where they lie, others are laid out in the workspace first. Outputs must not overlap inputs
+ * Sizes. M up to 2^21 (0 in the forward call: nothing is done), K and F from 1 to 2^20; calls of 2^32 threads a launch or more are
+ * refused (tiles of 256 x 128 of h: 2^23).
+ *
+ * Memory. Rows are contiguous with a row stride `ld_*` in elements, at least the row's length, below 2^31. Any alignment; rows that
+ * begin and end on 16 bytes (address, stride and length) are used where they lie, others are laid out in the workspace first. Outputs must not overlap inputs
  * or each other. Calls are asynchronous on `stream`, allocate nothing and may be captured into a graph. Workspaces are the
  * caller's (sdm_ffn_workspace bytes, 256-byte aligned, contents free to lose after the call).
  */

@@ -19,7 +19,8 @@
  * Types. x, y, z and their gradients are float32, bfloat16 or float16 (dtype); g and dg that or float32 (gtype); states
  * float32, and so is every sum. No atomics in sums and an order of operations set by the sizes and the sequences' lengths: the
  * same bits in every run.
- * Gates may grow (g > 0) and fall as far as the states stay in float32: products of decays over many tokens need not.
+ * exp(g) below 2^-126 may be zero. Gates may grow (g > 0) and fall as far as the states stay in float32: products of decays over many
+ * tokens need not.
  * Values that are not finite stay in their channel and sequence; what they make of later tokens is not finite or NaN.
  *
  * Where few runs are long, the forward call's workgroups wait on the GPU for one another's states. Each of those waits ends by
@@ -27,7 +28,8 @@
  * states that come after it in its run are NaN. The status, that of the launch, does not tell.
  *
  * Memory. sdm_seq_t: element (b, t, c) is data[b*batch + t*token + c], strides in elements; token strides below 2^31, any
- * element alignment. The states are contiguous [sequences][D], marks [sdm_glr_marks rows][D]. Outputs must not overlap
+ * element alignment. 1 <= D <= SDM_GLR_MAX_D; B and nseq below 2^20, B T up to 2^30, pool below 2^31. The states are contiguous
+ * [sequences][D], marks [sdm_glr_marks rows][D]. Outputs must not overlap
  * inputs or each other. Calls are asynchronous on `stream`, allocate nothing and may be captured into a graph.
  * Workspaces are the caller's (sdm_glr_workspace bytes, 16-byte aligned, contents free to lose after the call).
  */

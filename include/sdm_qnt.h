@@ -8,11 +8,11 @@
  *     s  = max(max |y| / 448, 2^-126);   q = e4m3(y / s)
  * q is OCP e4m3 (one byte: sign, 4 bits of exponent, 3 of fraction, no infinities), to the nearest, ties to even; q s stands
  * for y within 2^-4 of it where |y| >= 2^-6 s and within 2^-10 s below. y / s is taken as y times the float32 nearest 1 / s:
- * 2^-23 before a rounding of 2^-4. A row with a value that is not finite (or a mean that leaves float32) gets s = NaN and
- * q = NaN throughout.
+ * 2^-23 before a rounding of 2^-4. A row with a value that is not finite, or whose sum of squares or largest |x' w|
+ * leaves float32, gets s = NaN and q = NaN throughout.
  *
  * Types: x, r, x' float32, bfloat16 or float16 (dtype, sdm_gdr.h); w in wtype, that or float32; s float32. Rows are
- * contiguous with a row stride `ld_*` >= D in elements (of q: bytes). 1 <= D <= SDM_QNT_MAX_D. Outputs must not overlap
+ * contiguous with a row stride `ld_*` >= D in elements (of q: bytes), below 2^31. 1 <= D <= SDM_QNT_MAX_D; rows below 2^40. Outputs must not overlap
  * inputs, except that x_new may be x or r exactly (same address and stride). Asynchronous on `stream`; nothing is
  * allocated; calls may be captured into a graph.
  */
