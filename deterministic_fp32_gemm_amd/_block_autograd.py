@@ -37,11 +37,11 @@ class GatedFeedForward(torch.autograd.Function):
     """(h, g, u); the products are not differentiable outputs."""
 
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, act):
+    def forward(ctx, x, w_gate, w_up, act, precise):
         ctx.set_materialize_grads(False)
         h, kept = block.ffn_forward(x, w_gate, w_up, act=act, keep=True)
         ctx.save_for_backward(x, w_gate, w_up, *kept)
-        ctx.act = act
+        ctx.act, ctx.precise = act, precise
         ctx.mark_non_differentiable(*kept)
         return (h, *kept)
 
@@ -49,9 +49,9 @@ class GatedFeedForward(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dh, *_):
         if dh is None:
-            return (None,) * 4
+            return (None,) * 5
         x, w_gate, w_up, *kept = ctx.saved_tensors
-        return (*block.ffn_backward(dh, x, w_gate, w_up, kept, act=ctx.act), None)
+        return (*block.ffn_backward(dh, x, w_gate, w_up, kept, act=ctx.act, precise=ctx.precise), None, None)
 
 
 class NoGradient(torch.autograd.Function):

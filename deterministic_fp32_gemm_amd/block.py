@@ -58,7 +58,7 @@ class sdm_qnt_args_t(ctypes.Structure):
 
 
 class sdm_ffn_args_t(ctypes.Structure):
-    _fields_ = [("dtype", _i32), ("otype", _i32), ("act", _i32), ("reserved", _i32), ("M", _i64), ("K", _i64), ("F", _i64),
+    _fields_ = [("dtype", _i32), ("otype", _i32), ("act", _i32), ("precise", _i32), ("M", _i64), ("K", _i64), ("F", _i64),
                 ("x", _vp), ("wg", _vp), ("wu", _vp), ("ld_x", _i64), ("ld_wg", _i64), ("ld_wu", _i64), ("sx", _vp),
                 ("sg", _vp), ("su", _vp), ("h", _vp), ("ld_h", _i64), ("gate", _vp), ("up", _vp), ("ld_gate", _i64),
                 ("ld_up", _i64), ("dh", _vp), ("ld_dh", _i64), ("dx", _vp), ("dwg", _vp), ("dwu", _vp), ("ld_dx", _i64),
@@ -491,14 +491,14 @@ def _ffn_plan(x, wg, wu, act, scales, dtype, dh=None, kept=None):
 
 
 def ffn_forward(x, w_gate, w_up, *, act="silu", keep=False, x_scale=None, gate_scale=None, up_scale=None, dtype=None,
-                stream=None):
+                precise=False, stream=None):
     """The gated feed-forward product ``h = act(x w_gate^T) * (x w_up^T)``, both projections, the activation and the product
     in one kernel: h [..., F], or with keep ``(h, kept)``, kept the pair of products (float32) that ffn_backward reads.
 
     x [..., K], w_gate, w_up [F, K] of one type: float32, bfloat16, float16, or float8_e4m3fn with x_scale [...],
     gate_scale and up_scale [F] float32 (what norm_quant and quant_rows return); h has that type, or for 8-bit operands
     ``dtype``, bfloat16 (the default) or float16. act: "none", "sigmoid", "silu" or "gelu" (with the normal distribution's
-    integral)."""
+    integral). precise: ffn_backward's, for the gradient through torch's graph."""
     import torch
     scales = (x_scale, gate_scale, up_scale)
     key = ("ffn", _layout(x), _layout(w_gate), _layout(w_up), act, _layout(x_scale), _layout(gate_scale), _layout(up_scale),
@@ -511,11 +511,11 @@ def ffn_forward(x, w_gate, w_up, *, act="silu", keep=False, x_scale=None, gate_s
     if stream is not None:
         with _under(stream, dev):
             return ffn_forward(x, w_gate, w_up, act=act, keep=keep, x_scale=x_scale, gate_scale=gate_scale, up_scale=up_scale,
-                               dtype=dtype)
+                               dtype=dtype, precise=precise)
     recorded = torch.is_grad_enabled() and _requires_grad(x, w_gate, w_up, *scales)
     if recorded and x_scale is None:
         from ._block_autograd import GatedFeedForward
-        h, *kept = GatedFeedForward.apply(x, w_gate, w_up, act)
+        h, *kept = GatedFeedForward.apply(x, w_gate, w_up, act, precise)
         return (h, tuple(kept)) if keep else h
     h, kept = whole(otype), (whole(torch.float32), whole(torch.float32)) if keep else (None, None)
     inputs = (x, w_gate, w_up, *scales)
@@ -537,9 +537,11 @@ def ffn_forward(x, w_gate, w_up, *, act="silu", keep=False, x_scale=None, gate_s
     return (h, kept) if keep else h
 
 
-def ffn_backward(dh, x, w_gate, w_up, kept, *, act="silu", stream=None):
+def ffn_backward(dh, x, w_gate, w_up, kept, *, act="silu", precise=False, stream=None):
     """The gradient of ffn_forward: ``(dx, dw_gate, dw_up)`` from dh and what ffn_forward(keep=True) kept. Gradients have
-    their tensors' shapes and types (float32, bfloat16 or float16)."""
+    their tensors' shapes and types (float32, bfloat16 or float16). 16-bit types: the gradients of both products are rounded to the
+    type on their way, which makes the result's error 1.4 times that of its own rounding; with precise they are not, and the
+    products take twice as long."""
     import torch
     if not isinstance(kept, (tuple, list)) or len(kept) != 2:
         raise TypeError("kept: the pair that ffn_forward(keep=True) returned")
@@ -553,7 +555,7 @@ def ffn_backward(dh, x, w_gate, w_up, kept, *, act="silu", stream=None):
     struct, _, otype, dev, copied = plan
     if stream is not None:
         with _under(stream, dev):
-            return ffn_backward(dh, x, w_gate, w_up, kept, act=act)
+            return ffn_backward(dh, x, w_gate, w_up, kept, act=act, precise=precise)
     make = torch.empty if struct.M else torch.zeros
     dx = torch.empty(x.shape, dtype=otype, device=dev)
     dwg, dwu = (make(w_gate.shape, dtype=otype, device=dev) for _ in range(2))
@@ -564,7 +566,7 @@ def ffn_backward(dh, x, w_gate, w_up, kept, *, act="silu", stream=None):
         dh, x, w_gate, w_up, gate, up = (_flat(t) for t in (dh, x, w_gate, w_up, gate, up))
     a = sdm_ffn_args_t.from_buffer_copy(struct)
     a.dh, a.x, a.wg, a.wu, a.gate, a.up = (t.data_ptr() for t in (dh, x, w_gate, w_up, gate, up))
-    a.dx, a.dwg, a.dwu = dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr()
+    a.dx, a.dwg, a.dwu, a.precise = dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), bool(precise)
     n = load().sdm_ffn_workspace(ctypes.byref(a), 1)
     if n < 0:
         _raise(n, "ffn_backward")

@@ -149,8 +149,11 @@ Forward forward_plan(const sdm_ffn_args_t* a, char* ws) {
 // sqrt(2) times the error of the rounded result alone. The fewer values there are of dg and du (M F) and of the gradients (M K, F
 // K), the further a call is from that average: with 4096 of the fewest the errors of 500 random calls are up to 1.53 times the
 // rounded result's, with 256 up to 1.7, with 4 up to 15. Up to 4096 dg and du come in two parts, and what they meet in the products
-// twice: 1.0 (8192 rows of 64 to 64: 29 us, in one part 23).
-int gradient_parts(const sdm_ffn_args_t* a) { return a->dtype != SDM_F32 && std::min(a->M, std::max(a->K, a->F)) * std::min(a->K, a->F) <= 4096 ? 2 : 1; }
+// twice: 1.0 (8192 rows of 64 to 64: 29 us, in one part 23). Above, as the caller has it (8192 rows of 4096 to 8192: 3800 us, in one part 2000).
+int gradient_parts(const sdm_ffn_args_t* a) {
+    if (a->dtype == SDM_F32) return 1;
+    return a->precise || std::min(a->M, std::max(a->K, a->F)) * std::min(a->K, a->F) <= 4096 ? 2 : 1;
+}
 
 // A product of few tiles and a long sum is cut into parts along the sum, up to two workgroups a CU (tiles of 256: one), of 8
 // steps of 128 bytes at the least, where that saves 40 steps: joining them is one more launch (333 rows of 1111 to 777 in

@@ -20,7 +20,8 @@
  * absolute sum in all, beside operands that are rounded to 2^-4. In the backward call of 16-bit types dg and du
  * are rounded to dtype before their products (dtype's matrix instructions take no more): a gradient's error is about 1.4
  * times that of rounding it. Where the values are too few for that to average out (M K, M F or F K up to 4096) what the rounding lost
- * goes through the products as well, and it is 1.0 times. In float16 a dg or du beyond 65504 becomes infinite. The order of every
+ * goes through the products as well, and it is 1.0 times; so it does wherever the caller asks for it (`precise`: the products take
+ * twice as long). In float16 a dg or du beyond 65504 becomes infinite. The order of every
  * sum is set by the sizes alone and there are no atomics: the same bits in every run.
  * Values that are not finite make NaN or infinities of the outputs that depend on them; with float32 operands (and, in the
  * same way, operands within 2^-8 of the largest float32) an infinity may come out as NaN.
@@ -48,7 +49,8 @@ enum { SDM_E4M3 = 3 };      /* after sdm_dtype's */
 enum { SDM_ACT_GELU = 3 };  /* after sdm_act's */
 
 typedef struct sdm_ffn_args {
-    int32_t dtype, otype, act, reserved;
+    int32_t dtype, otype, act;
+    int32_t precise;             /* backward, 16-bit types: not 0: dg and du in two parts, whatever the sizes */
     int64_t M, K, F;
     const void *x, *wg, *wu;
     int64_t ld_x, ld_wg, ld_wu;
