@@ -133,3 +133,35 @@ def test_a_run_does_not_go_by_its_neighbours():
         assert torch.isfinite(y).all() and torch.isfinite(h).all()
         want = y[:, :300] if want is None else want
         assert ((y[:, :300] - want).abs() <= 300 * 8 * 2.0 ** -24 * (want.abs() + x.cuda().abs().cumsum(1))).all()
+
+
+@pytest.mark.parametrize("T,lens", [(140, None), (1300, None), (None, [900, 400])])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 100.0])
+def test_a_gate_that_is_not_finite_or_leaves_float32_stays_in_its_channel(value, T, lens):
+    """It reaches the later states of its channel and run, the gradient of what comes before, and no others."""
+    T, cu = lengths(T, lens)
+    n, D, at = 1 if lens is None else len(lens), 6, 130
+    gen = torch.Generator().manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    t = dict(x=r(1, T, D), g=-r(1, T, D).abs(), z=r(1, T, D), h0=r(n, D), dy=r(1, T, D), dh=r(n, D))
+    c = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+    def run():
+        d = {k: v.cuda() for k, v in t.items()}
+        y, h, marks = sdm.glr_forward(d["x"], d["g"], d["z"], act="sigmoid", initial_state=d["h0"], cu_seqlens=c)
+        dx, dg, dz, dh0 = sdm.glr_backward(d["x"], d["g"], d["z"], d["dy"], marks, act="sigmoid", initial_state=d["h0"], dfinal_state=d["dh"], cu_seqlens=c)
+        return {"y": y, "dx": dx, "dg": dg, "dz": dz}, h, dh0
+
+    want, h, dh0 = run()
+    t["g"][0, at, 2] = value
+    got, hh, ddh0 = run()
+    other = [0, 1, 3, 4, 5]
+    for k in got:
+        assert torch.equal(got[k][..., other], want[k][..., other]), k
+        if lens:
+            assert torch.equal(got[k][:, 900:], want[k][:, 900:]), k
+    assert torch.equal(hh[:, other], h[:, other]) and torch.equal(ddh0[:, other], dh0[:, other])
+    end = 900 if lens else T
+    # to within roundings: a channel's sums are joined the same way wherever its gates are of one kind
+    assert torch.equal(got["y"][:, :at, 2], want["y"][:, :at, 2]) and not torch.isfinite(got["y"][0, at:end, 2]).any()
+    assert torch.equal(got["dx"][:, at:, 2], want["dx"][:, at:, 2]) and not torch.isfinite(got["dx"][0, :at, 2]).any()
