@@ -18,8 +18,8 @@
 // place c ^ (r / 2 % 8). A 16-byte read serves 16 lanes at once from 64 banks, two rows' worth, and not 16 neighbouring lanes:
 // with c ^ (r % 8) half of all LDS cycles were conflicts.
 //
-// 8192 rows of 4096 to 8192: 8 bits 506 us, 2.17 PFLOP/s (the library's product of 8192^3 2.72); bfloat16 as a pair with g and u
-// kept 923 us, 1.19, and the gradient's two products 1708 us, 1.29 (1.43). The matrix cores are busy 55, 70 and 78% of the cycles
+// 8192 rows of 4096 to 8192: 8 bits 505 us, 2.18 PFLOP/s (the library's product of 8192^3 2.72); bfloat16 as a pair with g and u
+// kept 905 us, 1.21, and the gradient's two products 1671 us, 1.32 (1.43). The matrix cores are busy 55, 70 and 78% of the cycles
 // (counters); loads alone take 88% of the time and products alone 63% (timed apart): what they share is LDS and the power.
 // Rows past M or N and pieces past the row's end read as zero by the buffer's bounds.
 #include <hip/hip_runtime.h>

@@ -18,9 +18,9 @@ struct GlrPlan {
     int64_t rows;       // forward: rows of marks, whose tiles are taken from a queue (packed runs: perhaps); 0: a workgroup walks a run
     int segs;           // backward: parts that a run is cut into
 };
-// Whether runs are walked: a workgroup takes 2.7 us a tile of the longest run, the queue 10 us and 4.6 us for 256 tiles (bfloat16;
-// 2 rows of 4096 tokens and 4096 channels: 88 us walked, 73 from the queue; 7 of 2048 and 2048: 50 and 64; 16 packed runs of 512
-// tokens, 2048 channels: 33 and 52; one of 6784 and 22 of 64: 146 and 61).
+// Whether runs are walked: a workgroup takes 2.7 us a tile of the longest run, the queue 10 us and 4.6 us for 256 tiles (bfloat16,
+// whole calls; 2 rows of 4096 tokens and 4096 channels: 106 us walked, 83 from the queue; 7 of 2048 and 2048: 65 and 73; 16 packed runs
+// of 512 tokens, 2048 channels: 46 and 62, 52 where the GPU chooses; one of 6784 and 22 of 64: 168 and 71).
 __host__ __device__ inline bool glr_walks(int64_t longest, int64_t tickets) { return 27 * longest <= 100 + 46 * tickets / 256; }
 // Words of 8 bytes of the forward's workspace: the queue's counter and the choice in the first 64, then two for each tile
 // and channel.

@@ -6,7 +6,7 @@
 // from its load to its store. Since r1 is one positive number a row and rounding is monotonic, max |x' w r1| is the rounded
 // max |x' w| r1: the sum and the maximum of a row go through the workgroup together, one barrier a row. The maximum is taken
 // of the bits of |x' w|, whose order as integers is that of the values with infinities and then NaN on top: one comparison
-// finds a row that cannot be scaled. 16384 rows of 4096 in bfloat16 with a residual: 79 us, 5.9 TB/s; 5000 of 2050 in float32,
+// finds a row that cannot be scaled. 16384 rows of 4096 in bfloat16 with a residual: 80 us, 5.9 TB/s; 5000 of 2050 in float32,
 // whose rows begin on 8 bytes: 15.5 us, 3.3 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
