@@ -60,7 +60,7 @@ __device__ __forceinline__ void mma(f32x16& acc, const Piece& a, const Piece& b)
 }
 
 // Eight float32 in three bfloat16 parts each: x = h + m + l with h = bf16(x), m = bf16(x - h), l = bf16(x - h - m), every
-// difference exact: 24 bits. Products whose parts' numbers add up to 2 or less are kept, smallest first; what is left out, m l
+// difference exact: 24 bits (from 2^-110 on; below, the multiples of bfloat16's smallest step, 2^-133). Products whose parts' numbers add up to 2 or less are kept, smallest first; what is left out, m l
 // twice and l l, is below 2^-24 of the product (it comes near for 1 + 2^-8 - 2^-17 squared).
 struct Parts {
     bf16x8 p[3];

@@ -14,15 +14,17 @@
  * float32 scale for each of their rows (sx [M], sg and su [F]: the value is the byte's times its row's), h in otype,
  * bfloat16 or float16; for the other types otype is dtype. Products run on the matrix cores and are summed in float32; h and
  * the gradients are rounded once, and the kept g and u not at all (rounded to 16 bits they would add as much to the error of
- * the gradients as the rounding of dg and du does). float32 operands are split into three bfloat16 parts and six part products kept, which
- * hold float32's 24 bits; few rows take float32 matrix instructions instead. The 8-bit matrix instructions cut each product
- * of a group of 8 adjacent elements off below 2^-13 of the group's largest before they add it: about 2^-16 of the products'
- * absolute sum in all, beside operands that are rounded to 2^-4. In the backward call of 16-bit types dg and du
- * are rounded to dtype before their products (dtype's matrix instructions take no more): a gradient's error is about 1.4
- * times that of rounding it. Where the values are too few for that to average out (M K, M F or F K up to 4096) what the rounding lost
- * goes through the products as well, and it is 1.0 times; so it does wherever the caller asks for it (`precise`: the products take
- * twice as long). In float16 a dg or du beyond 65504 becomes infinite. The order of every
- * sum is set by the sizes alone and there are no atomics: the same bits in every run.
+ * the gradients as the rounding of dg and du does).
+ *
+ * float32 operands are split into three bfloat16 parts and six part products kept, which hold float32's 24 bits of operands from
+ * 2^-110 on and multiples of 2^-133 below; few rows take float32 matrix instructions instead. The 8-bit matrix instructions cut
+ * each product of a group of 8 adjacent elements off below 2^-13 of the group's largest before they add it: about 2^-16 of the
+ * products' absolute sum in all, beside operands that are rounded to 2^-4. In the backward call of 16-bit types dg and du are
+ * rounded to dtype before their products (dtype's matrix instructions take no more): a gradient's error is about 1.4 times that of
+ * rounding it. Where the values are too few for that to average out (M K, M F or F K up to 4096), or where the caller asks for it
+ * (`precise`: the products take twice as long), what the rounding lost goes through the products as well, and it is 1.0 times. In
+ * float16 a dg or du beyond 65504 becomes infinite. The order of every sum is set by the sizes and `precise` alone and there are no
+ * atomics: the same bits in every run.
  * Values that are not finite make NaN or infinities of the outputs that depend on them; with float32 operands (and, in the
  * same way, operands within 2^-8 of the largest float32) an infinity may come out as NaN.
  *
